@@ -275,6 +275,133 @@ MUON_API int muon_adamw_step(void* const* P, const void* const* G, float* const*
                              float lr, float beta1, float beta2, float eps, float wd, int step,
                              cudaStream_t stream);
 
+/*
+ * Operators around the step: routing, the experts' 8-bit products, and the
+ * global gradient norm in front of the update.  They keep the conventions
+ * above (current device, asynchronous on `stream`, validated before anything is
+ * enqueued) and neither allocate nor keep device memory: a call that needs
+ * scratch takes it as an argument.  They may be captured in a CUDA graph from
+ * their first call on.  Device pointers need the alignment of their elements
+ * unless a call says more.
+ */
+
+/*
+ * Global 2-norm of a list of gradients, sqrt(sum of squares over every
+ * element of every tensor).
+ *   G[i], numel[i], dtypes[i]  flat tensor, its elements (0 = skipped), its
+ *                     muon_dtype; bf16 and fp32 tensors may be mixed.
+ *   workspace         device, 16-byte aligned, muon_grad_norm_workspace_bytes(...)
+ *   norm              device float that receives the norm.
+ * Squares are summed in fp32 over at most 128 elements, then in fp64; tensors
+ * whose squares over- or underflow fp32 are summed in fp64 throughout.  The
+ * order is fixed: the same list gives the same bits.  An infinite or NaN
+ * gradient gives an infinite or NaN norm.  An empty list gives 0.
+ */
+MUON_API size_t muon_grad_norm_workspace_bytes(const long long* numel, int count);
+MUON_API int muon_grad_norm(const void* const* G, const long long* numel, const int* dtypes, int count,
+                            void* workspace, size_t workspace_bytes, float* norm, cudaStream_t stream);
+
+/*
+ * muon_grad_norm, then every gradient times min(1, max_norm / (norm + 1e-6)),
+ * rounded once: in place (out NULL; nothing is written where the factor is 1)
+ * or to out[i] (same dtypes; not overlapping other gradients).  norm receives the norm before
+ * clipping.  max_norm >= 0.
+ */
+MUON_API int muon_grad_clip(void* const* G, void* const* out, const long long* numel, const int* dtypes, int count,
+                            float max_norm, void* workspace, size_t workspace_bytes, float* norm,
+                            cudaStream_t stream);
+
+/*
+ * Routing of tokens to experts -- "Domyn is training a 1T-parameter MoE on
+ * Europe's Jupiter supercomputer...": 384 experts, 8 chosen (table "The model
+ * and the machine"), group-limited routing (section "What moved the number").
+ *   s = softmax(logits) or sigmoid(logits); c = s + bias (NULL: 0), for the
+ *   choice only; of the `groups` equal groups of experts the top_groups with the
+ *   largest sum of their two largest c stay; of their experts the top_k largest c
+ *   are chosen, in descending order, equal values by ascending index.
+ *   weights = scale * s / (sum of the chosen s) (renormalize) or scale * s.
+ *   logits   tokens x experts, `dtype`, row stride ld >= experts
+ *   weights  tokens x top_k (fp32);  chosen  tokens x top_k
+ *   counts   experts: how many tokens chose each expert (overwritten)
+ * A logit of -inf (or a bias of -inf) masks an expert; places for which no
+ * expert is left get expert -1 and weight 0 and are not counted.
+ * Limits: experts <= 1024, top_k <= 32, groups <= 32 dividing experts, and at
+ * most 32 * 2^floor(log2(32 / groups)) experts in a group (always so up to 512).
+ */
+typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score;
+typedef struct {
+    int top_k;                /* default 1 */
+    int groups, top_groups;   /* default 1, 1 */
+    int score;                /* muon_score, default MUON_SCORE_SOFTMAX */
+    int renormalize;          /* default 1 */
+    float scale;              /* default 1 */
+} muon_route_opts;
+MUON_API void muon_route_opts_init(muon_route_opts* opts);
+MUON_API int muon_route(const void* logits, int dtype, long long tokens, int experts, long long ld,
+                        const float* bias, const muon_route_opts* opts, float* weights, int* chosen, int* counts,
+                        cudaStream_t stream);
+
+/*
+ * Gradient of the logits from the gradient of the weights, for the experts
+ * that muon_route chose (entries of -1 take no part).  d_logits: tokens x
+ * experts, of the logits' dtype, row stride ld_d, not overlapping the logits.
+ * The bias gets no gradient.
+ */
+MUON_API int muon_route_backward(const float* d_weights, const void* logits, int dtype, long long tokens,
+                                 int experts, long long ld, const int* chosen, const muon_route_opts* opts,
+                                 void* d_logits, long long ld_d, cudaStream_t stream);
+
+/*
+ * E4M3 codes with one power-of-two scale for each block of 128 -- the experts'
+ * products in 8 bits (the open question of the same page's section "What moved
+ * the number").  e is the smallest integer with max|x| <= 448 * 2^e over a
+ * block (0 for a zero block), stored as the byte e + 127 (E8M0); a code is
+ * x * 2^-e rounded to E4M3, nearest even.  A NaN or an infinity becomes E4M3's
+ * NaN.  Codes keep the layout of x with rows of `cols` rounded up to 128 bytes,
+ * zero past the last column; 16-byte aligned.
+ *   x           rows x cols, `dtype`, row stride ld
+ *   row blocks  128 columns of one row:  row_codes rows x up128(cols),
+ *               row_scale (up128(cols) / 128) x rows
+ *   col blocks  128 rows of one column, anew at the first row of each of
+ *               `groups` groups (offsets: groups + 1 device ints, rows
+ *               [offsets[g], offsets[g + 1]); NULL: one group of all rows), each
+ *               group padded with zero rows to a multiple of 128:
+ *               col_codes muon_fp8_padded_rows(rows, groups) x up128(cols),
+ *               col_scale (padded rows / 128) x up128(cols)
+ * Either pair of outputs may be NULL; both come from one read of x.  With
+ * groups, rows outside every group are left out.
+ */
+MUON_API long long muon_fp8_padded_rows(long long rows, int groups);
+MUON_API int muon_fp8_quantize(const void* x, int dtype, long long rows, long long cols, long long ld, int groups,
+                               const int* offsets, void* row_codes, void* row_scale, void* col_codes,
+                               void* col_scale, cudaStream_t stream);
+
+/* The same for `batch` weights, rows x cols each, contiguous, with 128 x 128
+ * blocks: codes batch x rows x up128(cols), scale batch x ceil(rows / 128) x
+ * ceil(cols / 128). */
+MUON_API int muon_fp8_quantize_weight(const void* w, int dtype, int batch, long long rows, long long cols,
+                                      void* codes, void* scale, cudaStream_t stream);
+
+/*
+ * The products of one linear layer, or of the layers of `groups` experts over
+ * tokens sorted by expert (rows [offsets[g], offsets[g + 1]) are expert g's;
+ * offsets stay on the device; NULL: one group of all rows).  W is n x k.
+ *   MUON_FP8_FORWARD      out[t, n] = sum_k x[t, k] W_g[n, k]
+ *                         a: x's row blocks;  b: W's 128 x 128 blocks
+ *   MUON_FP8_GRAD_INPUT   out[t, k] = sum_n dy[t, n] W_g[n, k]
+ *                         a: dy's row blocks; b: W's 128 x 128 blocks
+ *   MUON_FP8_GRAD_WEIGHT  out[g, n, k] = sum over group g's t of dy[t, n] x[t, k]
+ *                         a: dy's col blocks; b: x's col blocks
+ * Sums in fp32 (in the tensor core, scales included), rounded once to out_dtype.
+ * out has row stride ld_out (grad weight: groups x n rows).  Rows outside every
+ * group are left as they are; the weight gradient of an empty group is zero.
+ * Offsets that descend or leave [0, tokens] are clamped.
+ */
+typedef enum { MUON_FP8_FORWARD = 0, MUON_FP8_GRAD_INPUT = 1, MUON_FP8_GRAD_WEIGHT = 2 } muon_fp8_products;
+MUON_API int muon_fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes,
+                              const void* b_scale, long long tokens, int n, int k, int groups, const int* offsets,
+                              void* out, int out_dtype, long long ld_out, cudaStream_t stream);
+
 /* Device workspace (bytes) that one call on these shapes needs; 0 on bad args. */
 MUON_API size_t muon_workspace_bytes(const int* rows, const int* cols, int count);
 
@@ -301,7 +428,8 @@ MUON_API void muon_release_workspace(void);
  * per-kernel totals.  Disabled by default; enabling adds two event records per
  * launch.  Names: norm_pass, norm_finalize, pack, ns_gemm_gram, ns_gemm_poly,
  * ns_gemm_update, ns_gemm_final (the last update with the weight update or
- * the store of O in its epilogue), ns_small, unpack, adamw.
+ * the store of O in its epilogue), ns_small, unpack, adamw, grad_norm, grad_clip,
+ * route, route_backward, fp8_quantize, fp8_gemm.
  */
 typedef struct {
     char name[40];            /* kernel name */

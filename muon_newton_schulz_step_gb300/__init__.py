@@ -14,13 +14,19 @@ The functions mirror the C ABI in ``include/muon.h``:
     muon_device_status(stream=None)
     muon_release_workspace()
     muon_profile_enable(on), muon_profile_read()
+    muon_grad_norm(G), muon_grad_clip(G, max_norm, out=None)
+    muon_route(logits, top_k, ...), muon_route_backward(d_weights, logits, chosen, ...)
+    muon_fp8_quantize(x, ...), muon_fp8_quantize_weight(w), muon_fp8_product(product, a, b, ...)
+    muon_fp8_linear(x, w, offsets), muon_fp8_linear_backward(dy, x, w, offsets)
 
 The method: the per-matrix Muon step over whole matrices held on one rank
 ("How PyTorch Scaled a Near-1T MoE on Europe's Public Supercomputer", section
 "Three optimizations that changed the economics", FlexShard bullet).
 """
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -30,6 +36,9 @@ __all__ = [
     "muon_device_status", "muon_release_workspace", "muon_profile_enable",
     "muon_profile_read", "muon_status_string", "MuonStepBatch", "muon_ns5_batched_static",
     "MUON_STATIC_SCRATCH_BYTES", "muon_step_host", "muon_ns_batched_ex", "muon_adamw_step",
+    "muon_grad_norm", "muon_grad_clip", "muon_route", "muon_route_backward", "Fp8Matrix", "muon_fp8_quantize",
+    "muon_fp8_quantize_weight", "muon_fp8_product", "muon_fp8_padded_rows", "muon_fp8_linear",
+    "muon_fp8_linear_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +51,9 @@ EXPORTS = (
     "muon_workspace_bytes", "muon_status_string", "muon_last_error",
     "muon_device_status", "muon_release_workspace", "muon_profile_enable",
     "muon_profile_read", "muon_ns5_batched_static", "muon_step_host", "muon_ns_batched_ex",
-    "muon_adamw_step",
+    "muon_adamw_step", "muon_grad_norm_workspace_bytes", "muon_grad_norm", "muon_grad_clip", "muon_route_opts_init",
+    "muon_route", "muon_route_backward", "muon_fp8_padded_rows", "muon_fp8_quantize", "muon_fp8_quantize_weight",
+    "muon_fp8_product",
 )
 
 MUON_STATIC_SCRATCH_BYTES = 64 << 20
@@ -62,6 +73,11 @@ class _Opts(ctypes.Structure):
                 ("nesterov", ctypes.c_int), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("o_out", ctypes.POINTER(ctypes.c_void_p)),
                 ("coeffs_per_step", ctypes.c_int), ("g_count", ctypes.c_int), ("ns_fp8_gram", ctypes.c_int)]
+
+
+class _RouteOpts(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("score", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class _KernelStat(ctypes.Structure):
@@ -119,6 +135,28 @@ def lib():
     L.muon_profile_enable.restype = ctypes.c_int
     L.muon_profile_read.argtypes = [ctypes.POINTER(_KernelStat), ctypes.c_int, ip]
     L.muon_profile_read.restype = ctypes.c_int
+    ci, ll, sz, llp = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(ctypes.c_longlong)
+    rop = ctypes.POINTER(_RouteOpts)
+    L.muon_grad_norm_workspace_bytes.argtypes = [llp, ci]
+    L.muon_grad_norm_workspace_bytes.restype = sz
+    L.muon_grad_norm.argtypes = [vpp, llp, ip, ci, vp, sz, vp, vp]
+    L.muon_grad_norm.restype = ci
+    L.muon_grad_clip.argtypes = [vpp, vpp, llp, ip, ci, ctypes.c_float, vp, sz, vp, vp]
+    L.muon_grad_clip.restype = ci
+    L.muon_route_opts_init.argtypes = [rop]
+    L.muon_route_opts_init.restype = None
+    L.muon_route.argtypes = [vp, ci, ll, ci, ll, vp, rop, vp, vp, vp, vp]
+    L.muon_route.restype = ci
+    L.muon_route_backward.argtypes = [vp, vp, ci, ll, ci, ll, vp, rop, vp, ll, vp]
+    L.muon_route_backward.restype = ci
+    L.muon_fp8_padded_rows.argtypes = [ll, ci]
+    L.muon_fp8_padded_rows.restype = ll
+    L.muon_fp8_quantize.argtypes = [vp, ci, ll, ll, ll, ci, vp, vp, vp, vp, vp, vp]
+    L.muon_fp8_quantize.restype = ci
+    L.muon_fp8_quantize_weight.argtypes = [vp, ci, ci, ll, ll, vp, vp, vp]
+    L.muon_fp8_quantize_weight.restype = ci
+    L.muon_fp8_product.argtypes = [ci, vp, vp, vp, vp, ll, ci, ci, ci, vp, vp, ci, ll, vp]
+    L.muon_fp8_product.restype = ci
     _lib = L
     return L
 
@@ -423,9 +461,9 @@ def muon_profile_enable(on: bool = True) -> None:
 
 
 def muon_profile_read():
-    arr = (_KernelStat * 16)()
+    arr = (_KernelStat * 32)()
     n = ctypes.c_int(0)
-    _check(lib().muon_profile_read(arr, 16, ctypes.byref(n)))
+    _check(lib().muon_profile_read(arr, 32, ctypes.byref(n)))
     return [{"name": arr[i].name.decode(), "launches": arr[i].launches, "total_ms": arr[i].total_ms,
              "flops": arr[i].flops, "bytes": arr[i].bytes} for i in range(n.value)]
 
@@ -453,3 +491,335 @@ class MuonStepBatch:
         _check(lib().muon_step_ex(self._w, self._g, self._m, self._rows, self._cols, len(self.W),
                                   float(lr), float(mu), float(wd), ctypes.byref(self._opts),
                                   _stream_handle(stream)))
+
+
+# ----------------------------------------------- operators around the step --
+def _on(stream):
+    """Context in which new tensors belong to ``stream`` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _check_flat(name, tensors, like=None):
+    device = torch.cuda.current_device() if tensors else None
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _FLOATS or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
+        if t.get_device() != device:
+            _check_device(f"{name}[{i}]", t, device)
+        if like is not None and (t.dtype != like[i].dtype or t.numel() != like[i].numel()):
+            raise ValueError(f"{name}[{i}] must have G[{i}]'s dtype and number of elements")
+
+
+def _norm_args(G, stream):
+    n = len(G)
+    numel = (ctypes.c_longlong * max(1, n))(*[t.numel() for t in G])
+    dtypes = (ctypes.c_int * max(1, n))(*[1 if t.dtype is torch.float32 else 0 for t in G])
+    need = lib().muon_grad_norm_workspace_bytes(numel, n)
+    # one allocation: the norm first, the partial sums behind it
+    buf = torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")
+    return numel, dtypes, need, buf
+
+
+def muon_grad_norm(G, stream=None) -> torch.Tensor:
+    """Global 2-norm of a list of contiguous CUDA gradients (bf16 and fp32 may
+    be mixed), as a 0-dim fp32 CUDA tensor."""
+    G = list(G)
+    _check_flat("G", G)
+    with _on(stream):
+        numel, dtypes, need, buf = _norm_args(G, stream)
+        _check(lib().muon_grad_norm(_ptr_array(G), numel, dtypes, len(G), buf.data_ptr() + 16, need, buf.data_ptr(),
+                                    _stream_handle(stream)))
+    return buf[0]
+
+
+def muon_grad_clip(G, max_norm: float, out=None, stream=None) -> torch.Tensor:
+    """Scale every gradient by min(1, max_norm / (norm + 1e-6)), in place or
+    into ``out`` (tensors like G); returns the norm before clipping (0-dim
+    fp32 CUDA tensor).  Nothing is read back to the host."""
+    G = list(G)
+    _check_flat("G", G)
+    optr = None
+    if out is not None:
+        out = list(out)
+        if len(out) != len(G):
+            raise ValueError("out must have one tensor for each of G")
+        _check_flat("out", out, like=G)
+        optr = _ptr_array(out)
+    with _on(stream):
+        numel, dtypes, need, buf = _norm_args(G, stream)
+        _check(lib().muon_grad_clip(_ptr_array(G), optr, numel, dtypes, len(G), float(max_norm), buf.data_ptr() + 16,
+                                    need, buf.data_ptr(), _stream_handle(stream)))
+    return buf[0]
+
+
+def _check_rows(name, t, dtypes, rows=None, cols=None):
+    """A 2-D CUDA tensor whose rows are contiguous (any row stride that does not
+    overlap them); returns the row stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of {dtypes}")
+    _check_device(name, t)
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected ({rows}, {cols})")
+    if t.shape[0] <= 1:
+        ld = t.shape[1]
+    else:
+        ld = t.stride(0)
+    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or ld < t.shape[1]):
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return max(ld, t.shape[1])
+
+
+def _check_vector(name, t, dtype, n):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != (n,) \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    _check_device(name, t)
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_opts(top_k, score, groups, top_groups, renormalize, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}")
+    return _RouteOpts(int(top_k), int(groups), int(groups if top_groups is None else top_groups), _SCORES[score],
+                      1 if renormalize else 0, float(scale))
+
+
+def muon_route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, top_groups=None,
+               renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Choose ``top_k`` experts for each row of ``logits`` (tokens x experts,
+    bf16 or fp32): (weights fp32 tokens x top_k, experts int32 tokens x top_k,
+    tokens of each expert int32).  ``bias`` (fp32, one per expert) steers the
+    choice only; ``groups`` / ``top_groups`` limit it to the best groups of
+    consecutive experts.  Experts masked by a logit of -inf are not chosen;
+    places left over get expert -1 and weight 0."""
+    ld = _check_rows("logits", logits, _FLOATS)
+    tokens, experts = logits.shape
+    if bias is not None:
+        _check_vector("bias", bias, torch.float32, experts)
+    o = _route_opts(top_k, score, groups, top_groups, renormalize, scale)
+    with _on(stream):
+        weights = torch.empty((tokens, int(top_k)), dtype=torch.float32, device="cuda")
+        chosen = torch.empty((tokens, int(top_k)), dtype=torch.int32, device="cuda")
+        counts = torch.empty(experts, dtype=torch.int32, device="cuda")
+        _check(lib().muon_route(logits.data_ptr(), _dtype_code(logits), tokens, experts, ld,
+                                None if bias is None else bias.data_ptr(), ctypes.byref(o), weights.data_ptr(),
+                                chosen.data_ptr(), counts.data_ptr(), _stream_handle(stream)))
+    return weights, chosen, counts
+
+
+def muon_route_backward(d_weights, logits, chosen, *, score: str = "softmax", renormalize: bool = True,
+                        scale: float = 1.0, stream=None) -> torch.Tensor:
+    """Gradient of the logits (their dtype) from that of ``muon_route``'s
+    weights, for the experts it chose."""
+    ld = _check_rows("logits", logits, _FLOATS)
+    tokens, experts = logits.shape
+    if not isinstance(chosen, torch.Tensor) or chosen.dim() != 2:
+        raise ValueError("chosen must be a 2-D CUDA tensor")
+    top_k = chosen.shape[1]
+    for name, t, dt in (("chosen", chosen, torch.int32), ("d_weights", d_weights, torch.float32)):
+        _check_rows(name, t, (dt,), tokens, top_k)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    o = _route_opts(top_k, score, 1, 1, renormalize, scale)
+    with _on(stream):
+        d = torch.empty((tokens, experts), dtype=logits.dtype, device="cuda")
+        _check(lib().muon_route_backward(d_weights.data_ptr(), logits.data_ptr(), _dtype_code(logits), tokens, experts,
+                                         ld, chosen.data_ptr(), ctypes.byref(o), d.data_ptr(), experts,
+                                         _stream_handle(stream)))
+    return d
+
+
+class Fp8Matrix(NamedTuple):
+    """E4M3 codes with one E8M0 scale byte (exponent + 127) for each block of 128.
+
+    ``kind`` "row" (128 columns of one row), "col" (128 rows of one column,
+    groups padded to multiples of 128 rows) or "block" (128 x 128).
+    ``codes``: float8_e4m3fn, rows x cols rounded up to 128, zero past ``cols``
+    ("block": optionally stacked, experts x rows x ...).  ``scale``: uint8 --
+    "row" (column blocks, rows), "col" (row blocks, codes' columns), "block"
+    (..., row blocks, column blocks)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    kind: str
+    cols: int
+
+
+def _up128(n):
+    return (n + 127) // 128 * 128
+
+
+def _check_offsets(offsets, groups=None):
+    """(groups, device pointer or None) of the row offsets of tokens sorted by expert."""
+    if offsets is None:
+        return 1, None
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a 1-D int32 CUDA tensor of groups + 1 entries")
+    _check_vector("offsets", offsets, torch.int32, offsets.numel() if groups is None else groups + 1)
+    return offsets.numel() - 1, offsets.data_ptr()
+
+
+def muon_fp8_padded_rows(rows: int, groups: int = 1) -> int:
+    """Rows of the "col" codes of ``rows`` rows in ``groups`` groups."""
+    return int(lib().muon_fp8_padded_rows(int(rows), int(groups)))
+
+
+def muon_fp8_quantize(x, *, row: bool = True, col: bool = False, offsets=None, stream=None):
+    """``x`` (2-D, bf16 or fp32) as E4M3 with scales for blocks of 128 along its
+    rows (``row``), along its columns (``col``; blocks start anew at each group
+    of ``offsets``), or both from one read: (row Fp8Matrix or None, col
+    Fp8Matrix or None)."""
+    ld = _check_rows("x", x, _FLOATS)
+    rows, cols = x.shape
+    groups, optr = _check_offsets(offsets)
+    ldq = _up128(cols)
+    with _on(stream):
+        r = c = None
+        if row:
+            r = Fp8Matrix(torch.empty((rows, ldq), dtype=torch.float8_e4m3fn, device="cuda"),
+                          torch.empty((ldq // 128, rows), dtype=torch.uint8, device="cuda"), "row", cols)
+        if col:
+            padded = muon_fp8_padded_rows(rows, groups)
+            c = Fp8Matrix(torch.empty((padded, ldq), dtype=torch.float8_e4m3fn, device="cuda"),
+                          torch.empty((padded // 128, ldq), dtype=torch.uint8, device="cuda"), "col", cols)
+        _check(lib().muon_fp8_quantize(x.data_ptr(), _dtype_code(x), rows, cols, ld, groups, optr,
+                                       r.codes.data_ptr() if row else None, r.scale.data_ptr() if row else None,
+                                       c.codes.data_ptr() if col else None, c.scale.data_ptr() if col else None,
+                                       _stream_handle(stream)))
+    return r, c
+
+
+def muon_fp8_quantize_weight(w, stream=None) -> Fp8Matrix:
+    """A weight (rows x cols, or stacked experts x rows x cols; bf16 or fp32,
+    contiguous) as E4M3 with a scale for each 128 x 128 block."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3) or not w.is_cuda or w.dtype not in _FLOATS \
+            or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous 2-D or 3-D CUDA tensor of {_FLOATS}")
+    _check_device("w", w)
+    rows, cols = w.shape[-2:]
+    with _on(stream):
+        m = Fp8Matrix(torch.empty((*w.shape[:-1], _up128(cols)), dtype=torch.float8_e4m3fn, device="cuda"),
+                      torch.empty((*w.shape[:-2], _up128(rows) // 128, _up128(cols) // 128), dtype=torch.uint8,
+                                  device="cuda"), "block", cols)
+        _check(lib().muon_fp8_quantize_weight(w.data_ptr(), _dtype_code(w), w.shape[0] if w.dim() == 3 else 1, rows, cols,
+                                              m.codes.data_ptr(), m.scale.data_ptr(), _stream_handle(stream)))
+    return m
+
+
+def _check_fp8(name, m, kind, codes_shape, scale_shape):
+    if not isinstance(m, Fp8Matrix) or m.kind != kind:
+        raise ValueError(f'{name} must be an Fp8Matrix of kind "{kind}"')
+    for what, t, dt, shape in (("codes", m.codes, torch.float8_e4m3fn, codes_shape),
+                               ("scale", m.scale, torch.uint8, scale_shape)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt or not t.is_contiguous() \
+                or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}.{what} must be a contiguous CUDA tensor of {dt} with shape {tuple(shape)}")
+        _check_device(f"{name}.{what}", t)
+
+
+def _check_weight(w, offsets):
+    """(n, k, groups) of a "block" weight that goes with ``offsets``."""
+    if not isinstance(w, Fp8Matrix) or not isinstance(w.codes, torch.Tensor) or w.codes.dim() not in (2, 3):
+        raise ValueError('the weight must be an Fp8Matrix of kind "block" with 2-D or 3-D codes')
+    n, k = w.codes.shape[-2], int(w.cols)
+    lead = tuple(w.codes.shape[:-2])
+    if bool(lead) != (offsets is not None):
+        raise ValueError("a stacked weight goes with offsets, a single one without")
+    _check_fp8("the weight", w, "block", (*lead, n, _up128(k)), (*lead, _up128(n) // 128, _up128(k) // 128))
+    return n, k, lead[0] if lead else 1
+
+
+def _product(code, a, b, tokens, n, k, groups, optr, out, ld, stream):
+    _check(lib().muon_fp8_product(code, a.codes.data_ptr(), a.scale.data_ptr(), b.codes.data_ptr(), b.scale.data_ptr(),
+                                  tokens, n, k, groups, optr, out.data_ptr(), _dtype_code(out), ld,
+                                  _stream_handle(stream)))
+
+
+def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None, out_dtype=torch.bfloat16,
+                     stream=None):
+    """One product of a linear layer on E4M3 operands (``Fp8Matrix``):
+
+    "forward"      out[t, n] = sum_k a[t, k] b[g, n, k]     a "row", b "block"
+    "grad_input"   out[t, k] = sum_n a[t, n] b[g, n, k]     a "row", b "block"
+    "grad_weight"  out[g, n, k] = sum_t a[t, n] b[t, k]     a "col", b "col"
+
+    With ``offsets`` (int32, experts + 1, on the device) rows offsets[g] to
+    offsets[g + 1] are expert g's and b (or out) is stacked over experts.
+    ``tokens`` (grad_weight): the rows that the operands were made from.
+    ``out``: optional preallocated result, bf16 or fp32 (rows contiguous)."""
+    if product in ("forward", "grad_input"):
+        n, k, groups = _check_weight(b, offsets)
+        _, optr = _check_offsets(offsets, groups)
+        inner, red = (n, k) if product == "forward" else (k, n)
+        if not isinstance(a, Fp8Matrix) or not isinstance(a.codes, torch.Tensor) or a.codes.dim() != 2 or a.cols != red:
+            raise ValueError(f'a must be an Fp8Matrix of kind "row" with {red} columns')
+        tokens = a.codes.shape[0]
+        _check_fp8("a", a, "row", (tokens, _up128(red)), (_up128(red) // 128, tokens))
+        with _on(stream):
+            if out is None:
+                out = torch.empty((tokens, inner), dtype=out_dtype, device="cuda")
+            ld = _check_rows("out", out, _FLOATS, tokens, inner)
+            _product(0 if product == "forward" else 1, a, b, tokens, n, k, groups, optr, out, ld, stream)
+        return out
+    if product != "grad_weight":
+        raise ValueError('product must be "forward", "grad_input" or "grad_weight"')
+    groups, optr = _check_offsets(offsets)
+    if tokens is None:
+        raise ValueError('"grad_weight" needs tokens, the number of rows that the operands were made from')
+    tokens = int(tokens)
+    padded = muon_fp8_padded_rows(tokens, groups)
+    for name, m in (("a", a), ("b", b)):
+        if not isinstance(m, Fp8Matrix):
+            raise ValueError(f'{name} must be an Fp8Matrix of kind "col"')
+        _check_fp8(name, m, "col", (padded, _up128(m.cols)), (padded // 128, _up128(m.cols)))
+    n, k = int(a.cols), int(b.cols)
+    shape = (n, k) if offsets is None else (groups, n, k)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device="cuda")
+        elif not isinstance(out, torch.Tensor) or not out.is_cuda or out.dtype not in _FLOATS \
+                or tuple(out.shape) != shape or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous CUDA tensor of {_FLOATS} with shape {shape}")
+        _check_device("out", out)
+        _product(2, a, b, tokens, n, k, groups, optr, out, k, stream)
+    return out
+
+
+def muon_fp8_linear(x, w, *, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = x W^T in 8 bits: ``x`` (tokens x k, bf16 or fp32) is rounded to E4M3 by
+    row blocks and multiplied with ``w`` (``muon_fp8_quantize_weight``).  With
+    ``offsets``, tokens are sorted by expert and ``w`` is stacked over experts."""
+    n, k, _ = _check_weight(w, offsets)
+    _check_rows("x", x, _FLOATS, None, k)
+    q, _ = muon_fp8_quantize(x, stream=stream)
+    return muon_fp8_product("forward", q, w, offsets=offsets, out_dtype=out_dtype, stream=stream)
+
+
+def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, need_dw: bool = True,
+                             dx_dtype=torch.bfloat16, dw_dtype=torch.bfloat16, stream=None):
+    """(dx, dW) of ``muon_fp8_linear`` from dy (tokens x n): dx = dy W with dy by
+    row blocks, dW = dy^T x with both by col blocks; either may be left out
+    (None).  dy is read once for both."""
+    n, k, groups = _check_weight(w, offsets)
+    tokens = dy.shape[0] if isinstance(dy, torch.Tensor) and dy.dim() == 2 else None
+    _check_rows("dy", dy, _FLOATS, None, n)
+    _check_rows("x", x, _FLOATS, tokens, k)
+    _check_offsets(offsets, groups)
+    dx = dw = None
+    if need_dx or need_dw:
+        dr, dc = muon_fp8_quantize(dy, row=need_dx, col=need_dw, offsets=offsets if need_dw else None, stream=stream)
+        if need_dx:
+            dx = muon_fp8_product("grad_input", dr, w, offsets=offsets, out_dtype=dx_dtype, stream=stream)
+        if need_dw:
+            _, xc = muon_fp8_quantize(x, row=False, col=True, offsets=offsets, stream=stream)
+            dw = muon_fp8_product("grad_weight", dc, xc, tokens=tokens, offsets=offsets, out_dtype=dw_dtype,
+                                  stream=stream)
+    return dx, dw

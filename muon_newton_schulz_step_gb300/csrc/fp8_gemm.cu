@@ -1,0 +1,504 @@
+// Products of E4M3 matrices with one power-of-two scale for each block of 128
+// along the reduction, on pairs of SMs (tcgen05 cta_group::2, block scaling in
+// the tensor core).
+//
+//   forward       y[t, n]    = sum_k  x[t, k]  W_g[n, k]     tokens t of group g
+//   grad input    dx[t, k]   = sum_n dy[t, n]  W_g[n, k]
+//   grad weight   dW_g[n, k] = sum_t dy[t, n]   x[t, k]      t over group g
+//
+// The experts' products of the pages' model (384 experts, 96 whole ones on a
+// rank; 8-bit products for expert matrices are the open question of "Domyn is
+// training a 1T-parameter MoE on Europe's Jupiter supercomputer, and published
+// the recipe", section "What moved the number").
+//
+// Scales are powers of two (E8M0), the form that tcgen05.mma takes itself: the
+// accumulators stay in TMEM over the whole reduction and no register ever
+// rescales them.  One scale covers 128 elements, four K = 32 instructions; the
+// scale words hold four reduction blocks' bytes, so one 32 x 16-byte copy per
+// 128 rows feeds sixteen instructions, each naming its byte.
+//
+// Layout of a tile: MMA rows (256, 128 per CTA) run along the output's
+// contiguous index, MMA columns along its rows.  So tokens are MMA columns,
+// and a group's tile is as wide as the group needs (a multiple of 32 up to
+// 256): an expert with 40 tokens costs a 64-column tile and not 256 rows.  It
+// also makes the epilogue store 32 consecutive outputs per warp instruction,
+// at any row start and any row stride, with no alignment to keep.
+//
+// Codes keep one layout: the weight is read along either dimension (K-major or
+// MN-major operand descriptors), so nothing is transposed.
+//
+// Per CTA: warp 0 TMA producer (6 stages of 32 KB), warp 1 MMA issuer (leader
+// only), warp 2 scale words, warps 4-11 epilogue.  Two accumulators of 256
+// columns and the scales do not fit in 512 TMEM columns: the second accumulator
+// starts at column 224, and the 32 columns that both own are drained first, so
+// the next tile's products wait for an eighth of the epilogue.  Every wait is
+// bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "groups.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace muon {
+
+// Device-side status word of this kernel: 0, or MUON_ERR_TIMEOUT (5).
+__device__ int g_muon_fp8_error = 0;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 256;
+constexpr int kHalf = 128;
+constexpr int kStages = 6;
+constexpr int kScaleStages = 3;
+constexpr uint32_t kStageIn = kHalf * kFp8Block;        // 16 KB
+constexpr uint32_t kStageOut = kHalf * kFp8Block;       // 16 KB
+constexpr uint32_t kBoxRows = 32;                       // outer operand, K-major: rows per TMA box
+constexpr uint32_t kScaleBytes = 3 * 512;               // inner 128 rows, outer 2 x 128 columns
+constexpr uint32_t kAcc1 = 224;                         // second accumulator's first TMEM column
+constexpr uint32_t kScaleCol = 480;                     // scale words' first TMEM column
+constexpr uint32_t kScaleBuf = 16;                      // columns per scale buffer (4 inner + 8 outer)
+constexpr uint32_t kTmemCols = 512;
+constexpr int kPanel = 16;                              // column tiles per panel of the tile order
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 20000000ull;
+constexpr int kErrTimeout = 5;
+
+struct Barriers {
+    uint64_t full[kStages];          // both CTAs' loads -> MMA (the leader's are used)
+    uint64_t empty[kStages];         // MMA -> this CTA's producer
+    uint64_t sfull[kScaleStages];    // both CTAs' scale words -> MMA (the leader's are used)
+    uint64_t sempty[kScaleStages];   // MMA -> this CTA's scale warp
+    uint64_t tfull[2];               // MMA -> this CTA's epilogue
+    uint64_t tempty[2];              // both epilogues -> MMA: accumulator drained
+    uint64_t shared_free[2];         // both epilogues -> MMA: its part of the common columns drained
+    uint32_t tmem;
+    int abort;
+    int tiles;                       // of the launch
+};
+
+// Group table: first row, rows, first tile, first padded reduction block.
+struct Groups {
+    int lo[kFp8MaxGroups];
+    int cnt[kFp8MaxGroups];
+    int tile0[kFp8MaxGroups + 1];
+    int block0[kFp8MaxGroups];
+};
+
+struct Tile {
+    int g;
+    int m0;          // first inner index of the pair's tile
+    int c0;          // first outer index (row of the outer operand and of the output)
+    int cols;        // outer indices in the tile
+    int width;       // MMA columns: cols rounded up to 32
+    int kb0, nkb;    // reduction blocks
+};
+
+__device__ __forceinline__ void split_columns(int n, int& tiles, int& width) {
+    tiles = (n + kTile - 1) / kTile;
+    width = tiles > 0 ? ((n + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+}
+
+// Tile t of the launch; `g` only moves forward.
+__device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g) {
+    while (t >= gs.tile0[g + 1]) ++g;
+    const int mt = (p.inner + kTile - 1) / kTile;
+    const bool gw = p.mode == kFp8GradWeight;
+    const int n = gw ? p.outer : gs.cnt[g];
+    int nt, width;
+    split_columns(n, nt, width);
+    int l = t - gs.tile0[g];
+    const int full = nt / kPanel * kPanel;
+    int m, c;
+    if (l < full * mt) {
+        const int panel = l / (kPanel * mt), r = l - panel * kPanel * mt;
+        m = r / kPanel;
+        c = panel * kPanel + r % kPanel;
+    } else {
+        l -= full * mt;
+        const int w = nt - full;
+        m = l / w;
+        c = full + l % w;
+    }
+    Tile x;
+    x.g = g;
+    x.m0 = m * kTile;
+    const int off = c * width;
+    x.cols = n - off < width ? n - off : width;
+    x.width = (x.cols + 31) / 32 * 32;
+    x.c0 = gw ? off : gs.lo[g] + off;
+    x.kb0 = gw ? gs.block0[g] : 0;
+    x.nkb = gw ? (gs.cnt[g] + kFp8Block - 1) / kFp8Block : p.kblocks;
+    return x;
+}
+
+__device__ __forceinline__ void record_failure(volatile int* abort) {
+    atomicCAS(&g_muon_fp8_error, 0, kErrTimeout);
+    *abort = 1;
+}
+
+// Scale bytes of reduction blocks 4 c .. 4 c + 3 of one index; scale 1 outside.
+__device__ __forceinline__ uint32_t scale_word(const Fp8Scale& s, int g, int idx, int c, int kb0, int kb1) {
+    uint32_t w = 0x7f7f7f7fu;
+    if (idx < s.limit) {
+        const uint8_t* q = s.p + g * s.batch + static_cast<long long>(idx >> s.shift) * s.idx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kb = 4 * c + i;
+            if (kb >= kb0 && kb < kb1) {
+                const uint32_t b = q[static_cast<long long>(kb) * s.red];
+                w = (w & ~(0xffu << (8 * i))) | (b << (8 * i));
+            }
+        }
+    }
+    return w;
+}
+
+template <int MODE, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
+    constexpr bool kInMn = MODE != kFp8Forward;          // inner operand MN-major
+    constexpr bool kOutMn = MODE == kFp8GradWeight;      // outer operand MN-major
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* s_in = smem;
+    uint8_t* s_out = s_in + kStages * kStageIn;
+    uint8_t* s_sc = s_out + kStages * kStageOut;
+    Barriers& b = *reinterpret_cast<Barriers*>(s_sc + kScaleStages * kScaleBytes);
+    Groups& gs = *reinterpret_cast<Groups*>(s_sc + kScaleStages * kScaleBytes + 512);
+    volatile int* abort = &b.abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = static_cast<int>(ptx::cluster_id_x());
+    const int npairs = static_cast<int>(ptx::num_clusters_x());
+    const uint64_t limit = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&b.full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.empty[s]), 1);
+        }
+        for (int s = 0; s < kScaleStages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&b.sfull[s]), 2);
+            ptx::mbar_init(ptx::smem_addr(&b.sempty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(ptx::smem_addr(&b.tfull[a]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.tempty[a]), 16);       // 8 epilogue warps of both CTAs
+            ptx::mbar_init(ptx::smem_addr(&b.shared_free[a]), 8);   // 4 of them
+        }
+        b.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&p.tm_in);
+        ptx::prefetch_tmap(&p.tm_out);
+    }
+    if (warp == 0) {
+        const int mt = (p.inner + kTile - 1) / kTile;
+        int low = 0, tiles = 0, blocks = 0;
+        const int rows = MODE == kFp8GradWeight ? p.rows : p.outer;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            const GroupSpan sp = warp_group_spans(p.offsets, p.groups, rows, g0, low);
+            const int g = g0 + lane;
+            int nt, width;
+            split_columns(MODE == kFp8GradWeight ? p.outer : sp.cnt, nt, width);
+            const int n = g < p.groups ? nt * mt : 0;
+            const int nb = (sp.cnt + kFp8Block - 1) / kFp8Block;
+            const int it = warp_inclusive_sum(n), ib = warp_inclusive_sum(nb);
+            if (g < p.groups) {
+                gs.lo[g] = sp.lo;
+                gs.cnt[g] = sp.cnt;
+                gs.tile0[g] = tiles + it - n;
+                gs.block0[g] = blocks + ib - nb;
+            }
+            tiles += __shfl_sync(0xffffffffu, it, 31);
+            blocks += __shfl_sync(0xffffffffu, ib, 31);
+        }
+        if (lane == 0) {
+            gs.tile0[p.groups] = tiles;
+            b.tiles = tiles;
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&b.tmem), kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();   // barriers of both CTAs initialised, TMEM allocated, group table written
+    ptx::tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    const int tiles = b.tiles;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer --
+        if (lane == 0) {
+            int stage = 0, g = 0;
+            uint32_t phase = 0, armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += npairs) {
+                const Tile x = decode_tile(p, gs, t, g);
+                const int m = x.m0 + static_cast<int>(rank) * kHalf;
+                const int half = x.width / 2;
+                const int c = x.c0 + static_cast<int>(rank) * half;
+                const int boxes = kOutMn ? 4 : (half + static_cast<int>(kBoxRows) - 1) / static_cast<int>(kBoxRows);
+                const uint32_t bytes = 2 * (kStageIn + boxes * kBoxRows * kFp8Block);
+                const int gb = MODE == kFp8GradWeight ? 0 : x.g;
+                for (int kb = x.kb0; kb < x.kb0 + x.nkb; ++kb) {
+                    if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.empty[stage]), phase ^ 1u, abort, limit)) {
+                        record_failure(abort);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t local = ptx::smem_addr(&b.full[stage]);
+                    const uint32_t fb = ptx::mapa_shared(local, 0);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(local, bytes);
+                        armed |= 1u << stage;
+                        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    }
+                    const uint32_t di = ptx::smem_addr(s_in + stage * kStageIn);
+                    const uint32_t d_o = ptx::smem_addr(s_out + stage * kStageOut);
+                    if (kInMn) ptx::tma_load_3d_pair(di, &p.tm_in, fb, m, kb * kFp8Block, gb);
+                    else ptx::tma_load_3d_pair(di, &p.tm_in, fb, kb * kFp8Block, m, gb);
+                    if (kOutMn) {
+                        ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, c & ~15, kb * kFp8Block, 0);
+                    } else {
+                        for (int i = 0; i < boxes; ++i)
+                            ptx::tma_load_3d_pair(d_o + i * kBoxRows * kFp8Block, &p.tm_out, fb, kb * kFp8Block,
+                                                  c + i * static_cast<int>(kBoxRows), 0);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (leader && (!ok || *abort)) {
+                // loads in flight land before the CTAs leave
+                for (int s = 0; s < kStages; ++s)
+                    if ((armed >> s) & 1u)
+                        ptx::wait_parity_cluster(ptx::smem_addr(&b.full[s]), (armed_parity >> s) & 1u, nullptr,
+                                                 kDrainLimitNs);
+            }
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------------- MMA --
+        if (leader && lane == 0) {
+            const uint64_t ad0 = ptx::sdesc_sw128(ptx::smem_addr(s_in), 16, 1024);
+            const uint64_t bd0 = ptx::sdesc_sw128(ptx::smem_addr(s_out), 16, 1024);
+            // next 32 elements of K: 32 bytes of a row (K-major) or 32 rows of 128 bytes (MN-major)
+            constexpr uint64_t a_k = (kInMn ? 4096 : 32) >> 4;
+            constexpr uint64_t b_k = (kOutMn ? 4096 : 32) >> 4;
+            int stage = 0, sstage = 0, it = 0, g = 0;
+            uint32_t phase = 0, sphase = 0, sbuf = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += npairs, ++it) {
+                const Tile x = decode_tile(p, gs, t, g);
+                const int acc = it & 1;
+                const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
+                if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tempty[acc]), use ^ 1u, abort, limit) ||
+                    (it > 0 && !ptx::wait_parity_cluster(ptx::smem_addr(&b.shared_free[acc ^ 1]),
+                                                         static_cast<uint32_t>((it - 1) >> 1) & 1u, abort, limit))) {
+                    record_failure(abort);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + (acc ? kAcc1 : 0u);
+                uint32_t sfa = 0, sfb = 0;
+                const uint32_t idesc0 = ptx::idesc_mxf8(kTile, x.width, kInMn, kOutMn, 0);
+                for (int i = 0; i < x.nkb; ++i) {
+                    const int kb = x.kb0 + i;
+                    if (i == 0 || (kb & 3) == 0) {
+                        if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sfull[sstage]), sphase, abort, limit)) {
+                            record_failure(abort);
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t src = ptx::smem_addr(s_sc + sstage * kScaleBytes);
+                        sfa = tmem + kScaleCol + sbuf * kScaleBuf;
+                        sfb = sfa + 4;
+                        ptx::tmem_copy_scales_pair(sfa, ptx::sdesc_rows16(src));
+                        ptx::tmem_copy_scales_pair(sfb, ptx::sdesc_rows16(src + 512));
+                        if (x.width > 128) ptx::tmem_copy_scales_pair(sfb + 4, ptx::sdesc_rows16(src + 1024));
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.sempty[sstage]), 0x3u);
+                        sbuf ^= 1u;
+                        if (++sstage == kScaleStages) {
+                            sstage = 0;
+                            sphase ^= 1u;
+                        }
+                    }
+                    if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.full[stage]), phase, abort, limit)) {
+                        record_failure(abort);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t ad = ad0 + static_cast<uint64_t>(stage) * (kStageIn >> 4);
+                    const uint64_t bd = bd0 + static_cast<uint64_t>(stage) * (kStageOut >> 4);
+                    const uint32_t sf = static_cast<uint32_t>(kb & 3);
+                    const uint32_t idesc = idesc0 | (sf << 4) | (sf << 29);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfb, (kk != 0 || i != 0) ? 1u : 0u);
+                    ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), 0x3u);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit_pair(ptx::smem_addr(&b.tfull[acc]), 0x3u);
+            }
+        }
+    } else if (warp == 2) {
+        // --------------------------------------------------------- scales --
+        int sstage = 0, g = 0;
+        uint32_t sphase = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += npairs) {
+            const Tile x = decode_tile(p, gs, t, g);
+            if (x.nkb == 0) continue;
+            const int kb1 = x.kb0 + x.nkb;
+            const int m = x.m0 + static_cast<int>(rank) * kHalf + lane;
+            const int gi = MODE == kFp8GradWeight ? 0 : x.g;
+            for (int c = x.kb0 >> 2; c <= (kb1 - 1) >> 2; ++c) {
+                uint32_t w[12];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = scale_word(p.s_in, gi, m + 32 * i, c, x.kb0, kb1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[4 + i] = 32 * i < x.width ? scale_word(p.s_out, 0, x.c0 + lane + 32 * i, c, x.kb0, kb1) : 0x7f7f7f7fu;
+                if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sempty[sstage]), sphase ^ 1u, abort, limit)) {
+                    record_failure(abort);
+                    ok = false;
+                    break;
+                }
+                uint8_t* dst = s_sc + sstage * kScaleBytes + lane * 16;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    *reinterpret_cast<uint4*>(dst + 512 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[sstage]), 0));
+                if (++sstage == kScaleStages) {
+                    sstage = 0;
+                    sphase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------ epilogue --
+        const int q = warp & 3;
+        const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
+        int it = 0, g = 0;
+        for (int t = pair; t < tiles; t += npairs, ++it) {
+            const Tile x = decode_tile(p, gs, t, g);
+            const int acc = it & 1;
+            const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
+            const int m = x.m0 + static_cast<int>(rank) * kHalf + q * 32 + lane;
+            const long long batch = MODE == kFp8GradWeight ? x.g * p.out_batch : 0;
+            if (!ptx::wait_parity_cluster_backoff(ptx::smem_addr(&b.tfull[acc]), use, abort, limit, 64)) {
+                record_failure(abort);
+                break;
+            }
+            ptx::tc_fence_after();
+            const int chunks = x.width / 32;
+            // the accumulators' common columns (first: chunk 7, odd; second: chunk 0, even) first
+            const bool owner = (acc == 0) == (half == 1);
+            bool told = !owner;
+            for (int i = 0; i < 4; ++i) {
+                const int ch = acc == 0 && half == 1 ? 7 - 2 * i : half + 2 * i;
+                if (ch < chunks) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(tmem + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(ch * 32) +
+                                                (static_cast<uint32_t>(q * 32) << 16), r);
+                    ptx::tmem_wait_ld();
+                    if (!told) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
+                        told = true;
+                    }
+                    const int left = x.cols - ch * 32;
+                    if (m < p.inner && left > 0) {
+                        const long long at = batch + static_cast<long long>(x.c0 + ch * 32) * p.ld + m;
+                        if (F32) {
+                            float* o = static_cast<float*>(p.out) + at;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < left) o[j * p.ld] = x.nkb ? __uint_as_float(r[j]) : 0.0f;
+                        } else {
+                            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < left) o[j * p.ld] = __float2bfloat16_rn(x.nkb ? __uint_as_float(r[j]) : 0.0f);
+                        }
+                    }
+                } else if (!told) {
+                    // a narrow tile: chunk 7 holds none of it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
+                    told = true;
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();   // no CTA leaves while its peer may still signal its barriers
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+static_assert(sizeof(Barriers) <= 512, "barrier block");
+constexpr size_t kSmem = 1024 + kStages * (kStageIn + kStageOut) + kScaleStages * kScaleBytes + 512 + sizeof(Groups);
+static_assert(kSmem <= 232448, "shared memory");
+
+template <int MODE, bool F32>
+cudaError_t run(const Fp8GemmParams& p, int pairs, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    k_fp8_gemm<MODE, F32><<<2 * pairs, kThreads, kSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s) {
+    const long long mt = (p.inner + kTile - 1) / kTile;
+    const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.outer + kTile - 1) / kTile)
+                                                  : p.outer / kTile + p.groups;
+    const long long most = mt * nt;
+    const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
+    switch (p.mode) {
+        case kFp8Forward: return p.out_f32 ? run<kFp8Forward, true>(p, pairs, s) : run<kFp8Forward, false>(p, pairs, s);
+        case kFp8GradInput:
+            return p.out_f32 ? run<kFp8GradInput, true>(p, pairs, s) : run<kFp8GradInput, false>(p, pairs, s);
+        default: return p.out_f32 ? run<kFp8GradWeight, true>(p, pairs, s) : run<kFp8GradWeight, false>(p, pairs, s);
+    }
+}
+
+cudaError_t read_and_clear_fp8_error(int* code) {
+    int v = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(&v, g_muon_fp8_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    *code = v;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_muon_fp8_error, &zero, sizeof(int));
+}
+
+}  // namespace muon

@@ -9,6 +9,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime_api.h>
 
+#include <functional>
+
 namespace muon {
 
 // ------------------------------------------------------------ elementwise --
@@ -186,6 +188,131 @@ struct AdamWParams {
 cudaError_t launch_adamw(const AdamWParams& p, int sms, cudaStream_t s);
 long long adamw_tile_elems();
 
+// ----------------------------------------------------------- gradient norm --
+// One descriptor per tensor of a launch; tiles of kNormTileBytes of one tensor.
+constexpr int kNormTileBytes = 32768;
+constexpr int kNormMaxTensors = 640;
+constexpr int kNormFewTensors = 40;      // launches of up to this many take the small parameter block
+constexpr int kNormMaxBlocks = 1216;     // partial sums per launch
+
+struct NormTensor {
+    const void* g;            // gradient (bf16 or fp32)
+    void* out;                // clip: where the scaled gradient goes (may be g)
+    long long n;              // elements
+    int tile0;                // first tile of this tensor in this launch
+    int bf16;                 // 1: bf16, 0: fp32
+};
+
+struct NormHead {
+    int ntensors;
+    int total_tiles;
+    int npartials;            // clip / finish: partial sums of the whole list
+    int in_place;             // clip: out is g for every tensor
+    float max_norm;
+    double* partials;         // norm: this launch's; clip / finish: the whole list's
+    float* norm;              // the norm, written by the finishing launch (clip: its first block)
+};
+
+template <int N>
+struct NormParams {
+    NormHead h;
+    NormTensor t[N];
+};
+
+int norm_grid(int total_tiles, int sms);
+template <int N>
+cudaError_t launch_grad_norm(const NormParams<N>& p, int grid, cudaStream_t s);
+template <int N>
+cudaError_t launch_grad_clip(const NormParams<N>& p, int grid, bool first, cudaStream_t s);
+cudaError_t launch_grad_norm_finish(const NormHead& h, cudaStream_t s);
+
+// ----------------------------------------------------------------- routing --
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteMaxPerLane = 32;
+
+struct RouteParams {
+    const void* logits;       // tokens x experts, row stride ld
+    const float* bias;        // experts, or nullptr
+    float* weights;           // tokens x top_k
+    int* chosen;              // tokens x top_k
+    int* counts;              // experts
+    const float* d_weights;   // backward: tokens x top_k
+    void* d_logits;           // backward: tokens x experts, row stride ld_d
+    long long tokens, ld, ld_d;
+    int experts, top_k, groups, top_groups;
+    int group_size;           // experts / groups
+    int lanes;                // lanes per group (a power of two)
+    int per_lane;             // experts per lane, consecutive
+    int sigmoid, renormalize;
+    int bf16;
+    int vec;                  // 1: four consecutive experts of a lane load as one vector
+    float scale;
+};
+
+cudaError_t launch_route(const RouteParams& p, int sms, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteParams& p, int sms, cudaStream_t s);
+
+// ------------------------------------------------------ 8-bit block products --
+constexpr int kFp8Block = 128;           // elements per scale along the reduction
+constexpr int kFp8MaxGroups = 1024;
+
+struct QuantParams {
+    const void* x;            // rows x cols of `batch` matrices, row stride ld, matrix stride ldb
+    long long rows, cols, ld, ldb;
+    int batch;
+    int bf16;
+    int vec;                  // 16-byte loads are legal
+    int groups;               // col blocks start anew at each group's first row (0: one group, all rows)
+    const int* offsets;       // groups + 1 row offsets on the device
+    uint8_t* row_q;           // rows x ldq E4M3 codes (row blocks), or nullptr
+    uint8_t* row_scale;       // col blocks x rows
+    uint8_t* col_q;           // padded rows x ldq codes (col blocks), or nullptr
+    uint8_t* col_scale;       // padded row blocks x ldq
+    uint8_t* blk_q;           // batch x rows x ldq codes (128 x 128 blocks), or nullptr
+    uint8_t* blk_scale;       // batch x row blocks x col blocks
+    long long ldq;            // cols rounded up to 128
+    long long row_blocks;     // grid bound of 128-row blocks (per matrix)
+};
+
+cudaError_t launch_fp8_quantize(const QuantParams& p, cudaStream_t s);
+
+enum Fp8Mode : int {
+    kFp8Forward = 0,          // outer operand's rows grouped; inner operand: batch g, K-major
+    kFp8GradInput = 1,        // outer operand's rows grouped; inner operand: batch g, MN-major
+    kFp8GradWeight = 2        // reduction grouped; both operands MN-major
+};
+
+// Scale bytes of one operand: byte (index, reduction block) of batch g at
+// p + g * batch + (index >> shift) * idx + block * red.
+struct Fp8Scale {
+    const uint8_t* p;
+    long long batch, idx, red;
+    int shift;
+    int limit;                // indices from here on take scale 1
+};
+
+struct Fp8GemmParams {
+    CUtensorMap tm_in;        // inner operand (the output's contiguous index; MMA rows)
+    CUtensorMap tm_out;       // outer operand (the output's row index; MMA columns)
+    Fp8Scale s_in, s_out;
+    void* out;                // out[row][inner], row stride ld
+    long long ld;
+    long long out_batch;      // grad weight: elements between groups' outputs
+    int mode;
+    int out_f32;
+    int inner;                // extent of the inner index
+    int outer;                // rows (forward, grad input) or extent of the outer index (grad weight)
+    int kblocks;              // reduction blocks (forward, grad input)
+    int groups;               // >= 1
+    const int* offsets;       // groups + 1 row offsets, or nullptr: one group of all rows
+    int rows;                 // grad weight: rows reduced over in all
+    unsigned long long wait_ns;
+};
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s);
+cudaError_t read_and_clear_fp8_error(int* code);
+
 // Launch helpers implemented in the .cu files.
 // `sms`: the grid is one CTA per resident slot on every SM (capped by the tiles).
 cudaError_t launch_momentum_norm(const EwParams& p, int sms, cudaStream_t s);
@@ -226,6 +353,13 @@ cudaError_t read_and_clear_guard_error(int* code);
 int ns5_batched_on_workspace(void* const* ptrs, const int* rows, const int* cols, int count, int steps,
                              const float* coeffs, void* ws, size_t ws_bytes, cudaStream_t stream);
 int set_last_error(int status, const char* msg);
+
+// What the operators around the step (train_abi.cu) share with it.
+enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpEnd };
+int op_device(int* sms);                       // the current device, checked; its SM count
+int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
+int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
+                    int box_inner, int box_outer);
 cudaError_t launch_ns_small(const SmallParams& p, size_t smem, cudaStream_t s);
 size_t ns_small_smem_bytes(int r, int k);
 

@@ -120,11 +120,14 @@ int device_state(DeviceState** out) {
 
 // --------------------------------------------------------------- profiling --
 enum Kind : int {
-    kKNorm = 0, kKFinalize, kKPack, kKGram, kKPoly, kKUpdate, kKSmall, kKUnpack, kKAdamW, kKFinal, kNumKinds
+    kKNorm = 0, kKFinalize, kKPack, kKGram, kKPoly, kKUpdate, kKSmall, kKUnpack, kKAdamW, kKFinal,
+    kNumStepKinds, kNumKinds = kOpEnd
 };
+static_assert(kNumStepKinds == static_cast<int>(kOpGradNorm), "the operators' kinds follow the step's");
 const char* const kKindNames[kNumKinds] = {"norm_pass",    "norm_finalize",  "pack",     "ns_gemm_gram",
                                            "ns_gemm_poly", "ns_gemm_update", "ns_small", "unpack",
-                                           "adamw",        "ns_gemm_final"};
+                                           "adamw",        "ns_gemm_final", "grad_norm", "grad_clip",
+                                           "route",        "route_backward", "fp8_quantize", "fp8_gemm"};
 struct ProfRec {
     int kind;
     cudaEvent_t a, b;
@@ -1049,6 +1052,33 @@ int ns5_batched_on_workspace(void* const* ptrs, const int* rows, const int* cols
 
 int set_last_error(int status, const char* msg) { return fail(status, "%s", msg); }
 
+int op_device(int* sms) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* d = nullptr;
+    const int rc = device_state(&d);
+    if (rc == MUON_OK) *sms = d->sms;
+    return rc;
+}
+
+int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    return launch(kind, flops, bytes, s, f);
+}
+
+int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
+                    int box_inner, int box_outer) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                                static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return MUON_OK;
+}
+
 }  // namespace muon
 
 using namespace muon;
@@ -1243,10 +1273,11 @@ int muon_device_status(cudaStream_t stream, int* device_status) {
     if (device_status == nullptr) return fail(MUON_ERR_INVALID_ARG, "device_status is NULL");
     std::lock_guard<std::mutex> lock(g_mu);
     MUON_CUDA_TRY(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-    int code = 0, code2 = 0;
+    int code = 0, code2 = 0, code3 = 0;
     MUON_CUDA_TRY(read_and_clear_pair_error(&code), "reading the device status");
     MUON_CUDA_TRY(read_and_clear_guard_error(&code2), "reading the device status");
-    *device_status = code != 0 ? code : code2;
+    MUON_CUDA_TRY(read_and_clear_fp8_error(&code3), "reading the device status");
+    *device_status = code != 0 ? code : code2 != 0 ? code2 : code3;
     return MUON_OK;
 }
 

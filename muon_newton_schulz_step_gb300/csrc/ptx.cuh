@@ -321,6 +321,27 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
+// Pair MMA with E4M3 operands scaled block by block (kind::mxf8f6f4, one E8M0
+// scale byte per 32 elements of K; K = 32 per instruction): the scale bytes of
+// A's rows and B's columns lie in TMEM at sfa / sfb, the byte of the 32-bit
+// word taken is named in the instruction descriptor.
+__device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// 32 lanes x 16 bytes of each CTA's shared memory (its own, at the same offset)
+// to four TMEM columns of that CTA, repeated for the four 32-lane quadrants.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 // When the pair MMAs issued so far are done, arrive once on the mbarrier at
 // shared::cta offset `bar` in every CTA of `cta_mask`.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask) {
@@ -341,6 +362,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
            (static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32) |
            (static_cast<uint64_t>(1u) << 46) |      // descriptor version (sm_100 family)
            (static_cast<uint64_t>(2u) << 61);       // SWIZZLE_128B
+}
+
+// Shared-memory descriptor of unswizzled rows of 16 bytes (scale bytes: 32 rows,
+// 8-row groups 128 bytes apart).
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
+           (static_cast<uint64_t>(1u) << 46);
 }
 
 // Two fp32 values to two E4M3 codes, round to nearest even, saturating; the
@@ -382,6 +410,18 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_ma
            | (static_cast<uint32_t>(b_mn_major) << 16) // B major-ness
            | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// Instruction descriptor for kind::mxf8f6f4 with E8M0 scales: E4M3 x E4M3 ->
+// fp32; `sf`: which byte of the scale words, for both operands.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, bool a_mn_major, bool b_mn_major, uint32_t sf) {
+    return (sf << 4)                                   // B scale byte
+           | (static_cast<uint32_t>(a_mn_major) << 15) // A major-ness
+           | (static_cast<uint32_t>(b_mn_major) << 16) // B major-ness
+           | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+           | (1u << 23)                                // scale format: E8M0
+           | (static_cast<uint32_t>(M >> 7) << 27)     // M / 128
+           | (sf << 29);                               // A scale byte
 }
 
 }  // namespace ptx
