@@ -139,21 +139,23 @@ __device__ __forceinline__ void record_failure(volatile int* abort) {
     *abort = 1;
 }
 
-// Scale bytes of reduction blocks 4 c .. 4 c + 3 of one index; scale 1 outside.
-__device__ __forceinline__ uint32_t scale_word(const Fp8Scale& s, int g, int idx, int c, int kb0, int kb1) {
-    uint32_t w = 0x7f7f7f7fu;
-    if (idx < s.limit) {
-        const uint8_t* q = s.p + g * s.batch + static_cast<long long>(idx >> s.shift) * s.idx;
+// The scale words (four reduction blocks' bytes) of N x 32 indices, this lane's
+// every 32nd from idx on, for blocks 4 c .. 4 c + 3 below kb1.  Indices and
+// blocks past the end take the last one's bytes: their products are zero or are
+// not stored.  No load depends on another or on a branch, so all are in flight
+// at once: one chain of L2 latencies per word would starve the tensor core.
+template <int N>
+__device__ __forceinline__ void scale_words(const Fp8Scale& s, long long base, int idx, int c, int kb1, uint32_t* w) {
+    uint32_t v[N][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int kb = 4 * c + i;
-            if (kb >= kb0 && kb < kb1) {
-                const uint32_t b = q[static_cast<long long>(kb) * s.red];
-                w = (w & ~(0xffu << (8 * i))) | (b << (8 * i));
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int kb = min(4 * c + i, kb1 - 1);
+        const uint8_t* q = s.p + base + static_cast<long long>(kb) * s.red;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j][i] = q[static_cast<long long>(min(idx + 32 * j, s.limit - 1) >> s.shift) * s.idx];
     }
-    return w;
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] = v[j][0] | (v[j][1] << 8) | (v[j][2] << 16) | (v[j][3] << 24);
 }
 
 template <int MODE, bool F32>
@@ -366,14 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (x.nkb == 0) continue;
             const int kb1 = x.kb0 + x.nkb;
             const int m = x.m0 + static_cast<int>(rank) * kHalf + lane;
-            const int gi = MODE == kFp8GradWeight ? 0 : x.g;
             for (int c = x.kb0 >> 2; c <= (kb1 - 1) >> 2; ++c) {
                 uint32_t w[12];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = scale_word(p.s_in, gi, m + 32 * i, c, x.kb0, kb1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[4 + i] = 32 * i < x.width ? scale_word(p.s_out, 0, x.c0 + lane + 32 * i, c, x.kb0, kb1) : 0x7f7f7f7fu;
+                if (MODE == kFp8GradWeight) {
+                    scale_words<4>(p.s_in, 0, m, c, kb1, w);
+                } else {
+                    // 128 x 128 blocks: one scale for this CTA's 128 indices
+                    scale_words<1>(p.s_in, x.g * p.s_in.batch, m, c, kb1, w);
+                    w[1] = w[2] = w[3] = w[0];
+                }
+                scale_words<8>(p.s_out, 0, x.c0 + lane, c, kb1, w + 4);
                 if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sempty[sstage]), sphase ^ 1u, abort, limit)) {
                     record_failure(abort);
                     ok = false;

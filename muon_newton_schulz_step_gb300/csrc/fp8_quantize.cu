@@ -17,11 +17,13 @@
 // weights: the same codes and scales read along either dimension.
 //
 // Bound by HBM: one read of x and one write per code.  A 256-thread block takes
-// a 128 x 128 tile: a warp two rows at a time, 16 lanes x 8 consecutive columns
-// a row, so a lane's 64 values stay in registers between the maximum and the
-// codes, row maxima meet in four shuffles and column maxima in one shuffle and
-// one exchange through shared memory, and the row and the col codes of one
-// matrix come from a single read.
+// 128 x 128 tiles of one row block: a warp two rows at a time, 16 lanes x 8
+// consecutive columns a row.  All of a thread's eight vectors are loaded before
+// the first is looked at (a conditional load per vector would make eight DRAM
+// latencies of one) and stay in registers in their own type between the maximum
+// and the codes: bf16 magnitudes are compared two at a time as integers, row
+// maxima meet in four shuffles, column maxima in one shuffle and one exchange
+// through shared memory, and the row and the col codes come from a single read.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -55,21 +57,86 @@ __device__ __forceinline__ float inverse_scale(int e) {
     return e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-__device__ __forceinline__ uint32_t magnitude(float v) {
-    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
-    return b >= 0x7f800000u ? 0u : b;                    // not finite: no part in the maximum
+// Eight consecutive elements as loaded: bf16 in a, fp32 in a and b.
+struct Raw {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <bool BF16>
+__device__ __forceinline__ float element(const Raw& r, int j) {
+    if (BF16) {
+        const uint32_t w = word(r.a, j >> 1);
+        return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    return __uint_as_float(j < 4 ? word(r.a, j) : word(r.b, j - 4));
 }
 
-__device__ __forceinline__ uint2 codes(const float (&v)[8], const float (&by)[8]) {
+constexpr uint32_t kInf = 0x7f800000u;
+
+// Largest magnitudes of columns over rows, as fp32 bits (bf16: two packed).
+template <bool BF16>
+struct Maxima {
+    uint32_t m[BF16 ? 4 : 8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t& v : m) v = 0;
+    }
+    __device__ __forceinline__ void add(const Raw& r) {
+        if (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = __vmaxu2(m[i], word(r.a, i) & 0x7fff7fffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m[i] = max(m[i], word(r.a, i) & 0x7fffffffu);
+                m[i + (BF16 ? 0 : 4)] = max(m[i + (BF16 ? 0 : 4)], word(r.b, i) & 0x7fffffffu);
+            }
+        }
+    }
+    // of elements that are not finite: nothing
+    __device__ __forceinline__ void add_finite(const Raw& r) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t v = __float_as_uint(element<BF16>(r, j)) & 0x7fffffffu;
+            if (v >= kInf) v = 0;
+            if (BF16) {
+                const uint32_t h = v >> 16;
+                m[j >> 1] = __vmaxu2(m[j >> 1], (j & 1) ? h << 16 : h);
+            } else {
+                m[BF16 ? 0 : j] = max(m[BF16 ? 0 : j], v);
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t column(int j) const {
+        if (BF16) return (j & 1) ? (m[j >> 1] & 0xffff0000u) : (m[j >> 1] << 16);
+        return m[BF16 ? 0 : j];
+    }
+    __device__ __forceinline__ uint32_t all() const {
+        if (BF16) {
+            const uint32_t v = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+            return max(v & 0xffff0000u, v << 16);
+        }
+        uint32_t v = 0;
+#pragma unroll
+        for (uint32_t x : m) v = max(v, x);
+        return v;
+    }
+};
+
+// Codes of eight elements; ODD: infinities among them (the conversion would
+// saturate them) become NaN.
+template <bool BF16, bool ODD>
+__device__ __forceinline__ uint2 codes(const Raw& r, const float (&by)[8]) {
     uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // infinities saturate in the conversion: make them NaN (inf * 0 + ...) first
-        float lo = v[2 * i], hi = v[2 * i + 1];
-        lo = __fmul_rn(lo, by[2 * i]);
-        hi = __fmul_rn(hi, by[2 * i + 1]);
-        if (isinf(v[2 * i])) lo = __uint_as_float(0x7fffffffu);
-        if (isinf(v[2 * i + 1])) hi = __uint_as_float(0x7fffffffu);
+        float lo = __fmul_rn(element<BF16>(r, 2 * i), by[2 * i]), hi = __fmul_rn(element<BF16>(r, 2 * i + 1), by[2 * i + 1]);
+        if (ODD) {
+            if (isinf(element<BF16>(r, 2 * i))) lo = __uint_as_float(0x7fffffffu);
+            if (isinf(element<BF16>(r, 2 * i + 1))) hi = __uint_as_float(0x7fffffffu);
+        }
         q[i] = ptx::cvt_e4m3x2(hi, lo);
     }
     return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
@@ -84,7 +151,7 @@ struct RowBlock {
 
 // Row block `rb` of the groups' padded row blocks (one group: rb itself).  Warp 0
 // adds up the groups' blocks; offsets outside [0, rows] or descending are clamped.
-__device__ __forceinline__ void find_row_block(const QuantParams& p, long long rb, RowBlock* out) {
+__device__ __forceinline__ void find_row_block(const QuantParams& p, const int* offsets, long long rb, RowBlock* out) {
     if (p.groups == 0) {
         if (threadIdx.x == 0) {
             out->row0 = rb * 128;
@@ -100,7 +167,7 @@ __device__ __forceinline__ void find_row_block(const QuantParams& p, long long r
     __syncwarp();
     int before = 0, low = 0;                             // row blocks of the groups so far; their last row
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
-        const GroupSpan span = warp_group_spans(p.offsets, p.groups, static_cast<int>(p.rows), g0, low);
+        const GroupSpan span = warp_group_spans(offsets, p.groups, static_cast<int>(p.rows), g0, low);
         const int nb = (span.cnt + 127) >> 7;
         const int inc = warp_inclusive_sum(nb);
         const int k = static_cast<int>(rb) - (before + inc - nb);
@@ -115,31 +182,128 @@ __device__ __forceinline__ void find_row_block(const QuantParams& p, long long r
     }
 }
 
+// Eight elements at the matrix's edge, or without the alignment for vectors.
 template <bool BF16>
-__device__ __forceinline__ void load8(const QuantParams& p, const char* base, long long row, long long col, float (&v)[8]) {
-    const long long off = row * p.ld + col;
-    if (p.vec && col + 8 <= p.cols) {
-        if (BF16) {
-            const uint4 r = *reinterpret_cast<const uint4*>(base + off * 2);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ Raw load_edge(const QuantParams& p, const char* base, long long row, long long col) {
+    uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-            const float4* s = reinterpret_cast<const float4*>(base + off * 4);
-            const float4 a = s[0], b = s[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int i = 0; i < 8; ++i) {
+        w[i] = 0;
+        if (col + i < p.cols) {
+            const long long at = row * p.ld + col + i;
+            w[i] = BF16 ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[at])
+                        : reinterpret_cast<const uint32_t*>(base)[at];
         }
+    }
+    Raw r;
+    if (BF16) {
+        r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+        r.b = r.a;
     } else {
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return r;
+}
+
+// One tile's maxima, scales and codes.  ODD: some element is not finite.
+template <bool BF16, bool ROW, bool COL, bool BLK, bool ODD>
+__device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, const Raw (&v)[kRowsPerThread],
+                                     uint32_t (&part)[8][128], long long cb, long long batch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cg = lane & 15, half = lane >> 4;
+    const long long col = cb * 128 + cg * 8;
+    if (ROW) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = 0.0f;
-            if (col + i < p.cols)
-                v[i] = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[off + i])
-                            : reinterpret_cast<const float*>(base)[off + i];
+        for (int i = 0; i < kRowsPerThread; ++i) {
+            const int lr = i * 16 + warp * 2 + half;
+            Maxima<BF16> m;
+            m.clear();
+            if (ODD) m.add_finite(v[i]); else m.add(v[i]);
+            uint32_t top = m.all();
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = scale_exponent(top);
+            float by[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
+            if (lr < r.rows) {
+                *reinterpret_cast<uint2*>(p.row_q + (r.row0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
+                if (cg == 0) p.row_scale[cb * p.rows + r.row0 + lr] = static_cast<uint8_t>(e + 127);
+            }
+        }
+    }
+    if (COL || BLK) {
+        Maxima<BF16> m;
+        m.clear();
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) {
+            if (ODD) m.add_finite(v[i]); else m.add(v[i]);
+        }
+        uint32_t top[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            top[j] = m.column(j);
+            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+        }
+        __syncthreads();                                 // part's last readers are done
+        if (half == 0) {
+            uint4* dst = reinterpret_cast<uint4*>(&part[warp][cg * 8]);
+            dst[0] = make_uint4(top[0], top[1], top[2], top[3]);
+            dst[1] = make_uint4(top[4], top[5], top[6], top[7]);
+        }
+        __syncthreads();
+        if (COL) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 t = *reinterpret_cast<const uint4*>(&part[0][cg * 8 + 4 * h]);
+#pragma unroll
+                for (int w = 1; w < 8; ++w) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(&part[w][cg * 8 + 4 * h]);
+                    t = make_uint4(max(t.x, u.x), max(t.y, u.y), max(t.z, u.z), max(t.w, u.w));
+                }
+                top[4 * h] = t.x;
+                top[4 * h + 1] = t.y;
+                top[4 * h + 2] = t.z;
+                top[4 * h + 3] = t.w;
+            }
+            float by[8];
+            uint32_t sc[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = scale_exponent(top[j]);
+                by[j] = inverse_scale(e);
+                sc[j >> 2] |= static_cast<uint32_t>(e + 127) << (8 * (j & 3));
+            }
+#pragma unroll
+            for (int i = 0; i < kRowsPerThread; ++i) {
+                const int lr = i * 16 + warp * 2 + half;
+                *reinterpret_cast<uint2*>(p.col_q + (r.padded0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
+            }
+            if (threadIdx.x < 16)
+                *reinterpret_cast<uint2*>(p.col_scale + (r.padded0 >> 7) * p.ldq + col) = make_uint2(sc[0], sc[1]);
+        }
+        if (BLK) {
+            uint32_t t = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const uint4 u = *reinterpret_cast<const uint4*>(&part[w][lane * 4]);
+                t = max(max(t, max(u.x, u.y)), max(u.z, u.w));
+            }
+            t = __reduce_max_sync(0xffffffffu, t);
+            const int e = scale_exponent(t);
+            float by[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
+            uint8_t* q = p.blk_q + batch * p.rows * p.ldq;
+#pragma unroll
+            for (int i = 0; i < kRowsPerThread; ++i) {
+                const int lr = i * 16 + warp * 2 + half;
+                if (lr < r.rows) *reinterpret_cast<uint2*>(q + (r.row0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
+            }
+            if (threadIdx.x == 0)
+                p.blk_scale[(batch * ((p.rows + 127) >> 7) + (r.row0 >> 7)) * (p.ldq >> 7) + cb] =
+                    static_cast<uint8_t>(e + 127);
         }
     }
 }
@@ -148,107 +312,70 @@ template <bool BF16, bool ROW, bool COL, bool BLK>
 __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const __grid_constant__ QuantParams p) {
     __shared__ uint32_t part[8][128];
     __shared__ RowBlock rb;
+    __shared__ int offsets[COL ? kFp8MaxGroups + 1 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cg = lane & 15, half = lane >> 4;
-    const long long cb = blockIdx.x;
-    const long long batch = blockIdx.z;
+    const long long batch = blockIdx.z, colblocks = p.ldq >> 7;
     const char* base = static_cast<const char*>(p.x) + batch * p.ldb * (BF16 ? 2 : 4);
+    if (COL && p.groups > 0) {
+        for (int g = threadIdx.x; g <= p.groups; g += kThreads) offsets[g] = p.offsets[g];
+        __syncthreads();
+    }
 
     for (long long y = blockIdx.y; y < p.row_blocks; y += gridDim.y) {
-        find_row_block(p, y, &rb);
+        find_row_block(p, offsets, y, &rb);
         __syncthreads();
         const RowBlock r = rb;
         if (!r.valid) return;                            // the blocks past the last one
-        const long long col = cb * 128 + cg * 8;
-        float v[kRowsPerThread][8];
+        for (long long cb = blockIdx.x; cb < colblocks; cb += gridDim.x) {
+            const long long col = cb * 128 + cg * 8;
+            Raw v[kRowsPerThread];
+            if (p.vec && cb * 128 + 128 <= p.cols && r.rows == 128) {
+                const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
+                const long long step = 16 * p.ld * (BF16 ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            const int lr = i * 16 + warp * 2 + half;
-            if (lr < r.rows) {
-                load8<BF16>(p, base, r.row0 + lr, col, v[i]);
+                for (int i = 0; i < kRowsPerThread; ++i) {
+                    v[i].a = *reinterpret_cast<const uint4*>(src + i * step);
+                    v[i].b = BF16 ? v[i].a : *reinterpret_cast<const uint4*>(src + i * step + 16);
+                }
+            } else if (p.vec && cb * 128 + 128 <= p.cols) {
+                // a group's last rows
+                const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
+                const long long step = 16 * p.ld * (BF16 ? 2 : 4);
+#pragma unroll
+                for (int i = 0; i < kRowsPerThread; ++i) {
+                    v[i].a = v[i].b = make_uint4(0, 0, 0, 0);
+                    if (i * 16 + warp * 2 + half < r.rows) {
+                        v[i].a = *reinterpret_cast<const uint4*>(src + i * step);
+                        if (!BF16) v[i].b = *reinterpret_cast<const uint4*>(src + i * step + 16);
+                    }
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-            }
-        }
-        if (ROW) {
-#pragma unroll
-            for (int i = 0; i < kRowsPerThread; ++i) {
-                const int lr = i * 16 + warp * 2 + half;
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[i][j]));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int e = scale_exponent(top);
-                float by[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
-                if (lr < r.rows) {
-                    *reinterpret_cast<uint2*>(p.row_q + (r.row0 + lr) * p.ldq + col) = codes(v[i], by);
-                    if (cg == 0) p.row_scale[cb * p.rows + r.row0 + lr] = static_cast<uint8_t>(e + 127);
-                }
-            }
-        }
-        if (COL || BLK) {
-            uint32_t top[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                top[j] = 0;
-#pragma unroll
-                for (int i = 0; i < kRowsPerThread; ++i) top[j] = max(top[j], magnitude(v[i][j]));
-                top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-            }
-            if (half == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) part[warp][cg * 8 + j] = top[j];
-            }
-            __syncthreads();
-            if (threadIdx.x < 128) {
-                uint32_t t = 0;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) t = max(t, part[w][threadIdx.x]);
-                part[0][threadIdx.x] = t;
-            }
-            __syncthreads();
-            if (COL) {
-                float by[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) by[j] = inverse_scale(scale_exponent(part[0][cg * 8 + j]));
-#pragma unroll
                 for (int i = 0; i < kRowsPerThread; ++i) {
                     const int lr = i * 16 + warp * 2 + half;
-                    *reinterpret_cast<uint2*>(p.col_q + (r.padded0 + lr) * p.ldq + col) = codes(v[i], by);
+                    v[i].a = v[i].b = make_uint4(0, 0, 0, 0);
+                    if (lr < r.rows) v[i] = load_edge<BF16>(p, base, r.row0 + lr, col);
                 }
-                if (threadIdx.x < 128)
-                    p.col_scale[(r.padded0 >> 7) * p.ldq + cb * 128 + threadIdx.x] =
-                        static_cast<uint8_t>(scale_exponent(part[0][threadIdx.x]) + 127);
             }
-            if (BLK) {
-                uint32_t t = max(max(part[0][lane], part[0][lane + 32]), max(part[0][lane + 64], part[0][lane + 96]));
-                t = __reduce_max_sync(0xffffffffu, t);
-                const int e = scale_exponent(t);
-                float by[8];
+            Maxima<BF16> m;
+            m.clear();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
-                uint8_t* q = p.blk_q + batch * p.rows * p.ldq;
-#pragma unroll
-                for (int i = 0; i < kRowsPerThread; ++i) {
-                    const int lr = i * 16 + warp * 2 + half;
-                    if (lr < r.rows) *reinterpret_cast<uint2*>(q + (r.row0 + lr) * p.ldq + col) = codes(v[i], by);
-                }
-                if (threadIdx.x == 0)
-                    p.blk_scale[(batch * ((p.rows + 127) >> 7) + (r.row0 >> 7)) * gridDim.x + cb] =
-                        static_cast<uint8_t>(e + 127);
-            }
+            for (int i = 0; i < kRowsPerThread; ++i) m.add(v[i]);
+            if (__syncthreads_or(m.all() >= kInf)) tile<BF16, ROW, COL, BLK, true>(p, r, v, part, cb, batch);
+            else tile<BF16, ROW, COL, BLK, false>(p, r, v, part, cb, batch);
         }
-        __syncthreads();                                 // rb and part are written anew
+        __syncthreads();                                 // rb is written anew
     }
 }
 
 template <bool BF16>
 cudaError_t run(const QuantParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.ldq / 128),
+    // several tiles of a row block per block of threads where there are enough of
+    // both: finding a group's row block costs about as much as half a tile
+    const long long colblocks = p.ldq / 128;
+    const long long share = p.groups > 0 && colblocks * p.row_blocks > 4096 ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>((colblocks + share - 1) / share),
                     static_cast<unsigned>(p.row_blocks < 65535 ? p.row_blocks : 65535),
                     static_cast<unsigned>(p.batch));
     if (p.blk_q != nullptr) k_fp8_quantize<BF16, false, false, true><<<grid, kThreads, 0, s>>>(p);

@@ -289,7 +289,7 @@ struct Fp8Scale {
     const uint8_t* p;
     long long batch, idx, red;
     int shift;
-    int limit;                // indices from here on take scale 1
+    int limit;                // number of indices
 };
 
 struct Fp8GemmParams {
