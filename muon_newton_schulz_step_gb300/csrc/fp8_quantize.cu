@@ -75,71 +75,90 @@ __device__ __forceinline__ float element(const Raw& r, int j) {
 
 constexpr uint32_t kInf = 0x7f800000u;
 
-// Largest magnitudes of columns over rows, as fp32 bits (bf16: two packed).
+// Largest magnitude of eight elements, as fp32 bits (NaN and infinity at or above kInf).
 template <bool BF16>
-struct Maxima {
+__device__ __forceinline__ uint32_t row_max(const Raw& r) {
+    if (BF16) {
+        const uint32_t k = 0x7fff7fffu;
+        const uint32_t v = __vmaxu2(__vmaxu2(r.a.x & k, r.a.y & k), __vmaxu2(r.a.z & k, r.a.w & k));
+        return max(v & 0xffff0000u, v << 16);
+    }
+    const uint32_t k = 0x7fffffffu;
+    return max(max(max(r.a.x & k, r.a.y & k), max(r.a.z & k, r.a.w & k)),
+               max(max(r.b.x & k, r.b.y & k), max(r.b.z & k, r.b.w & k)));
+}
+
+// Largest magnitudes of eight columns over rows: bf16 two to a word, fp32 bits one.
+template <bool BF16>
+struct ColMax {
     uint32_t m[BF16 ? 4 : 8];
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (uint32_t& v : m) v = 0;
     }
     __device__ __forceinline__ void add(const Raw& r) {
-        if (BF16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = __vmaxu2(m[i], word(r.a, i) & 0x7fff7fffu);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
+                m[i] = __vmaxu2(m[i], word(r.a, i) & 0x7fff7fffu);
+            } else {
                 m[i] = max(m[i], word(r.a, i) & 0x7fffffffu);
-                m[i + (BF16 ? 0 : 4)] = max(m[i + (BF16 ? 0 : 4)], word(r.b, i) & 0x7fffffffu);
+                m[i + 4] = max(m[i + 4], word(r.b, i) & 0x7fffffffu);
             }
         }
     }
-    // of elements that are not finite: nothing
-    __device__ __forceinline__ void add_finite(const Raw& r) {
+    __device__ __forceinline__ void meet(int lane_mask) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t v = __float_as_uint(element<BF16>(r, j)) & 0x7fffffffu;
-            if (v >= kInf) v = 0;
-            if (BF16) {
-                const uint32_t h = v >> 16;
-                m[j >> 1] = __vmaxu2(m[j >> 1], (j & 1) ? h << 16 : h);
-            } else {
-                m[BF16 ? 0 : j] = max(m[BF16 ? 0 : j], v);
-            }
+        for (uint32_t& v : m) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, v, lane_mask);
+            v = BF16 ? __vmaxu2(v, o) : max(v, o);
         }
     }
     __device__ __forceinline__ uint32_t column(int j) const {
-        if (BF16) return (j & 1) ? (m[j >> 1] & 0xffff0000u) : (m[j >> 1] << 16);
-        return m[BF16 ? 0 : j];
+        if constexpr (BF16) return (j & 1) ? (m[j >> 1] & 0xffff0000u) : (m[j >> 1] << 16);
+        else return m[j];
     }
     __device__ __forceinline__ uint32_t all() const {
-        if (BF16) {
-            const uint32_t v = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
-            return max(v & 0xffff0000u, v << 16);
-        }
         uint32_t v = 0;
 #pragma unroll
-        for (uint32_t x : m) v = max(v, x);
+        for (int j = 0; j < 8; ++j) v = max(v, column(j));
         return v;
     }
 };
 
-// Codes of eight elements; ODD: infinities among them (the conversion would
-// saturate them) become NaN.
-template <bool BF16, bool ODD>
+// Elements that are not finite: NaN in their place (infinities would saturate in
+// the conversion), zero for the maxima.
+template <bool BF16>
+__device__ __noinline__ Raw replace_odd(Raw r, bool zero) {
+    uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+        if (BF16) {
+            if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = zero ? w[i] & 0x0000ffffu : w[i] | 0x7fff0000u;
+            if ((w[i] & 0x7f80u) == 0x7f80u) w[i] = zero ? w[i] & 0xffff0000u : w[i] | 0x7fffu;
+        } else if ((w[i] & kInf) == kInf) {
+            w[i] = zero ? 0u : w[i] | 0x7fffffffu;
+        }
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    return r;
+}
+
+template <bool BF16>
 __device__ __forceinline__ uint2 codes(const Raw& r, const float (&by)[8]) {
     uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo = __fmul_rn(element<BF16>(r, 2 * i), by[2 * i]), hi = __fmul_rn(element<BF16>(r, 2 * i + 1), by[2 * i + 1]);
-        if (ODD) {
-            if (isinf(element<BF16>(r, 2 * i))) lo = __uint_as_float(0x7fffffffu);
-            if (isinf(element<BF16>(r, 2 * i + 1))) hi = __uint_as_float(0x7fffffffu);
-        }
-        q[i] = ptx::cvt_e4m3x2(hi, lo);
-    }
+    for (int i = 0; i < 4; ++i)
+        q[i] = ptx::cvt_e4m3x2(__fmul_rn(element<BF16>(r, 2 * i + 1), by[2 * i + 1]),
+                               __fmul_rn(element<BF16>(r, 2 * i), by[2 * i]));
     return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint2 codes(const Raw& r, float by) {
+    const float b[8] = {by, by, by, by, by, by, by, by};
+    return codes<BF16>(r, b);
 }
 
 struct RowBlock {
@@ -184,7 +203,7 @@ __device__ __forceinline__ void find_row_block(const QuantParams& p, const int* 
 
 // Eight elements at the matrix's edge, or without the alignment for vectors.
 template <bool BF16>
-__device__ __forceinline__ Raw load_edge(const QuantParams& p, const char* base, long long row, long long col) {
+__device__ __noinline__ Raw load_edge(const QuantParams& p, const char* base, long long row, long long col) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -206,111 +225,120 @@ __device__ __forceinline__ Raw load_edge(const QuantParams& p, const char* base,
     return r;
 }
 
-// One tile's maxima, scales and codes.  ODD: some element is not finite.
-template <bool BF16, bool ROW, bool COL, bool BLK, bool ODD>
-__device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, const Raw (&v)[kRowsPerThread],
-                                     uint32_t (&part)[8][128], long long cb, long long batch) {
+// Shared memory of a block of threads.
+struct Tile {
+    uint32_t part[8][128];       // column maxima of each warp's rows
+    float by[128];               // col blocks: 2^-e of each column
+};
+
+// One tile's maxima, scales and codes.
+template <bool BF16, bool ROW, bool COL, bool BLK>
+__device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Raw (&v)[kRowsPerThread], Tile& sh,
+                                     long long cb, long long batch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cg = lane & 15, half = lane >> 4;
     const long long col = cb * 128 + cg * 8;
-    if (ROW) {
+    uint32_t rm[kRowsPerThread];
+    ColMax<BF16> cm;
+    cm.clear();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+        if (ROW) top = max(top, rm[i] = row_max<BF16>(v[i]));
+        if (COL || BLK) cm.add(v[i]);
+    }
+    if (!ROW) top = cm.all();
+    if (ROW && !COL ? __any_sync(0xffffffffu, top >= kInf) : __syncthreads_or(top >= kInf)) {
+        cm.clear();
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i) {
-            const int lr = i * 16 + warp * 2 + half;
-            Maxima<BF16> m;
-            m.clear();
-            if (ODD) m.add_finite(v[i]); else m.add(v[i]);
-            uint32_t top = m.all();
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = scale_exponent(top);
-            float by[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
-            if (lr < r.rows) {
-                *reinterpret_cast<uint2*>(p.row_q + (r.row0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
-                if (cg == 0) p.row_scale[cb * p.rows + r.row0 + lr] = static_cast<uint8_t>(e + 127);
-            }
+            const Raw f = replace_odd<BF16>(v[i], true);
+            v[i] = replace_odd<BF16>(v[i], false);
+            if (ROW) rm[i] = row_max<BF16>(f);
+            if (COL || BLK) cm.add(f);
         }
     }
     if (COL || BLK) {
-        Maxima<BF16> m;
-        m.clear();
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            if (ODD) m.add_finite(v[i]); else m.add(v[i]);
-        }
-        uint32_t top[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            top[j] = m.column(j);
-            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-        }
-        __syncthreads();                                 // part's last readers are done
+        cm.meet(16);
         if (half == 0) {
-            uint4* dst = reinterpret_cast<uint4*>(&part[warp][cg * 8]);
-            dst[0] = make_uint4(top[0], top[1], top[2], top[3]);
-            dst[1] = make_uint4(top[4], top[5], top[6], top[7]);
+            uint4* dst = reinterpret_cast<uint4*>(&sh.part[warp][cg * 8]);
+            dst[0] = make_uint4(cm.column(0), cm.column(1), cm.column(2), cm.column(3));
+            dst[1] = make_uint4(cm.column(4), cm.column(5), cm.column(6), cm.column(7));
         }
         __syncthreads();
-        if (COL) {
+    }
+    if (ROW) {
+        // eight rows' maxima over 16 lanes: halve the rows a lane keeps at each
+        // exchange; lane pair k of a half ends up with row k
+        const bool b3 = cg & 8, b2 = cg & 4, b1 = cg & 2;
+        uint32_t q[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint4 t = *reinterpret_cast<const uint4*>(&part[0][cg * 8 + 4 * h]);
+        for (int i = 0; i < 4; ++i)
+            q[i] = max(b3 ? rm[i + 4] : rm[i], __shfl_xor_sync(0xffffffffu, b3 ? rm[i] : rm[i + 4], 8));
 #pragma unroll
-                for (int w = 1; w < 8; ++w) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(&part[w][cg * 8 + 4 * h]);
-                    t = make_uint4(max(t.x, u.x), max(t.y, u.y), max(t.z, u.z), max(t.w, u.w));
-                }
-                top[4 * h] = t.x;
-                top[4 * h + 1] = t.y;
-                top[4 * h + 2] = t.z;
-                top[4 * h + 3] = t.w;
-            }
-            float by[8];
-            uint32_t sc[2] = {0, 0};
+        for (int i = 0; i < 2; ++i) q[i] = max(b2 ? q[i + 2] : q[i], __shfl_xor_sync(0xffffffffu, b2 ? q[i] : q[i + 2], 4));
+        uint32_t m = max(b1 ? q[1] : q[0], __shfl_xor_sync(0xffffffffu, b1 ? q[0] : q[1], 2));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const int e = scale_exponent(m);
+        const float inv = inverse_scale(e);
+        const int mine = (cg >> 1) * 16 + warp * 2 + half;
+        if ((cg & 1) == 0 && mine < r.rows) p.row_scale[cb * p.rows + r.row0 + mine] = static_cast<uint8_t>(e + 127);
+        uint8_t* dst = p.row_q + (r.row0 + warp * 2 + half) * p.ldq + col;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = scale_exponent(top[j]);
-                by[j] = inverse_scale(e);
-                sc[j >> 2] |= static_cast<uint32_t>(e + 127) << (8 * (j & 3));
-            }
-#pragma unroll
-            for (int i = 0; i < kRowsPerThread; ++i) {
-                const int lr = i * 16 + warp * 2 + half;
-                *reinterpret_cast<uint2*>(p.col_q + (r.padded0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
-            }
-            if (threadIdx.x < 16)
-                *reinterpret_cast<uint2*>(p.col_scale + (r.padded0 >> 7) * p.ldq + col) = make_uint2(sc[0], sc[1]);
-        }
-        if (BLK) {
-            uint32_t t = 0;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint4 u = *reinterpret_cast<const uint4*>(&part[w][lane * 4]);
-                t = max(max(t, max(u.x, u.y)), max(u.z, u.w));
-            }
-            t = __reduce_max_sync(0xffffffffu, t);
-            const int e = scale_exponent(t);
-            float by[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) by[j] = inverse_scale(e);
-            uint8_t* q = p.blk_q + batch * p.rows * p.ldq;
-#pragma unroll
-            for (int i = 0; i < kRowsPerThread; ++i) {
-                const int lr = i * 16 + warp * 2 + half;
-                if (lr < r.rows) *reinterpret_cast<uint2*>(q + (r.row0 + lr) * p.ldq + col) = codes<BF16, ODD>(v[i], by);
-            }
-            if (threadIdx.x == 0)
-                p.blk_scale[(batch * ((p.rows + 127) >> 7) + (r.row0 >> 7)) * (p.ldq >> 7) + cb] =
-                    static_cast<uint8_t>(e + 127);
+        for (int i = 0; i < kRowsPerThread; ++i) {
+            const float by = __shfl_sync(0xffffffffu, inv, (lane & 16) + 2 * i);
+            if (i * 16 + warp * 2 + half < r.rows)
+                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
         }
     }
+    if (COL) {
+        if (threadIdx.x < 128) {
+            uint32_t t = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) t = max(t, sh.part[w][threadIdx.x]);
+            const int e = scale_exponent(t);
+            sh.by[threadIdx.x] = inverse_scale(e);
+            p.col_scale[(r.padded0 >> 7) * p.ldq + cb * 128 + threadIdx.x] = static_cast<uint8_t>(e + 127);
+        }
+        __syncthreads();
+        float by[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 f = *reinterpret_cast<const float4*>(&sh.by[cg * 8 + 4 * h]);
+            by[4 * h] = f.x;
+            by[4 * h + 1] = f.y;
+            by[4 * h + 2] = f.z;
+            by[4 * h + 3] = f.w;
+        }
+        uint8_t* dst = p.col_q + (r.padded0 + warp * 2 + half) * p.ldq + col;
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
+    }
+    if (BLK) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const uint4 u = *reinterpret_cast<const uint4*>(&sh.part[w][lane * 4]);
+            t = max(max(t, max(u.x, u.y)), max(u.z, u.w));
+        }
+        t = __reduce_max_sync(0xffffffffu, t);
+        const int e = scale_exponent(t);
+        const float by = inverse_scale(e);
+        uint8_t* dst = p.blk_q + (batch * p.rows + r.row0 + warp * 2 + half) * p.ldq + col;
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i)
+            if (i * 16 + warp * 2 + half < r.rows)
+                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
+        if (threadIdx.x == 0)
+            p.blk_scale[(batch * ((p.rows + 127) >> 7) + (r.row0 >> 7)) * (p.ldq >> 7) + cb] = static_cast<uint8_t>(e + 127);
+    }
+    // the next tile writes `part` after its vote, a barrier that follows every
+    // thread's last read here
 }
 
 template <bool BF16, bool ROW, bool COL, bool BLK>
-__global__ void __launch_bounds__(kThreads) k_fp8_quantize(const __grid_constant__ QuantParams p) {
-    __shared__ uint32_t part[8][128];
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const __grid_constant__ QuantParams p) {
+    __shared__ Tile sh;
     __shared__ RowBlock rb;
     __shared__ int offsets[COL ? kFp8MaxGroups + 1 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -330,22 +358,14 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const __grid_constant
         for (long long cb = blockIdx.x; cb < colblocks; cb += gridDim.x) {
             const long long col = cb * 128 + cg * 8;
             Raw v[kRowsPerThread];
-            if (p.vec && cb * 128 + 128 <= p.cols && r.rows == 128) {
+            if (p.vec && cb * 128 + 128 <= p.cols) {
                 const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
                 const long long step = 16 * p.ld * (BF16 ? 2 : 4);
-#pragma unroll
-                for (int i = 0; i < kRowsPerThread; ++i) {
-                    v[i].a = *reinterpret_cast<const uint4*>(src + i * step);
-                    v[i].b = BF16 ? v[i].a : *reinterpret_cast<const uint4*>(src + i * step + 16);
-                }
-            } else if (p.vec && cb * 128 + 128 <= p.cols) {
-                // a group's last rows
-                const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
-                const long long step = 16 * p.ld * (BF16 ? 2 : 4);
+                const int rows = r.rows - warp * 2 - half;
 #pragma unroll
                 for (int i = 0; i < kRowsPerThread; ++i) {
                     v[i].a = v[i].b = make_uint4(0, 0, 0, 0);
-                    if (i * 16 + warp * 2 + half < r.rows) {
+                    if (i * 16 < rows) {
                         v[i].a = *reinterpret_cast<const uint4*>(src + i * step);
                         if (!BF16) v[i].b = *reinterpret_cast<const uint4*>(src + i * step + 16);
                     }
@@ -358,12 +378,7 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize(const __grid_constant
                     if (lr < r.rows) v[i] = load_edge<BF16>(p, base, r.row0 + lr, col);
                 }
             }
-            Maxima<BF16> m;
-            m.clear();
-#pragma unroll
-            for (int i = 0; i < kRowsPerThread; ++i) m.add(v[i]);
-            if (__syncthreads_or(m.all() >= kInf)) tile<BF16, ROW, COL, BLK, true>(p, r, v, part, cb, batch);
-            else tile<BF16, ROW, COL, BLK, false>(p, r, v, part, cb, batch);
+            tile<BF16, ROW, COL, BLK>(p, r, v, sh, cb, batch);
         }
         __syncthreads();                                 // rb is written anew
     }
