@@ -395,7 +395,7 @@ MUON_API int muon_fp8_quantize_weight(const void* w, int dtype, int batch, long 
  * Sums in fp32 (in the tensor core, scales included), rounded once to out_dtype.
  * out has row stride ld_out (grad weight: groups x n rows).  Rows outside every
  * group are left as they are; the weight gradient of an empty group is zero.
- * Offsets that descend or leave [0, tokens] are clamped.
+ * Offsets that descend or leave [0, tokens] are clamped.  At most 512 groups.
  */
 typedef enum { MUON_FP8_FORWARD = 0, MUON_FP8_GRAD_INPUT = 1, MUON_FP8_GRAD_WEIGHT = 2 } muon_fp8_products;
 MUON_API int muon_fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes,

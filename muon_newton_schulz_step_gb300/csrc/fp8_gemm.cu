@@ -61,6 +61,7 @@ constexpr uint32_t kAcc1 = 224;                         // second accumulator's 
 constexpr uint32_t kScaleCol = 480;                     // scale words' first TMEM column
 constexpr uint32_t kScaleBuf = 16;                      // columns per scale buffer (4 inner + 8 outer)
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kEpiBytes = 32 * 32 * 2;             // one 32 x 32 block per epilogue warp
 constexpr int kPanel = 16;                              // column tiles per panel of the tile order
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
@@ -83,7 +84,7 @@ struct Barriers {
 struct Groups {
     int lo[kFp8MaxGroups];
     int cnt[kFp8MaxGroups];
-    int tile0[kFp8MaxGroups + 1];
+    int tile0[kFp8MaxGroups + 4];    // groups + 1 used
     int block0[kFp8MaxGroups];
 };
 
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint8_t* s_in = smem;
     uint8_t* s_out = s_in + kStages * kStageIn;
     uint8_t* s_sc = s_out + kStages * kStageOut;
+    uint8_t* s_epi = s_sc + kScaleStages * kScaleBytes + 512 + sizeof(Groups);
     Barriers& b = *reinterpret_cast<Barriers*>(s_sc + kScaleStages * kScaleBytes);
     Groups& gs = *reinterpret_cast<Groups*>(s_sc + kScaleStages * kScaleBytes + 512);
     volatile int* abort = &b.abort;
@@ -198,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.tm_in);
         ptx::prefetch_tmap(&p.tm_out);
+        if (!kOutMn) ptx::prefetch_tmap(&p.tm_part);
     }
     if (warp == 0) {
         const int mt = (p.inner + kTile - 1) / kTile;
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ producer --
-        if (lane == 0) {
+        {
             int stage = 0, g = 0;
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int half = x.width / 2;
                 const int c = x.c0 + static_cast<int>(rank) * half;
                 const int boxes = kOutMn ? 4 : (half + static_cast<int>(kBoxRows) - 1) / static_cast<int>(kBoxRows);
+                const bool whole = boxes == kHalf / static_cast<int>(kBoxRows);
                 const uint32_t bytes = 2 * (kStageIn + boxes * kBoxRows * kFp8Block);
                 const int gb = MODE == kFp8GradWeight ? 0 : x.g;
                 for (int kb = x.kb0; kb < x.kb0 + x.nkb; ++kb) {
@@ -259,21 +263,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const uint32_t local = ptx::smem_addr(&b.full[stage]);
                     const uint32_t fb = ptx::mapa_shared(local, 0);
                     if (leader) {
-                        ptx::mbar_arrive_expect_tx(local, bytes);
                         armed |= 1u << stage;
                         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     }
-                    const uint32_t di = ptx::smem_addr(s_in + stage * kStageIn);
-                    const uint32_t d_o = ptx::smem_addr(s_out + stage * kStageOut);
-                    if (kInMn) ptx::tma_load_3d_pair(di, &p.tm_in, fb, m, kb * kFp8Block, gb);
-                    else ptx::tma_load_3d_pair(di, &p.tm_in, fb, kb * kFp8Block, m, gb);
-                    if (kOutMn) {
-                        ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, c & ~15, kb * kFp8Block, 0);
-                    } else {
-                        for (int i = 0; i < boxes; ++i)
-                            ptx::tma_load_3d_pair(d_o + i * kBoxRows * kFp8Block, &p.tm_out, fb, kb * kFp8Block,
-                                                  c + i * static_cast<int>(kBoxRows), 0);
+                    if (ptx::elect_one()) {
+                        if (leader) ptx::mbar_arrive_expect_tx(local, bytes);
+                        const uint32_t di = ptx::smem_addr(s_in + stage * kStageIn);
+                        const uint32_t d_o = ptx::smem_addr(s_out + stage * kStageOut);
+                        if (kInMn) ptx::tma_load_3d_pair(di, &p.tm_in, fb, m, kb * kFp8Block, gb);
+                        else ptx::tma_load_3d_pair(di, &p.tm_in, fb, kb * kFp8Block, m, gb);
+                        if (kOutMn) {
+                            ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, c & ~15, kb * kFp8Block, 0);
+                        } else if (whole) {
+                            ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, kb * kFp8Block, c, 0);
+                        } else {
+                            for (int i = 0; i < boxes; ++i)
+                                ptx::tma_load_3d_pair(d_o + i * kBoxRows * kFp8Block, &p.tm_part, fb, kb * kFp8Block,
+                                                      c + i * static_cast<int>(kBoxRows), 0);
+                        }
                     }
+                    __syncwarp();
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -290,20 +299,45 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 1) {
         // ----------------------------------------------------------- MMA --
-        if (leader && lane == 0) {
+        // The whole warp runs the loop and one elected lane issues: descriptors stay
+        // warp-uniform, which a loop under `lane == 0` would not let the compiler see.
+        if (leader) {
             const uint64_t ad0 = ptx::sdesc_sw128(ptx::smem_addr(s_in), 16, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ptx::smem_addr(s_out), 16, 1024);
             // next 32 elements of K: 32 bytes of a row (K-major) or 32 rows of 128 bytes (MN-major)
             constexpr uint64_t a_k = (kInMn ? 4096 : 32) >> 4;
             constexpr uint64_t b_k = (kOutMn ? 4096 : 32) >> 4;
             int stage = 0, sstage = 0, it = 0, g = 0;
-            uint32_t phase = 0, sphase = 0, sbuf = 0;
+            uint32_t phase = 0, sphase = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs, ++it) {
                 const Tile x = decode_tile(p, gs, t, g);
                 const int acc = it & 1;
                 const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
-                if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tempty[acc]), use ^ 1u, abort, limit) ||
+                // The copy of four blocks' scale words is issued a block before the first
+                // of them, into the other of two buffers: the copies run in order with the
+                // products, and one that its products wait for leaves the tensor core idle
+                // for a copy's latency (155 cycles of 2048, measured).
+                auto copy_scales = [&](int kb) -> bool {
+                    if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sfull[sstage]), sphase, abort, limit)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t src = ptx::smem_addr(s_sc + sstage * kScaleBytes);
+                    const uint32_t dst = tmem + kScaleCol + static_cast<uint32_t>((kb >> 2) & 1) * kScaleBuf;
+                    if (ptx::elect_one()) {
+                        ptx::tmem_copy_scales_pair(dst, ptx::sdesc_rows16(src));
+                        ptx::tmem_copy_scales_pair(dst + 4, ptx::sdesc_rows16(src + 512));
+                        if (x.width > 128) ptx::tmem_copy_scales_pair(dst + 8, ptx::sdesc_rows16(src + 1024));
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.sempty[sstage]), 0x3u);
+                    }
+                    __syncwarp();
+                    if (++sstage == kScaleStages) {
+                        sstage = 0;
+                        sphase ^= 1u;
+                    }
+                    return true;
+                };
+                if ((x.nkb > 0 && !copy_scales(x.kb0)) ||
+                    !ptx::wait_parity_cluster(ptx::smem_addr(&b.tempty[acc]), use ^ 1u, abort, limit) ||
                     (it > 0 && !ptx::wait_parity_cluster(ptx::smem_addr(&b.shared_free[acc ^ 1]),
                                                          static_cast<uint32_t>((it - 1) >> 1) & 1u, abort, limit))) {
                     record_failure(abort);
@@ -311,29 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (acc ? kAcc1 : 0u);
-                uint32_t sfa = 0, sfb = 0;
                 const uint32_t idesc0 = ptx::idesc_mxf8(kTile, x.width, kInMn, kOutMn, 0);
-                for (int i = 0; i < x.nkb; ++i) {
-                    const int kb = x.kb0 + i;
-                    if (i == 0 || (kb & 3) == 0) {
-                        if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sfull[sstage]), sphase, abort, limit)) {
-                            record_failure(abort);
-                            ok = false;
-                            break;
-                        }
-                        ptx::tc_fence_after();
-                        const uint32_t src = ptx::smem_addr(s_sc + sstage * kScaleBytes);
-                        sfa = tmem + kScaleCol + sbuf * kScaleBuf;
-                        sfb = sfa + 4;
-                        ptx::tmem_copy_scales_pair(sfa, ptx::sdesc_rows16(src));
-                        ptx::tmem_copy_scales_pair(sfb, ptx::sdesc_rows16(src + 512));
-                        if (x.width > 128) ptx::tmem_copy_scales_pair(sfb + 4, ptx::sdesc_rows16(src + 1024));
-                        ptx::mma_commit_pair(ptx::smem_addr(&b.sempty[sstage]), 0x3u);
-                        sbuf ^= 1u;
-                        if (++sstage == kScaleStages) {
-                            sstage = 0;
-                            sphase ^= 1u;
-                        }
+                const int kb1 = x.kb0 + x.nkb;
+                for (int kb = x.kb0; kb < kb1; ++kb) {
+                    if ((kb & 3) == 3 && kb + 1 < kb1 && !copy_scales(kb + 1)) {
+                        record_failure(abort);
+                        ok = false;
+                        break;
                     }
                     if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.full[stage]), phase, abort, limit)) {
                         record_failure(abort);
@@ -345,17 +363,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const uint64_t bd = bd0 + static_cast<uint64_t>(stage) * (kStageOut >> 4);
                     const uint32_t sf = static_cast<uint32_t>(kb & 3);
                     const uint32_t idesc = idesc0 | (sf << 4) | (sf << 29);
+                    const uint32_t sfa = tmem + kScaleCol + static_cast<uint32_t>((kb >> 2) & 1) * kScaleBuf;
+                    if (ptx::elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfb, (kk != 0 || i != 0) ? 1u : 0u);
-                    ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), 0x3u);
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfa + 4,
+                                               (kk != 0 || kb != x.kb0) ? 1u : 0u);
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), 0x3u);
+                    }
+                    __syncwarp();
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                ptx::mma_commit_pair(ptx::smem_addr(&b.tfull[acc]), 0x3u);
+                if (ptx::elect_one()) ptx::mma_commit_pair(ptx::smem_addr(&b.tfull[acc]), 0x3u);
+                __syncwarp();
             }
         }
     } else if (warp == 2) {
@@ -400,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // ------------------------------------------------------ epilogue --
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
+        uint8_t* const stage = s_epi + (warp - 4) * kEpiBytes;
+        const uint32_t stage_addr = ptx::smem_addr(stage);
         int it = 0, g = 0;
         for (int t = pair; t < tiles; t += npairs, ++it) {
             const Tile x = decode_tile(p, gs, t, g);
@@ -407,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
             const int m = x.m0 + static_cast<int>(rank) * kHalf + q * 32 + lane;
             const long long batch = MODE == kFp8GradWeight ? x.g * p.out_batch : 0;
-            if (!ptx::wait_parity_cluster_backoff(ptx::smem_addr(&b.tfull[acc]), use, abort, limit, 64)) {
+            // no sleep between polls: the next tile's products wait for the first chunk
+            if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tfull[acc]), use, abort, limit)) {
                 record_failure(abort);
                 break;
             }
@@ -419,9 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int i = 0; i < 4; ++i) {
                 const int ch = acc == 0 && half == 1 ? 7 - 2 * i : half + 2 * i;
                 if (ch < chunks) {
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(tmem + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(ch * 32) +
-                                                (static_cast<uint32_t>(q * 32) << 16), r);
+                    const uint32_t src = tmem + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(ch * 32) +
+                                         (static_cast<uint32_t>(q * 32) << 16);
+                    uint32_t r[2][16];
+                    if (!F32 && p.vec) {
+                        ptx::tmem_ld_16x256b_x4(src, r[0]);
+                        ptx::tmem_ld_16x256b_x4(src + (16u << 16), r[1]);
+                    } else {
+                        ptx::tmem_ld_32x32b_x32(src, reinterpret_cast<uint32_t(&)[32]>(r));
+                    }
                     ptx::tmem_wait_ld();
                     if (!told) {
                         ptx::tc_fence_before();
@@ -430,18 +463,54 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         told = true;
                     }
                     const int left = x.cols - ch * 32;
-                    if (m < p.inner && left > 0) {
-                        const long long at = batch + static_cast<long long>(x.c0 + ch * 32) * p.ld + m;
-                        if (F32) {
-                            float* o = static_cast<float*>(p.out) + at;
+                    const long long row0 = batch + static_cast<long long>(x.c0 + ch * 32) * p.ld;
+                    if (!F32 && p.vec) {
+                        // 8 x 8 blocks through shared memory, transposed: four lanes then
+                        // hold 32 consecutive outputs of one row in 16-byte units
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < left) o[j * p.ld] = x.nkb ? __uint_as_float(r[j]) : 0.0f;
-                        } else {
-                            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < left) o[j * p.ld] = __float2bfloat16_rn(x.nkb ? __uint_as_float(r[j]) : 0.0f);
+                            for (int h = 0; h < 4; ++h) {
+                                const __nv_bfloat162 v =
+                                    __floats2bfloat162_rn(__uint_as_float(r[h >> 1][4 * j + 2 * (h & 1)]),
+                                                          __uint_as_float(r[h >> 1][4 * j + 2 * (h & 1) + 1]));
+                                w[h] = x.nkb ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+                            }
+                            const int row = 8 * j + (lane & 7);
+                            ptx::stmatrix_x4_trans(stage_addr + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0],
+                                                   w[1], w[2], w[3]);
+                        }
+                        __syncwarp();
+                        const int mm = m - lane + 8 * (lane & 3);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 8 * i + (lane >> 2);
+                            const uint4 v = *reinterpret_cast<const uint4*>(
+                                stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                            if (row < left) {
+                                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 + row * p.ld + mm;
+                                if (mm + 8 <= p.inner) {
+                                    *reinterpret_cast<uint4*>(o) = v;
+                                } else {
+                                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        if (mm + e < p.inner)
+                                            o[e] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1))));
+                                }
+                            }
+                        }
+                        __syncwarp();                    // the next chunk writes the blocks anew
+                    } else if (m < p.inner && left > 0) {
+                        const long long at = row0 + m;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float v = x.nkb ? __uint_as_float(r[j >> 4][j & 15]) : 0.0f;
+                            if (j < left) {
+                                if (F32) static_cast<float*>(p.out)[at + j * p.ld] = v;
+                                else static_cast<__nv_bfloat16*>(p.out)[at + j * p.ld] = __float2bfloat16_rn(v);
+                            }
                         }
                     }
                 } else if (!told) {
@@ -468,7 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 static_assert(sizeof(Barriers) <= 512, "barrier block");
-constexpr size_t kSmem = 1024 + kStages * (kStageIn + kStageOut) + kScaleStages * kScaleBytes + 512 + sizeof(Groups);
+static_assert(sizeof(Groups) % 16 == 0, "the epilogue's blocks follow the group table");
+constexpr size_t kSmem = 1024 + kStages * (kStageIn + kStageOut) + kScaleStages * kScaleBytes + 512 + sizeof(Groups) +
+                         8 * kEpiBytes;
 static_assert(kSmem <= 232448, "shared memory");
 
 template <int MODE, bool F32>

@@ -255,7 +255,7 @@ cudaError_t launch_route_backward(const RouteParams& p, int sms, cudaStream_t s)
 
 // ------------------------------------------------------ 8-bit block products --
 constexpr int kFp8Block = 128;           // elements per scale along the reduction
-constexpr int kFp8MaxGroups = 1024;
+constexpr int kFp8MaxGroups = 512;
 
 struct QuantParams {
     const void* x;            // rows x cols of `batch` matrices, row stride ld, matrix stride ldb
@@ -294,13 +294,15 @@ struct Fp8Scale {
 
 struct Fp8GemmParams {
     CUtensorMap tm_in;        // inner operand (the output's contiguous index; MMA rows)
-    CUtensorMap tm_out;       // outer operand (the output's row index; MMA columns)
+    CUtensorMap tm_out;       // outer operand (the output's row index; MMA columns), 128 indices at a time
+    CUtensorMap tm_part;      // forward, grad input: the outer operand 32 rows at a time (narrow tiles)
     Fp8Scale s_in, s_out;
     void* out;                // out[row][inner], row stride ld
     long long ld;
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
     int out_f32;
+    int vec;                  // bf16 output whose rows start on 16 bytes: 16-byte stores
     int inner;                // extent of the inner index
     int outer;                // rows (forward, grad input) or extent of the outer index (grad weight)
     int kblocks;              // reduction blocks (forward, grad input)

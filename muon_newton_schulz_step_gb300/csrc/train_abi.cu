@@ -436,6 +436,7 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
     p.out = out;
     p.ld = ld_out;
     p.out_f32 = out_dtype == MUON_F32;
+    p.vec = out_dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld_out % 8 == 0;
     p.inner = inner;
     p.groups = groups;
     p.offsets = offsets;
@@ -459,7 +460,8 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
                      : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
         p.s_out = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
         if ((rc = op_encode_bytes(&p.tm_in, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_out, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_out, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
     }
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
