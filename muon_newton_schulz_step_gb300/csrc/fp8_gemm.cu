@@ -28,7 +28,7 @@
 // MN-major operand descriptors), so nothing is transposed.
 //
 // Per CTA: warp 0 TMA producer (6 stages of 32 KB), warp 1 MMA issuer (leader
-// only), warp 2 scale words, warps 4-11 epilogue.  Two accumulators of 256
+// only), warps 2-3 scale words, warps 4-11 epilogue.  Two accumulators of 256
 // columns and the scales do not fit in 512 TMEM columns: the second accumulator
 // starts at column 224, and the 32 columns that both own are drained first, so
 // the next tile's products wait for an eighth of the epilogue.  Every wait is
@@ -52,7 +52,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 256;
 constexpr int kHalf = 128;
 constexpr int kStages = 6;
-constexpr int kScaleStages = 3;
+constexpr int kScaleStages = 4;
 constexpr uint32_t kStageIn = kHalf * kFp8Block;        // 16 KB
 constexpr uint32_t kStageOut = kHalf * kFp8Block;       // 16 KB
 constexpr uint32_t kBoxRows = 32;                       // outer operand, K-major: rows per TMA box
@@ -62,7 +62,7 @@ constexpr uint32_t kScaleCol = 480;                     // scale words' first TM
 constexpr uint32_t kScaleBuf = 16;                      // columns per scale buffer (4 inner + 8 outer)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kEpiBytes = 32 * 32 * 2;             // one 32 x 32 block per epilogue warp
-constexpr int kPanel = 16;                              // column tiles per panel of the tile order
+constexpr int kPanel = 8;                               // column tiles per panel of the tile order
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 constexpr int kErrTimeout = 5;
@@ -140,24 +140,31 @@ __device__ __forceinline__ void record_failure(volatile int* abort) {
     *abort = 1;
 }
 
-// The scale words (four reduction blocks' bytes) of N x 32 indices, this lane's
-// every 32nd from idx on, for blocks 4 c .. 4 c + 3 below kb1.  Indices and
-// blocks past the end take the last one's bytes: their products are zero or are
-// not stored.  No load depends on another or on a branch, so all are in flight
-// at once: one chain of L2 latencies per word would starve the tensor core.
+// The scale bytes of four reduction blocks of N x 32 indices, this lane's every
+// 32nd from idx on, for blocks 4 c .. 4 c + 3 below kb1.  Indices and blocks past
+// the end take the last one's bytes: their products are zero or are not stored.
+// No load depends on another or on a branch, so all are in flight at once, and
+// nothing here looks at a byte: the caller packs them when it needs them.
 template <int N>
-__device__ __forceinline__ void scale_words(const Fp8Scale& s, long long base, int idx, int c, int kb1, uint32_t* w) {
+struct ScaleBytes {
     uint32_t v[N][4];
+    __device__ __forceinline__ void load(const Fp8Scale& s, long long base, int idx, int c, int kb1, int width) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int kb = min(4 * c + i, kb1 - 1);
-        const uint8_t* q = s.p + base + static_cast<long long>(kb) * s.red;
+        for (int i = 0; i < 4; ++i) {
+            const int kb = min(4 * c + i, kb1 - 1);
+            const uint8_t* q = s.p + base + static_cast<long long>(kb) * s.red;
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j][i] = q[static_cast<long long>(min(idx + 32 * j, s.limit - 1) >> s.shift) * s.idx];
+            for (int j = 0; j < N; ++j) {
+                v[j][i] = 0x7f;
+                if (32 * j < width)
+                    v[j][i] = q[static_cast<long long>(min(idx + 32 * j, s.limit - 1) >> s.shift) * s.idx];
+            }
+        }
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) w[j] = v[j][0] | (v[j][1] << 8) | (v[j][2] << 16) | (v[j][3] << 24);
-}
+    __device__ __forceinline__ uint32_t word(int j) const {
+        return v[j][0] | (v[j][1] << 8) | (v[j][2] << 16) | (v[j][3] << 24);
+    }
+};
 
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -382,43 +389,58 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 __syncwarp();
             }
         }
-    } else if (warp == 2) {
+    } else if (warp < 4) {
         // --------------------------------------------------------- scales --
-        int sstage = 0, g = 0;
-        uint32_t sphase = 0;
+        // Warps 2 and 3 take turns by groups of four reduction blocks; each loads
+        // its next group's bytes before it stores the current one's, so that four
+        // groups are on their way: one load latency per group, waited for group by
+        // group, is longer than the products of a group of a narrow tile.
+        constexpr int kIn = MODE == kFp8GradWeight ? 4 : 1;   // 128 x 128 blocks: one scale for the CTA's 128 indices
+        ScaleBytes<kIn> vi[2];
+        ScaleBytes<8> vo[2];
+        int seq = 0, waiting = -1, g = 0;
         bool ok = true;
+        auto store = [&](const ScaleBytes<kIn>& si, const ScaleBytes<8>& so, int n) -> bool {
+            const int st = n % kScaleStages;
+            const uint32_t use = static_cast<uint32_t>(n / kScaleStages) & 1u;
+            if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sempty[st]), use ^ 1u, abort, limit)) {
+                record_failure(abort);
+                return false;
+            }
+            uint8_t* dst = s_sc + st * kScaleBytes + lane * 16;
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(si.word(0), si.word(kIn > 1 ? 1 : 0), si.word(kIn > 2 ? 2 : 0), si.word(kIn > 3 ? 3 : 0));
+            *reinterpret_cast<uint4*>(dst + 512) = make_uint4(so.word(0), so.word(1), so.word(2), so.word(3));
+            *reinterpret_cast<uint4*>(dst + 1024) = make_uint4(so.word(4), so.word(5), so.word(6), so.word(7));
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[st]), 0));
+            return true;
+        };
         for (int t = pair; ok && t < tiles; t += npairs) {
             const Tile x = decode_tile(p, gs, t, g);
             if (x.nkb == 0) continue;
             const int kb1 = x.kb0 + x.nkb;
             const int m = x.m0 + static_cast<int>(rank) * kHalf + lane;
-            for (int c = x.kb0 >> 2; c <= (kb1 - 1) >> 2; ++c) {
-                uint32_t w[12];
-                if (MODE == kFp8GradWeight) {
-                    scale_words<4>(p.s_in, 0, m, c, kb1, w);
+            const long long base = MODE == kFp8GradWeight ? 0 : x.g * p.s_in.batch;
+            for (int c = x.kb0 >> 2; ok && c <= (kb1 - 1) >> 2; ++c, ++seq) {
+                if ((seq & 1) != warp - 2) continue;
+                const bool second = (seq >> 1) & 1;      // which of the two register sets
+                if (second) {
+                    vi[1].load(p.s_in, base, m, c, kb1, 32 * kIn);
+                    vo[1].load(p.s_out, 0, x.c0 + lane, c, kb1, x.width);
+                    if (waiting >= 0) ok = store(vi[0], vo[0], waiting);
                 } else {
-                    // 128 x 128 blocks: one scale for this CTA's 128 indices
-                    scale_words<1>(p.s_in, x.g * p.s_in.batch, m, c, kb1, w);
-                    w[1] = w[2] = w[3] = w[0];
+                    vi[0].load(p.s_in, base, m, c, kb1, 32 * kIn);
+                    vo[0].load(p.s_out, 0, x.c0 + lane, c, kb1, x.width);
+                    if (waiting >= 0) ok = store(vi[1], vo[1], waiting);
                 }
-                scale_words<8>(p.s_out, 0, x.c0 + lane, c, kb1, w + 4);
-                if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sempty[sstage]), sphase ^ 1u, abort, limit)) {
-                    record_failure(abort);
-                    ok = false;
-                    break;
-                }
-                uint8_t* dst = s_sc + sstage * kScaleBytes + lane * 16;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    *reinterpret_cast<uint4*>(dst + 512 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[sstage]), 0));
-                if (++sstage == kScaleStages) {
-                    sstage = 0;
-                    sphase ^= 1u;
-                }
+                waiting = seq;
             }
+        }
+        if (ok && waiting >= 0) {
+            if ((waiting >> 1) & 1) store(vi[1], vo[1], waiting);
+            else store(vi[0], vo[0], waiting);
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
