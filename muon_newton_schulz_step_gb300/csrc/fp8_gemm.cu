@@ -17,17 +17,16 @@
 // scale words hold four reduction blocks' bytes, so one 32 x 16-byte copy per
 // 128 rows feeds sixteen instructions, each naming its byte.
 //
-// Layout of a tile: MMA rows (256, 128 per CTA) run along the output's
-// contiguous index, MMA columns along its rows.  So tokens are MMA columns,
-// and a group's tile is as wide as the group needs (a multiple of 32 up to
-// 256): an expert with 40 tokens costs a 64-column tile and not 256 rows.  It
-// also makes the epilogue store 32 consecutive outputs per warp instruction,
-// at any row start and any row stride, with no alignment to keep.
+// Layout of a tile: forward and grad input put tokens on the MMA's columns, and
+// the weight's other dimension on its 256 rows (128 per CTA).  So a group's tile
+// is as wide as the group needs (a multiple of 32 up to 256): an expert with 40
+// tokens costs a 64-column tile and not 256 rows.  The weight gradient has n on
+// the rows and k on the columns.
 //
 // Codes keep one layout: the weight is read along either dimension (K-major or
 // MN-major operand descriptors), so nothing is transposed.
 //
-// Per CTA: warp 0 TMA producer (6 stages of 32 KB), warp 1 MMA issuer (leader
+// Per CTA: warp 0 TMA producer (stages of 32 KB), warp 1 MMA issuer (leader
 // only), warps 2-3 scale words, warps 4-11 epilogue.  Two accumulators of 256
 // columns and the scales do not fit in 512 TMEM columns: the second accumulator
 // starts at column 224, and the 32 columns that both own are drained first, so
@@ -51,25 +50,34 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 256;
 constexpr int kHalf = 128;
-constexpr int kStages = 6;
+constexpr int kMaxStages = 5;
 constexpr int kScaleStages = 4;
-constexpr uint32_t kStageIn = kHalf * kFp8Block;        // 16 KB
-constexpr uint32_t kStageOut = kHalf * kFp8Block;       // 16 KB
-constexpr uint32_t kBoxRows = 32;                       // outer operand, K-major: rows per TMA box
-constexpr uint32_t kScaleBytes = 3 * 512;               // inner 128 rows, outer 2 x 128 columns
+constexpr uint32_t kStageA = kHalf * kFp8Block;        // 16 KB
+constexpr uint32_t kStageB = kHalf * kFp8Block;       // 16 KB
+constexpr uint32_t kBoxRows = 32;                       // B operand, K-major: rows per TMA box
+constexpr uint32_t kScaleBytes = 3 * 512;               // A 128 rows, B 2 x 128 columns
 constexpr uint32_t kAcc1 = 224;                         // second accumulator's first TMEM column
 constexpr uint32_t kScaleCol = 480;                     // scale words' first TMEM column
-constexpr uint32_t kScaleBuf = 16;                      // columns per scale buffer (4 inner + 8 outer)
+constexpr uint32_t kScaleBuf = 16;                      // columns per scale buffer (4 A + 8 B)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kEpiBytes = 32 * 32 * 2;             // one 32 x 32 block per epilogue warp
+constexpr int kEpiBufs = 2;                             // blocks per epilogue warp on their way out
 constexpr int kPanel = 8;                               // column tiles per panel of the tile order
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 20000000ull;
 constexpr int kErrTimeout = 5;
 
+// Pipeline stages, and bytes of one block of results on its way out (32 rows of
+// 64 bytes; of 128 bytes for the weight gradient, whose reductions are short).
+template <int MODE>
+struct Ring {
+    static constexpr int stages = MODE == kFp8GradWeight ? 4 : kMaxStages;
+    static constexpr uint32_t block = MODE == kFp8GradWeight ? 32 * 128 : 32 * 64;
+    static constexpr size_t bytes = 1024 + stages * (kStageA + kStageB) + 8 * kEpiBufs * block + kScaleStages * kScaleBytes;
+};
+
 struct Barriers {
-    uint64_t full[kStages];          // both CTAs' loads -> MMA (the leader's are used)
-    uint64_t empty[kStages];         // MMA -> this CTA's producer
+    uint64_t full[kMaxStages];          // both CTAs' loads -> MMA (the leader's are used)
+    uint64_t empty[kMaxStages];         // MMA -> this CTA's producer
     uint64_t sfull[kScaleStages];    // both CTAs' scale words -> MMA (the leader's are used)
     uint64_t sempty[kScaleStages];   // MMA -> this CTA's scale warp
     uint64_t tfull[2];               // MMA -> this CTA's epilogue
@@ -90,26 +98,29 @@ struct Groups {
 
 struct Tile {
     int g;
-    int m0;          // first inner index of the pair's tile
-    int c0;          // first outer index (row of the outer operand and of the output)
-    int cols;        // outer indices in the tile
-    int width;       // MMA columns: cols rounded up to 32
+    int m0;          // first MMA row of the pair's tile
+    int c0;          // first MMA column
+    int cols;        // MMA columns that are in use
+    int width;       // MMA columns: cols rounded up
     int kb0, nkb;    // reduction blocks
 };
 
-__device__ __forceinline__ void split_columns(int n, int& tiles, int& width) {
+// n columns in equal tiles of at most 256, in multiples of `unit`: 32, or the 64
+// columns of the weight gradient's result blocks.
+__device__ __forceinline__ void split_columns(int n, int unit, int& tiles, int& width) {
     tiles = (n + kTile - 1) / kTile;
-    width = tiles > 0 ? ((n + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+    width = tiles > 0 ? ((n + tiles - 1) / tiles + unit - 1) / unit * unit : unit;
 }
 
 // Tile t of the launch; `g` only moves forward.
 __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g) {
     while (t >= gs.tile0[g + 1]) ++g;
-    const int mt = (p.inner + kTile - 1) / kTile;
+    const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
-    const int n = gw ? p.outer : gs.cnt[g];
+    const int n = gw ? p.n_ext : gs.cnt[g];
     int nt, width;
-    split_columns(n, nt, width);
+    const int unit = gw ? 64 : 32;
+    split_columns(n, unit, nt, width);
     int l = t - gs.tile0[g];
     const int full = nt / kPanel * kPanel;
     int m, c;
@@ -128,7 +139,7 @@ __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups
     x.m0 = m * kTile;
     const int off = c * width;
     x.cols = n - off < width ? n - off : width;
-    x.width = (x.cols + 31) / 32 * 32;
+    x.width = (x.cols + unit - 1) / unit * unit;
     x.c0 = gw ? off : gs.lo[g] + off;
     x.kb0 = gw ? gs.block0[g] : 0;
     x.nkb = gw ? (gs.cnt[g] + kFp8Block - 1) / kFp8Block : p.kblocks;
@@ -141,17 +152,17 @@ __device__ __forceinline__ void record_failure(volatile int* abort) {
 }
 
 // The scale bytes of four reduction blocks of N x 32 indices, this lane's every
-// 32nd from idx on, for blocks 4 c .. 4 c + 3 below kb1.  Indices and blocks past
+// 32nd from idx on, for blocks kb0 .. kb0 + 3 below kb1.  Indices and blocks past
 // the end take the last one's bytes: their products are zero or are not stored.
 // No load depends on another or on a branch, so all are in flight at once, and
 // nothing here looks at a byte: the caller packs them when it needs them.
 template <int N>
 struct ScaleBytes {
     uint32_t v[N][4];
-    __device__ __forceinline__ void load(const Fp8Scale& s, long long base, int idx, int c, int kb1, int width) {
+    __device__ __forceinline__ void load(const Fp8Scale& s, long long base, int idx, int kb0, int kb1, int width) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int kb = min(4 * c + i, kb1 - 1);
+            const int kb = min(kb0 + i, kb1 - 1);
             const uint8_t* q = s.p + base + static_cast<long long>(kb) * s.red;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -169,15 +180,17 @@ struct ScaleBytes {
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
-    constexpr bool kInMn = MODE != kFp8Forward;          // inner operand MN-major
-    constexpr bool kOutMn = MODE == kFp8GradWeight;      // outer operand MN-major
+    constexpr int kStages = Ring<MODE>::stages;
+    constexpr uint32_t kEpiBytes = Ring<MODE>::block;
+    constexpr bool kAMn = MODE != kFp8Forward;          // A operand MN-major
+    constexpr bool kBMn = MODE == kFp8GradWeight;      // B operand MN-major
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* s_in = smem;
-    uint8_t* s_out = s_in + kStages * kStageIn;
-    uint8_t* s_sc = s_out + kStages * kStageOut;
-    uint8_t* s_epi = s_sc + kScaleStages * kScaleBytes + 512 + sizeof(Groups);
+    uint8_t* sm_a = smem;
+    uint8_t* sm_b = sm_a + kStages * kStageA;
+    uint8_t* s_epi = sm_b + kStages * kStageB;
+    uint8_t* s_sc = s_epi + 8 * kEpiBufs * kEpiBytes;
     Barriers& b = *reinterpret_cast<Barriers*>(s_sc + kScaleStages * kScaleBytes);
     Groups& gs = *reinterpret_cast<Groups*>(s_sc + kScaleStages * kScaleBytes + 512);
     volatile int* abort = &b.abort;
@@ -205,19 +218,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         b.abort = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_tmap(&p.tm_in);
-        ptx::prefetch_tmap(&p.tm_out);
-        if (!kOutMn) ptx::prefetch_tmap(&p.tm_part);
+        ptx::prefetch_tmap(&p.tm_a);
+        ptx::prefetch_tmap(&p.tm_b);
+        if (!kBMn) ptx::prefetch_tmap(&p.tm_part);
+        if (p.vec) ptx::prefetch_tmap(&p.tm_res);
     }
     if (warp == 0) {
-        const int mt = (p.inner + kTile - 1) / kTile;
+        const int mt = (p.m_ext + kTile - 1) / kTile;
         int low = 0, tiles = 0, blocks = 0;
-        const int rows = MODE == kFp8GradWeight ? p.rows : p.outer;
+        const int rows = MODE == kFp8GradWeight ? p.rows : p.n_ext;
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
             const GroupSpan sp = warp_group_spans(p.offsets, p.groups, rows, g0, low);
             const int g = g0 + lane;
             int nt, width;
-            split_columns(MODE == kFp8GradWeight ? p.outer : sp.cnt, nt, width);
+            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, MODE == kFp8GradWeight ? 64 : 32, nt, width);
             const int n = g < p.groups ? nt * mt : 0;
             const int nb = (sp.cnt + kFp8Block - 1) / kFp8Block;
             const int it = warp_inclusive_sum(n), ib = warp_inclusive_sum(nb);
@@ -257,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int m = x.m0 + static_cast<int>(rank) * kHalf;
                 const int half = x.width / 2;
                 const int c = x.c0 + static_cast<int>(rank) * half;
-                const int boxes = kOutMn ? 4 : (half + static_cast<int>(kBoxRows) - 1) / static_cast<int>(kBoxRows);
+                const int boxes = kBMn ? 4 : (half + static_cast<int>(kBoxRows) - 1) / static_cast<int>(kBoxRows);
                 const bool whole = boxes == kHalf / static_cast<int>(kBoxRows);
-                const uint32_t bytes = 2 * (kStageIn + boxes * kBoxRows * kFp8Block);
+                const uint32_t bytes = 2 * (kStageA + boxes * kBoxRows * kFp8Block);
                 const int gb = MODE == kFp8GradWeight ? 0 : x.g;
                 for (int kb = x.kb0; kb < x.kb0 + x.nkb; ++kb) {
                     if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.empty[stage]), phase ^ 1u, abort, limit)) {
@@ -275,14 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     if (ptx::elect_one()) {
                         if (leader) ptx::mbar_arrive_expect_tx(local, bytes);
-                        const uint32_t di = ptx::smem_addr(s_in + stage * kStageIn);
-                        const uint32_t d_o = ptx::smem_addr(s_out + stage * kStageOut);
-                        if (kInMn) ptx::tma_load_3d_pair(di, &p.tm_in, fb, m, kb * kFp8Block, gb);
-                        else ptx::tma_load_3d_pair(di, &p.tm_in, fb, kb * kFp8Block, m, gb);
-                        if (kOutMn) {
-                            ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, c & ~15, kb * kFp8Block, 0);
+                        const uint32_t di = ptx::smem_addr(sm_a + stage * kStageA);
+                        const uint32_t d_o = ptx::smem_addr(sm_b + stage * kStageB);
+                        if (kAMn) ptx::tma_load_3d_pair(di, &p.tm_a, fb, m, kb * kFp8Block, gb);
+                        else ptx::tma_load_3d_pair(di, &p.tm_a, fb, kb * kFp8Block, m, gb);
+                        if (kBMn) {
+                            ptx::tma_load_3d_pair(d_o, &p.tm_b, fb, c & ~15, kb * kFp8Block, 0);
                         } else if (whole) {
-                            ptx::tma_load_3d_pair(d_o, &p.tm_out, fb, kb * kFp8Block, c, 0);
+                            ptx::tma_load_3d_pair(d_o, &p.tm_b, fb, kb * kFp8Block, c, 0);
                         } else {
                             for (int i = 0; i < boxes; ++i)
                                 ptx::tma_load_3d_pair(d_o + i * kBoxRows * kFp8Block, &p.tm_part, fb, kb * kFp8Block,
@@ -309,11 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // The whole warp runs the loop and one elected lane issues: descriptors stay
         // warp-uniform, which a loop under `lane == 0` would not let the compiler see.
         if (leader) {
-            const uint64_t ad0 = ptx::sdesc_sw128(ptx::smem_addr(s_in), 16, 1024);
-            const uint64_t bd0 = ptx::sdesc_sw128(ptx::smem_addr(s_out), 16, 1024);
+            const uint64_t ad0 = ptx::sdesc_sw128(ptx::smem_addr(sm_a), 16, 1024);
+            const uint64_t bd0 = ptx::sdesc_sw128(ptx::smem_addr(sm_b), 16, 1024);
             // next 32 elements of K: 32 bytes of a row (K-major) or 32 rows of 128 bytes (MN-major)
-            constexpr uint64_t a_k = (kInMn ? 4096 : 32) >> 4;
-            constexpr uint64_t b_k = (kOutMn ? 4096 : 32) >> 4;
+            constexpr uint64_t a_k = (kAMn ? 4096 : 32) >> 4;
+            constexpr uint64_t b_k = (kBMn ? 4096 : 32) >> 4;
             int stage = 0, sstage = 0, it = 0, g = 0;
             uint32_t phase = 0, sphase = 0;
             bool ok = true;
@@ -325,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 // of them, into the other of two buffers: the copies run in order with the
                 // products, and one that its products wait for leaves the tensor core idle
                 // for a copy's latency (155 cycles of 2048, measured).
-                auto copy_scales = [&](int kb) -> bool {
+                auto copy_scales = [&](int i) -> bool {
                     if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sfull[sstage]), sphase, abort, limit)) return false;
                     ptx::tc_fence_after();
                     const uint32_t src = ptx::smem_addr(s_sc + sstage * kScaleBytes);
-                    const uint32_t dst = tmem + kScaleCol + static_cast<uint32_t>((kb >> 2) & 1) * kScaleBuf;
+                    const uint32_t dst = tmem + kScaleCol + static_cast<uint32_t>((i >> 2) & 1) * kScaleBuf;
                     if (ptx::elect_one()) {
                         ptx::tmem_copy_scales_pair(dst, ptx::sdesc_rows16(src));
                         ptx::tmem_copy_scales_pair(dst + 4, ptx::sdesc_rows16(src + 512));
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     return true;
                 };
-                if ((x.nkb > 0 && !copy_scales(x.kb0)) ||
+                if ((x.nkb > 0 && !copy_scales(0)) ||
                     !ptx::wait_parity_cluster(ptx::smem_addr(&b.tempty[acc]), use ^ 1u, abort, limit) ||
                     (it > 0 && !ptx::wait_parity_cluster(ptx::smem_addr(&b.shared_free[acc ^ 1]),
                                                          static_cast<uint32_t>((it - 1) >> 1) & 1u, abort, limit))) {
@@ -352,10 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (acc ? kAcc1 : 0u);
-                const uint32_t idesc0 = ptx::idesc_mxf8(kTile, x.width, kInMn, kOutMn, 0);
+                const uint32_t idesc0 = ptx::idesc_mxf8(kTile, x.width, kAMn, kBMn, 0);
                 const int kb1 = x.kb0 + x.nkb;
                 for (int kb = x.kb0; kb < kb1; ++kb) {
-                    if ((kb & 3) == 3 && kb + 1 < kb1 && !copy_scales(kb + 1)) {
+                    const int i = kb - x.kb0;
+                    if ((i & 3) == 3 && kb + 1 < kb1 && !copy_scales(i + 1)) {
                         record_failure(abort);
                         ok = false;
                         break;
@@ -366,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint64_t ad = ad0 + static_cast<uint64_t>(stage) * (kStageIn >> 4);
-                    const uint64_t bd = bd0 + static_cast<uint64_t>(stage) * (kStageOut >> 4);
-                    const uint32_t sf = static_cast<uint32_t>(kb & 3);
+                    const uint64_t ad = ad0 + static_cast<uint64_t>(stage) * (kStageA >> 4);
+                    const uint64_t bd = bd0 + static_cast<uint64_t>(stage) * (kStageB >> 4);
+                    const uint32_t sf = static_cast<uint32_t>(i & 3);
                     const uint32_t idesc = idesc0 | (sf << 4) | (sf << 29);
-                    const uint32_t sfa = tmem + kScaleCol + static_cast<uint32_t>((kb >> 2) & 1) * kScaleBuf;
+                    const uint32_t sfa = tmem + kScaleCol + static_cast<uint32_t>((i >> 2) & 1) * kScaleBuf;
                     if (ptx::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -422,17 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (x.nkb == 0) continue;
             const int kb1 = x.kb0 + x.nkb;
             const int m = x.m0 + static_cast<int>(rank) * kHalf + lane;
-            const long long base = MODE == kFp8GradWeight ? 0 : x.g * p.s_in.batch;
-            for (int c = x.kb0 >> 2; ok && c <= (kb1 - 1) >> 2; ++c, ++seq) {
+            const long long base = MODE == kFp8GradWeight ? 0 : x.g * p.s_a.batch;
+            for (int kb = x.kb0; ok && kb < kb1; kb += 4, ++seq) {
                 if ((seq & 1) != warp - 2) continue;
                 const bool second = (seq >> 1) & 1;      // which of the two register sets
                 if (second) {
-                    vi[1].load(p.s_in, base, m, c, kb1, 32 * kIn);
-                    vo[1].load(p.s_out, 0, x.c0 + lane, c, kb1, x.width);
+                    vi[1].load(p.s_a, base, m, kb, kb1, 32 * kIn);
+                    vo[1].load(p.s_b, 0, x.c0 + lane, kb, kb1, x.width);
                     if (waiting >= 0) ok = store(vi[0], vo[0], waiting);
                 } else {
-                    vi[0].load(p.s_in, base, m, c, kb1, 32 * kIn);
-                    vo[0].load(p.s_out, 0, x.c0 + lane, c, kb1, x.width);
+                    vi[0].load(p.s_a, base, m, kb, kb1, 32 * kIn);
+                    vo[0].load(p.s_b, 0, x.c0 + lane, kb, kb1, x.width);
                     if (waiting >= 0) ok = store(vi[1], vo[1], waiting);
                 }
                 waiting = seq;
@@ -444,109 +459,207 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
+        // Results leave by TMA where their rows start on 16 bytes: it cuts off what lies
+        // beyond the output, and stores by the warps themselves held the next block's
+        // read back (weight gradients of 96 experts, whose tiles are nearly all
+        // epilogue: 975 us by 16-byte stores, 888 by 64-byte rows, @@ by 128-byte rows).
+        //   weight gradient: a lane holds consecutive results of one row, written as
+        //   they are, 32 rows of 128 bytes a block;
+        //   else: lanes run along the row; 8 x 8 blocks of bf16 go through shared memory
+        //   transposed, 32 rows of 64 bytes a block.
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
-        uint8_t* const stage = s_epi + (warp - 4) * kEpiBytes;
-        const uint32_t stage_addr = ptx::smem_addr(stage);
-        int it = 0, g = 0;
+        uint8_t* const stage = s_epi + (warp - 4) * kEpiBufs * kEpiBytes;
+        int it = 0, g = 0, nbuf = 0;            // tiles, group, blocks on their way so far
         for (int t = pair; t < tiles; t += npairs, ++it) {
             const Tile x = decode_tile(p, gs, t, g);
             const int acc = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
-            const int m = x.m0 + static_cast<int>(rank) * kHalf + q * 32 + lane;
-            const long long batch = MODE == kFp8GradWeight ? x.g * p.out_batch : 0;
+            const int m0 = x.m0 + static_cast<int>(rank) * kHalf + q * 32;
+            const int batch = MODE == kFp8GradWeight ? x.g : 0;
+            const int chunks = x.width / 32;
+            const uint32_t src = tmem + (acc ? kAcc1 : 0u) + (static_cast<uint32_t>(q * 32) << 16);
+            // the accumulators' common columns (of the first its last 32, second half; of the
+            // second its first 32, first half) are read first
+            const bool owner = (acc == 0) == (half == 1);
+            auto release_shared = [&] {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
+            };
+            auto release = [&] {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
+            };
             // no sleep between polls: the next tile's products wait for the first chunk
             if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tfull[acc]), use, abort, limit)) {
                 record_failure(abort);
                 break;
             }
             ptx::tc_fence_after();
-            const int chunks = x.width / 32;
-            // the accumulators' common columns (first: chunk 7, odd; second: chunk 0, even) first
-            const bool owner = (acc == 0) == (half == 1);
-            bool told = !owner;
-            for (int i = 0; i < 4; ++i) {
-                const int ch = acc == 0 && half == 1 ? 7 - 2 * i : half + 2 * i;
-                if (ch < chunks) {
-                    const uint32_t src = tmem + (acc ? kAcc1 : 0u) + static_cast<uint32_t>(ch * 32) +
-                                         (static_cast<uint32_t>(q * 32) << 16);
-                    uint32_t r[2][16];
-                    if (!F32 && p.vec) {
-                        ptx::tmem_ld_16x256b_x4(src, r[0]);
-                        ptx::tmem_ld_16x256b_x4(src + (16u << 16), r[1]);
-                    } else {
-                        ptx::tmem_ld_32x32b_x32(src, reinterpret_cast<uint32_t(&)[32]>(r));
-                    }
+            if constexpr (MODE == kFp8GradWeight) {
+                // groups of 64 columns: 0, 2 and 1, 3; the second half of the first accumulator from its end
+                uint32_t r[2][32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int pr = acc == 0 && half == 1 ? 3 - 2 * i : half + 2 * i;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (2 * pr + h < chunks) ptx::tmem_ld_32x32b_x32(src + static_cast<uint32_t>(64 * pr + 32 * h), r[h]);
                     ptx::tmem_wait_ld();
-                    if (!told) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
-                        told = true;
+                    if (i == 0 && owner) release_shared();
+                    if (i == 1) release();
+                    if (x.nkb == 0) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0u;
                     }
-                    const int left = x.cols - ch * 32;
-                    const long long row0 = batch + static_cast<long long>(x.c0 + ch * 32) * p.ld;
-                    if (!F32 && p.vec) {
-                        // 8 x 8 blocks through shared memory, transposed: four lanes then
-                        // hold 32 consecutive outputs of one row in 16-byte units
+                    if (2 * pr >= chunks) continue;
+                    if (p.vec) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t w[4];
+                        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+                            if (F32 && 2 * pr + h >= chunks) continue;
+                            uint8_t* const row = stage + (nbuf & (kEpiBufs - 1)) * kEpiBytes + lane * 128;
+                            if (lane == 0) ptx::bulk_wait_group_read<kEpiBufs - 1>();   // its last store has read it
+                            __syncwarp();
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const __nv_bfloat162 v =
-                                    __floats2bfloat162_rn(__uint_as_float(r[h >> 1][4 * j + 2 * (h & 1)]),
-                                                          __uint_as_float(r[h >> 1][4 * j + 2 * (h & 1) + 1]));
-                                w[h] = x.nkb ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+                            for (int u = 0; u < 8; ++u) {
+                                uint4 v;
+                                if (F32) {
+                                    v = make_uint4(r[h][4 * u], r[h][4 * u + 1], r[h][4 * u + 2], r[h][4 * u + 3]);
+                                } else {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const int j = 8 * u + 2 * e;
+                                        const __nv_bfloat162 f = __floats2bfloat162_rn(__uint_as_float(r[j >> 5][j & 31]),
+                                                                                       __uint_as_float(r[j >> 5][(j & 31) + 1]));
+                                        w[e] = *reinterpret_cast<const uint32_t*>(&f);
+                                    }
+                                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                                *reinterpret_cast<uint4*>(row + ((u ^ (lane & 7)) << 4)) = v;
                             }
-                            const int row = 8 * j + (lane & 7);
-                            ptx::stmatrix_x4_trans(stage_addr + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0],
-                                                   w[1], w[2], w[3]);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                const int col = x.c0 + 64 * pr + 32 * h;
+                                if (m0 < p.m_ext && col < p.n_ext)
+                                    ptx::tma_store_3d(&p.tm_res, ptx::smem_addr(row), col, m0, batch);
+                                ptx::bulk_commit_group();
+                            }
+                            ++nbuf;
                         }
+                    } else if (m0 + lane < p.m_ext) {
+                        const long long at = batch * p.out_batch + static_cast<long long>(m0 + lane) * p.ld + x.c0 + 64 * pr;
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) {
+                            if (64 * pr + j < x.cols) {
+                                const float v = __uint_as_float(r[j >> 5][j & 31]);
+                                if (F32) static_cast<float*>(p.out)[at + j] = v;
+                                else static_cast<__nv_bfloat16*>(p.out)[at + j] = __float2bfloat16_rn(v);
+                            }
+                        }
+                    }
+                }
+                continue;
+            }
+            auto chunk = [&](int i) { return acc == 0 && half == 1 ? 7 - 2 * i : half + 2 * i; };
+            auto read = [&](int ch, uint32_t (&r)[2][16]) {
+                if (ch >= chunks) return;
+                if (!F32 && p.vec) {
+                    ptx::tmem_ld_16x256b_x4(src + static_cast<uint32_t>(ch * 32), r[0]);
+                    ptx::tmem_ld_16x256b_x4(src + static_cast<uint32_t>(ch * 32) + (16u << 16), r[1]);
+                } else {
+                    ptx::tmem_ld_32x32b_x32(src + static_cast<uint32_t>(ch * 32), reinterpret_cast<uint32_t(&)[32]>(r));
+                }
+            };
+            auto write = [&](int ch, uint32_t (&r)[2][16]) {
+                if (ch >= chunks) return;
+                const int left = x.cols - ch * 32;
+                const int c = x.c0 + ch * 32;
+                if (!F32 && p.vec) {
+                    uint8_t* const buf = stage + (nbuf & (kEpiBufs - 1)) * kEpiBytes;
+                    const uint32_t buf_addr = ptx::smem_addr(buf);
+                    if (lane == 0) ptx::bulk_wait_group_read<kEpiBufs - 1>();   // its last store has read it
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const __nv_bfloat162 v =
+                                __floats2bfloat162_rn(__uint_as_float(r[h >> 1][4 * j + 2 * (h & 1)]),
+                                                      __uint_as_float(r[h >> 1][4 * j + 2 * (h & 1) + 1]));
+                            w[h] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        const int row = 8 * j + (lane & 7);
+                        ptx::stmatrix_x4_trans(buf_addr + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0], w[1],
+                                               w[2], w[3]);
+                    }
+                    if (left >= 32) {
+                        ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        const int mm = m - lane + 8 * (lane & 3);
+                        if (lane == 0) {
+                            if (m0 < p.m_ext) ptx::tma_store_3d(&p.tm_res, buf_addr, m0, c, 0);
+                            ptx::bulk_commit_group();
+                        }
+                    } else {
+                        // a group's last rows: the next group's lie behind them
+                        __syncwarp();
+                        const int mm = m0 + 8 * (lane & 3);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int row = 8 * i + (lane >> 2);
-                            const uint4 v = *reinterpret_cast<const uint4*>(
-                                stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                            const uint4 v =
+                                *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
                             if (row < left) {
-                                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 + row * p.ld + mm;
-                                if (mm + 8 <= p.inner) {
+                                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(c + row) * p.ld + mm;
+                                if (mm + 8 <= p.m_ext) {
                                     *reinterpret_cast<uint4*>(o) = v;
                                 } else {
                                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                     for (int e = 0; e < 8; ++e)
-                                        if (mm + e < p.inner)
+                                        if (mm + e < p.m_ext)
                                             o[e] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1))));
                                 }
                             }
                         }
-                        __syncwarp();                    // the next chunk writes the blocks anew
-                    } else if (m < p.inner && left > 0) {
-                        const long long at = row0 + m;
+                        if (lane == 0) ptx::bulk_commit_group();   // an empty group keeps the count of buffers
+                    }
+                    ++nbuf;
+                } else if (m0 + lane < p.m_ext) {
+                    const long long at = static_cast<long long>(c) * p.ld + m0 + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = x.nkb ? __uint_as_float(r[j >> 4][j & 15]) : 0.0f;
-                            if (j < left) {
-                                if (F32) static_cast<float*>(p.out)[at + j * p.ld] = v;
-                                else static_cast<__nv_bfloat16*>(p.out)[at + j * p.ld] = __float2bfloat16_rn(v);
-                            }
+                    for (int j = 0; j < 32; ++j) {
+                        const float v = __uint_as_float(r[j >> 4][j & 15]);
+                        if (j < left) {
+                            if (F32) static_cast<float*>(p.out)[at + j * p.ld] = v;
+                            else static_cast<__nv_bfloat16*>(p.out)[at + j * p.ld] = __float2bfloat16_rn(v);
                         }
                     }
-                } else if (!told) {
-                    // a narrow tile: chunk 7 holds none of it
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
-                    told = true;
                 }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
+            };
+            // each chunk is read while the one before it is written
+            uint32_t ra[2][16], rb[2][16];
+            read(chunk(0), ra);
+            ptx::tmem_wait_ld();
+            if (owner) release_shared();
+            read(chunk(1), rb);
+            write(chunk(0), ra);
+            ptx::tmem_wait_ld();
+            read(chunk(2), ra);
+            write(chunk(1), rb);
+            ptx::tmem_wait_ld();
+            read(chunk(3), rb);
+            write(chunk(2), ra);
+            ptx::tmem_wait_ld();
+            release();
+            write(chunk(3), rb);
         }
+        if (lane == 0) ptx::bulk_wait_group_all();       // every block written
+        __syncwarp();
     }
 
     ptx::tc_fence_before();
@@ -559,26 +672,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 static_assert(sizeof(Barriers) <= 512, "barrier block");
-static_assert(sizeof(Groups) % 16 == 0, "the epilogue's blocks follow the group table");
-constexpr size_t kSmem = 1024 + kStages * (kStageIn + kStageOut) + kScaleStages * kScaleBytes + 512 + sizeof(Groups) +
-                         8 * kEpiBytes;
-static_assert(kSmem <= 232448, "shared memory");
+template <int MODE>
+constexpr size_t smem_bytes() {
+    return Ring<MODE>::bytes + 512 + sizeof(Groups);
+}
+static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
 template <int MODE, bool F32>
 cudaError_t run(const Fp8GemmParams& p, int pairs, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kSmem));
+                                               static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
-    k_fp8_gemm<MODE, F32><<<2 * pairs, kThreads, kSmem, s>>>(p);
+    k_fp8_gemm<MODE, F32><<<2 * pairs, kThreads, smem_bytes<MODE>(), s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s) {
-    const long long mt = (p.inner + kTile - 1) / kTile;
-    const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.outer + kTile - 1) / kTile)
-                                                  : p.outer / kTile + p.groups;
+    const long long mt = (p.m_ext + kTile - 1) / kTile;
+    const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
+                                                  : p.n_ext / kTile + p.groups;
     const long long most = mt * nt;
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {

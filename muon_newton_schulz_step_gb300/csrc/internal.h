@@ -278,8 +278,8 @@ struct QuantParams {
 cudaError_t launch_fp8_quantize(const QuantParams& p, cudaStream_t s);
 
 enum Fp8Mode : int {
-    kFp8Forward = 0,          // outer operand's rows grouped; inner operand: batch g, K-major
-    kFp8GradInput = 1,        // outer operand's rows grouped; inner operand: batch g, MN-major
+    kFp8Forward = 0,          // tokens grouped; the weight of group g K-major
+    kFp8GradInput = 1,        // tokens grouped; the weight of group g MN-major
     kFp8GradWeight = 2        // reduction grouped; both operands MN-major
 };
 
@@ -293,22 +293,23 @@ struct Fp8Scale {
 };
 
 struct Fp8GemmParams {
-    CUtensorMap tm_in;        // inner operand (the output's contiguous index; MMA rows)
-    CUtensorMap tm_out;       // outer operand (the output's row index; MMA columns), 128 indices at a time
-    CUtensorMap tm_part;      // forward, grad input: the outer operand 32 rows at a time (narrow tiles)
-    Fp8Scale s_in, s_out;
-    void* out;                // out[row][inner], row stride ld
+    CUtensorMap tm_a;         // MMA rows' operand: the weight (forward, grad input), dy (grad weight)
+    CUtensorMap tm_b;         // MMA columns' operand: the tokens, x (grad weight); 128 indices at a time
+    CUtensorMap tm_part;      // forward, grad input: the tokens 32 rows at a time (narrow tiles)
+    CUtensorMap tm_res;       // vec: the output by blocks
+    Fp8Scale s_a, s_b;
+    void* out;                // row stride ld
     long long ld;
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
     int out_f32;
-    int vec;                  // bf16 output whose rows start on 16 bytes: 16-byte stores
-    int inner;                // extent of the inner index
-    int outer;                // rows (forward, grad input) or extent of the outer index (grad weight)
+    int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only): it leaves by TMA
+    int m_ext;                // extent along the MMA's rows: n (forward, grad weight), k (grad input)
+    int n_ext;                // extent along its columns: tokens; k (grad weight)
     int kblocks;              // reduction blocks (forward, grad input)
     int groups;               // >= 1
     const int* offsets;       // groups + 1 row offsets, or nullptr: one group of all rows
-    int rows;                 // grad weight: rows reduced over in all
+    int rows;                 // grad weight: tokens
     unsigned long long wait_ns;
 };
 
@@ -362,6 +363,8 @@ int op_device(int* sms);                       // the current device, checked; i
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
 int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
                     int box_inner, int box_outer);
+int op_encode_result(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
+                     long long ld, long long batch_stride, int box_inner, bool f32);
 cudaError_t launch_ns_small(const SmallParams& p, size_t smem, cudaStream_t s);
 size_t ns_small_smem_bytes(int r, int k);
 

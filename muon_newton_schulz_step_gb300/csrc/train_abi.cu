@@ -436,32 +436,40 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
     p.out = out;
     p.ld = ld_out;
     p.out_f32 = out_dtype == MUON_F32;
-    p.vec = out_dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(out) % 16 == 0 && ld_out % 8 == 0;
-    p.inner = inner;
+    const bool rows16 = reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                        ld_out * static_cast<long long>(dtype_size(out_dtype)) % 16 == 0;
+    p.vec = rows16 && (gw || out_dtype == MUON_BF16);
+    p.m_ext = gw ? n : inner;
     p.groups = groups;
     p.offsets = offsets;
     p.rows = static_cast<int>(tokens);
     if (gw) {
         // a: dy's col codes (padded tokens x ldn); b: x's col codes (padded tokens x ldk)
         const long long padded = muon_fp8_padded_rows(tokens, groups);
-        p.outer = n;
+        p.n_ext = k;
         p.out_batch = static_cast<long long>(n) * ld_out;
-        p.s_in = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
-        p.s_out = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
-        if ((rc = op_encode_bytes(&p.tm_in, b_codes, ldk, padded, 1, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_out, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
+        p.s_a = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
+        p.s_b = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
+        if ((rc = op_encode_bytes(&p.tm_a, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_b, b_codes, ldk, padded, 1, 128, 128)) != MUON_OK) return rc;
     } else {
         // a: x's or dy's row codes (tokens x ld); b: the weight's codes (groups x n x ldk)
         const bool fwd = product == MUON_FP8_FORWARD;
         const long long lda = fwd ? ldk : ldn;
-        p.outer = static_cast<int>(tokens);
+        p.n_ext = static_cast<int>(tokens);
         p.kblocks = static_cast<int>(fwd ? kb : nb);
-        p.s_in = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
+        p.s_a = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
                      : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
-        p.s_out = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
-        if ((rc = op_encode_bytes(&p.tm_in, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_out, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
+        p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
+        if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
+    }
+    if (p.vec) {
+        const long long rows = gw ? n : tokens, batch = gw ? groups : 1;
+        if ((rc = op_encode_result(&p.tm_res, out, inner, rows, batch, ld_out, gw ? p.out_batch : rows * ld_out,
+                                   gw && !p.out_f32 ? 64 : 32, p.out_f32 != 0)) != MUON_OK)
+            return rc;
     }
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
