@@ -70,9 +70,10 @@ constexpr int kErrTimeout = 5;
 // 64 bytes; of 128 bytes for the weight gradient, whose reductions are short).
 template <int MODE>
 struct Ring {
-    static constexpr int stages = MODE == kFp8GradWeight ? 4 : kMaxStages;
+    static constexpr int stages = kMaxStages;
     static constexpr uint32_t block = MODE == kFp8GradWeight ? 32 * 128 : 32 * 64;
-    static constexpr size_t bytes = 1024 + stages * (kStageA + kStageB) + 8 * kEpiBufs * block + kScaleStages * kScaleBytes;
+    static constexpr int blocks = MODE == kFp8GradWeight ? 1 : kEpiBufs;   // per epilogue warp
+    static constexpr size_t bytes = 1024 + stages * (kStageA + kStageB) + 8 * blocks * block + kScaleStages * kScaleBytes;
 };
 
 struct Barriers {
@@ -94,7 +95,18 @@ struct Groups {
     int cnt[kFp8MaxGroups];
     int tile0[kFp8MaxGroups + 4];    // groups + 1 used
     int block0[kFp8MaxGroups];
+    int width[kFp8MaxGroups];        // columns of the group's tiles
 };
+
+// a / d for 0 <= a < 2^31, with inv = 1 / d in fp32: the estimate is off by at
+// most one while the quotient stays below 2^22.
+__device__ __forceinline__ int quotient(int a, int d, float inv) {
+    int q = __float2int_rz(__int2float_rn(a) * inv);
+    const int r = a - q * d;
+    if (r < 0) --q;
+    else if (r >= d) ++q;
+    return q;
+}
 
 struct Tile {
     int g;
@@ -112,33 +124,34 @@ __device__ __forceinline__ void split_columns(int n, int unit, int& tiles, int& 
     width = tiles > 0 ? ((n + tiles - 1) / tiles + unit - 1) / unit * unit : unit;
 }
 
-// Tile t of the launch; `g` only moves forward.
+// Tile t of the launch; `g` only moves forward.  Integer divisions are avoided:
+// four of them took 900 cycles of every tile in every role.
 __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g) {
     while (t >= gs.tile0[g + 1]) ++g;
     const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
     const int n = gw ? p.n_ext : gs.cnt[g];
-    int nt, width;
-    const int unit = gw ? 64 : 32;
-    split_columns(n, unit, nt, width);
+    const int nt = (n + kTile - 1) / kTile, width = gs.width[g];
     int l = t - gs.tile0[g];
     const int full = nt / kPanel * kPanel;
     int m, c;
     if (l < full * mt) {
-        const int panel = l / (kPanel * mt), r = l - panel * kPanel * mt;
+        const int per = kPanel * mt;
+        const int panel = quotient(l, per, __frcp_rn(__int2float_rn(per))), r = l - panel * per;
         m = r / kPanel;
         c = panel * kPanel + r % kPanel;
     } else {
         l -= full * mt;
         const int w = nt - full;
-        m = l / w;
-        c = full + l % w;
+        m = quotient(l, w, __frcp_rn(__int2float_rn(w)));
+        c = full + l - m * w;
     }
     Tile x;
     x.g = g;
     x.m0 = m * kTile;
     const int off = c * width;
     x.cols = n - off < width ? n - off : width;
+    const int unit = gw ? 64 : 32;
     x.width = (x.cols + unit - 1) / unit * unit;
     x.c0 = gw ? off : gs.lo[g] + off;
     x.kb0 = gw ? gs.block0[g] : 0;
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint8_t* sm_a = smem;
     uint8_t* sm_b = sm_a + kStages * kStageA;
     uint8_t* s_epi = sm_b + kStages * kStageB;
-    uint8_t* s_sc = s_epi + 8 * kEpiBufs * kEpiBytes;
+    uint8_t* s_sc = s_epi + 8 * Ring<MODE>::blocks * kEpiBytes;
     Barriers& b = *reinterpret_cast<Barriers*>(s_sc + kScaleStages * kScaleBytes);
     Groups& gs = *reinterpret_cast<Groups*>(s_sc + kScaleStages * kScaleBytes + 512);
     volatile int* abort = &b.abort;
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         ptx::prefetch_tmap(&p.tm_a);
         ptx::prefetch_tmap(&p.tm_b);
         if (!kBMn) ptx::prefetch_tmap(&p.tm_part);
-        if (p.vec) ptx::prefetch_tmap(&p.tm_res);
+        if (MODE != kFp8GradWeight && p.vec) ptx::prefetch_tmap(&p.tm_res);
     }
     if (warp == 0) {
         const int mt = (p.m_ext + kTile - 1) / kTile;
@@ -240,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 gs.cnt[g] = sp.cnt;
                 gs.tile0[g] = tiles + it - n;
                 gs.block0[g] = blocks + ib - nb;
+                gs.width[g] = width;
             }
             tiles += __shfl_sync(0xffffffffu, it, 31);
             blocks += __shfl_sync(0xffffffffu, ib, 31);
@@ -459,17 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
-        // Results leave by TMA where their rows start on 16 bytes: it cuts off what lies
-        // beyond the output, and stores by the warps themselves held the next block's
-        // read back (weight gradients of 96 experts, whose tiles are nearly all
-        // epilogue: 975 us by 16-byte stores, 888 by 64-byte rows, @@ by 128-byte rows).
-        //   weight gradient: a lane holds consecutive results of one row, written as
-        //   they are, 32 rows of 128 bytes a block;
+        // Where rows of the result start on 16 bytes:
+        //   weight gradient: a lane holds consecutive results of one row; blocks of 32
+        //   rows of 128 bytes go through shared memory and leave in whole lines.  These
+        //   tiles are nearly all epilogue, and their stores are the warps' own: TMA
+        //   stores wait behind the loads that the producer has asked for ahead (2500
+        //   cycles; 784 against @@ us for 96 experts' weights);
         //   else: lanes run along the row; 8 x 8 blocks of bf16 go through shared memory
-        //   transposed, 32 rows of 64 bytes a block.
+        //   transposed and leave by TMA, 32 rows of 64 bytes at a time.
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
-        uint8_t* const stage = s_epi + (warp - 4) * kEpiBufs * kEpiBytes;
+        uint8_t* const stage = s_epi + (warp - 4) * Ring<MODE>::blocks * kEpiBytes;
         int it = 0, g = 0, nbuf = 0;            // tiles, group, blocks on their way so far
         for (int t = pair; t < tiles; t += npairs, ++it) {
             const Tile x = decode_tile(p, gs, t, g);
@@ -485,12 +499,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             auto release_shared = [&] {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
             };
             auto release = [&] {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
             };
             // no sleep between polls: the next tile's products wait for the first chunk
             if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tfull[acc]), use, abort, limit)) {
@@ -519,9 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                         for (int h = 0; h < (F32 ? 2 : 1); ++h) {
                             if (F32 && 2 * pr + h >= chunks) continue;
-                            uint8_t* const row = stage + (nbuf & (kEpiBufs - 1)) * kEpiBytes + lane * 128;
-                            if (lane == 0) ptx::bulk_wait_group_read<kEpiBufs - 1>();   // its last store has read it
-                            __syncwarp();
+                            uint8_t* const row = stage + lane * 128;
+                            __syncwarp();                // the last block has been read
 #pragma unroll
                             for (int u = 0; u < 8; ++u) {
                                 uint4 v;
@@ -540,15 +553,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                 }
                                 *reinterpret_cast<uint4*>(row + ((u ^ (lane & 7)) << 4)) = v;
                             }
-                            ptx::fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) {
-                                const int col = x.c0 + 64 * pr + 32 * h;
-                                if (m0 < p.m_ext && col < p.n_ext)
-                                    ptx::tma_store_3d(&p.tm_res, ptx::smem_addr(row), col, m0, batch);
-                                ptx::bulk_commit_group();
+                            constexpr int kPer = F32 ? 4 : 8, kSize = F32 ? 4 : 2;   // elements per 16 bytes
+                            const int col = x.c0 + 64 * pr + 32 * h + kPer * (lane & 7);
+                            char* o = static_cast<char*>(p.out) +
+                                      (batch * p.out_batch + static_cast<long long>(m0 + (lane >> 3)) * p.ld + col) * kSize;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int rr = 4 * k + (lane >> 3);
+                                const uint4 v = *reinterpret_cast<const uint4*>(
+                                    stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                                if (m0 + rr < p.m_ext) {
+                                    if (col + kPer <= p.n_ext) {
+                                        *reinterpret_cast<uint4*>(o) = v;
+                                    } else {
+                                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                        for (int e = 0; e < kPer; ++e) {
+                                            if (col + e >= p.n_ext) continue;
+                                            if (F32) reinterpret_cast<uint32_t*>(o)[e] = w[e];
+                                            else reinterpret_cast<uint16_t*>(o)[e] =
+                                                static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+                                        }
+                                    }
+                                }
+                                o += 4 * p.ld * kSize;
                             }
-                            ++nbuf;
                         }
                     } else if (m0 + lane < p.m_ext) {
                         const long long at = batch * p.out_batch + static_cast<long long>(m0 + lane) * p.ld + x.c0 + 64 * pr;

@@ -296,14 +296,14 @@ struct Fp8GemmParams {
     CUtensorMap tm_a;         // MMA rows' operand: the weight (forward, grad input), dy (grad weight)
     CUtensorMap tm_b;         // MMA columns' operand: the tokens, x (grad weight); 128 indices at a time
     CUtensorMap tm_part;      // forward, grad input: the tokens 32 rows at a time (narrow tiles)
-    CUtensorMap tm_res;       // vec: the output by blocks
+    CUtensorMap tm_res;       // vec, forward and grad input: the output in 32 x 32 blocks
     Fp8Scale s_a, s_b;
     void* out;                // row stride ld
     long long ld;
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
     int out_f32;
-    int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only): it leaves by TMA
+    int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only)
     int m_ext;                // extent along the MMA's rows: n (forward, grad weight), k (grad input)
     int n_ext;                // extent along its columns: tokens; k (grad weight)
     int kblocks;              // reduction blocks (forward, grad input)
@@ -363,8 +363,7 @@ int op_device(int* sms);                       // the current device, checked; i
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
 int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
                     int box_inner, int box_outer);
-int op_encode_result(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
-                     long long ld, long long batch_stride, int box_inner, bool f32);
+int op_encode_result(CUtensorMap* map, const void* base, long long cols, long long rows, long long ld);
 cudaError_t launch_ns_small(const SmallParams& p, size_t smem, cudaStream_t s);
 size_t ns_small_smem_bytes(int r, int k);
 

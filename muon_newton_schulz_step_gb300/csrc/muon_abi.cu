@@ -1065,18 +1065,14 @@ int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::f
     return launch(kind, flops, bytes, s, f);
 }
 
-// A result in blocks of 32 rows of 64 or 128 bytes, swizzled as wide; strides in elements.
-int op_encode_result(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
-                     long long ld, long long batch_stride, int box_inner, bool f32) {
-    const cuuint64_t sz = f32 ? 4 : 2;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
-                                static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * sz, static_cast<cuuint64_t>(batch_stride) * sz};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), 32, 1};
+// A bf16 result in blocks of 32 x 32 (64-byte rows, 64-byte swizzle).
+int op_encode_result(CUtensorMap* map, const void* base, long long cols, long long rows, long long ld) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * dims[1] * 2};
+    const cuuint32_t box[3] = {32, 32, 1};
     const cuuint32_t es[3] = {1, 1, 1};
-    const CUresult r = g_encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                                const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                box_inner * sz == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return MUON_OK;

@@ -465,12 +465,7 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
         if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
     }
-    if (p.vec) {
-        const long long rows = gw ? n : tokens, batch = gw ? groups : 1;
-        if ((rc = op_encode_result(&p.tm_res, out, inner, rows, batch, ld_out, gw ? p.out_batch : rows * ld_out,
-                                   gw && !p.out_f32 ? 64 : 32, p.out_f32 != 0)) != MUON_OK)
-            return rc;
-    }
+    if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
     return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, stream); });
