@@ -391,7 +391,7 @@ MUON_API int muon_fp8_quantize_weight(const void* w, int dtype, int batch, long 
  *   MUON_FP8_GRAD_INPUT   out[t, k] = sum_n dy[t, n] W_g[n, k]
  *                         a: dy's row blocks; b: W's 128 x 128 blocks
  *   MUON_FP8_GRAD_WEIGHT  out[g, n, k] = sum over group g's t of dy[t, n] x[t, k]
- *                         a: dy's col blocks; b: x's col blocks
+ *                         a: dy's col blocks; b: x's col blocks (scales 4-byte aligned)
  * Sums in fp32 (in the tensor core, scales included), rounded once to out_dtype.
  * out has row stride ld_out (grad weight: groups x n rows).  Rows outside every
  * group are left as they are; the weight gradient of an empty group is zero.

@@ -190,6 +190,62 @@ struct ScaleBytes {
     }
 };
 
+// The scale words of one group of four reduction blocks on their way to shared
+// memory: A's 128 rows, B's 256 columns.
+template <int MODE>
+struct ScaleGroup {
+    ScaleBytes<1> a;                 // 128 x 128 blocks: one scale for the CTA's 128 rows
+    ScaleBytes<8> b;
+    __device__ __forceinline__ void load(const Fp8GemmParams& p, const Tile& x, int m, int kb, int lane) {
+        const int kb1 = x.kb0 + x.nkb;
+        a.load(p.s_a, x.g * p.s_a.batch, m, kb, kb1, 32);
+        b.load(p.s_b, 0, x.c0 + lane, kb, kb1, x.width);
+    }
+    __device__ __forceinline__ void store(uint8_t* dst, int lane) const {
+        const uint32_t w = a.word(0);
+        uint4* d = reinterpret_cast<uint4*>(dst + lane * 16);
+        d[0] = make_uint4(w, w, w, w);
+        d[32] = make_uint4(b.word(0), b.word(1), b.word(2), b.word(3));
+        d[64] = make_uint4(b.word(4), b.word(5), b.word(6), b.word(7));
+    }
+};
+
+// Weight gradient: both operands' bytes lie along the index, four to a load, and
+// become words by a 4 x 4 transpose (48 byte loads a group kept a warp busy for
+// longer than the group's products).
+template <>
+struct ScaleGroup<kFp8GradWeight> {
+    uint32_t v[3][4];                // A's rows, B's columns 0-127, 128-255; this lane's four of block kb + i
+    __device__ __forceinline__ void load(const Fp8GemmParams& p, const Tile& x, int m, int kb, int lane) {
+        const int kb1 = x.kb0 + x.nkb;
+        // rows and columns past the end: the last whole word (s_a, s_b hold multiples of 128)
+        const int ia = min(m + 4 * lane, p.s_a.limit - 4);
+        const int ib0 = min(x.c0 + 4 * lane, p.s_b.limit - 4), ib1 = min(x.c0 + 128 + 4 * lane, p.s_b.limit - 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long r = min(kb + i, kb1 - 1);
+            const uint8_t* qa = p.s_a.p + r * p.s_a.red;
+            const uint8_t* qb = p.s_b.p + r * p.s_b.red;
+            v[0][i] = *reinterpret_cast<const uint32_t*>(qa + ia);
+            v[1][i] = *reinterpret_cast<const uint32_t*>(qb + ib0);
+            v[2][i] = *reinterpret_cast<const uint32_t*>(qb + ib1);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* dst, int lane) const {
+#pragma unroll
+        for (int o = 0; o < 3; ++o) {
+            const uint32_t lo0 = __byte_perm(v[o][0], v[o][1], 0x5140), hi0 = __byte_perm(v[o][0], v[o][1], 0x7362);
+            const uint32_t lo1 = __byte_perm(v[o][2], v[o][3], 0x5140), hi1 = __byte_perm(v[o][2], v[o][3], 0x7362);
+            const uint32_t w[4] = {__byte_perm(lo0, lo1, 0x5410), __byte_perm(lo0, lo1, 0x7632),
+                                   __byte_perm(hi0, hi1, 0x5410), __byte_perm(hi0, hi1, 0x7632)};
+            // index 4 lane + i: word (4 lane + i) / 32 of 16-byte row (4 lane + i) % 32
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint32_t*>(dst + 512 * o + ((4 * lane + i) & 31) * 16 + (lane >> 3) * 4) = w[i];
+        }
+    }
+};
+
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
@@ -424,23 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // its next group's bytes before it stores the current one's, so that four
         // groups are on their way: one load latency per group, waited for group by
         // group, is longer than the products of a group of a narrow tile.
-        constexpr int kIn = MODE == kFp8GradWeight ? 4 : 1;   // 128 x 128 blocks: one scale for the CTA's 128 indices
-        ScaleBytes<kIn> vi[2];
-        ScaleBytes<8> vo[2];
+        ScaleGroup<MODE> v[2];
         int seq = 0, waiting = -1, g = 0;
         bool ok = true;
-        auto store = [&](const ScaleBytes<kIn>& si, const ScaleBytes<8>& so, int n) -> bool {
+        auto store = [&](const ScaleGroup<MODE>& w, int n) -> bool {
             const int st = n % kScaleStages;
             const uint32_t use = static_cast<uint32_t>(n / kScaleStages) & 1u;
             if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.sempty[st]), use ^ 1u, abort, limit)) {
                 record_failure(abort);
                 return false;
             }
-            uint8_t* dst = s_sc + st * kScaleBytes + lane * 16;
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(si.word(0), si.word(kIn > 1 ? 1 : 0), si.word(kIn > 2 ? 2 : 0), si.word(kIn > 3 ? 3 : 0));
-            *reinterpret_cast<uint4*>(dst + 512) = make_uint4(so.word(0), so.word(1), so.word(2), so.word(3));
-            *reinterpret_cast<uint4*>(dst + 1024) = make_uint4(so.word(4), so.word(5), so.word(6), so.word(7));
+            w.store(s_sc + st * kScaleBytes, lane);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[st]), 0));
@@ -448,28 +498,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         };
         for (int t = pair; ok && t < tiles; t += npairs) {
             const Tile x = decode_tile(p, gs, t, g);
-            if (x.nkb == 0) continue;
-            const int kb1 = x.kb0 + x.nkb;
-            const int m = x.m0 + static_cast<int>(rank) * kHalf + lane;
-            const long long base = MODE == kFp8GradWeight ? 0 : x.g * p.s_a.batch;
-            for (int kb = x.kb0; ok && kb < kb1; kb += 4, ++seq) {
+            const int m = x.m0 + static_cast<int>(rank) * kHalf;
+            for (int i = 0; ok && i < x.nkb; i += 4, ++seq) {
                 if ((seq & 1) != warp - 2) continue;
-                const bool second = (seq >> 1) & 1;      // which of the two register sets
-                if (second) {
-                    vi[1].load(p.s_a, base, m, kb, kb1, 32 * kIn);
-                    vo[1].load(p.s_b, 0, x.c0 + lane, kb, kb1, x.width);
-                    if (waiting >= 0) ok = store(vi[0], vo[0], waiting);
+                if ((seq >> 1) & 1) {                    // which of the two register sets
+                    v[1].load(p, x, m, x.kb0 + i, lane);
+                    if (waiting >= 0) ok = store(v[0], waiting);
                 } else {
-                    vi[0].load(p.s_a, base, m, kb, kb1, 32 * kIn);
-                    vo[0].load(p.s_b, 0, x.c0 + lane, kb, kb1, x.width);
-                    if (waiting >= 0) ok = store(vi[1], vo[1], waiting);
+                    v[0].load(p, x, m, x.kb0 + i, lane);
+                    if (waiting >= 0) ok = store(v[1], waiting);
                 }
                 waiting = seq;
             }
         }
         if (ok && waiting >= 0) {
-            if ((waiting >> 1) & 1) store(vi[1], vo[1], waiting);
-            else store(vi[0], vo[0], waiting);
+            if ((waiting >> 1) & 1) store(v[1], waiting);
+            else store(v[0], waiting);
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --

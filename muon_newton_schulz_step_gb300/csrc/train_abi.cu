@@ -419,7 +419,10 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
     if (tokens > 0 && ((rc = check_align(a_codes, 16, "a_codes")) != MUON_OK ||
                        (rc = check_align(b_codes, 16, "b_codes")) != MUON_OK))
         return rc;
-    if (tokens > 0 && (a_scale == nullptr || b_scale == nullptr)) return fail(MUON_ERR_INVALID_ARG, "a scale is NULL");
+    const size_t scale_align = gw ? 4 : 1;               // col blocks' bytes are read four at a time
+    if (tokens > 0 && ((rc = check_align(a_scale, scale_align, "a_scale")) != MUON_OK ||
+                       (rc = check_align(b_scale, scale_align, "b_scale")) != MUON_OK))
+        return rc;
     int sms = 0;
     if ((rc = op_device(&sms)) != MUON_OK) return rc;
     if (gw && tokens == 0) {
