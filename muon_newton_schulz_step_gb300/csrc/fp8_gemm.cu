@@ -522,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         //   rows of 128 bytes go through shared memory and leave in whole lines.  These
         //   tiles are nearly all epilogue, and their stores are the warps' own: TMA
         //   stores wait behind the loads that the producer has asked for ahead (2500
-        //   cycles; 784 against @@ us for 96 experts' weights);
+        //   cycles; in 128-byte blocks they brought the weights of 96 experts to 784 us, the
+        //   rest of the tile as it is now to 532);
         //   else: lanes run along the row; 8 x 8 blocks of bf16 go through shared memory
         //   transposed and leave by TMA, 32 rows of 64 bytes at a time.
         const int q = warp & 3;

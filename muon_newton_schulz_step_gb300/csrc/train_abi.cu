@@ -323,6 +323,9 @@ int muon_route_backward(const float* d_weights, const void* logits, int dtype, l
     p.chosen = const_cast<int*>(chosen);
     p.d_logits = d_logits;
     p.ld_d = ld_d;
+    const size_t four = 4 * dtype_size(dtype);           // four consecutive elements as one vector
+    p.vec = experts % 4 == 0 && ld % 4 == 0 && ld_d % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % four == 0 &&
+            reinterpret_cast<uintptr_t>(d_logits) % four == 0;
     const double bytes = static_cast<double>(tokens) * (2.0 * experts * dtype_size(dtype) + 8.0 * opts->top_k);
     return op_launch(kOpRouteGrad, 0.0, bytes, stream, [&] { return launch_route_backward(p, sms, stream); });
 }
