@@ -402,6 +402,32 @@ MUON_API int muon_fp8_product(int product, const void* a_codes, const void* a_sc
                               const void* b_scale, long long tokens, int n, int k, int groups, const int* offsets,
                               void* out, int out_dtype, long long ld_out, cudaStream_t stream);
 
+/*
+ * A linear layer (or the layers of `groups` experts) on 8-bit weights in one
+ * call: x (tokens x k, row stride ld_x) is rounded by row blocks and multiplied
+ * with w (codes and scale of muon_fp8_quantize_weight, groups x n x k).  Few
+ * tokens (up to 8, or up to two for each expert) take a single launch that
+ * streams the weight.  workspace: device, 16-byte aligned.
+ */
+MUON_API size_t muon_fp8_linear_workspace_bytes(long long tokens, int k);
+MUON_API int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
+                             const void* w_scale, int n, int k, int groups, const int* offsets, void* workspace,
+                             size_t workspace_bytes, void* out, int out_dtype, long long ld_out,
+                             cudaStream_t stream);
+
+/*
+ * Its gradients: dx = dy W with dy by row blocks (dx NULL: left out), dW_g =
+ * dy_g^T x_g with both by col blocks (dw NULL: left out; groups x n x k,
+ * contiguous).  dy is read once for both.
+ */
+MUON_API size_t muon_fp8_linear_backward_workspace_bytes(long long tokens, int n, int k, int groups, int need_dx,
+                                                         int need_dw);
+MUON_API int muon_fp8_linear_backward(const void* dy, int dy_dtype, long long ld_dy, const void* x, int x_dtype,
+                                      long long ld_x, long long tokens, const void* w_codes, const void* w_scale,
+                                      int n, int k, int groups, const int* offsets, void* workspace,
+                                      size_t workspace_bytes, void* dx, int dx_dtype, long long ld_dx, void* dw,
+                                      int dw_dtype, cudaStream_t stream);
+
 /* Device workspace (bytes) that one call on these shapes needs; 0 on bad args. */
 MUON_API size_t muon_workspace_bytes(const int* rows, const int* cols, int count);
 
@@ -429,7 +455,7 @@ MUON_API void muon_release_workspace(void);
  * launch.  Names: norm_pass, norm_finalize, pack, ns_gemm_gram, ns_gemm_poly,
  * ns_gemm_update, ns_gemm_final (the last update with the weight update or
  * the store of O in its epilogue), ns_small, unpack, adamw, grad_norm, grad_clip,
- * route, route_backward, fp8_quantize, fp8_gemm.
+ * route, route_backward, fp8_quantize, fp8_gemm, fp8_token.
  */
 typedef struct {
     char name[40];            /* kernel name */

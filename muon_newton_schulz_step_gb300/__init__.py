@@ -25,6 +25,7 @@ The method: the per-matrix Muon step over whole matrices held on one rank
 """
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -53,7 +54,8 @@ EXPORTS = (
     "muon_profile_read", "muon_ns5_batched_static", "muon_step_host", "muon_ns_batched_ex",
     "muon_adamw_step", "muon_grad_norm_workspace_bytes", "muon_grad_norm", "muon_grad_clip", "muon_route_opts_init",
     "muon_route", "muon_route_backward", "muon_fp8_padded_rows", "muon_fp8_quantize", "muon_fp8_quantize_weight",
-    "muon_fp8_product",
+    "muon_fp8_product", "muon_fp8_linear_workspace_bytes", "muon_fp8_linear", "muon_fp8_linear_backward_workspace_bytes",
+    "muon_fp8_linear_backward",
 )
 
 MUON_STATIC_SCRATCH_BYTES = 64 << 20
@@ -157,6 +159,14 @@ def lib():
     L.muon_fp8_quantize_weight.restype = ci
     L.muon_fp8_product.argtypes = [ci, vp, vp, vp, vp, ll, ci, ci, ci, vp, vp, ci, ll, vp]
     L.muon_fp8_product.restype = ci
+    L.muon_fp8_linear_workspace_bytes.argtypes = [ll, ci]
+    L.muon_fp8_linear_workspace_bytes.restype = sz
+    L.muon_fp8_linear.argtypes = [vp, ci, ll, ll, vp, vp, ci, ci, ci, vp, vp, sz, vp, ci, ll, vp]
+    L.muon_fp8_linear.restype = ci
+    L.muon_fp8_linear_backward_workspace_bytes.argtypes = [ll, ci, ci, ci, ci, ci]
+    L.muon_fp8_linear_backward_workspace_bytes.restype = sz
+    L.muon_fp8_linear_backward.argtypes = [vp, ci, ll, vp, ci, ll, ll, vp, vp, ci, ci, ci, vp, vp, sz, vp, ci, ll, vp, ci, vp]
+    L.muon_fp8_linear_backward.restype = ci
     _lib = L
     return L
 
@@ -494,6 +504,13 @@ class MuonStepBatch:
 
 
 # ----------------------------------------------- operators around the step --
+# These calls run in front of kernels of a few microseconds: their checks read
+# each tensor property once, and torch is asked for the current device and
+# stream by the cheapest way it has.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on(stream):
     """Context in which new tensors belong to ``stream`` (None: the current one)."""
     if stream is None:
@@ -503,39 +520,56 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _handle(stream):
+    """The raw handle of ``stream`` (None: the current stream)."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _here(name, t):
+    """``t`` is a CUDA tensor on the current device (the library launches there)."""
+    if t.get_device() != _current_device():
+        _check_device(name, t)
+
+
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
-def _check_flat(name, tensors, like=None):
-    device = torch.cuda.current_device() if tensors else None
+def _check_flat(name, tensors):
+    """(elements, element type codes) of contiguous CUDA tensors on the current device."""
+    numel, dtypes = [], []
+    device = _current_device() if tensors else None
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _FLOATS or not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
         if t.get_device() != device:
             _check_device(f"{name}[{i}]", t, device)
-        if like is not None and (t.dtype != like[i].dtype or t.numel() != like[i].numel()):
-            raise ValueError(f"{name}[{i}] must have G[{i}]'s dtype and number of elements")
+        numel.append(t.numel())
+        dtypes.append(1 if t.dtype is torch.float32 else 0)
+    return numel, dtypes
 
 
-def _norm_args(G, stream):
-    n = len(G)
-    numel = (ctypes.c_longlong * max(1, n))(*[t.numel() for t in G])
-    dtypes = (ctypes.c_int * max(1, n))(*[1 if t.dtype is torch.float32 else 0 for t in G])
-    need = lib().muon_grad_norm_workspace_bytes(numel, n)
-    # one allocation: the norm first, the partial sums behind it
-    buf = torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")
-    return numel, dtypes, need, buf
+def _norm_buffer(numel, dtypes):
+    """C arrays of a list's sizes and types, and one buffer: the norm, then the partial sums from byte 16 on."""
+    n = len(numel)
+    cn = (ctypes.c_longlong * max(1, n))(*numel)
+    cd = (ctypes.c_int * max(1, n))(*dtypes)
+    need = lib().muon_grad_norm_workspace_bytes(cn, n)
+    return cn, cd, need, torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")
 
 
 def muon_grad_norm(G, stream=None) -> torch.Tensor:
     """Global 2-norm of a list of contiguous CUDA gradients (bf16 and fp32 may
     be mixed), as a 0-dim fp32 CUDA tensor."""
     G = list(G)
-    _check_flat("G", G)
+    numel, dtypes = _check_flat("G", G)
     with _on(stream):
-        numel, dtypes, need, buf = _norm_args(G, stream)
-        _check(lib().muon_grad_norm(_ptr_array(G), numel, dtypes, len(G), buf.data_ptr() + 16, need, buf.data_ptr(),
-                                    _stream_handle(stream)))
+        cn, cd, need, buf = _norm_buffer(numel, dtypes)
+        at = buf.data_ptr()
+        _check(lib().muon_grad_norm(_ptr_array(G), cn, cd, len(G), at + 16, need, at, _handle(stream)))
     return buf[0]
 
 
@@ -544,53 +578,57 @@ def muon_grad_clip(G, max_norm: float, out=None, stream=None) -> torch.Tensor:
     into ``out`` (tensors like G); returns the norm before clipping (0-dim
     fp32 CUDA tensor).  Nothing is read back to the host."""
     G = list(G)
-    _check_flat("G", G)
+    numel, dtypes = _check_flat("G", G)
     optr = None
     if out is not None:
         out = list(out)
         if len(out) != len(G):
             raise ValueError("out must have one tensor for each of G")
-        _check_flat("out", out, like=G)
+        if _check_flat("out", out) != (numel, dtypes):
+            raise ValueError("out must have the dtype and number of elements of G, tensor by tensor")
         optr = _ptr_array(out)
     with _on(stream):
-        numel, dtypes, need, buf = _norm_args(G, stream)
-        _check(lib().muon_grad_clip(_ptr_array(G), optr, numel, dtypes, len(G), float(max_norm), buf.data_ptr() + 16,
-                                    need, buf.data_ptr(), _stream_handle(stream)))
+        cn, cd, need, buf = _norm_buffer(numel, dtypes)
+        at = buf.data_ptr()
+        _check(lib().muon_grad_clip(_ptr_array(G), optr, cn, cd, len(G), float(max_norm), at + 16, need, at,
+                                    _handle(stream)))
     return buf[0]
 
 
 def _check_rows(name, t, dtypes, rows=None, cols=None):
     """A 2-D CUDA tensor whose rows are contiguous (any row stride that does not
-    overlap them); returns the row stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in dtypes:
+    overlap them): (rows, cols, row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of {dtypes}")
-    _check_device(name, t)
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected ({rows}, {cols})")
-    if t.shape[0] <= 1:
-        ld = t.shape[1]
-    else:
-        ld = t.stride(0)
-    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or ld < t.shape[1]):
+    _here(name, t)
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} has shape {(r, c)}; expected ({rows}, {cols})")
+    ld, inner = t.stride()
+    if r <= 1 or c == 0:
+        ld = max(ld, c)
+    if r * c and ((c > 1 and inner != 1) or ld < c):
         raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
-    return max(ld, t.shape[1])
+    return r, c, max(ld, c)
 
 
 def _check_vector(name, t, dtype, n):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != (n,) \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
-    _check_device(name, t)
+    _here(name, t)
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+@functools.lru_cache(maxsize=256)
 def _route_opts(top_k, score, groups, top_groups, renormalize, scale):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {tuple(_SCORES)}")
-    return _RouteOpts(int(top_k), int(groups), int(groups if top_groups is None else top_groups), _SCORES[score],
-                      1 if renormalize else 0, float(scale))
+    o = _RouteOpts(int(top_k), int(groups), int(groups if top_groups is None else top_groups), _SCORES[score],
+                   1 if renormalize else 0, float(scale))
+    return o, ctypes.byref(o)
 
 
 def muon_route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, top_groups=None,
@@ -601,18 +639,17 @@ def muon_route(logits, top_k: int, *, bias=None, score: str = "softmax", groups:
     choice only; ``groups`` / ``top_groups`` limit it to the best groups of
     consecutive experts.  Experts masked by a logit of -inf are not chosen;
     places left over get expert -1 and weight 0."""
-    ld = _check_rows("logits", logits, _FLOATS)
-    tokens, experts = logits.shape
+    tokens, experts, ld = _check_rows("logits", logits, _FLOATS)
     if bias is not None:
         _check_vector("bias", bias, torch.float32, experts)
-    o = _route_opts(top_k, score, groups, top_groups, renormalize, scale)
+    o, ref = _route_opts(top_k, score, groups, top_groups, renormalize, scale)
     with _on(stream):
-        weights = torch.empty((tokens, int(top_k)), dtype=torch.float32, device="cuda")
-        chosen = torch.empty((tokens, int(top_k)), dtype=torch.int32, device="cuda")
+        weights = torch.empty((tokens, o.top_k), dtype=torch.float32, device="cuda")
+        chosen = torch.empty((tokens, o.top_k), dtype=torch.int32, device="cuda")
         counts = torch.empty(experts, dtype=torch.int32, device="cuda")
         _check(lib().muon_route(logits.data_ptr(), _dtype_code(logits), tokens, experts, ld,
-                                None if bias is None else bias.data_ptr(), ctypes.byref(o), weights.data_ptr(),
-                                chosen.data_ptr(), counts.data_ptr(), _stream_handle(stream)))
+                                None if bias is None else bias.data_ptr(), ref, weights.data_ptr(),
+                                chosen.data_ptr(), counts.data_ptr(), _handle(stream)))
     return weights, chosen, counts
 
 
@@ -620,21 +657,16 @@ def muon_route_backward(d_weights, logits, chosen, *, score: str = "softmax", re
                         scale: float = 1.0, stream=None) -> torch.Tensor:
     """Gradient of the logits (their dtype) from that of ``muon_route``'s
     weights, for the experts it chose."""
-    ld = _check_rows("logits", logits, _FLOATS)
-    tokens, experts = logits.shape
-    if not isinstance(chosen, torch.Tensor) or chosen.dim() != 2:
-        raise ValueError("chosen must be a 2-D CUDA tensor")
-    top_k = chosen.shape[1]
-    for name, t, dt in (("chosen", chosen, torch.int32), ("d_weights", d_weights, torch.float32)):
-        _check_rows(name, t, (dt,), tokens, top_k)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    o = _route_opts(top_k, score, 1, 1, renormalize, scale)
+    tokens, experts, ld = _check_rows("logits", logits, _FLOATS)
+    _, top_k, _ = _check_rows("chosen", chosen, (torch.int32,), tokens)
+    _check_rows("d_weights", d_weights, (torch.float32,), tokens, top_k)
+    if not chosen.is_contiguous() or not d_weights.is_contiguous():
+        raise ValueError("chosen and d_weights must be contiguous")
+    _, ref = _route_opts(top_k, score, 1, 1, renormalize, scale)
     with _on(stream):
         d = torch.empty((tokens, experts), dtype=logits.dtype, device="cuda")
         _check(lib().muon_route_backward(d_weights.data_ptr(), logits.data_ptr(), _dtype_code(logits), tokens, experts,
-                                         ld, chosen.data_ptr(), ctypes.byref(o), d.data_ptr(), experts,
-                                         _stream_handle(stream)))
+                                         ld, chosen.data_ptr(), ref, d.data_ptr(), experts, _handle(stream)))
     return d
 
 
@@ -677,8 +709,7 @@ def muon_fp8_quantize(x, *, row: bool = True, col: bool = False, offsets=None, s
     rows (``row``), along its columns (``col``; blocks start anew at each group
     of ``offsets``), or both from one read: (row Fp8Matrix or None, col
     Fp8Matrix or None)."""
-    ld = _check_rows("x", x, _FLOATS)
-    rows, cols = x.shape
+    rows, cols, ld = _check_rows("x", x, _FLOATS)
     groups, optr = _check_offsets(offsets)
     ldq = _up128(cols)
     with _on(stream):
@@ -693,7 +724,7 @@ def muon_fp8_quantize(x, *, row: bool = True, col: bool = False, offsets=None, s
         _check(lib().muon_fp8_quantize(x.data_ptr(), _dtype_code(x), rows, cols, ld, groups, optr,
                                        r.codes.data_ptr() if row else None, r.scale.data_ptr() if row else None,
                                        c.codes.data_ptr() if col else None, c.scale.data_ptr() if col else None,
-                                       _stream_handle(stream)))
+                                       _handle(stream)))
     return r, c
 
 
@@ -710,7 +741,7 @@ def muon_fp8_quantize_weight(w, stream=None) -> Fp8Matrix:
                       torch.empty((*w.shape[:-2], _up128(rows) // 128, _up128(cols) // 128), dtype=torch.uint8,
                                   device="cuda"), "block", cols)
         _check(lib().muon_fp8_quantize_weight(w.data_ptr(), _dtype_code(w), w.shape[0] if w.dim() == 3 else 1, rows, cols,
-                                              m.codes.data_ptr(), m.scale.data_ptr(), _stream_handle(stream)))
+                                              m.codes.data_ptr(), m.scale.data_ptr(), _handle(stream)))
     return m
 
 
@@ -740,7 +771,7 @@ def _check_weight(w, offsets):
 def _product(code, a, b, tokens, n, k, groups, optr, out, ld, stream):
     _check(lib().muon_fp8_product(code, a.codes.data_ptr(), a.scale.data_ptr(), b.codes.data_ptr(), b.scale.data_ptr(),
                                   tokens, n, k, groups, optr, out.data_ptr(), _dtype_code(out), ld,
-                                  _stream_handle(stream)))
+                                  _handle(stream)))
 
 
 def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None, out_dtype=torch.bfloat16,
@@ -766,7 +797,7 @@ def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None,
         with _on(stream):
             if out is None:
                 out = torch.empty((tokens, inner), dtype=out_dtype, device="cuda")
-            ld = _check_rows("out", out, _FLOATS, tokens, inner)
+            _, _, ld = _check_rows("out", out, _FLOATS, tokens, inner)
             _product(0 if product == "forward" else 1, a, b, tokens, n, k, groups, optr, out, ld, stream)
         return out
     if product != "grad_weight":
@@ -797,10 +828,19 @@ def muon_fp8_linear(x, w, *, offsets=None, out_dtype=torch.bfloat16, stream=None
     """y = x W^T in 8 bits: ``x`` (tokens x k, bf16 or fp32) is rounded to E4M3 by
     row blocks and multiplied with ``w`` (``muon_fp8_quantize_weight``).  With
     ``offsets``, tokens are sorted by expert and ``w`` is stacked over experts."""
-    n, k, _ = _check_weight(w, offsets)
-    _check_rows("x", x, _FLOATS, None, k)
-    q, _ = muon_fp8_quantize(x, stream=stream)
-    return muon_fp8_product("forward", q, w, offsets=offsets, out_dtype=out_dtype, stream=stream)
+    n, k, groups = _check_weight(w, offsets)
+    tokens, _, ld = _check_rows("x", x, _FLOATS, None, k)
+    _, optr = _check_offsets(offsets, groups)
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    with _on(stream):
+        out = torch.empty((tokens, n), dtype=out_dtype, device="cuda")
+        need = lib().muon_fp8_linear_workspace_bytes(tokens, k)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        _check(lib().muon_fp8_linear(x.data_ptr(), _dtype_code(x), tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(), n, k,
+                                     groups, optr, ws.data_ptr(), need, out.data_ptr(), _dtype_code(out), n,
+                                     _handle(stream)))
+    return out
 
 
 def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, need_dw: bool = True,
@@ -809,17 +849,22 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
     row blocks, dW = dy^T x with both by col blocks; either may be left out
     (None).  dy is read once for both."""
     n, k, groups = _check_weight(w, offsets)
-    tokens = dy.shape[0] if isinstance(dy, torch.Tensor) and dy.dim() == 2 else None
-    _check_rows("dy", dy, _FLOATS, None, n)
-    _check_rows("x", x, _FLOATS, tokens, k)
-    _check_offsets(offsets, groups)
+    tokens, _, ld_dy = _check_rows("dy", dy, _FLOATS, None, n)
+    _, _, ld_x = _check_rows("x", x, _FLOATS, tokens, k)
+    _, optr = _check_offsets(offsets, groups)
+    if dx_dtype not in _FLOATS or dw_dtype not in _FLOATS:
+        raise ValueError(f"dx_dtype and dw_dtype must be of {_FLOATS}")
     dx = dw = None
-    if need_dx or need_dw:
-        dr, dc = muon_fp8_quantize(dy, row=need_dx, col=need_dw, offsets=offsets if need_dw else None, stream=stream)
+    with _on(stream):
         if need_dx:
-            dx = muon_fp8_product("grad_input", dr, w, offsets=offsets, out_dtype=dx_dtype, stream=stream)
+            dx = torch.empty((tokens, k), dtype=dx_dtype, device="cuda")
         if need_dw:
-            _, xc = muon_fp8_quantize(x, row=False, col=True, offsets=offsets, stream=stream)
-            dw = muon_fp8_product("grad_weight", dc, xc, tokens=tokens, offsets=offsets, out_dtype=dw_dtype,
-                                  stream=stream)
+            dw = torch.empty((n, k) if offsets is None else (groups, n, k), dtype=dw_dtype, device="cuda")
+        need = lib().muon_fp8_linear_backward_workspace_bytes(tokens, n, k, groups, int(need_dx), int(need_dw))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        _check(lib().muon_fp8_linear_backward(
+            dy.data_ptr(), _dtype_code(dy), ld_dy, x.data_ptr(), _dtype_code(x), ld_x, tokens, w.codes.data_ptr(),
+            w.scale.data_ptr(), n, k, groups, optr, ws.data_ptr(), need, dx.data_ptr() if need_dx and tokens else None,
+            MUON_F32 if dx_dtype == torch.float32 else MUON_BF16, k, dw.data_ptr() if need_dw else None,
+            MUON_F32 if dw_dtype == torch.float32 else MUON_BF16, _handle(stream)))
     return dx, dw

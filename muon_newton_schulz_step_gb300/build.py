@@ -17,8 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon_gb300.so")
 SOURCES = ["ns_gemm_pair.cu", "ns_small.cu", "elementwise.cu", "muon_abi.cu", "muon_static.cu", "muon_offload.cu", "adamw.cu", "guard.cu",
-           "grad_norm.cu", "route.cu", "fp8_quantize.cu", "fp8_gemm.cu", "train_abi.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "groups.cuh"]
+           "grad_norm.cu", "route.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_token.cu", "train_abi.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "groups.cuh", "fp8_codes.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = b.tmem;
     const int tiles = b.tiles;
+    // everything so far may run while the launch before drains; its codes are read from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
         // ------------------------------------------------------ producer --
@@ -754,27 +756,41 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
 template <int MODE, bool F32>
-cudaError_t run(const Fp8GemmParams& p, int pairs, cudaStream_t s) {
+cudaError_t run(const Fp8GemmParams& p, int pairs, bool after, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
-    k_fp8_gemm<MODE, F32><<<2 * pairs, kThreads, smem_bytes<MODE>(), s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<MODE>();
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 1 : 0;
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32>, p);
+    return l != cudaSuccess ? l : cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t run(const Fp8GemmParams& p, int pairs, bool after, cudaStream_t s) {
+    return p.out_f32 ? run<MODE, true>(p, pairs, after, s) : run<MODE, false>(p, pairs, after, s);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, bool after, cudaStream_t s) {
     const long long mt = (p.m_ext + kTile - 1) / kTile;
     const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
                                                   : p.n_ext / kTile + p.groups;
     const long long most = mt * nt;
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {
-        case kFp8Forward: return p.out_f32 ? run<kFp8Forward, true>(p, pairs, s) : run<kFp8Forward, false>(p, pairs, s);
-        case kFp8GradInput:
-            return p.out_f32 ? run<kFp8GradInput, true>(p, pairs, s) : run<kFp8GradInput, false>(p, pairs, s);
-        default: return p.out_f32 ? run<kFp8GradWeight, true>(p, pairs, s) : run<kFp8GradWeight, false>(p, pairs, s);
+        case kFp8Forward: return run<kFp8Forward>(p, pairs, after, s);
+        case kFp8GradInput: return run<kFp8GradInput>(p, pairs, after, s);
+        default: return run<kFp8GradWeight>(p, pairs, after, s);
     }
 }
 

@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "fp8_codes.cuh"
 #include "groups.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -36,26 +37,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsPerThread = 8;
-
-// The block's exponent from the bits of its largest finite magnitude.
-// 448 = 1.75 * 2^8: with max = m * 2^q, 1 <= m < 2, e = q - 8 where m <= 1.75, else q - 7.
-__device__ __forceinline__ int scale_exponent(uint32_t top) {
-    if (top == 0u) return 0;
-    int q = static_cast<int>(top >> 23) - 127;
-    uint32_t frac = top & 0x7fffffu;
-    if (q == -127) {                                     // subnormal: normalise
-        const int up = __clz(frac) - 8;
-        q = -126 - up;
-        frac = (frac << up) & 0x7fffffu;
-    }
-    const int e = frac <= 0x600000u ? q - 8 : q - 7;
-    return e < -127 ? -127 : e;
-}
-
-// 2^-e for e in [-127, 127]
-__device__ __forceinline__ float inverse_scale(int e) {
-    return e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-}
 
 // Eight consecutive elements as loaded: bf16 in a, fp32 in a and b.
 struct Raw {
@@ -341,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const _
     __shared__ Tile sh;
     __shared__ RowBlock rb;
     __shared__ int offsets[COL ? kFp8MaxGroups + 1 : 1];
+    asm volatile("griddepcontrol.launch_dependents;");   // the product's set-up may overlap; it waits for the codes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cg = lane & 15, half = lane >> 4;
     const long long batch = blockIdx.z, colblocks = p.ldq >> 7;

@@ -313,7 +313,24 @@ struct Fp8GemmParams {
     unsigned long long wait_ns;
 };
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s);
+// `after`: the launch before it on the stream wrote its operands and let it start early.
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, bool after, cudaStream_t s);
+
+// The forward product of few tokens, x rounded on the way.
+struct Fp8TokenParams {
+    const void* x;            // tokens x k, row stride ld_x
+    const uint8_t* w;         // groups x n x ldk codes
+    const uint8_t* w_scale;   // groups x n blocks x k blocks
+    void* out;                // tokens x n, row stride ld_out
+    const int* offsets;       // groups + 1, or nullptr
+    long long ld_x, ldk, ld_out;
+    int tokens, n, k, groups;
+    int bf16;                 // x
+    int vec;                  // 16-byte loads of x are legal
+    int out_f32;
+};
+
+cudaError_t launch_fp8_token(const Fp8TokenParams& p, cudaStream_t s);
 cudaError_t read_and_clear_fp8_error(int* code);
 
 // Launch helpers implemented in the .cu files.
@@ -358,7 +375,7 @@ int ns5_batched_on_workspace(void* const* ptrs, const int* rows, const int* cols
 int set_last_error(int status, const char* msg);
 
 // What the operators around the step (train_abi.cu) share with it.
-enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpEnd };
+enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpFp8Token, kOpEnd };
 int op_device(int* sms);                       // the current device, checked; its SM count
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
 int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,

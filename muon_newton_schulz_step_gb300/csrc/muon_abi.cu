@@ -127,7 +127,8 @@ static_assert(kNumStepKinds == static_cast<int>(kOpGradNorm), "the operators' ki
 const char* const kKindNames[kNumKinds] = {"norm_pass",    "norm_finalize",  "pack",     "ns_gemm_gram",
                                            "ns_gemm_poly", "ns_gemm_update", "ns_small", "unpack",
                                            "adamw",        "ns_gemm_final", "grad_norm", "grad_clip",
-                                           "route",        "route_backward", "fp8_quantize", "fp8_gemm"};
+                                           "route",        "route_backward", "fp8_quantize", "fp8_gemm",
+                                           "fp8_token"};
 struct ProfRec {
     int kind;
     cudaEvent_t a, b;

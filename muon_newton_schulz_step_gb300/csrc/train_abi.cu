@@ -246,6 +246,122 @@ int check_dim(long long n, const char* what) {
 
 long long up128(long long n) { return (n + 127) / 128 * 128; }
 
+// Codes of one matrix in a workspace: codes, then scales, each from a multiple of 256 bytes on.
+size_t up256(long long n) { return static_cast<size_t>((n + 255) / 256 * 256); }
+
+struct RowCodes {
+    size_t code_bytes, scale_bytes;
+    char *codes, *scale;
+    RowCodes(void* at, long long rows, long long cols)
+        : code_bytes(up256(rows * up128(cols))), scale_bytes(up256(rows * (up128(cols) / 128))),
+          codes(static_cast<char*>(at)), scale(at != nullptr ? codes + code_bytes : nullptr) {}
+    size_t bytes() const { return code_bytes + scale_bytes; }
+};
+
+struct ColCodes {
+    size_t code_bytes, scale_bytes;
+    char *codes, *scale;
+    ColCodes(void* at, long long rows, long long cols, int groups)
+        : code_bytes(up256(muon_fp8_padded_rows(rows, groups) * up128(cols))),
+          scale_bytes(up256(muon_fp8_padded_rows(rows, groups) / 128 * up128(cols))),
+          codes(static_cast<char*>(at)), scale(at != nullptr ? codes + code_bytes : nullptr) {}
+    size_t bytes() const { return code_bytes + scale_bytes; }
+};
+
+// Up to this many tokens (for each of several experts) the weight is streamed.
+constexpr long long kTokenMax = 8, kTokenMaxPerGroup = 2;
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    const int rc = check_align(ws, 16, "workspace");
+    if (rc != MUON_OK) return rc;
+    if (have < need) return fail(MUON_ERR_OOM, "workspace has %zu bytes; %zu are needed", have, need);
+    return MUON_OK;
+}
+
+int check_linear(int dtype, const char* what, long long tokens, long long ld, int cols, int n, int k, int groups,
+                 const int* offsets, const void* w_codes, const void* w_scale) {
+    int rc = check_dtype(dtype, what);
+    if (rc != MUON_OK) return rc;
+    if ((rc = check_groups(tokens, groups, offsets)) != MUON_OK) return rc;
+    if ((rc = check_dim(n, "n")) != MUON_OK || (rc = check_dim(k, "k")) != MUON_OK) return rc;
+    if (ld < cols) return fail(MUON_ERR_INVALID_ARG, "%s's row stride is below its columns", what);
+    if ((rc = check_align(w_codes, 16, "w_codes")) != MUON_OK) return rc;
+    if (w_scale == nullptr) return fail(MUON_ERR_INVALID_ARG, "w_scale is NULL");
+    return MUON_OK;
+}
+
+int fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes, const void* b_scale,
+                long long tokens, int n, int k, int groups, const int* offsets, void* out, int out_dtype,
+                long long ld_out, bool after, cudaStream_t stream) {
+    int rc = check_dtype(out_dtype, "out");
+    if (rc != MUON_OK) return rc;
+    if (product != MUON_FP8_FORWARD && product != MUON_FP8_GRAD_INPUT && product != MUON_FP8_GRAD_WEIGHT)
+        return fail(MUON_ERR_INVALID_ARG, "unknown product %d", product);
+    if ((rc = check_groups(tokens, groups, offsets)) != MUON_OK) return rc;
+    if ((rc = check_dim(n, "n")) != MUON_OK || (rc = check_dim(k, "k")) != MUON_OK) return rc;
+    const bool gw = product == MUON_FP8_GRAD_WEIGHT;
+    const int inner = product == MUON_FP8_FORWARD ? n : k;
+    if (ld_out < inner) return fail(MUON_ERR_INVALID_ARG, "the output's row stride is below its columns");
+    if (tokens == 0 && !gw) return MUON_OK;
+    if ((rc = check_align(out, dtype_size(out_dtype), "out")) != MUON_OK) return rc;
+    if (tokens > 0 && ((rc = check_align(a_codes, 16, "a_codes")) != MUON_OK ||
+                       (rc = check_align(b_codes, 16, "b_codes")) != MUON_OK))
+        return rc;
+    const size_t scale_align = gw ? 4 : 1;               // col blocks' bytes are read four at a time
+    if (tokens > 0 && ((rc = check_align(a_scale, scale_align, "a_scale")) != MUON_OK ||
+                       (rc = check_align(b_scale, scale_align, "b_scale")) != MUON_OK))
+        return rc;
+    int sms = 0;
+    if ((rc = op_device(&sms)) != MUON_OK) return rc;
+    if (gw && tokens == 0) {
+        const size_t sz = dtype_size(out_dtype);
+        const cudaError_t e = cudaMemset2DAsync(out, ld_out * sz, 0, inner * sz, static_cast<size_t>(groups) * n, stream);
+        if (e != cudaSuccess) return fail(MUON_ERR_CUDA, "cudaMemset2DAsync: %s", cudaGetErrorString(e));
+        return MUON_OK;
+    }
+    Fp8GemmParams p = {};
+    const long long ldn = up128(n), ldk = up128(k), nb = ldn / 128, kb = ldk / 128;
+    const uint8_t* as = static_cast<const uint8_t*>(a_scale);
+    const uint8_t* bs = static_cast<const uint8_t*>(b_scale);
+    p.mode = product;
+    p.out = out;
+    p.ld = ld_out;
+    p.out_f32 = out_dtype == MUON_F32;
+    const bool rows16 = reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                        ld_out * static_cast<long long>(dtype_size(out_dtype)) % 16 == 0;
+    p.vec = rows16 && (gw || out_dtype == MUON_BF16);
+    p.m_ext = gw ? n : inner;
+    p.groups = groups;
+    p.offsets = offsets;
+    p.rows = static_cast<int>(tokens);
+    if (gw) {
+        // a: dy's col codes (padded tokens x ldn); b: x's col codes (padded tokens x ldk)
+        const long long padded = muon_fp8_padded_rows(tokens, groups);
+        p.n_ext = k;
+        p.out_batch = static_cast<long long>(n) * ld_out;
+        p.s_a = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
+        p.s_b = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
+        if ((rc = op_encode_bytes(&p.tm_a, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_b, b_codes, ldk, padded, 1, 128, 128)) != MUON_OK) return rc;
+    } else {
+        // a: x's or dy's row codes (tokens x ld); b: the weight's codes (groups x n x ldk)
+        const bool fwd = product == MUON_FP8_FORWARD;
+        const long long lda = fwd ? ldk : ldn;
+        p.n_ext = static_cast<int>(tokens);
+        p.kblocks = static_cast<int>(fwd ? kb : nb);
+        p.s_a = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
+                     : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
+        p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
+        if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
+    }
+    if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
+    const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
+    const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
+    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, after, stream); });
+}
+
 }  // namespace
 }  // namespace muon
 
@@ -408,73 +524,109 @@ int muon_fp8_quantize_weight(const void* w, int dtype, int batch, long long rows
 int muon_fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes, const void* b_scale,
                      long long tokens, int n, int k, int groups, const int* offsets, void* out, int out_dtype,
                      long long ld_out, cudaStream_t stream) {
-    int rc = check_dtype(out_dtype, "out");
+    return fp8_product(product, a_codes, a_scale, b_codes, b_scale, tokens, n, k, groups, offsets, out, out_dtype, ld_out,
+                       false, stream);
+}
+
+size_t muon_fp8_linear_workspace_bytes(long long tokens, int k) {
+    if (tokens <= 0 || k < 1) return 16;
+    return RowCodes(nullptr, tokens, k).bytes();
+}
+
+int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
+                    const void* w_scale, int n, int k, int groups, const int* offsets, void* workspace,
+                    size_t workspace_bytes, void* out, int out_dtype, long long ld_out, cudaStream_t stream) {
+    int rc = check_linear(x_dtype, "x", tokens, ld_x, k, n, k, groups, offsets, w_codes, w_scale);
     if (rc != MUON_OK) return rc;
-    if (product != MUON_FP8_FORWARD && product != MUON_FP8_GRAD_INPUT && product != MUON_FP8_GRAD_WEIGHT)
-        return fail(MUON_ERR_INVALID_ARG, "unknown product %d", product);
-    if ((rc = check_groups(tokens, groups, offsets)) != MUON_OK) return rc;
-    if ((rc = check_dim(n, "n")) != MUON_OK || (rc = check_dim(k, "k")) != MUON_OK) return rc;
-    const bool gw = product == MUON_FP8_GRAD_WEIGHT;
-    const int inner = product == MUON_FP8_FORWARD ? n : k;
-    if (ld_out < inner) return fail(MUON_ERR_INVALID_ARG, "the output's row stride is below its columns");
-    if (tokens == 0 && !gw) return MUON_OK;
+    if ((rc = check_dtype(out_dtype, "out")) != MUON_OK) return rc;
+    if (ld_out < n) return fail(MUON_ERR_INVALID_ARG, "the output's row stride is below its columns");
+    if (tokens == 0) return MUON_OK;
+    if ((rc = check_align(x, dtype_size(x_dtype), "x")) != MUON_OK) return rc;
     if ((rc = check_align(out, dtype_size(out_dtype), "out")) != MUON_OK) return rc;
-    if (tokens > 0 && ((rc = check_align(a_codes, 16, "a_codes")) != MUON_OK ||
-                       (rc = check_align(b_codes, 16, "b_codes")) != MUON_OK))
-        return rc;
-    const size_t scale_align = gw ? 4 : 1;               // col blocks' bytes are read four at a time
-    if (tokens > 0 && ((rc = check_align(a_scale, scale_align, "a_scale")) != MUON_OK ||
-                       (rc = check_align(b_scale, scale_align, "b_scale")) != MUON_OK))
-        return rc;
-    int sms = 0;
-    if ((rc = op_device(&sms)) != MUON_OK) return rc;
-    if (gw && tokens == 0) {
-        const size_t sz = dtype_size(out_dtype);
-        const cudaError_t e = cudaMemset2DAsync(out, ld_out * sz, 0, inner * sz, static_cast<size_t>(groups) * n, stream);
-        if (e != cudaSuccess) return fail(MUON_ERR_CUDA, "cudaMemset2DAsync: %s", cudaGetErrorString(e));
-        return MUON_OK;
+    if (tokens <= kTokenMax || (offsets != nullptr && tokens <= kTokenMaxPerGroup * static_cast<long long>(groups))) {
+        int sms = 0;
+        if ((rc = op_device(&sms)) != MUON_OK) return rc;
+        Fp8TokenParams p = {};
+        p.x = x;
+        p.w = static_cast<const uint8_t*>(w_codes);
+        p.w_scale = static_cast<const uint8_t*>(w_scale);
+        p.out = out;
+        p.offsets = offsets;
+        p.ld_x = ld_x;
+        p.ldk = up128(k);
+        p.ld_out = ld_out;
+        p.tokens = static_cast<int>(tokens);
+        p.n = n;
+        p.k = k;
+        p.groups = groups;
+        p.bf16 = x_dtype == MUON_BF16;
+        p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * static_cast<long long>(dtype_size(x_dtype)) % 16 == 0;
+        p.out_f32 = out_dtype == MUON_F32;
+        const double bytes = static_cast<double>(groups) * n * k;
+        return op_launch(kOpFp8Token, 2.0 * tokens * n * k, bytes, stream, [&] { return launch_fp8_token(p, stream); });
     }
-    Fp8GemmParams p = {};
-    const long long ldn = up128(n), ldk = up128(k), nb = ldn / 128, kb = ldk / 128;
-    const uint8_t* as = static_cast<const uint8_t*>(a_scale);
-    const uint8_t* bs = static_cast<const uint8_t*>(b_scale);
-    p.mode = product;
-    p.out = out;
-    p.ld = ld_out;
-    p.out_f32 = out_dtype == MUON_F32;
-    const bool rows16 = reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
-                        ld_out * static_cast<long long>(dtype_size(out_dtype)) % 16 == 0;
-    p.vec = rows16 && (gw || out_dtype == MUON_BF16);
-    p.m_ext = gw ? n : inner;
-    p.groups = groups;
-    p.offsets = offsets;
-    p.rows = static_cast<int>(tokens);
-    if (gw) {
-        // a: dy's col codes (padded tokens x ldn); b: x's col codes (padded tokens x ldk)
-        const long long padded = muon_fp8_padded_rows(tokens, groups);
-        p.n_ext = k;
-        p.out_batch = static_cast<long long>(n) * ld_out;
-        p.s_a = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
-        p.s_b = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
-        if ((rc = op_encode_bytes(&p.tm_a, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_b, b_codes, ldk, padded, 1, 128, 128)) != MUON_OK) return rc;
-    } else {
-        // a: x's or dy's row codes (tokens x ld); b: the weight's codes (groups x n x ldk)
-        const bool fwd = product == MUON_FP8_FORWARD;
-        const long long lda = fwd ? ldk : ldn;
-        p.n_ext = static_cast<int>(tokens);
-        p.kblocks = static_cast<int>(fwd ? kb : nb);
-        p.s_a = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
-                     : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
-        p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
-        if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
-        if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, muon_fp8_linear_workspace_bytes(tokens, k))) != MUON_OK) return rc;
+    const RowCodes q(workspace, tokens, k);
+    rc = muon_fp8_quantize(x, x_dtype, tokens, k, ld_x, 1, nullptr, q.codes, q.scale, nullptr, nullptr, stream);
+    if (rc != MUON_OK) return rc;
+    return fp8_product(MUON_FP8_FORWARD, q.codes, q.scale, w_codes, w_scale, tokens, n, k, groups, offsets, out, out_dtype,
+                       ld_out, true, stream);
+}
+
+size_t muon_fp8_linear_backward_workspace_bytes(long long tokens, int n, int k, int groups, int need_dx, int need_dw) {
+    if (tokens <= 0 || n < 1 || k < 1 || groups < 1) return 16;
+    size_t bytes = 16;
+    if (need_dx) bytes += RowCodes(nullptr, tokens, n).bytes();
+    if (need_dw) bytes += ColCodes(nullptr, tokens, n, groups).bytes() + ColCodes(nullptr, tokens, k, groups).bytes();
+    return bytes;
+}
+
+int muon_fp8_linear_backward(const void* dy, int dy_dtype, long long ld_dy, const void* x, int x_dtype, long long ld_x,
+                             long long tokens, const void* w_codes, const void* w_scale, int n, int k, int groups,
+                             const int* offsets, void* workspace, size_t workspace_bytes, void* dx, int dx_dtype,
+                             long long ld_dx, void* dw, int dw_dtype, cudaStream_t stream) {
+    int rc = check_linear(dy_dtype, "dy", tokens, ld_dy, n, n, k, groups, offsets, w_codes, w_scale);
+    if (rc != MUON_OK) return rc;
+    if (dx == nullptr && dw == nullptr && tokens > 0) return MUON_OK;
+    if (dx != nullptr) {
+        if ((rc = check_dtype(dx_dtype, "dx")) != MUON_OK) return rc;
+        if (ld_dx < k) return fail(MUON_ERR_INVALID_ARG, "dx's row stride is below its columns");
+        if ((rc = check_align(dx, dtype_size(dx_dtype), "dx")) != MUON_OK) return rc;
     }
-    if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
-    const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
-    const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
-    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, stream); });
+    if (dw != nullptr) {
+        if ((rc = check_dtype(dw_dtype, "dw")) != MUON_OK || (rc = check_dtype(x_dtype, "x")) != MUON_OK) return rc;
+        if (ld_x < k) return fail(MUON_ERR_INVALID_ARG, "x's row stride is below its columns");
+        if ((rc = check_align(dw, dtype_size(dw_dtype), "dw")) != MUON_OK) return rc;
+        if (tokens > 0 && (rc = check_align(x, dtype_size(x_dtype), "x")) != MUON_OK) return rc;
+    }
+    if (tokens == 0) {
+        if (dw == nullptr) return MUON_OK;
+        return fp8_product(MUON_FP8_GRAD_WEIGHT, nullptr, nullptr, nullptr, nullptr, 0, n, k, groups, offsets, dw, dw_dtype,
+                           k, false, stream);
+    }
+    if ((rc = check_align(dy, dtype_size(dy_dtype), "dy")) != MUON_OK) return rc;
+    const size_t need = muon_fp8_linear_backward_workspace_bytes(tokens, n, k, groups, dx != nullptr, dw != nullptr);
+    if ((rc = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return rc;
+    char* at = static_cast<char*>(workspace);
+    const RowCodes r(dx != nullptr ? at : nullptr, tokens, n);
+    if (dx != nullptr) at += r.bytes();
+    const ColCodes c(dw != nullptr ? at : nullptr, tokens, n, groups);
+    if (dw != nullptr) at += c.bytes();
+    rc = muon_fp8_quantize(dy, dy_dtype, tokens, n, ld_dy, groups, offsets, r.codes, r.scale, c.codes, c.scale, stream);
+    if (rc != MUON_OK) return rc;
+    if (dx != nullptr) {
+        rc = fp8_product(MUON_FP8_GRAD_INPUT, r.codes, r.scale, w_codes, w_scale, tokens, n, k, groups, offsets, dx, dx_dtype,
+                         ld_dx, true, stream);
+        if (rc != MUON_OK) return rc;
+    }
+    if (dw != nullptr) {
+        const ColCodes xc(at, tokens, k, groups);
+        rc = muon_fp8_quantize(x, x_dtype, tokens, k, ld_x, groups, offsets, nullptr, nullptr, xc.codes, xc.scale, stream);
+        if (rc != MUON_OK) return rc;
+        rc = fp8_product(MUON_FP8_GRAD_WEIGHT, c.codes, c.scale, xc.codes, xc.scale, tokens, n, k, groups, offsets, dw,
+                         dw_dtype, k, true, stream);
+    }
+    return rc;
 }
 
 }  // extern "C"
