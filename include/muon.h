@@ -405,11 +405,12 @@ MUON_API int muon_fp8_product(int product, const void* a_codes, const void* a_sc
 /*
  * A linear layer (or the layers of `groups` experts) on 8-bit weights in one
  * call: x (tokens x k, row stride ld_x) is rounded by row blocks and multiplied
- * with w (codes and scale of muon_fp8_quantize_weight, groups x n x k).  Few
- * tokens (up to 8, or up to two for each expert) take a single launch that
- * streams the weight.  workspace: device, 16-byte aligned.
+ * with w (codes and scale of muon_fp8_quantize_weight, groups x n x k).  A few
+ * tokens of a single weight (offsets NULL) take one launch that streams the
+ * weight.  workspace: device, 16-byte aligned; none (NULL) where
+ * ..._workspace_bytes (grouped: offsets are given) is 0.
  */
-MUON_API size_t muon_fp8_linear_workspace_bytes(long long tokens, int k);
+MUON_API size_t muon_fp8_linear_workspace_bytes(long long tokens, int n, int k, int grouped);
 MUON_API int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
                              const void* w_scale, int n, int k, int groups, const int* offsets, void* workspace,
                              size_t workspace_bytes, void* out, int out_dtype, long long ld_out,

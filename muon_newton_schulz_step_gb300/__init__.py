@@ -27,6 +27,7 @@ import contextlib
 import ctypes
 import functools
 import os
+from array import array
 from typing import NamedTuple
 
 import torch
@@ -137,13 +138,13 @@ def lib():
     L.muon_profile_enable.restype = ctypes.c_int
     L.muon_profile_read.argtypes = [ctypes.POINTER(_KernelStat), ctypes.c_int, ip]
     L.muon_profile_read.restype = ctypes.c_int
-    ci, ll, sz, llp = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(ctypes.c_longlong)
+    ci, ll, sz = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
     rop = ctypes.POINTER(_RouteOpts)
-    L.muon_grad_norm_workspace_bytes.argtypes = [llp, ci]
+    L.muon_grad_norm_workspace_bytes.argtypes = [vp, ci]
     L.muon_grad_norm_workspace_bytes.restype = sz
-    L.muon_grad_norm.argtypes = [vpp, llp, ip, ci, vp, sz, vp, vp]
+    L.muon_grad_norm.argtypes = [vp, vp, vp, ci, vp, sz, vp, vp]
     L.muon_grad_norm.restype = ci
-    L.muon_grad_clip.argtypes = [vpp, vpp, llp, ip, ci, ctypes.c_float, vp, sz, vp, vp]
+    L.muon_grad_clip.argtypes = [vp, vp, vp, vp, ci, ctypes.c_float, vp, sz, vp, vp]
     L.muon_grad_clip.restype = ci
     L.muon_route_opts_init.argtypes = [rop]
     L.muon_route_opts_init.restype = None
@@ -159,7 +160,7 @@ def lib():
     L.muon_fp8_quantize_weight.restype = ci
     L.muon_fp8_product.argtypes = [ci, vp, vp, vp, vp, ll, ci, ci, ci, vp, vp, ci, ll, vp]
     L.muon_fp8_product.restype = ci
-    L.muon_fp8_linear_workspace_bytes.argtypes = [ll, ci]
+    L.muon_fp8_linear_workspace_bytes.argtypes = [ll, ci, ci, ci]
     L.muon_fp8_linear_workspace_bytes.restype = sz
     L.muon_fp8_linear.argtypes = [vp, ci, ll, ll, vp, vp, ci, ci, ci, vp, vp, sz, vp, ci, ll, vp]
     L.muon_fp8_linear.restype = ci
@@ -538,38 +539,42 @@ def _here(name, t):
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
-def _check_flat(name, tensors):
-    """(elements, element type codes) of contiguous CUDA tensors on the current device."""
-    numel, dtypes = [], []
+_FLOAT_CODE = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
+
+
+def _flat_list(name, tensors):
+    """Contiguous CUDA tensors on the current device as C arrays: (pointers,
+    elements, element type codes)."""
+    ptrs, numel, dtypes = array("Q"), array("q"), array("i")
     device = _current_device() if tensors else None
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _FLOATS or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
-        if t.get_device() != device:
+        code = _FLOAT_CODE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+        if code is None or not t.is_contiguous() or t.get_device() != device:
+            if code is None or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
             _check_device(f"{name}[{i}]", t, device)
+        ptrs.append(t.data_ptr())
         numel.append(t.numel())
-        dtypes.append(1 if t.dtype is torch.float32 else 0)
-    return numel, dtypes
+        dtypes.append(code)
+    return ptrs, numel, dtypes
 
 
-def _norm_buffer(numel, dtypes):
-    """C arrays of a list's sizes and types, and one buffer: the norm, then the partial sums from byte 16 on."""
-    n = len(numel)
-    cn = (ctypes.c_longlong * max(1, n))(*numel)
-    cd = (ctypes.c_int * max(1, n))(*dtypes)
-    need = lib().muon_grad_norm_workspace_bytes(cn, n)
-    return cn, cd, need, torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")
+def _at(a):
+    """Address of a C array."""
+    return a.buffer_info()[0]
 
 
 def muon_grad_norm(G, stream=None) -> torch.Tensor:
     """Global 2-norm of a list of contiguous CUDA gradients (bf16 and fp32 may
     be mixed), as a 0-dim fp32 CUDA tensor."""
     G = list(G)
-    numel, dtypes = _check_flat("G", G)
+    ptrs, numel, dtypes = _flat_list("G", G)
+    L = lib()
+    need = L.muon_grad_norm_workspace_bytes(_at(numel), len(G))
     with _on(stream):
-        cn, cd, need, buf = _norm_buffer(numel, dtypes)
+        buf = torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")   # the norm, partial sums from byte 16 on
         at = buf.data_ptr()
-        _check(lib().muon_grad_norm(_ptr_array(G), cn, cd, len(G), at + 16, need, at, _handle(stream)))
+        _check(L.muon_grad_norm(_at(ptrs), _at(numel), _at(dtypes), len(G), at + 16, need, at, _handle(stream)))
     return buf[0]
 
 
@@ -578,20 +583,22 @@ def muon_grad_clip(G, max_norm: float, out=None, stream=None) -> torch.Tensor:
     into ``out`` (tensors like G); returns the norm before clipping (0-dim
     fp32 CUDA tensor).  Nothing is read back to the host."""
     G = list(G)
-    numel, dtypes = _check_flat("G", G)
-    optr = None
+    ptrs, numel, dtypes = _flat_list("G", G)
+    optrs = None
     if out is not None:
         out = list(out)
         if len(out) != len(G):
             raise ValueError("out must have one tensor for each of G")
-        if _check_flat("out", out) != (numel, dtypes):
+        optrs, onumel, odtypes = _flat_list("out", out)
+        if onumel != numel or odtypes != dtypes:
             raise ValueError("out must have the dtype and number of elements of G, tensor by tensor")
-        optr = _ptr_array(out)
+    L = lib()
+    need = L.muon_grad_norm_workspace_bytes(_at(numel), len(G))
     with _on(stream):
-        cn, cd, need, buf = _norm_buffer(numel, dtypes)
+        buf = torch.empty(need // 4 + 4, dtype=torch.float32, device="cuda")
         at = buf.data_ptr()
-        _check(lib().muon_grad_clip(_ptr_array(G), optr, cn, cd, len(G), float(max_norm), at + 16, need, at,
-                                    _handle(stream)))
+        _check(L.muon_grad_clip(_at(ptrs), None if optrs is None else _at(optrs), _at(numel), _at(dtypes), len(G),
+                                float(max_norm), at + 16, need, at, _handle(stream)))
     return buf[0]
 
 
@@ -757,15 +764,26 @@ def _check_fp8(name, m, kind, codes_shape, scale_shape):
 
 
 def _check_weight(w, offsets):
-    """(n, k, groups) of a "block" weight that goes with ``offsets``."""
-    if not isinstance(w, Fp8Matrix) or not isinstance(w.codes, torch.Tensor) or w.codes.dim() not in (2, 3):
+    """(n, k, groups, offsets' pointer) of a "block" weight that goes with ``offsets``."""
+    codes, scale = w.codes, w.scale
+    shape, k = codes.shape, int(w.cols)
+    stacked = len(shape) == 3
+    if w.kind != "block" or len(shape) not in (2, 3):
         raise ValueError('the weight must be an Fp8Matrix of kind "block" with 2-D or 3-D codes')
-    n, k = w.codes.shape[-2], int(w.cols)
-    lead = tuple(w.codes.shape[:-2])
-    if bool(lead) != (offsets is not None):
+    if stacked != (offsets is not None):
         raise ValueError("a stacked weight goes with offsets, a single one without")
-    _check_fp8("the weight", w, "block", (*lead, n, _up128(k)), (*lead, _up128(n) // 128, _up128(k) // 128))
-    return n, k, lead[0] if lead else 1
+    n = shape[-2]
+    kb, nb = (k + 127) // 128, (n + 127) // 128
+    if codes.dtype != torch.float8_e4m3fn or shape[-1] != 128 * kb or not codes.is_cuda or not codes.is_contiguous():
+        raise ValueError(f"the weight's codes must be a contiguous CUDA tensor of {torch.float8_e4m3fn} with rows of {128 * kb}")
+    if scale.dtype != torch.uint8 or tuple(scale.shape) != (*shape[:-2], nb, kb) or not scale.is_cuda \
+            or not scale.is_contiguous():
+        raise ValueError(f"the weight's scale must be a contiguous CUDA tensor of {torch.uint8} with shape "
+                         f"{(*shape[:-2], nb, kb)}")
+    _here("the weight's codes", codes)
+    _here("the weight's scale", scale)
+    groups, optr = _check_offsets(offsets, shape[0] if stacked else 1)
+    return n, k, groups, optr
 
 
 def _product(code, a, b, tokens, n, k, groups, optr, out, ld, stream):
@@ -787,8 +805,7 @@ def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None,
     ``tokens`` (grad_weight): the rows that the operands were made from.
     ``out``: optional preallocated result, bf16 or fp32 (rows contiguous)."""
     if product in ("forward", "grad_input"):
-        n, k, groups = _check_weight(b, offsets)
-        _, optr = _check_offsets(offsets, groups)
+        n, k, groups, optr = _check_weight(b, offsets)
         inner, red = (n, k) if product == "forward" else (k, n)
         if not isinstance(a, Fp8Matrix) or not isinstance(a.codes, torch.Tensor) or a.codes.dim() != 2 or a.cols != red:
             raise ValueError(f'a must be an Fp8Matrix of kind "row" with {red} columns')
@@ -828,18 +845,17 @@ def muon_fp8_linear(x, w, *, offsets=None, out_dtype=torch.bfloat16, stream=None
     """y = x W^T in 8 bits: ``x`` (tokens x k, bf16 or fp32) is rounded to E4M3 by
     row blocks and multiplied with ``w`` (``muon_fp8_quantize_weight``).  With
     ``offsets``, tokens are sorted by expert and ``w`` is stacked over experts."""
-    n, k, groups = _check_weight(w, offsets)
+    n, k, groups, optr = _check_weight(w, offsets)
     tokens, _, ld = _check_rows("x", x, _FLOATS, None, k)
-    _, optr = _check_offsets(offsets, groups)
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    L = lib()
+    need = L.muon_fp8_linear_workspace_bytes(tokens, n, k, offsets is not None)
     with _on(stream):
         out = torch.empty((tokens, n), dtype=out_dtype, device="cuda")
-        need = lib().muon_fp8_linear_workspace_bytes(tokens, k)
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-        _check(lib().muon_fp8_linear(x.data_ptr(), _dtype_code(x), tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(), n, k,
-                                     groups, optr, ws.data_ptr(), need, out.data_ptr(), _dtype_code(out), n,
-                                     _handle(stream)))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        _check(L.muon_fp8_linear(x.data_ptr(), _dtype_code(x), tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(), n, k,
+                                 groups, optr, None if ws is None else ws.data_ptr(), need, out.data_ptr(), _dtype_code(out), n, _handle(stream)))
     return out
 
 
@@ -848,10 +864,9 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
     """(dx, dW) of ``muon_fp8_linear`` from dy (tokens x n): dx = dy W with dy by
     row blocks, dW = dy^T x with both by col blocks; either may be left out
     (None).  dy is read once for both."""
-    n, k, groups = _check_weight(w, offsets)
+    n, k, groups, optr = _check_weight(w, offsets)
     tokens, _, ld_dy = _check_rows("dy", dy, _FLOATS, None, n)
     _, _, ld_x = _check_rows("x", x, _FLOATS, tokens, k)
-    _, optr = _check_offsets(offsets, groups)
     if dx_dtype not in _FLOATS or dw_dtype not in _FLOATS:
         raise ValueError(f"dx_dtype and dw_dtype must be of {_FLOATS}")
     dx = dw = None
@@ -864,7 +879,7 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
         ws = torch.empty(need, dtype=torch.uint8, device="cuda")
         _check(lib().muon_fp8_linear_backward(
             dy.data_ptr(), _dtype_code(dy), ld_dy, x.data_ptr(), _dtype_code(x), ld_x, tokens, w.codes.data_ptr(),
-            w.scale.data_ptr(), n, k, groups, optr, ws.data_ptr(), need, dx.data_ptr() if need_dx and tokens else None,
+            w.scale.data_ptr(), n, k, groups, optr, ws.data_ptr() if need else None, need, dx.data_ptr() if need_dx and tokens else None,
             MUON_F32 if dx_dtype == torch.float32 else MUON_BF16, k, dw.data_ptr() if need_dw else None,
             MUON_F32 if dw_dtype == torch.float32 else MUON_BF16, _handle(stream)))
     return dx, dw

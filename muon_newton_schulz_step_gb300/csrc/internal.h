@@ -316,20 +316,20 @@ struct Fp8GemmParams {
 // `after`: the launch before it on the stream wrote its operands and let it start early.
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, bool after, cudaStream_t s);
 
-// The forward product of few tokens, x rounded on the way.
+// The forward product of few tokens and one weight, x rounded on the way.
 struct Fp8TokenParams {
     const void* x;            // tokens x k, row stride ld_x
-    const uint8_t* w;         // groups x n x ldk codes
-    const uint8_t* w_scale;   // groups x n blocks x k blocks
+    const uint8_t* w;         // n x ldk codes
+    const uint8_t* w_scale;   // n blocks x k blocks
     void* out;                // tokens x n, row stride ld_out
-    const int* offsets;       // groups + 1, or nullptr
     long long ld_x, ldk, ld_out;
-    int tokens, n, k, groups;
+    int tokens, n, k;
     int bf16;                 // x
     int vec;                  // 16-byte loads of x are legal
     int out_f32;
 };
 
+bool fp8_token_serves(long long tokens, long long n, long long k);
 cudaError_t launch_fp8_token(const Fp8TokenParams& p, cudaStream_t s);
 cudaError_t read_and_clear_fp8_error(int* code);
 

@@ -29,13 +29,16 @@
 // consecutive experts of one group, in index order over the warp: so the lowest
 // index among equal values is the lowest lane's, a group's two largest values
 // meet in log2(lanes) exchanges for all groups at once, and everything stays
-// in registers.  The top_k largest lane maxima bound the choice from below:
-// whatever is chosen is at least the top_k-th of them.  The few experts at or
+// in registers.  The top_k-th largest lane maximum bounds the choice from
+// below.  The few experts at or
 // above that bound (8 to about 12 of 384) are written to shared memory in index
 // order, a lane takes one each and counts those before it: its place in the
 // result.  Should more than 32 qualify (equal values, few lanes left), the
-// largest is taken top_k times instead, which alone took 680 of about 1400
-// instructions a token (73 us for 32768 tokens x 384 experts in fp32; now @@).
+// largest is taken top_k times instead.  The choice works on scores from one ex2 and
+// one rcp; the weights of the chosen are computed anew.  Bound by instructions:
+// 32768 tokens x 384 experts in fp32, 4 of 8 groups: 73 us with the largest taken
+// top_k times for every token (about 1400 instructions each), 45 with the bound and
+// full-accuracy scores (1050), 34 now (780, four blocks per SM in one wave).
 //
 // Backward: one warp per token, lanes striped over the row in vectors of four.
 // Scores of the chosen are recomputed from their logits; only the softmax without
@@ -88,6 +91,22 @@ __device__ __forceinline__ float exp_fast(float x) {
 
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + exp_fast(-x)); }
 
+// For the choice: 2^x and 1 / x in one instruction each.  e^x by them is off by
+// |x| 2^-24 on top of 2 ulp; the weights of what is chosen are computed anew.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504f;
+
 // This lane's logits, -inf where it owns no expert.
 template <int NV>
 __device__ __forceinline__ void load_lane(const RouteParams& p, long long row, int e0, int n, float (&x)[NV]) {
@@ -118,12 +137,17 @@ __device__ __forceinline__ void load_lane(const RouteParams& p, long long row, i
     }
 }
 
+// Blocks per SM: the grid is that many, so that all are resident at once.
+template <int NV>
+constexpr int route_blocks() {
+    return NV <= 4 ? 6 : NV <= 12 ? 4 : 2;
+}
+
 template <int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) k_route(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __grid_constant__ RouteParams p) {
     extern __shared__ int hist[];
-    __shared__ float2 pool[kWarps][32];                  // choice value, score
-    __shared__ int pool_e[kWarps][32];
-    __shared__ float2 order[kWarps][32];                 // score, expert
+    __shared__ float2 pool[kWarps][32];                  // choice value, expert
+    __shared__ int order[kWarps][32];                    // experts by place
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = threadIdx.x; e < p.experts; e += kThreads) hist[e] = 0;
     __syncthreads();
@@ -135,36 +159,59 @@ __global__ void __launch_bounds__(kThreads) k_route(const __grid_constant__ Rout
     float bias[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) bias[j] = p.bias != nullptr && j < n ? p.bias[e0 + j] : 0.0f;
+    bool odd_bias = false;                               // of any lane: some bias is not finite
+#pragma unroll
+    for (int j = 0; j < NV; ++j) odd_bias |= !(fabsf(bias[j]) <= FLT_MAX);
+    odd_bias = __any_sync(kAll, odd_bias);
 
     for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < p.tokens;
          row += static_cast<long long>(gridDim.x) * kWarps) {
-        float x[NV];
-        load_lane<NV>(p, row, e0, n, x);
-        // scores
-        float top = 0.0f, scale = 1.0f;
-        if (!SIGMOID) {
+        float c[NV];                                     // logits, then choice values; -inf: masked
+        load_lane<NV>(p, row, e0, n, c);
+        float top = 0.0f, inv = 1.0f;                    // softmax: largest logit, 1 / sum
+        float seen = 0.0f;                               // not finite: masked experts or NaN in this lane
+        if (SIGMOID) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) seen += c[j];
+        } else {
             float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
+            for (int j = 0; j < NV; ++j) {
+                m = fmaxf(m, c[j]);
+                seen += c[j];
+            }
             top = warp_max(m);
         }
-        float c[NV];                                     // choice values; -inf: masked
-        float a = 0.0f;
+        const bool plain = __all_sync(kAll, fabsf(seen) <= FLT_MAX) && top > -FLT_MAX;
+        uint32_t masked = 0;                             // bit j: no expert, or masked
+        if (!plain) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool masked = x[j] == -INFINITY;
-            x[j] = SIGMOID ? sigmoid_fast(x[j]) : exp_fast(x[j] - top);
-            if (masked) x[j] = 0.0f;
-            if (!SIGMOID) a += x[j];
-            c[j] = masked ? -INFINITY : 0.0f;
+            for (int j = 0; j < NV; ++j) masked |= (c[j] == -INFINITY ? 1u : 0u) << j;
         }
-        if (!SIGMOID) scale = __fdiv_rn(1.0f, warp_sum(a));
+        if (SIGMOID) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!SIGMOID) x[j] *= scale;
+            for (int j = 0; j < NV; ++j) c[j] = rcp_approx(1.0f + exp2_approx(c[j] * -kLog2e));
+        } else {
+            float a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                c[j] = exp2_approx((c[j] - top) * kLog2e);
+                if (!plain && (masked >> j & 1u)) c[j] = 0.0f;
+                a += c[j];
+            }
+            inv = __fdiv_rn(1.0f, warp_sum(a));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) c[j] *= inv;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) c[j] += bias[j];
+        if (!plain || odd_bias) {
             // a NaN orders below every number
-            const float v = x[j] + bias[j];
-            c[j] = c[j] < 0.0f ? c[j] : (v == v ? v : -FLT_MAX);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const float v = c[j] == c[j] ? c[j] : -FLT_MAX;
+                c[j] = masked >> j & 1u ? -INFINITY : v;
+            }
         }
         // group scores
         if (p.groups > 1) {
@@ -193,61 +240,43 @@ __global__ void __launch_bounds__(kThreads) k_route(const __grid_constant__ Rout
         float best = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NV; ++j) best = fmaxf(best, c[j]);
-        // the top_k-th largest lane maximum, by a bitonic sort of the maxima (descending)
-        float v = best;
-#pragma unroll
-        for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-            for (int o = k >> 1; o > 0; o >>= 1) {
-                const float w = __shfl_xor_sync(kAll, v, o);
-                const bool larger = ((lane & o) == 0) == ((lane & k) == 0);
-                v = larger ? fmaxf(v, w) : fminf(v, w);
-            }
+        // a bound that at least top_k choice values reach: take the largest lane maximum
+        // away top_k times (equal ones together: the bound is then lower)
+        float bound = -INFINITY, v = best;
+        for (int k = 0; k < p.top_k; ++k) {
+            bound = warp_max(v);
+            v = v == bound ? -INFINITY : v;
         }
-        const float bound = __shfl_sync(kAll, v, p.top_k - 1);
         int cnt = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) cnt += c[j] >= bound && c[j] > -INFINITY;
+        for (int j = 0; j < NV; ++j) cnt += c[j] >= bound;
         const int upto = warp_inclusive_sum(cnt);
         const int total = __shfl_sync(kAll, upto, 31);
         int my_e = -1;
-        float my_s = 0.0f;
-        if (total <= 32) {
-            int at = upto - cnt;
+        if (bound > -INFINITY && total <= 32) {
+            float2* at = &pool[warp][upto - cnt];
+            if (cnt > 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (c[j] >= bound && c[j] > -INFINITY) {
-                    pool[warp][at] = make_float2(c[j], x[j]);
-                    pool_e[warp][at] = e0 + j;
-                    ++at;
-                }
+                for (int j = 0; j < NV; ++j)
+                    if (c[j] >= bound) *at++ = make_float2(c[j], __int_as_float(e0 + j));
             }
             __syncwarp();
             const float2 f = pool[warp][lane];
-            const int e = pool_e[warp][lane];
             const float mine = lane < total ? f.x : -INFINITY;
             int place = 0;
             for (int i = 0; i < total; ++i) {
                 const float o = __shfl_sync(kAll, mine, i);
                 place += o > mine || (o == mine && i < lane);
             }
-            __syncwarp();                                // the pool has been read
-            if (lane < total && place < p.top_k) {
-                order[warp][place] = make_float2(f.y, __int_as_float(e));
-            }
-            __syncwarp();
-            if (lane < p.top_k && lane < total) {
-                const float2 o = order[warp][lane];
-                my_s = o.x;
-                my_e = __float_as_int(o.y);
-            }
+            if (lane < total && place < p.top_k) order[warp][place] = __float_as_int(f.y);
+            __syncwarp();                                // and the pool has been read
+            if (lane < p.top_k) my_e = order[warp][lane];
         } else {
             for (int k = 0; k < p.top_k; ++k) {
                 const float m = warp_max(best);
                 if (m == -INFINITY) break;
                 const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
                 int e = -1;
-                float s = 0.0f;
                 if (lane == w) {
                     bool found = false;
                     best = -INFINITY;
@@ -256,34 +285,31 @@ __global__ void __launch_bounds__(kThreads) k_route(const __grid_constant__ Rout
                         if (!found && c[j] == m) {
                             found = true;
                             e = e0 + j;
-                            s = x[j];
                             c[j] = -INFINITY;
                         }
                         best = fmaxf(best, c[j]);
                     }
                 }
                 e = __shfl_sync(kAll, e, w);
-                s = __shfl_sync(kAll, s, w);
-                if (lane == k) {
-                    my_e = e;
-                    my_s = s;
-                }
+                if (lane == k) my_e = e;
             }
         }
-        const bool mine = lane < p.top_k;
-        float w = my_s;
+        // the scores of the chosen, from their logits
+        float w = 0.0f;
+        const float logit = my_e >= 0 ? load_logit(p, row, my_e) : -INFINITY;
+        if (SIGMOID) {
+            if (my_e >= 0) w = sigmoid_fast(logit);
+        } else {
+            // renormalised softmax = softmax over the chosen logits, which holds where
+            // every chosen score underflows, too (a NaN sum stays one)
+            const float m = p.renormalize ? warp_max(logit) : top;
+            if (my_e >= 0) w = exp_fast(logit - m) * (p.renormalize ? (inv == inv ? 1.0f : inv) : inv);
+        }
         if (p.renormalize) {
-            if (!SIGMOID) {
-                // renormalised softmax = softmax over the chosen logits, which holds
-                // where every chosen score underflows, too
-                const float v = my_e >= 0 ? load_logit(p, row, my_e) : -INFINITY;
-                const float m = warp_max(v);
-                if (my_e >= 0 && my_s == my_s) w = exp_fast(v - m);
-            }
             const float t = warp_sum(w);
             w = t == 0.0f ? 0.0f : __fdiv_rn(w, t);
         }
-        if (mine) {
+        if (lane < p.top_k) {
             p.weights[row * p.top_k + lane] = w * p.scale;
             p.chosen[row * p.top_k + lane] = my_e;
             if (my_e >= 0) atomicAdd(&hist[my_e], 1);
@@ -385,12 +411,13 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m = fmaxf(m, s[i][j]);
             m = warp_max(m);
+            const float m0 = m == -INFINITY ? 0.0f : m;   // every expert masked: all scores zero
             float a = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = s[i][j] == -INFINITY ? 0.0f : exp_fast(s[i][j] - m);
+                    s[i][j] = exp2_approx((s[i][j] - m0) * kLog2e);
                     a += s[i][j];
                 }
             const float sum = warp_sum(a);
@@ -440,7 +467,7 @@ int route_grid(const RouteParams& p, int sms, int per_sm) {
 template <int NV>
 cudaError_t run_route(const RouteParams& p, int sms, cudaStream_t s) {
     const size_t smem = sizeof(int) * p.experts;
-    const int grid = route_grid(p, sms, 4);
+    const int grid = route_grid(p, sms, route_blocks<NV>());
     if (grid > 1) {
         const cudaError_t e = cudaMemsetAsync(p.counts, 0, smem, s);
         if (e != cudaSuccess) return e;

@@ -268,10 +268,8 @@ struct ColCodes {
     size_t bytes() const { return code_bytes + scale_bytes; }
 };
 
-// Up to this many tokens (for each of several experts) the weight is streamed.
-constexpr long long kTokenMax = 8, kTokenMaxPerGroup = 2;
-
 int check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return MUON_OK;
     const int rc = check_align(ws, 16, "workspace");
     if (rc != MUON_OK) return rc;
     if (have < need) return fail(MUON_ERR_OOM, "workspace has %zu bytes; %zu are needed", have, need);
@@ -528,8 +526,8 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
                        false, stream);
 }
 
-size_t muon_fp8_linear_workspace_bytes(long long tokens, int k) {
-    if (tokens <= 0 || k < 1) return 16;
+size_t muon_fp8_linear_workspace_bytes(long long tokens, int n, int k, int grouped) {
+    if (tokens <= 0 || n < 1 || k < 1 || (!grouped && fp8_token_serves(tokens, n, k))) return 0;
     return RowCodes(nullptr, tokens, k).bytes();
 }
 
@@ -543,7 +541,7 @@ int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x
     if (tokens == 0) return MUON_OK;
     if ((rc = check_align(x, dtype_size(x_dtype), "x")) != MUON_OK) return rc;
     if ((rc = check_align(out, dtype_size(out_dtype), "out")) != MUON_OK) return rc;
-    if (tokens <= kTokenMax || (offsets != nullptr && tokens <= kTokenMaxPerGroup * static_cast<long long>(groups))) {
+    if (offsets == nullptr && fp8_token_serves(tokens, n, k)) {
         int sms = 0;
         if ((rc = op_device(&sms)) != MUON_OK) return rc;
         Fp8TokenParams p = {};
@@ -551,21 +549,19 @@ int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x
         p.w = static_cast<const uint8_t*>(w_codes);
         p.w_scale = static_cast<const uint8_t*>(w_scale);
         p.out = out;
-        p.offsets = offsets;
         p.ld_x = ld_x;
         p.ldk = up128(k);
         p.ld_out = ld_out;
         p.tokens = static_cast<int>(tokens);
         p.n = n;
         p.k = k;
-        p.groups = groups;
         p.bf16 = x_dtype == MUON_BF16;
         p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * static_cast<long long>(dtype_size(x_dtype)) % 16 == 0;
         p.out_f32 = out_dtype == MUON_F32;
-        const double bytes = static_cast<double>(groups) * n * k;
+        const double bytes = static_cast<double>(n) * k;
         return op_launch(kOpFp8Token, 2.0 * tokens * n * k, bytes, stream, [&] { return launch_fp8_token(p, stream); });
     }
-    if ((rc = check_workspace(workspace, workspace_bytes, muon_fp8_linear_workspace_bytes(tokens, k))) != MUON_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, muon_fp8_linear_workspace_bytes(tokens, n, k, offsets != nullptr))) != MUON_OK) return rc;
     const RowCodes q(workspace, tokens, k);
     rc = muon_fp8_quantize(x, x_dtype, tokens, k, ld_x, 1, nullptr, q.codes, q.scale, nullptr, nullptr, stream);
     if (rc != MUON_OK) return rc;
@@ -574,8 +570,8 @@ int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x
 }
 
 size_t muon_fp8_linear_backward_workspace_bytes(long long tokens, int n, int k, int groups, int need_dx, int need_dw) {
-    if (tokens <= 0 || n < 1 || k < 1 || groups < 1) return 16;
-    size_t bytes = 16;
+    if (tokens <= 0 || n < 1 || k < 1 || groups < 1) return 0;
+    size_t bytes = 0;
     if (need_dx) bytes += RowCodes(nullptr, tokens, n).bytes();
     if (need_dw) bytes += ColCodes(nullptr, tokens, n, groups).bytes() + ColCodes(nullptr, tokens, k, groups).bytes();
     return bytes;
