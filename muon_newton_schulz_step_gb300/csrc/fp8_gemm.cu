@@ -519,15 +519,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue --
-        // Where rows of the result start on 16 bytes:
         //   weight gradient: a lane holds consecutive results of one row; blocks of 32
         //   rows of 128 bytes go through shared memory and leave in whole lines.  These
         //   tiles are nearly all epilogue, and their stores are the warps' own: TMA
         //   stores wait behind the loads that the producer has asked for ahead (2500
         //   cycles; in 128-byte blocks they brought the weights of 96 experts to 784 us, the
         //   rest of the tile as it is now to 532);
-        //   else: lanes run along the row; 8 x 8 blocks of bf16 go through shared memory
-        //   transposed and leave by TMA, 32 rows of 64 bytes at a time.
+        //   else: lanes run along the row; where rows start on 16 bytes, 8 x 8 blocks of
+        //   bf16 go through shared memory transposed and leave by TMA, 32 rows of 64
+        //   bytes at a time.
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
         uint8_t* const stage = s_epi + (warp - 4) * Ring<MODE>::blocks * kEpiBytes;
@@ -576,35 +576,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0u;
                     }
                     if (2 * pr >= chunks) continue;
-                    if (p.vec) {
 #pragma unroll
-                        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
-                            if (F32 && 2 * pr + h >= chunks) continue;
-                            uint8_t* const row = stage + lane * 128;
-                            __syncwarp();                // the last block has been read
+                    for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+                        uint8_t* const row = stage + lane * 128;
+                        __syncwarp();                    // the last block has been read
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                uint4 v;
-                                if (F32) {
-                                    v = make_uint4(r[h][4 * u], r[h][4 * u + 1], r[h][4 * u + 2], r[h][4 * u + 3]);
-                                } else {
-                                    uint32_t w[4];
+                        for (int u = 0; u < 8; ++u) {
+                            uint4 v;
+                            if (F32) {
+                                v = make_uint4(r[h][4 * u], r[h][4 * u + 1], r[h][4 * u + 2], r[h][4 * u + 3]);
+                            } else {
+                                uint32_t w[4];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const int j = 8 * u + 2 * e;
-                                        const __nv_bfloat162 f = __floats2bfloat162_rn(__uint_as_float(r[j >> 5][j & 31]),
-                                                                                       __uint_as_float(r[j >> 5][(j & 31) + 1]));
-                                        w[e] = *reinterpret_cast<const uint32_t*>(&f);
-                                    }
-                                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int e = 0; e < 4; ++e) {
+                                    const int j = 8 * u + 2 * e;
+                                    const __nv_bfloat162 f = __floats2bfloat162_rn(__uint_as_float(r[j >> 5][j & 31]),
+                                                                                   __uint_as_float(r[j >> 5][(j & 31) + 1]));
+                                    w[e] = *reinterpret_cast<const uint32_t*>(&f);
                                 }
-                                *reinterpret_cast<uint4*>(row + ((u ^ (lane & 7)) << 4)) = v;
+                                v = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                            __syncwarp();
-                            constexpr int kPer = F32 ? 4 : 8, kSize = F32 ? 4 : 2;   // elements per 16 bytes
-                            const int col = x.c0 + 64 * pr + 32 * h + kPer * (lane & 7);
-                            char* o = static_cast<char*>(p.out) +
-                                      (batch * p.out_batch + static_cast<long long>(m0 + (lane >> 3)) * p.ld + col) * kSize;
+                            *reinterpret_cast<uint4*>(row + ((u ^ (lane & 7)) << 4)) = v;
+                        }
+                        __syncwarp();
+                        constexpr int kPer = F32 ? 4 : 8, kSize = F32 ? 4 : 2;   // elements per 16 bytes
+                        const int col0 = x.c0 + 64 * pr + 32 * h;
+                        char* const out0 = static_cast<char*>(p.out) +
+                                           (batch * p.out_batch + static_cast<long long>(m0) * p.ld + col0) * kSize;
+                        if (p.vec) {
+                            const int col = col0 + kPer * (lane & 7);
+                            char* o = out0 + ((lane >> 3) * p.ld + kPer * (lane & 7)) * kSize;
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 const int rr = 4 * k + (lane >> 3);
@@ -626,15 +627,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                 }
                                 o += 4 * p.ld * kSize;
                             }
-                        }
-                    } else if (m0 + lane < p.m_ext) {
-                        const long long at = batch * p.out_batch + static_cast<long long>(m0 + lane) * p.ld + x.c0 + 64 * pr;
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) {
-                            if (64 * pr + j < x.cols) {
-                                const float v = __uint_as_float(r[j >> 5][j & 31]);
-                                if (F32) static_cast<float*>(p.out)[at + j] = v;
-                                else static_cast<__nv_bfloat16*>(p.out)[at + j] = __float2bfloat16_rn(v);
+                        } else {
+                            // rows that start anywhere: one row per instruction, four bytes a lane where they are aligned
+                            const int rows = min(32, p.m_ext - m0);
+                            const int col = col0 + (F32 ? lane : 2 * lane);
+                            for (int rr = 0; rr < rows; ++rr) {
+                                const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                                    stage + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+                                char* o = out0 + rr * p.ld * kSize + 4 * lane;
+                                if (F32) {
+                                    if (col < p.n_ext) *reinterpret_cast<uint32_t*>(o) = v;
+                                } else if ((reinterpret_cast<uintptr_t>(o) & 3u) == 0 && col + 1 < p.n_ext) {
+                                    *reinterpret_cast<uint32_t*>(o) = v;
+                                } else {
+                                    if (col < p.n_ext) *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(v);
+                                    if (col + 1 < p.n_ext) reinterpret_cast<uint16_t*>(o)[1] = static_cast<uint16_t>(v >> 16);
+                                }
                             }
                         }
                     }

@@ -182,28 +182,92 @@ __device__ __forceinline__ void find_row_block(const QuantParams& p, const int* 
     }
 }
 
-// Eight elements at the matrix's edge, or without the alignment for vectors.
+// Eight elements from any element on: the 16-byte vectors that hold them, shifted
+// into place (rows of odd length start anywhere; element by element they loaded at
+// a quarter of the rate).
 template <bool BF16>
-__device__ __noinline__ Raw load_edge(const QuantParams& p, const char* base, long long row, long long col) {
+struct Shifted {
+    static constexpr int kSize = BF16 ? 2 : 4, kVecs = BF16 ? 2 : 3;
+    uint4 v[kVecs];
+    static __device__ __forceinline__ const char* from(const char* s) {
+        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(s) & ~static_cast<uintptr_t>(15));
+    }
+    // vectors that reach beyond the tensor must not be read
+    static __device__ __forceinline__ bool inside(const QuantParams& p, const char* s) {
+        return from(s) >= static_cast<const char*>(p.x) && from(s) + 16 * kVecs <= p.x_end;
+    }
+    __device__ __forceinline__ void load(const char* s) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = *reinterpret_cast<const uint4*>(from(s) + 16 * i);
+    }
+    // the elements at s, `left` of them
+    __device__ __forceinline__ Raw take(const char* s, int left) const {
+        constexpr int kWords = 8 * kSize / 4;            // result words; one more for the odd half
+        uint32_t w[12];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            w[4 * i] = v[i].x; w[4 * i + 1] = v[i].y; w[4 * i + 2] = v[i].z; w[4 * i + 3] = v[i].w;
+        }
+        const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(s)) & 15u;
+        const bool one = shift & 4, two = shift & 8;
+#pragma unroll
+        for (int i = 0; i <= kWords + 2; ++i) w[i] = one && i + 1 < 4 * kVecs ? w[i + 1] : w[i];
+#pragma unroll
+        for (int i = 0; i <= kWords; ++i) w[i] = two && i + 2 < 4 * kVecs ? w[i + 2] : w[i];
+        if (BF16) {
+            const unsigned bits = 8 * (shift & 2);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        }
+        if (left < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i >= left) {
+                    if (BF16) w[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                    else w[i] = 0;
+                }
+            }
+        }
+        Raw r;
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = BF16 ? r.a : make_uint4(w[4], w[5], w[6], w[7]);
+        return r;
+    }
+};
+
+// The same element by element where the vectors would reach beyond the tensor.
+template <bool BF16>
+__device__ __forceinline__ Raw load_any(const QuantParams& p, const char* base, long long row, long long col) {
+    constexpr int kSize = BF16 ? 2 : 4;
+    Raw r;
+    r.a = r.b = make_uint4(0, 0, 0, 0);
+    if (col >= p.cols) return r;
+    const char* s = base + (row * p.ld + col) * kSize;
+    const int left = static_cast<int>(p.cols - col < 8 ? p.cols - col : 8);
+    if (Shifted<BF16>::inside(p, s)) {
+        Shifted<BF16> x;
+        x.load(s);
+        return x.take(s, left);
+    }
     uint32_t w[8];
 #pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-        w[i] = 0;
-        if (col + i < p.cols) {
-            const long long at = row * p.ld + col + i;
-            w[i] = BF16 ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[at])
-                        : reinterpret_cast<const uint32_t*>(base)[at];
+        if (i < left) {
+            if (BF16) w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(s)[i]) << (16 * (i & 1));
+            else w[i] = reinterpret_cast<const uint32_t*>(s)[i];
         }
     }
-    Raw r;
-    if (BF16) {
-        r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-        r.b = r.a;
-    } else {
-        r.a = make_uint4(w[0], w[1], w[2], w[3]);
-        r.b = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    if (!BF16) r.b = make_uint4(w[4], w[5], w[6], w[7]);
     return r;
+}
+
+// The same out of line, for the edges.
+template <bool BF16>
+__device__ __noinline__ Raw load_last(const QuantParams& p, const char* base, long long row, long long col) {
+    return load_any<BF16>(p, base, row, col);
 }
 
 // Shared memory of a block of threads.
@@ -317,7 +381,8 @@ __device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Ra
     // thread's last read here
 }
 
-template <bool BF16, bool ROW, bool COL, bool BLK>
+// VEC: rows start on 16 bytes.
+template <bool BF16, bool ROW, bool COL, bool BLK, bool VEC>
 __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const __grid_constant__ QuantParams p) {
     __shared__ Tile sh;
     __shared__ RowBlock rb;
@@ -340,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const _
         for (long long cb = blockIdx.x; cb < colblocks; cb += gridDim.x) {
             const long long col = cb * 128 + cg * 8;
             Raw v[kRowsPerThread];
-            if (p.vec && cb * 128 + 128 <= p.cols) {
+            if (VEC && cb * 128 + 128 <= p.cols) {
                 const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
                 const long long step = 16 * p.ld * (BF16 ? 2 : 4);
                 const int rows = r.rows - warp * 2 - half;
@@ -353,11 +418,35 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const _
                     }
                 }
             } else {
+                bool done = false;
+                if constexpr (!VEC) {
+                    // away from the tensor's ends all of a warp's vectors can be loaded ahead
+                    const int rows = r.rows - warp * 2 - half;
+                    const char* src = base + ((r.row0 + warp * 2 + half) * p.ld + col) * (BF16 ? 2 : 4);
+                    const long long step = 16 * p.ld * (BF16 ? 2 : 4);
+                    done = __all_sync(0xffffffffu, rows > 16 * (kRowsPerThread - 1) && col < p.cols &&
+                                                       Shifted<BF16>::inside(p, src) &&
+                                                       Shifted<BF16>::inside(p, src + (kRowsPerThread - 1) * step));
+                    if (done) {
+                        const int left = static_cast<int>(p.cols - col < 8 ? p.cols - col : 8);
+                        constexpr int kAt = BF16 ? 4 : 2;    // rows at a time
 #pragma unroll
-                for (int i = 0; i < kRowsPerThread; ++i) {
-                    const int lr = i * 16 + warp * 2 + half;
-                    v[i].a = v[i].b = make_uint4(0, 0, 0, 0);
-                    if (lr < r.rows) v[i] = load_edge<BF16>(p, base, r.row0 + lr, col);
+                        for (int i = 0; i < kRowsPerThread; i += kAt) {
+                            Shifted<BF16> x[kAt];
+#pragma unroll
+                            for (int u = 0; u < kAt; ++u) x[u].load(src + (i + u) * step);
+#pragma unroll
+                            for (int u = 0; u < kAt; ++u) v[i + u] = x[u].take(src + (i + u) * step, left);
+                        }
+                    }
+                }
+                if (!done) {
+#pragma unroll
+                    for (int i = 0; i < kRowsPerThread; ++i) {
+                        const int lr = i * 16 + warp * 2 + half;
+                        v[i].a = v[i].b = make_uint4(0, 0, 0, 0);
+                        if (lr < r.rows) v[i] = load_last<BF16>(p, base, r.row0 + lr, col);
+                    }
                 }
             }
             tile<BF16, ROW, COL, BLK>(p, r, v, sh, cb, batch);
@@ -366,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const _
     }
 }
 
-template <bool BF16>
+template <bool BF16, bool VEC>
 cudaError_t run(const QuantParams& p, cudaStream_t s) {
     // several tiles of a row block per block of threads where there are enough of
     // both: finding a group's row block costs about as much as half a tile
@@ -375,17 +464,19 @@ cudaError_t run(const QuantParams& p, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>((colblocks + share - 1) / share),
                     static_cast<unsigned>(p.row_blocks < 65535 ? p.row_blocks : 65535),
                     static_cast<unsigned>(p.batch));
-    if (p.blk_q != nullptr) k_fp8_quantize<BF16, false, false, true><<<grid, kThreads, 0, s>>>(p);
-    else if (p.row_q != nullptr && p.col_q != nullptr) k_fp8_quantize<BF16, true, true, false><<<grid, kThreads, 0, s>>>(p);
-    else if (p.row_q != nullptr) k_fp8_quantize<BF16, true, false, false><<<grid, kThreads, 0, s>>>(p);
-    else k_fp8_quantize<BF16, false, true, false><<<grid, kThreads, 0, s>>>(p);
+    if (p.blk_q != nullptr) k_fp8_quantize<BF16, false, false, true, VEC><<<grid, kThreads, 0, s>>>(p);
+    else if (p.row_q != nullptr && p.col_q != nullptr)
+        k_fp8_quantize<BF16, true, true, false, VEC><<<grid, kThreads, 0, s>>>(p);
+    else if (p.row_q != nullptr) k_fp8_quantize<BF16, true, false, false, VEC><<<grid, kThreads, 0, s>>>(p);
+    else k_fp8_quantize<BF16, false, true, false, VEC><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const QuantParams& p, cudaStream_t s) {
-    return p.bf16 ? run<true>(p, s) : run<false>(p, s);
+    if (p.bf16) return p.vec ? run<true, true>(p, s) : run<true, false>(p, s);
+    return p.vec ? run<false, true>(p, s) : run<false, false>(p, s);
 }
 
 }  // namespace muon

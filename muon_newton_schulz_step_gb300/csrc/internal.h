@@ -259,6 +259,7 @@ constexpr int kFp8MaxGroups = 512;
 
 struct QuantParams {
     const void* x;            // rows x cols of `batch` matrices, row stride ld, matrix stride ldb
+    const char* x_end;        // one past the last element
     long long rows, cols, ld, ldb;
     int batch;
     int bf16;

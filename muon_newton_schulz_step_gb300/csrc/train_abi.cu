@@ -471,6 +471,7 @@ int muon_fp8_quantize(const void* x, int dtype, long long rows, long long cols, 
     p.rows = rows;
     p.cols = cols;
     p.ld = ld;
+    p.x_end = static_cast<const char*>(x) + ((rows - 1) * ld + cols) * static_cast<long long>(dtype_size(dtype));
     p.batch = 1;
     p.bf16 = dtype == MUON_BF16;
     p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * static_cast<long long>(dtype_size(dtype)) % 16 == 0;
@@ -507,6 +508,7 @@ int muon_fp8_quantize_weight(const void* w, int dtype, int batch, long long rows
     p.cols = cols;
     p.ld = cols;
     p.ldb = rows * cols;
+    p.x_end = static_cast<const char*>(w) + batch * rows * cols * static_cast<long long>(dtype_size(dtype));
     p.batch = batch;
     p.bf16 = dtype == MUON_BF16;
     const long long sz = static_cast<long long>(dtype_size(dtype));
