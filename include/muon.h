@@ -407,8 +407,9 @@ MUON_API int muon_fp8_product(int product, const void* a_codes, const void* a_sc
  * call: x (tokens x k, row stride ld_x) is rounded by row blocks and multiplied
  * with w (codes and scale of muon_fp8_quantize_weight, groups x n x k).  A few
  * tokens of a single weight (offsets NULL) take one launch that streams the
- * weight.  workspace: device, 16-byte aligned; none (NULL) where
- * ..._workspace_bytes (grouped: offsets are given) is 0.
+ * weight.  Rows of out that belong to no group become zero.  workspace: device,
+ * 16-byte aligned; none (NULL) where ..._workspace_bytes (grouped: offsets are
+ * given) is 0.
  */
 MUON_API size_t muon_fp8_linear_workspace_bytes(long long tokens, int n, int k, int grouped);
 MUON_API int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
@@ -419,7 +420,8 @@ MUON_API int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long 
 /*
  * Its gradients: dx = dy W with dy by row blocks (dx NULL: left out), dW_g =
  * dy_g^T x_g with both by col blocks (dw NULL: left out; groups x n x k,
- * contiguous).  dy is read once for both.
+ * contiguous).  dy is read once for both; rows of dx that belong to no group
+ * become zero.
  */
 MUON_API size_t muon_fp8_linear_backward_workspace_bytes(long long tokens, int n, int k, int groups, int need_dx,
                                                          int need_dw);

@@ -844,7 +844,8 @@ def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None,
 def muon_fp8_linear(x, w, *, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x W^T in 8 bits: ``x`` (tokens x k, bf16 or fp32) is rounded to E4M3 by
     row blocks and multiplied with ``w`` (``muon_fp8_quantize_weight``).  With
-    ``offsets``, tokens are sorted by expert and ``w`` is stacked over experts."""
+    ``offsets``, tokens are sorted by expert and ``w`` is stacked over experts;
+    rows of no expert give zero."""
     n, k, groups, optr = _check_weight(w, offsets)
     tokens, _, ld = _check_rows("x", x, _FLOATS, None, k)
     if out_dtype not in _FLOATS:
@@ -863,7 +864,7 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
                              dx_dtype=torch.bfloat16, dw_dtype=torch.bfloat16, stream=None):
     """(dx, dW) of ``muon_fp8_linear`` from dy (tokens x n): dx = dy W with dy by
     row blocks, dW = dy^T x with both by col blocks; either may be left out
-    (None).  dy is read once for both."""
+    (None).  dy is read once for both; rows of no expert give a zero dx."""
     n, k, groups, optr = _check_weight(w, offsets)
     tokens, _, ld_dy = _check_rows("dy", dy, _FLOATS, None, n)
     _, _, ld_x = _check_rows("x", x, _FLOATS, tokens, k)

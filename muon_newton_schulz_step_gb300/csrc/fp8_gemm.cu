@@ -743,6 +743,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             release();
             write(chunk(3), rb);
         }
+        if (MODE != kFp8GradWeight && p.zero_rest) {
+            // rows of no group: before the first group's and behind the last one's
+            const int head = gs.lo[0], tail = gs.lo[p.groups - 1] + gs.cnt[p.groups - 1];
+            const int rest = head + p.n_ext - tail;
+            for (int i = static_cast<int>(blockIdx.x) * 8 + warp - 4; i < rest; i += static_cast<int>(gridDim.x) * 8) {
+                const long long row = i < head ? i : tail + i - head;
+                for (int m = lane; m < p.m_ext; m += 32) {
+                    if (F32) static_cast<float*>(p.out)[row * p.ld + m] = 0.0f;
+                    else static_cast<__nv_bfloat16*>(p.out)[row * p.ld + m] = __float2bfloat16_rn(0.0f);
+                }
+            }
+        }
         if (lane == 0) ptx::bulk_wait_group_all();       // every block written
         __syncwarp();
     }

@@ -311,6 +311,7 @@ struct Fp8GemmParams {
     int groups;               // >= 1
     const int* offsets;       // groups + 1 row offsets, or nullptr: one group of all rows
     int rows;                 // grad weight: tokens
+    int zero_rest;            // forward, grad input: rows of no group become zero
     unsigned long long wait_ns;
 };
 

@@ -288,9 +288,11 @@ int check_linear(int dtype, const char* what, long long tokens, long long ld, in
     return MUON_OK;
 }
 
+// `layer`: a call of a whole layer: the launch before it wrote its codes, and rows of no
+// group become zero.
 int fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes, const void* b_scale,
                 long long tokens, int n, int k, int groups, const int* offsets, void* out, int out_dtype,
-                long long ld_out, bool after, cudaStream_t stream) {
+                long long ld_out, bool layer, cudaStream_t stream) {
     int rc = check_dtype(out_dtype, "out");
     if (rc != MUON_OK) return rc;
     if (product != MUON_FP8_FORWARD && product != MUON_FP8_GRAD_INPUT && product != MUON_FP8_GRAD_WEIGHT)
@@ -332,6 +334,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     p.groups = groups;
     p.offsets = offsets;
     p.rows = static_cast<int>(tokens);
+    p.zero_rest = layer && !gw;
     if (gw) {
         // a: dy's col codes (padded tokens x ldn); b: x's col codes (padded tokens x ldk)
         const long long padded = muon_fp8_padded_rows(tokens, groups);
@@ -357,7 +360,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
-    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, after, stream); });
+    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, layer, stream); });
 }
 
 }  // namespace

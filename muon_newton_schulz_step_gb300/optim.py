@@ -14,7 +14,7 @@ from collections import defaultdict
 
 import torch
 
-from . import muon_adamw_step, muon_step_ex
+from . import muon_adamw_step, muon_grad_clip, muon_step_ex
 
 
 class MuonAdamW(torch.optim.Optimizer):
@@ -23,16 +23,22 @@ class MuonAdamW(torch.optim.Optimizer):
     Parameter groups take ``use_muon`` (default: ``p.ndim == 2``), ``lr``,
     ``momentum``, ``weight_decay``, ``nesterov``, ``ns_steps`` (Muon) and
     ``adamw_lr``, ``betas``, ``eps``, ``adamw_weight_decay`` (AdamW).
+    ``max_grad_norm`` (for all groups together, default none): every step first
+    scales the gradients in place by min(1, max_grad_norm / (norm + 1e-6)), norm
+    their global 2-norm; it is kept in ``grad_norm`` (0-dim CUDA tensor).
     Parameters must be contiguous CUDA tensors in bf16 or fp32 with gradients
     of a supported dtype; those without a gradient are skipped.
     """
 
     def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.1, nesterov=True, ns_steps=5,
-                 adamw_lr=3e-4, betas=(0.9, 0.95), eps=1e-8, adamw_weight_decay=0.0, use_muon=None):
+                 adamw_lr=3e-4, betas=(0.9, 0.95), eps=1e-8, adamw_weight_decay=0.0, use_muon=None,
+                 max_grad_norm=None):
         defaults = dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
                         ns_steps=ns_steps, adamw_lr=adamw_lr, betas=betas, eps=eps,
                         adamw_weight_decay=adamw_weight_decay, use_muon=use_muon)
         super().__init__(params, defaults)
+        self.max_grad_norm = max_grad_norm
+        self.grad_norm = None
 
     @staticmethod
     def _is_muon(group, p):
@@ -45,6 +51,9 @@ class MuonAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if self.max_grad_norm is not None:
+            grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
+            self.grad_norm = muon_grad_clip(grads, self.max_grad_norm)
         for group in self.param_groups:
             muon = defaultdict(list)    # (W dtype, G dtype) -> [(p, grad, momentum)]
             adam = defaultdict(list)    # (P dtype, G dtype) -> [(p, grad, m, v, step)]
