@@ -118,20 +118,26 @@ struct Tile {
 };
 
 // n columns in equal tiles of at most 256, in multiples of `unit`: 32, or the 64
-// columns of the weight gradient's result blocks.
-__device__ __forceinline__ void split_columns(int n, int unit, int& tiles, int& width) {
-    tiles = (n + kTile - 1) / kTile;
+// columns of the weight gradient's result blocks.  `even`: an even number of tiles,
+// for clusters of two pairs; the last may then be empty (its products are not stored).
+__device__ __forceinline__ int column_tiles(int n, bool even) {
+    return even ? (n + 2 * kTile - 1) / (2 * kTile) * 2 : (n + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ void split_columns(int n, int unit, bool even, int& tiles, int& width) {
+    tiles = column_tiles(n, even);
     width = tiles > 0 ? ((n + tiles - 1) / tiles + unit - 1) / unit * unit : unit;
 }
 
 // Tile t of the launch; `g` only moves forward.  Integer divisions are avoided:
 // four of them took 900 cycles of every tile in every role.
+template <int CS>
 __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g) {
     while (t >= gs.tile0[g + 1]) ++g;
     const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
     const int n = gw ? p.n_ext : gs.cnt[g];
-    const int nt = (n + kTile - 1) / kTile, width = gs.width[g];
+    const int nt = column_tiles(n, CS == 4), width = gs.width[g];
     int l = t - gs.tile0[g];
     const int full = nt / kPanel * kPanel;
     int m, c;
@@ -150,9 +156,9 @@ __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups
     x.g = g;
     x.m0 = m * kTile;
     const int off = c * width;
-    x.cols = n - off < width ? n - off : width;
+    x.cols = max(0, n - off < width ? n - off : width);
     const int unit = gw ? 64 : 32;
-    x.width = (x.cols + unit - 1) / unit * unit;
+    x.width = max(unit, (x.cols + unit - 1) / unit * unit);
     x.c0 = gw ? off : gs.lo[g] + off;
     x.kb0 = gw ? gs.block0[g] : 0;
     x.nkb = gw ? (gs.cnt[g] + kFp8Block - 1) / kFp8Block : p.kblocks;
@@ -246,9 +252,11 @@ struct ScaleGroup<kFp8GradWeight> {
     }
 };
 
-template <int MODE, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
+// CS: CTAs per cluster, 2 (one pair) or 4 (two pairs with neighbouring column tiles
+// of the same rows, which share the A operand by multicast).
+template <int MODE, bool F32, int CS>
+__global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
+    static_assert(CS == 2 || (CS == 4 && MODE != kFp8GradWeight), "cluster size");
     constexpr int kStages = Ring<MODE>::stages;
     constexpr uint32_t kEpiBytes = Ring<MODE>::block;
     constexpr bool kAMn = MODE != kFp8Forward;          // A operand MN-major
@@ -265,16 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     volatile int* abort = &b.abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t crank = ptx::cluster_ctarank();
+    const uint32_t rank = crank & 1u, lead = crank & ~1u;   // in the pair; cluster rank of the pair's leader
+    const int pp = static_cast<int>(crank >> 1);            // pair in the cluster
     const bool leader = rank == 0;
-    const int pair = static_cast<int>(ptx::cluster_id_x());
-    const int npairs = static_cast<int>(ptx::num_clusters_x());
+    const int pair = static_cast<int>(ptx::cluster_id_x()) * (CS / 2) + pp;
+    const int npairs = static_cast<int>(ptx::num_clusters_x()) * (CS / 2);
     const uint64_t limit = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
 
     if (threadIdx.x == 32) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&b.full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.empty[s]), CS / 2);   // every pair that reads the stage
         }
         for (int s = 0; s < kScaleStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&b.sfull[s]), 2);
@@ -300,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const GroupSpan sp = warp_group_spans(p.offsets, p.groups, rows, g0, low);
             const int g = g0 + lane;
             int nt, width;
-            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, MODE == kFp8GradWeight ? 64 : 32, nt, width);
+            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, MODE == kFp8GradWeight ? 64 : 32, CS == 4, nt, width);
             const int n = g < p.groups ? nt * mt : 0;
             const int nb = (sp.cnt + kFp8Block - 1) / kFp8Block;
             const int it = warp_inclusive_sum(n), ib = warp_inclusive_sum(nb);
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs) {
-                const Tile x = decode_tile(p, gs, t, g);
+                const Tile x = decode_tile<CS>(p, gs, t, g);
                 const int m = x.m0 + static_cast<int>(rank) * kHalf;
                 const int half = x.width / 2;
                 const int c = x.c0 + static_cast<int>(rank) * half;
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         break;
                     }
                     const uint32_t local = ptx::smem_addr(&b.full[stage]);
-                    const uint32_t fb = ptx::mapa_shared(local, 0);
+                    const uint32_t fb = ptx::mapa_shared(local, lead);
                     if (leader) {
                         armed |= 1u << stage;
                         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -363,8 +373,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (leader) ptx::mbar_arrive_expect_tx(local, bytes);
                         const uint32_t di = ptx::smem_addr(sm_a + stage * kStageA);
                         const uint32_t d_o = ptx::smem_addr(sm_b + stage * kStageB);
-                        if (kAMn) ptx::tma_load_3d_pair(di, &p.tm_a, fb, m, kb * kFp8Block, gb);
-                        else ptx::tma_load_3d_pair(di, &p.tm_a, fb, kb * kFp8Block, m, gb);
+                        if constexpr (CS == 4) {
+                            // half of this CTA's A tile, for itself and its counterpart in the other pair
+                            const uint16_t mask = static_cast<uint16_t>((1u << rank) | (1u << (2u + rank)));
+                            const int h = pp * (kHalf / 2);
+                            ptx::tma_load_3d_pair_mc(di + pp * (kStageA / 2), &p.tm_a, fb, kAMn ? m : kb * kFp8Block,
+                                                     kAMn ? kb * kFp8Block + h : m + h, gb, mask);
+                        } else if (kAMn) {
+                            ptx::tma_load_3d_pair(di, &p.tm_a, fb, m, kb * kFp8Block, gb);
+                        } else {
+                            ptx::tma_load_3d_pair(di, &p.tm_a, fb, kb * kFp8Block, m, gb);
+                        }
                         if (kBMn) {
                             ptx::tma_load_3d_pair(d_o, &p.tm_b, fb, c & ~15, kb * kFp8Block, 0);
                         } else if (whole) {
@@ -400,11 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // next 32 elements of K: 32 bytes of a row (K-major) or 32 rows of 128 bytes (MN-major)
             constexpr uint64_t a_k = (kAMn ? 4096 : 32) >> 4;
             constexpr uint64_t b_k = (kBMn ? 4096 : 32) >> 4;
+            const uint16_t mine = static_cast<uint16_t>(0x3u << lead);
             int stage = 0, sstage = 0, it = 0, g = 0;
             uint32_t phase = 0, sphase = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs, ++it) {
-                const Tile x = decode_tile(p, gs, t, g);
+                const Tile x = decode_tile<CS>(p, gs, t, g);
                 const int acc = it & 1;
                 const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
                 // The copy of four blocks' scale words is issued a block before the first
@@ -420,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         ptx::tmem_copy_scales_pair(dst, ptx::sdesc_rows16(src));
                         ptx::tmem_copy_scales_pair(dst + 4, ptx::sdesc_rows16(src + 512));
                         if (x.width > 128) ptx::tmem_copy_scales_pair(dst + 8, ptx::sdesc_rows16(src + 1024));
-                        ptx::mma_commit_pair(ptx::smem_addr(&b.sempty[sstage]), 0x3u);
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.sempty[sstage]), mine);
                     }
                     __syncwarp();
                     if (++sstage == kScaleStages) {
@@ -463,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfa + 4,
                                                (kk != 0 || kb != x.kb0) ? 1u : 0u);
-                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), 0x3u);
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), CS == 4 ? 0xFu : 0x3u);
                     }
                     __syncwarp();
                     if (++stage == kStages) {
@@ -472,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 if (!ok) break;
-                if (ptx::elect_one()) ptx::mma_commit_pair(ptx::smem_addr(&b.tfull[acc]), 0x3u);
+                if (ptx::elect_one()) ptx::mma_commit_pair(ptx::smem_addr(&b.tfull[acc]), mine);
                 __syncwarp();
             }
         }
@@ -495,11 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             w.store(s_sc + st * kScaleBytes, lane);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[st]), 0));
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&b.sfull[st]), lead));
             return true;
         };
         for (int t = pair; ok && t < tiles; t += npairs) {
-            const Tile x = decode_tile(p, gs, t, g);
+            const Tile x = decode_tile<CS>(p, gs, t, g);
             const int m = x.m0 + static_cast<int>(rank) * kHalf;
             for (int i = 0; ok && i < x.nkb; i += 4, ++seq) {
                 if ((seq & 1) != warp - 2) continue;
@@ -533,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint8_t* const stage = s_epi + (warp - 4) * Ring<MODE>::blocks * kEpiBytes;
         int it = 0, g = 0, nbuf = 0;            // tiles, group, blocks on their way so far
         for (int t = pair; t < tiles; t += npairs, ++it) {
-            const Tile x = decode_tile(p, gs, t, g);
+            const Tile x = decode_tile<CS>(p, gs, t, g);
             const int acc = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
             const int m0 = x.m0 + static_cast<int>(rank) * kHalf + q * 32;
@@ -546,12 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             auto release_shared = [&] {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.shared_free[acc]), lead));
             };
             auto release = [&] {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_addr(&b.tempty[acc]), lead));
             };
             // no sleep between polls: the next tile's products wait for the first chunk
             if (!ptx::wait_parity_cluster(ptx::smem_addr(&b.tfull[acc]), use, abort, limit)) {
@@ -775,43 +795,94 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
-template <int MODE, bool F32>
-cudaError_t run(const Fp8GemmParams& p, int pairs, bool after, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int MODE, bool F32, int CS>
+cudaError_t run(const Fp8GemmParams& p, int clusters, bool after, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs);
+    cfg.gridDim = dim3(CS * clusters);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<MODE>();
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CS;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = after ? 1 : 0;
-    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32>, p);
+    cfg.numAttrs = after ? 2 : 1;
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, CS>, p);
     return l != cudaSuccess ? l : cudaGetLastError();
 }
 
-template <int MODE>
-cudaError_t run(const Fp8GemmParams& p, int pairs, bool after, cudaStream_t s) {
-    return p.out_f32 ? run<MODE, true>(p, pairs, after, s) : run<MODE, false>(p, pairs, after, s);
+template <int MODE, int CS>
+cudaError_t run(const Fp8GemmParams& p, int clusters, bool after, cudaStream_t s) {
+    return p.out_f32 ? run<MODE, true, CS>(p, clusters, after, s) : run<MODE, false, CS>(p, clusters, after, s);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, bool after, cudaStream_t s) {
+// Whether clusters of two pairs serve a product: one weight that many column tiles
+// share, a long reduction, and no wave of tiles more than pairs need (a wave of
+// clusters takes 0.95 of one of pairs).  Measured, pairs against clusters:
+// 8192 x 6144 x 6144 185 against 176 us, 2048 x 6144 x 6144 57.4 against 55.4; but
+// 9728 x 4096 x 6144 (8 waves of 76 pairs, 9 of 36 clusters) 139 against 143,
+// 4096 x 6144 x 512 24.5 against 26.6, 8192 x 1024 x 1024 18.5 against 19.9, and weights
+// of 8 to 96 experts 3 to 12 % slower (two pairs hold half as many different weight
+// bytes on their way).
+bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
+                        int clusters4) {
+    if (clusters4 < 1 || mode == kFp8GradWeight || groups != 1 || kblocks < 16) return false;
+    const long long mt = (m_ext + kTile - 1) / kTile;
+    const long long pairs = mt * ((tokens + kTile - 1) / kTile), fours = mt * ((tokens + 2 * kTile - 1) / (2 * kTile));
+    const long long waves2 = (pairs + sms / 2 - 1) / (sms / 2), waves4 = (fours + clusters4 - 1) / clusters4;
+    return fours >= clusters4 && 95 * waves4 < 100 * waves2;
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, bool after, cudaStream_t s) {
     const long long mt = (p.m_ext + kTile - 1) / kTile;
+    if (p.multicast) {
+        return p.mode == kFp8Forward ? run<kFp8Forward, 4>(p, clusters4, after, s)
+                                     : run<kFp8GradInput, 4>(p, clusters4, after, s);
+    }
     const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
                                                   : p.n_ext / kTile + p.groups;
     const long long most = mt * nt;
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {
-        case kFp8Forward: return run<kFp8Forward>(p, pairs, after, s);
-        case kFp8GradInput: return run<kFp8GradInput>(p, pairs, after, s);
-        default: return run<kFp8GradWeight>(p, pairs, after, s);
+        case kFp8Forward: return run<kFp8Forward, 2>(p, pairs, after, s);
+        case kFp8GradInput: return run<kFp8GradInput, 2>(p, pairs, after, s);
+        default: return run<kFp8GradWeight, 2>(p, pairs, after, s);
     }
+}
+
+// Clusters of four CTAs that the current device holds at once (0: none).
+int fp8_gemm_clusters4() {
+    if (cudaFuncSetAttribute(k_fp8_gemm<kFp8Forward, false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<kFp8Forward>())) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<kFp8Forward>();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 4;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_fp8_gemm<kFp8Forward, false, 4>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 cudaError_t read_and_clear_fp8_error(int* code) {

@@ -303,6 +303,7 @@ struct Fp8GemmParams {
     long long ld;
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
+    int multicast;            // forward, grad input: clusters of two pairs share A (tm_a: boxes of 64)
     int out_f32;
     int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only)
     int m_ext;                // extent along the MMA's rows: n (forward, grad weight), k (grad input)
@@ -316,7 +317,10 @@ struct Fp8GemmParams {
 };
 
 // `after`: the launch before it on the stream wrote its operands and let it start early.
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, bool after, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, bool after, cudaStream_t s);
+int fp8_gemm_clusters4();
+bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
+                        int clusters4);
 
 // The forward product of few tokens and one weight, x rounded on the way.
 struct Fp8TokenParams {
@@ -378,7 +382,7 @@ int set_last_error(int status, const char* msg);
 
 // What the operators around the step (train_abi.cu) share with it.
 enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpFp8Token, kOpEnd };
-int op_device(int* sms);                       // the current device, checked; its SM count
+int op_device(int* sms, int* clusters4 = nullptr);   // the current device, checked; its SMs, clusters of four CTAs
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
 int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
                     int box_inner, int box_outer);

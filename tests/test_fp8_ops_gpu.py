@@ -364,3 +364,66 @@ def test_refusals():
         mg.muon_fp8_quantize(x.t())
     with pytest.raises(ValueError, match="dy"):
         mg.muon_fp8_linear_backward(x, x, w)
+
+
+def dequantized(m):
+    """What an Fp8Matrix ("row" or "block") stands for, in 64 bits on the device."""
+    if m.kind == "row":
+        t = m.codes.shape[0]
+        return torch.ldexp(m.codes.double().view(t, -1, 128), (m.scale.t().int() - 127).unsqueeze(-1)).view(t, -1)[:, :m.cols]
+    e = (m.scale.int() - 127).repeat_interleave(128, -2).repeat_interleave(128, -1)
+    return torch.ldexp(m.codes.double(), e[..., :m.codes.shape[-2], :])[..., :m.cols]
+
+
+@pytest.mark.parametrize("offsets", [None, [0, 700, 700, 1301, 2600], [0, 30, 2560, 2600], [0, 1024, 1500, 2500],
+                                     [7, 520, 1033, 2599]])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_many_tiles_of_large_groups(offsets, out):
+    """Sizes at which two pairs of SMs share the weight's tiles: uneven, empty and
+    small groups, column tiles that come out empty, rows and columns past the end."""
+    t, inner, red = 2600, 3001, 640
+    g = 1 if offsets is None else len(offsets) - 1
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(31)
+    spread = torch.exp2(torch.randint(-6, 7, (t, 1), generator=gen, device=DEV).float())
+    x = (torch.randn(t, red, generator=gen, device=DEV) * spread).to(BF)
+    q, _ = mg.muon_fp8_quantize(x)
+    xv = dequantized(q)
+    for product, shape in (("forward", (inner, red)), ("grad_input", (red, inner))):
+        w = torch.randn(g, *shape, generator=gen, device=DEV)
+        m = mg.muon_fp8_quantize_weight(w if offsets is not None else w[0])
+        wv = dequantized(m)
+        y = torch.full((t, inner), 55.0, dtype=out, device=DEV)
+        mg.muon_fp8_product(product, q, m, offsets=off, out=y)
+        for i, (lo, hi) in enumerate(bounds_of(offsets, t)):
+            b = wv if offsets is None else wv[i]
+            b = b.t() if product == "forward" else b
+            ref = xv[lo:hi] @ b
+            tol = red * 2.0 ** -23 * (xv[lo:hi].abs() @ b.abs()) + (2.0 ** -8 if out == BF else 2.0 ** -23) * ref.abs()
+            assert bool(((y[lo:hi].double() - ref).abs() <= tol).all()), (product, i)
+        if offsets is not None:
+            assert bool((y[:offsets[0]] == 55.0).all()) and bool((y[offsets[-1]:] == 55.0).all())
+    assert mg.muon_device_status() == 0
+
+
+@pytest.mark.parametrize("t,inner,red", [(4100, 2500, 2100), (2500, 4611, 2048)])
+def test_one_weight_shared_by_many_tiles(t, inner, red):
+    """One weight, many column tiles and a long reduction: clusters of two pairs of
+    SMs, with an odd number of full column tiles and edges in every direction."""
+    gen = torch.Generator(device=DEV).manual_seed(t)
+    x = torch.randn(t, red, generator=gen, device=DEV).to(BF)
+    q, _ = mg.muon_fp8_quantize(x)
+    xv = dequantized(q)
+    for product, shape in (("forward", (inner, red)), ("grad_input", (red, inner))):
+        m = mg.muon_fp8_quantize_weight(torch.randn(*shape, generator=gen, device=DEV))
+        b = dequantized(m).t() if product == "forward" else dequantized(m)
+        for off in (None, torch.tensor([100, t - 77], dtype=torch.int32, device=DEV)):
+            lo, hi = (0, t) if off is None else (100, t - 77)
+            w = m if off is None else mg.Fp8Matrix(m.codes[None], m.scale[None], "block", m.cols)
+            y = torch.full((t, inner), 55.0, dtype=F32, device=DEV)
+            mg.muon_fp8_product(product, q, w, offsets=off, out=y)
+            ref = xv[lo:hi] @ b
+            tol = red * 2.0 ** -23 * (xv[lo:hi].abs() @ b.abs()) + 2.0 ** -23 * ref.abs()
+            assert bool(((y[lo:hi].double() - ref).abs() <= tol).all()), product
+            assert bool((y[:lo] == 55.0).all()) and bool((y[hi:] == 55.0).all())
+    assert mg.muon_device_status() == 0
