@@ -339,8 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     ptx::tc_fence_after();
     const uint32_t tmem = b.tmem;
     const int tiles = b.tiles;
-    // everything so far may run while the launch before drains; its codes are read from here on
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Everything so far may run while the launch before drains.  It wrote the codes, and
+    // they are read from here on; or (kSyncLate) it is the layer's other product, which
+    // itself began after the codes were complete and let this launch start only then:
+    // both run side by side, and this one ends after the other.
+    if (p.sync != kSyncLate) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0) {
         // ------------------------------------------------------ producer --
@@ -779,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         __syncwarp();
     }
 
+    if (p.sync == kSyncLate) asm volatile("griddepcontrol.wait;" ::: "memory");
     ptx::tc_fence_before();
     __syncthreads();
     ptx::cluster_sync();   // no CTA leaves while its peer may still signal its barriers
@@ -796,7 +801,7 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
 template <int MODE, bool F32, int CS>
-cudaError_t run(const Fp8GemmParams& p, int clusters, bool after, cudaStream_t s) {
+cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
@@ -813,14 +818,14 @@ cudaError_t run(const Fp8GemmParams& p, int clusters, bool after, cudaStream_t s
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = after ? 2 : 1;
+    cfg.numAttrs = p.sync != kSyncNone ? 2 : 1;
     const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, CS>, p);
     return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 template <int MODE, int CS>
-cudaError_t run(const Fp8GemmParams& p, int clusters, bool after, cudaStream_t s) {
-    return p.out_f32 ? run<MODE, true, CS>(p, clusters, after, s) : run<MODE, false, CS>(p, clusters, after, s);
+cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
+    return p.out_f32 ? run<MODE, true, CS>(p, clusters, s) : run<MODE, false, CS>(p, clusters, s);
 }
 
 }  // namespace
@@ -842,20 +847,20 @@ bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long k
     return fours >= clusters4 && 95 * waves4 < 100 * waves2;
 }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, bool after, cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s) {
     const long long mt = (p.m_ext + kTile - 1) / kTile;
     if (p.multicast) {
-        return p.mode == kFp8Forward ? run<kFp8Forward, 4>(p, clusters4, after, s)
-                                     : run<kFp8GradInput, 4>(p, clusters4, after, s);
+        return p.mode == kFp8Forward ? run<kFp8Forward, 4>(p, clusters4, s)
+                                     : run<kFp8GradInput, 4>(p, clusters4, s);
     }
     const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
                                                   : p.n_ext / kTile + p.groups;
     const long long most = mt * nt;
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {
-        case kFp8Forward: return run<kFp8Forward, 2>(p, pairs, after, s);
-        case kFp8GradInput: return run<kFp8GradInput, 2>(p, pairs, after, s);
-        default: return run<kFp8GradWeight, 2>(p, pairs, after, s);
+        case kFp8Forward: return run<kFp8Forward, 2>(p, pairs, s);
+        case kFp8GradInput: return run<kFp8GradInput, 2>(p, pairs, s);
+        default: return run<kFp8GradWeight, 2>(p, pairs, s);
     }
 }
 

@@ -381,16 +381,12 @@ __device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Ra
     // thread's last read here
 }
 
-// VEC: rows start on 16 bytes.
+// The tiles of one block of threads.  VEC: rows start on 16 bytes.
 template <bool BF16, bool ROW, bool COL, bool BLK, bool VEC>
-__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const __grid_constant__ QuantParams p) {
-    __shared__ Tile sh;
-    __shared__ RowBlock rb;
-    __shared__ int offsets[COL ? kFp8MaxGroups + 1 : 1];
-    asm volatile("griddepcontrol.launch_dependents;");   // the product's set-up may overlap; it waits for the codes
+__device__ __forceinline__ void quantize(const QuantParams& p, Tile& sh, RowBlock& rb, int* offsets, long long batch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cg = lane & 15, half = lane >> 4;
-    const long long batch = blockIdx.z, colblocks = p.ldq >> 7;
+    const long long colblocks = p.ldq >> 7;
     const char* base = static_cast<const char*>(p.x) + batch * p.ldb * (BF16 ? 2 : 4);
     if (COL && p.groups > 0) {
         for (int g = threadIdx.x; g <= p.groups; g += kThreads) offsets[g] = p.offsets[g];
@@ -455,15 +451,49 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const _
     }
 }
 
-template <bool BF16, bool VEC>
-cudaError_t run(const QuantParams& p, cudaStream_t s) {
-    // several tiles of a row block per block of threads where there are enough of
-    // both: finding a group's row block costs about as much as half a tile
+template <bool BF16, bool ROW, bool COL, bool BLK, bool VEC>
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) k_fp8_quantize(const __grid_constant__ QuantParams p) {
+    __shared__ Tile sh;
+    __shared__ RowBlock rb;
+    __shared__ int offsets[COL ? kFp8MaxGroups + 1 : 1];
+    asm volatile("griddepcontrol.launch_dependents;");   // the product's set-up may overlap; it waits for the codes
+    quantize<BF16, ROW, COL, BLK, VEC>(p, sh, rb, offsets, blockIdx.z);
+}
+
+// Two matrices: blockIdx.z 0 takes the first (row and col codes, or col codes
+// alone), 1 the second's col codes.
+template <bool BF16, bool ROW, bool VEC>
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2)
+    k_fp8_quantize_pair(const __grid_constant__ QuantParams p, const __grid_constant__ QuantParams q) {
+    __shared__ Tile sh;
+    __shared__ RowBlock rb;
+    __shared__ int offsets[kFp8MaxGroups + 1];
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.z == 0) quantize<BF16, ROW, true, false, VEC>(p, sh, rb, offsets, 0);
+    else quantize<BF16, false, true, false, VEC>(q, sh, rb, offsets, 0);
+}
+
+// Several tiles of a row block per block of threads where there are enough of
+// both: finding a group's row block costs about as much as half a tile.
+dim3 quantize_grid(const QuantParams& p) {
     const long long colblocks = p.ldq / 128;
     const long long share = p.groups > 0 && colblocks * p.row_blocks > 4096 ? 4 : 1;
-    const dim3 grid(static_cast<unsigned>((colblocks + share - 1) / share),
-                    static_cast<unsigned>(p.row_blocks < 65535 ? p.row_blocks : 65535),
-                    static_cast<unsigned>(p.batch));
+    return dim3(static_cast<unsigned>((colblocks + share - 1) / share),
+                static_cast<unsigned>(p.row_blocks < 65535 ? p.row_blocks : 65535), static_cast<unsigned>(p.batch));
+}
+
+template <bool BF16, bool VEC>
+cudaError_t run_pair(const QuantParams& p, const QuantParams& q, cudaStream_t s) {
+    const dim3 a = quantize_grid(p), b = quantize_grid(q);
+    const dim3 grid(a.x > b.x ? a.x : b.x, a.y > b.y ? a.y : b.y, 2);
+    if (p.row_q != nullptr) k_fp8_quantize_pair<BF16, true, VEC><<<grid, kThreads, 0, s>>>(p, q);
+    else k_fp8_quantize_pair<BF16, false, VEC><<<grid, kThreads, 0, s>>>(p, q);
+    return cudaGetLastError();
+}
+
+template <bool BF16, bool VEC>
+cudaError_t run(const QuantParams& p, cudaStream_t s) {
+    const dim3 grid = quantize_grid(p);
     if (p.blk_q != nullptr) k_fp8_quantize<BF16, false, false, true, VEC><<<grid, kThreads, 0, s>>>(p);
     else if (p.row_q != nullptr && p.col_q != nullptr)
         k_fp8_quantize<BF16, true, true, false, VEC><<<grid, kThreads, 0, s>>>(p);
@@ -477,6 +507,15 @@ cudaError_t run(const QuantParams& p, cudaStream_t s) {
 cudaError_t launch_fp8_quantize(const QuantParams& p, cudaStream_t s) {
     if (p.bf16) return p.vec ? run<true, true>(p, s) : run<true, false>(p, s);
     return p.vec ? run<false, true>(p, s) : run<false, false>(p, s);
+}
+
+bool fp8_quantize_pairs(const QuantParams& p, const QuantParams& q) {
+    return p.bf16 == q.bf16 && p.vec == q.vec && p.col_q != nullptr && q.col_q != nullptr && q.row_q == nullptr;
+}
+
+cudaError_t launch_fp8_quantize_pair(const QuantParams& p, const QuantParams& q, cudaStream_t s) {
+    if (p.bf16) return p.vec ? run_pair<true, true>(p, q, s) : run_pair<true, false>(p, q, s);
+    return p.vec ? run_pair<false, true>(p, q, s) : run_pair<false, false>(p, q, s);
 }
 
 }  // namespace muon

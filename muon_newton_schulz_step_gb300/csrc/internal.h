@@ -276,12 +276,23 @@ struct QuantParams {
     long long row_blocks;     // grid bound of 128-row blocks (per matrix)
 };
 
+// Two matrices with the same element type and row alignment in one launch: p as
+// launch_fp8_quantize, q's col blocks only.
+bool fp8_quantize_pairs(const QuantParams& p, const QuantParams& q);
+cudaError_t launch_fp8_quantize_pair(const QuantParams& p, const QuantParams& q, cudaStream_t s);
 cudaError_t launch_fp8_quantize(const QuantParams& p, cudaStream_t s);
 
 enum Fp8Mode : int {
     kFp8Forward = 0,          // tokens grouped; the weight of group g K-major
     kFp8GradInput = 1,        // tokens grouped; the weight of group g MN-major
     kFp8GradWeight = 2        // reduction grouped; both operands MN-major
+};
+
+// How a product's launch follows the one before it on the stream.
+enum Fp8Sync : int {
+    kSyncNone = 0,            // when that has ended
+    kSyncEarly = 1,           // set-up overlaps it, then waits: it wrote the operands
+    kSyncLate = 2             // beside it: it is a product that began after the operands were complete
 };
 
 // Scale bytes of one operand: byte (index, reduction block) of batch g at
@@ -303,6 +314,7 @@ struct Fp8GemmParams {
     long long ld;
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
+    int sync;                 // Fp8Sync
     int multicast;            // forward, grad input: clusters of two pairs share A (tm_a: boxes of 64)
     int out_f32;
     int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only)
@@ -316,8 +328,7 @@ struct Fp8GemmParams {
     unsigned long long wait_ns;
 };
 
-// `after`: the launch before it on the stream wrote its operands and let it start early.
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, bool after, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s);
 int fp8_gemm_clusters4();
 bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
                         int clusters4);

@@ -246,6 +246,30 @@ int check_dim(long long n, const char* what) {
 
 long long up128(long long n) { return (n + 127) / 128 * 128; }
 
+QuantParams quantize_params(const void* x, int dtype, long long rows, long long cols, long long ld, int groups,
+                            const int* offsets, void* row_codes, void* row_scale, void* col_codes, void* col_scale) {
+    QuantParams p = {};
+    p.x = x;
+    p.rows = rows;
+    p.cols = cols;
+    p.ld = ld;
+    p.x_end = static_cast<const char*>(x) + ((rows - 1) * ld + cols) * static_cast<long long>(dtype_size(dtype));
+    p.batch = 1;
+    p.bf16 = dtype == MUON_BF16;
+    p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * static_cast<long long>(dtype_size(dtype)) % 16 == 0;
+    p.row_q = static_cast<uint8_t*>(row_codes);
+    p.row_scale = static_cast<uint8_t*>(row_scale);
+    p.col_q = static_cast<uint8_t*>(col_codes);
+    p.col_scale = static_cast<uint8_t*>(col_scale);
+    p.ldq = up128(cols);
+    // groups matter to the col blocks alone
+    const bool grouped = offsets != nullptr && col_codes != nullptr;
+    p.groups = grouped ? groups : 0;
+    p.offsets = grouped ? offsets : nullptr;
+    p.row_blocks = grouped ? muon_fp8_padded_rows(rows, groups) / 128 : (rows + 127) / 128;
+    return p;
+}
+
 // Codes of one matrix in a workspace: codes, then scales, each from a multiple of 256 bytes on.
 size_t up256(long long n) { return static_cast<size_t>((n + 255) / 256 * 256); }
 
@@ -288,11 +312,10 @@ int check_linear(int dtype, const char* what, long long tokens, long long ld, in
     return MUON_OK;
 }
 
-// `layer`: a call of a whole layer: the launch before it wrote its codes, and rows of no
-// group become zero.
+// `sync` (Fp8Sync) other than none: one of a whole layer's calls; rows of no group become zero.
 int fp8_product(int product, const void* a_codes, const void* a_scale, const void* b_codes, const void* b_scale,
                 long long tokens, int n, int k, int groups, const int* offsets, void* out, int out_dtype,
-                long long ld_out, bool layer, cudaStream_t stream) {
+                long long ld_out, int sync, cudaStream_t stream) {
     int rc = check_dtype(out_dtype, "out");
     if (rc != MUON_OK) return rc;
     if (product != MUON_FP8_FORWARD && product != MUON_FP8_GRAD_INPUT && product != MUON_FP8_GRAD_WEIGHT)
@@ -334,7 +357,8 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     p.groups = groups;
     p.offsets = offsets;
     p.rows = static_cast<int>(tokens);
-    p.zero_rest = layer && !gw;
+    p.sync = sync;
+    p.zero_rest = sync != kSyncNone && !gw;
     if (gw) {
         // a: dy's col codes (padded tokens x ldn); b: x's col codes (padded tokens x ldk)
         const long long padded = muon_fp8_padded_rows(tokens, groups);
@@ -361,7 +385,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
-    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, clusters4, layer, stream); });
+    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, clusters4, stream); });
 }
 
 }  // namespace
@@ -470,25 +494,7 @@ int muon_fp8_quantize(const void* x, int dtype, long long rows, long long cols, 
     if (col_codes != nullptr && (rc = check_align(col_codes, 16, "col_codes")) != MUON_OK) return rc;
     int sms = 0;
     if ((rc = op_device(&sms)) != MUON_OK) return rc;
-    QuantParams p = {};
-    p.x = x;
-    p.rows = rows;
-    p.cols = cols;
-    p.ld = ld;
-    p.x_end = static_cast<const char*>(x) + ((rows - 1) * ld + cols) * static_cast<long long>(dtype_size(dtype));
-    p.batch = 1;
-    p.bf16 = dtype == MUON_BF16;
-    p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * static_cast<long long>(dtype_size(dtype)) % 16 == 0;
-    p.row_q = static_cast<uint8_t*>(row_codes);
-    p.row_scale = static_cast<uint8_t*>(row_scale);
-    p.col_q = static_cast<uint8_t*>(col_codes);
-    p.col_scale = static_cast<uint8_t*>(col_scale);
-    p.ldq = up128(cols);
-    // groups matter to the col blocks alone
-    const bool grouped = offsets != nullptr && col_codes != nullptr;
-    p.groups = grouped ? groups : 0;
-    p.offsets = grouped ? offsets : nullptr;
-    p.row_blocks = grouped ? muon_fp8_padded_rows(rows, groups) / 128 : (rows + 127) / 128;
+    const QuantParams p = quantize_params(x, dtype, rows, cols, ld, groups, offsets, row_codes, row_scale, col_codes, col_scale);
     const double n = static_cast<double>(rows) * cols;
     const double bytes = n * (dtype_size(dtype) + (row_codes != nullptr) + (col_codes != nullptr));
     return op_launch(kOpFp8Quantize, 0.0, bytes, stream, [&] { return launch_fp8_quantize(p, stream); });
@@ -529,7 +535,7 @@ int muon_fp8_product(int product, const void* a_codes, const void* a_scale, cons
                      long long tokens, int n, int k, int groups, const int* offsets, void* out, int out_dtype,
                      long long ld_out, cudaStream_t stream) {
     return fp8_product(product, a_codes, a_scale, b_codes, b_scale, tokens, n, k, groups, offsets, out, out_dtype, ld_out,
-                       false, stream);
+                       kSyncNone, stream);
 }
 
 size_t muon_fp8_linear_workspace_bytes(long long tokens, int n, int k, int grouped) {
@@ -572,7 +578,7 @@ int muon_fp8_linear(const void* x, int x_dtype, long long tokens, long long ld_x
     rc = muon_fp8_quantize(x, x_dtype, tokens, k, ld_x, 1, nullptr, q.codes, q.scale, nullptr, nullptr, stream);
     if (rc != MUON_OK) return rc;
     return fp8_product(MUON_FP8_FORWARD, q.codes, q.scale, w_codes, w_scale, tokens, n, k, groups, offsets, out, out_dtype,
-                       ld_out, true, stream);
+                       ld_out, kSyncEarly, stream);
 }
 
 size_t muon_fp8_linear_backward_workspace_bytes(long long tokens, int n, int k, int groups, int need_dx, int need_dw) {
@@ -604,9 +610,11 @@ int muon_fp8_linear_backward(const void* dy, int dy_dtype, long long ld_dy, cons
     if (tokens == 0) {
         if (dw == nullptr) return MUON_OK;
         return fp8_product(MUON_FP8_GRAD_WEIGHT, nullptr, nullptr, nullptr, nullptr, 0, n, k, groups, offsets, dw, dw_dtype,
-                           k, false, stream);
+                           k, kSyncNone, stream);
     }
     if ((rc = check_align(dy, dtype_size(dy_dtype), "dy")) != MUON_OK) return rc;
+    int sms = 0;
+    if ((rc = op_device(&sms)) != MUON_OK) return rc;
     const size_t need = muon_fp8_linear_backward_workspace_bytes(tokens, n, k, groups, dx != nullptr, dw != nullptr);
     if ((rc = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return rc;
     char* at = static_cast<char*>(workspace);
@@ -614,21 +622,34 @@ int muon_fp8_linear_backward(const void* dy, int dy_dtype, long long ld_dy, cons
     if (dx != nullptr) at += r.bytes();
     const ColCodes c(dw != nullptr ? at : nullptr, tokens, n, groups);
     if (dw != nullptr) at += c.bytes();
-    rc = muon_fp8_quantize(dy, dy_dtype, tokens, n, ld_dy, groups, offsets, r.codes, r.scale, c.codes, c.scale, stream);
+    if (dw == nullptr) {
+        rc = muon_fp8_quantize(dy, dy_dtype, tokens, n, ld_dy, groups, offsets, r.codes, r.scale, nullptr, nullptr, stream);
+        if (rc != MUON_OK) return rc;
+        return fp8_product(MUON_FP8_GRAD_INPUT, r.codes, r.scale, w_codes, w_scale, tokens, n, k, groups, offsets, dx,
+                           dx_dtype, ld_dx, kSyncEarly, stream);
+    }
+    const ColCodes xc(at, tokens, k, groups);
+    const QuantParams pd = quantize_params(dy, dy_dtype, tokens, n, ld_dy, groups, offsets, r.codes, r.scale, c.codes, c.scale);
+    const QuantParams px = quantize_params(x, x_dtype, tokens, k, ld_x, groups, offsets, nullptr, nullptr, xc.codes, xc.scale);
+    const double t = static_cast<double>(tokens);
+    const double dy_bytes = t * n * (dtype_size(dy_dtype) + 1.0 + (dx != nullptr)), x_bytes = t * k * (dtype_size(x_dtype) + 1.0);
+    if (fp8_quantize_pairs(pd, px)) {
+        rc = op_launch(kOpFp8Quantize, 0.0, dy_bytes + x_bytes, stream,
+                       [&] { return launch_fp8_quantize_pair(pd, px, stream); });
+    } else {
+        rc = op_launch(kOpFp8Quantize, 0.0, dy_bytes, stream, [&] { return launch_fp8_quantize(pd, stream); });
+        if (rc == MUON_OK)
+            rc = op_launch(kOpFp8Quantize, 0.0, x_bytes, stream, [&] { return launch_fp8_quantize(px, stream); });
+    }
     if (rc != MUON_OK) return rc;
+    // both products need the codes alone: the second may run beside the first
     if (dx != nullptr) {
         rc = fp8_product(MUON_FP8_GRAD_INPUT, r.codes, r.scale, w_codes, w_scale, tokens, n, k, groups, offsets, dx, dx_dtype,
-                         ld_dx, true, stream);
+                         ld_dx, kSyncEarly, stream);
         if (rc != MUON_OK) return rc;
     }
-    if (dw != nullptr) {
-        const ColCodes xc(at, tokens, k, groups);
-        rc = muon_fp8_quantize(x, x_dtype, tokens, k, ld_x, groups, offsets, nullptr, nullptr, xc.codes, xc.scale, stream);
-        if (rc != MUON_OK) return rc;
-        rc = fp8_product(MUON_FP8_GRAD_WEIGHT, c.codes, c.scale, xc.codes, xc.scale, tokens, n, k, groups, offsets, dw,
-                         dw_dtype, k, true, stream);
-    }
-    return rc;
+    return fp8_product(MUON_FP8_GRAD_WEIGHT, c.codes, c.scale, xc.codes, xc.scale, tokens, n, k, groups, offsets, dw, dw_dtype,
+                       k, dx != nullptr ? kSyncLate : kSyncEarly, stream);
 }
 
 }  // extern "C"

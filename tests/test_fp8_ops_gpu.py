@@ -427,3 +427,42 @@ def test_one_weight_shared_by_many_tiles(t, inner, red):
             assert bool(((y[lo:hi].double() - ref).abs() <= tol).all()), product
             assert bool((y[:lo] == 55.0).all()) and bool((y[hi:] == 55.0).all())
     assert mg.muon_device_status() == 0
+
+
+def test_backward_on_streams_in_a_graph_and_one_after_the_other():
+    """Both products of a layer's gradients may run side by side, and whatever
+    follows on the stream comes after both."""
+    gen = torch.Generator(device=DEV).manual_seed(77)
+    t, n, k, g = 900, 520, 640, 5
+    off = torch.tensor([0, 100, 100, 420, 800, 900], dtype=torch.int32, device=DEV)
+    x = torch.randn(t, k, generator=gen, device=DEV).to(BF)
+    dy = torch.randn(t, n, generator=gen, device=DEV).to(BF)
+    m = mg.muon_fp8_quantize_weight(torch.randn(g, n, k, generator=gen, device=DEV))
+    dx, dw = mg.muon_fp8_linear_backward(dy, x, m, offsets=off)
+    # each alone
+    only, none = mg.muon_fp8_linear_backward(dy, x, m, offsets=off, need_dw=False)
+    assert none is None and torch.equal(only, dx)
+    none, only = mg.muon_fp8_linear_backward(dy, x, m, offsets=off, need_dx=False)
+    assert none is None and torch.equal(only, dw)
+    # operands of two types take a launch each
+    _, w32 = mg.muon_fp8_linear_backward(dy, x.float(), m, offsets=off)
+    assert torch.equal(w32, dw)
+    for _ in range(20):                                  # consumers right behind
+        a, b = mg.muon_fp8_linear_backward(dy, x, m, offsets=off)
+        assert torch.equal(a + 0, dx) and torch.equal(b + 0, dw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a, b = mg.muon_fp8_linear_backward(dy, x, m, offsets=off, stream=s)
+    s.synchronize()
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = mg.muon_fp8_linear_backward(dy, x, m, offsets=off)
+        c, d = a * 2, b * 2
+    for _ in range(3):
+        c.zero_()
+        d.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, dx) and torch.equal(b, dw) and torch.equal(c, dx * 2) and torch.equal(d, dw * 2)
+    assert mg.muon_device_status() == 0
