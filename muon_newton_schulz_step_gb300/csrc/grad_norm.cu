@@ -234,7 +234,7 @@ __device__ __forceinline__ void tile_scale(const NormTensor& T, int tile, float 
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = load_stream(src + i * kThreads);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) dst[i * kThreads] = scale_vector<BF16>(v[i], by);
+        for (int i = 0; i < kVecs; ++i) __stcs(dst + i * kThreads, scale_vector<BF16>(v[i], by));   // not to push out what is still to be read
         return;
     }
     const long long end = base + kTile < T.n ? base + kTile : T.n;
