@@ -38,37 +38,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerThread = 8;
 
-// Eight consecutive elements as loaded: bf16 in a, fp32 in a and b.
-struct Raw {
-    uint4 a, b;
-};
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-template <bool BF16>
-__device__ __forceinline__ float element(const Raw& r, int j) {
-    if (BF16) {
-        const uint32_t w = word(r.a, j >> 1);
-        return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
-    }
-    return __uint_as_float(j < 4 ? word(r.a, j) : word(r.b, j - 4));
-}
-
-constexpr uint32_t kInf = 0x7f800000u;
-
-// Largest magnitude of eight elements, as fp32 bits (NaN and infinity at or above kInf).
-template <bool BF16>
-__device__ __forceinline__ uint32_t row_max(const Raw& r) {
-    if (BF16) {
-        const uint32_t k = 0x7fff7fffu;
-        const uint32_t v = __vmaxu2(__vmaxu2(r.a.x & k, r.a.y & k), __vmaxu2(r.a.z & k, r.a.w & k));
-        return max(v & 0xffff0000u, v << 16);
-    }
-    const uint32_t k = 0x7fffffffu;
-    return max(max(max(r.a.x & k, r.a.y & k), max(r.a.z & k, r.a.w & k)),
-               max(max(r.b.x & k, r.b.y & k), max(r.b.z & k, r.b.w & k)));
-}
-
 // Largest magnitudes of eight columns over rows: bf16 two to a word, fp32 bits one.
 template <bool BF16>
 struct ColMax {
@@ -106,41 +75,6 @@ struct ColMax {
         return v;
     }
 };
-
-// Elements that are not finite: NaN in their place (infinities would saturate in
-// the conversion), zero for the maxima.
-template <bool BF16>
-__device__ __noinline__ Raw replace_odd(Raw r, bool zero) {
-    uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
-        if (BF16) {
-            if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = zero ? w[i] & 0x0000ffffu : w[i] | 0x7fff0000u;
-            if ((w[i] & 0x7f80u) == 0x7f80u) w[i] = zero ? w[i] & 0xffff0000u : w[i] | 0x7fffu;
-        } else if ((w[i] & kInf) == kInf) {
-            w[i] = zero ? 0u : w[i] | 0x7fffffffu;
-        }
-    }
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-    r.b = make_uint4(w[4], w[5], w[6], w[7]);
-    return r;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint2 codes(const Raw& r, const float (&by)[8]) {
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        q[i] = ptx::cvt_e4m3x2(__fmul_rn(element<BF16>(r, 2 * i + 1), by[2 * i + 1]),
-                               __fmul_rn(element<BF16>(r, 2 * i), by[2 * i]));
-    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint2 codes(const Raw& r, float by) {
-    const float b[8] = {by, by, by, by, by, by, by, by};
-    return codes<BF16>(r, b);
-}
 
 struct RowBlock {
     long long row0;       // first row in x
@@ -333,7 +267,7 @@ __device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Ra
         for (int i = 0; i < kRowsPerThread; ++i) {
             const float by = __shfl_sync(0xffffffffu, inv, (lane & 16) + 2 * i);
             if (i * 16 + warp * 2 + half < r.rows)
-                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
+                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes_of<BF16>(v[i], by);
         }
     }
     if (COL) {
@@ -357,7 +291,7 @@ __device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Ra
         }
         uint8_t* dst = p.col_q + (r.padded0 + warp * 2 + half) * p.ldq + col;
 #pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
+        for (int i = 0; i < kRowsPerThread; ++i) *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes_of<BF16>(v[i], by);
     }
     if (BLK) {
         uint32_t t = 0;
@@ -373,7 +307,7 @@ __device__ __forceinline__ void tile(const QuantParams& p, const RowBlock& r, Ra
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i)
             if (i * 16 + warp * 2 + half < r.rows)
-                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes<BF16>(v[i], by);
+                *reinterpret_cast<uint2*>(dst + i * 16 * p.ldq) = codes_of<BF16>(v[i], by);
         if (threadIdx.x == 0)
             p.blk_scale[(batch * ((p.rows + 127) >> 7) + (r.row0 >> 7)) * (p.ldq >> 7) + cb] = static_cast<uint8_t>(e + 127);
     }

@@ -3,10 +3,11 @@
 //
 // Serving makes this product for one token at a time: its time is the weight's
 // bytes, read once, and the launch.  The tiled product would load 128 rows per CTA
-// on a third of the SMs and needs the codes of x from a launch before it.  One
-// token x 6144 x 6144: 19.4 us by tiles, 10.4 here; with experts the tiles fill the
-// SMs and win (32 tokens over 16 experts of 2048 x 6144: 43 us against 56 here),
-// so this kernel serves single weights.
+// on a third of the SMs and needs the codes of x from a launch before it.  One token
+// x 6144 x 6144: 18.5 us by tiles, 9.2 here (12.3 with the weight from memory, 3.1 TB/s;
+// the launch and the rounding of x take about 4).  With experts the tiles fill the SMs
+// and win (32 tokens over 16 experts of 2048 x 6144: 43 us against 56 here), so this
+// kernel serves single weights.
 //
 // A block takes 16 rows of the weight, its eight warps take the reduction's
 // blocks of 128 in turn.  A lane reads 16 consecutive bytes of a row at a time (the
@@ -15,7 +16,9 @@
 // the products of a block of 128 run on mma.sync: 16 rows x 8 tokens cost no more
 // than one token.  (tcgen05 has nothing to add: the tensor core idles either way,
 // and its operands would take a trip through shared memory.)  The block rounds x
-// into shared memory itself, while its first weight bytes are under way.
+// into shared memory itself, while its first weight bytes are under way.  Streaming
+// the weight through shared memory by bulk copies was no faster from memory (12.2
+// against 12.5 us) and slower from L2 (11.8 against 10.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -64,40 +67,33 @@ struct WeightBlock {
     }
 };
 
-// Eight consecutive elements of a token from column col on, as loaded; zero past the last.
+// Eight consecutive elements of a token from column col on; zero past the last.
 template <bool BF16>
-struct Eight {
-    uint4 a, b;                      // bf16 in a, fp32 in a and b
-    __device__ __forceinline__ void load(const Fp8TokenParams& p, long long row, int col) {
-        a = b = make_uint4(0, 0, 0, 0);
-        if (p.vec && col + 8 <= p.k) {
-            const char* s = static_cast<const char*>(p.x) + (row * p.ld_x + col) * (BF16 ? 2 : 4);
-            a = *reinterpret_cast<const uint4*>(s);
-            if (!BF16) b = *reinterpret_cast<const uint4*>(s + 16);
-        } else {
-            uint32_t w[8];
+__device__ __forceinline__ Raw load_eight(const Fp8TokenParams& p, long long row, int col) {
+    Raw r;
+    r.a = r.b = make_uint4(0, 0, 0, 0);
+    if (p.vec && col + 8 <= p.k) {
+        const char* s = static_cast<const char*>(p.x) + (row * p.ld_x + col) * (BF16 ? 2 : 4);
+        r.a = *reinterpret_cast<const uint4*>(s);
+        if (!BF16) r.b = *reinterpret_cast<const uint4*>(s + 16);
+        return r;
+    }
+    uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = 0;
-                const long long at = row * p.ld_x + col + i;
-                if (col + i < p.k)
-                    w[i] = BF16 ? static_cast<uint32_t>(static_cast<const uint16_t*>(p.x)[at])
-                                : static_cast<const uint32_t*>(p.x)[at];
-            }
-            if (BF16) {
-                a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-            } else {
-                a = make_uint4(w[0], w[1], w[2], w[3]);
-                b = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        }
+    for (int i = 0; i < 8; ++i) {
+        w[i] = 0;
+        const long long at = row * p.ld_x + col + i;
+        if (col + i < p.k)
+            w[i] = BF16 ? static_cast<uint32_t>(static_cast<const uint16_t*>(p.x)[at]) : static_cast<const uint32_t*>(p.x)[at];
     }
-    __device__ __forceinline__ float at(int i) const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if (BF16) return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-        return __uint_as_float(w[i]);
+    if (BF16) {
+        r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+    } else {
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = make_uint4(w[4], w[5], w[6], w[7]);
     }
-};
+    return r;
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 3) k_fp8_token(const __grid_constant__ Fp8TokenParams p) {
@@ -121,44 +117,46 @@ __global__ void __launch_bounds__(kThreads, 3) k_fp8_token(const __grid_constant
     for (int i = 0; i < kAhead; ++i)
         if (warp + i * kWarps < blocks) wb[i].load(lo, hi, warp + i * kWarps);
 
-    // half a warp rounds one block of 128, eight elements a lane; its next blocks' are on their way
+    // half a warp rounds one block of 128, eight elements a lane, kRound blocks at a time
     {
-        const int c = threadIdx.x & 15, items = p.tokens * blocks;
+        const int c = threadIdx.x & 15;
         constexpr int kStep = kThreads / 16;
         const uint32_t half = 0xffffu << (lane & 16);
-        for (int i0 = threadIdx.x >> 4; i0 < items; i0 += kRound * kStep) {
-            Eight<BF16> x[kRound];
+        int t = 0, kb = threadIdx.x >> 4;
+        auto settle = [&] {
+            while (kb >= blocks) {
+                kb -= blocks;
+                ++t;
+            }
+        };
+        settle();
+        while (t < p.tokens) {
+            Raw x[kRound];
+            int at[kRound], kbs[kRound];
 #pragma unroll
             for (int u = 0; u < kRound; ++u) {
-                const int i = min(i0 + u * kStep, items - 1);
-                const int t = i / blocks;
-                x[u].load(p, t, (i - t * blocks) * 128 + 8 * c);
+                at[u] = t;
+                kbs[u] = kb;
+                if (t < p.tokens) x[u] = load_eight<BF16>(p, t, kb * 128 + 8 * c);
+                kb += kStep;
+                settle();
             }
 #pragma unroll
             for (int u = 0; u < kRound; ++u) {
-                const int i = i0 + u * kStep;
-                if (i >= items) break;
-                const int t = i / blocks, kb = i - t * blocks;
-                uint32_t top = 0;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t m = __float_as_uint(x[u].at(q)) & 0x7fffffffu;
-                    top = max(top, m >= 0x7f800000u ? 0u : m);
-                }
+                if (at[u] >= p.tokens) break;
+                uint32_t top = row_max<BF16>(x[u]);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
-                const int e = scale_exponent(top);
-                const float by = inverse_scale(e);
-                uint32_t q[4];
+                if (top >= kInf) {                       // of the whole half warp
+                    top = row_max<BF16>(replace_odd<BF16>(x[u], true));
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const float x0 = x[u].at(2 * h), x1 = x[u].at(2 * h + 1);
-                    q[h] = ptx::cvt_e4m3x2(isinf(x1) ? __uint_as_float(0x7fffffffu) : __fmul_rn(x1, by),
-                                           isinf(x0) ? __uint_as_float(0x7fffffffu) : __fmul_rn(x0, by));
+                    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+                    x[u] = replace_odd<BF16>(x[u], false);
                 }
-                *reinterpret_cast<uint2*>(codes + t * pitch + kb * 128 + 8 * c) =
-                    make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-                if (c == 0) exps[t * blocks + kb] = static_cast<int16_t>(e);
+                const int e = scale_exponent(top);
+                *reinterpret_cast<uint2*>(codes + at[u] * pitch + kbs[u] * 128 + 8 * c) =
+                    codes_of<BF16>(x[u], inverse_scale(e));
+                if (c == 0) exps[at[u] * blocks + kbs[u]] = static_cast<int16_t>(e);
             }
         }
     }
@@ -237,8 +235,8 @@ cudaError_t run(const Fp8TokenParams& p, cudaStream_t s) {
 // Whether this kernel serves a call: the tokens take one matrix fragment, their codes
 // fit in shared memory, and rounding x in every block does not cost more than the
 // launch that the tiles need for it.  Measured, this kernel against tiles: 8 tokens
-// x 2048 x 6144 (1.0e8 products) 15.4 against 18.4 us, 4 x 6144 x 6144 (1.5e8) 16.9
-// against 18.4, 8 x 6144 x 6144 (3.0e8) 25.8 against 18.4.
+// x 2048 x 6144 (1.0e8 products) 15.8 against 18.8 us, 4 x 6144 x 6144 (1.5e8) 15.0
+// against 18.9, 8 x 6144 x 6144 (3.0e8) 25.8 against 18.4.
 bool fp8_token_serves(long long tokens, long long n, long long k) {
     const long long ldk = (k + 127) / 128 * 128;
     return tokens <= kTokens && token_smem(static_cast<int>(tokens), ldk) <= static_cast<size_t>(kMaxCodes) &&
