@@ -706,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                         ptx::stmatrix_x4_trans(buf_addr + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0], w[1],
                                                w[2], w[3]);
                     }
-                    if (left >= 32) {
+                    // a TMA store ends rows on 16 bytes: the last odd columns are the warp's own to write
+                    if (left >= 32 && (m0 + 32 <= p.m_ext || p.m_ext % 8 == 0)) {
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                             ptx::bulk_commit_group();
                         }
                     } else {
-                        // a group's last rows: the next group's lie behind them
+                        // or a group's last rows: the next group's lie behind them
                         __syncwarp();
                         const int mm = m0 + 8 * (lane & 3);
 #pragma unroll

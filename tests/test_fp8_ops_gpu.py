@@ -406,6 +406,23 @@ def test_many_tiles_of_large_groups(offsets, out):
     assert mg.muon_device_status() == 0
 
 
+@pytest.mark.parametrize("inner", [301, 302, 303, 304, 290, 513])
+def test_columns_behind_the_output_stay(inner):
+    """Rows that start on 16 bytes and end elsewhere: what lies between the last
+    column and the next row is not the product's."""
+    gen = torch.Generator(device=DEV).manual_seed(inner)
+    t, red, ld = 160, 300, (inner + 8) // 8 * 8
+    q, _ = mg.muon_fp8_quantize(torch.randn(t, red, generator=gen, device=DEV).to(BF))
+    for product, shape in (("forward", (inner, red)), ("grad_input", (red, inner))):
+        m = mg.muon_fp8_quantize_weight(torch.randn(*shape, generator=gen, device=DEV))
+        for out in (BF, F32):
+            y = mg.muon_fp8_product(product, q, m, out_dtype=out)
+            wide = torch.full((t, ld), 55.0, dtype=out, device=DEV)
+            mg.muon_fp8_product(product, q, m, out=wide[:, :inner])
+            assert torch.equal(wide[:, :inner], y) and bool((wide[:, inner:] == 55.0).all()), (product, out)
+    assert mg.muon_device_status() == 0
+
+
 @pytest.mark.parametrize("t,inner,red", [(4100, 2500, 2100), (2500, 4611, 2048)])
 def test_one_weight_shared_by_many_tiles(t, inner, red):
     """One weight, many column tiles and a long reduction: clusters of two pairs of
