@@ -132,8 +132,8 @@ __device__ __forceinline__ void split_columns(int n, int unit, bool even, int& t
 
 // Tile t of the launch; `g` only moves forward.  Integer divisions are avoided:
 // four of them took 900 cycles of every tile in every role.
-template <int CS>
-__device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g) {
+template <int CS, int SK>
+__device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g, int pp) {
     while (t >= gs.tile0[g + 1]) ++g;
     const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
@@ -163,6 +163,11 @@ __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups
     x.c0 = gw ? off : gs.lo[g] + off;
     x.kb0 = gw ? gs.block0[g] : 0;
     x.nkb = gw ? (gs.cnt[g] + kFp8Block - 1) / kFp8Block : p.kblocks;
+    if (SK > 1) {                    // this pair's slice, in whole groups of four blocks
+        const int quads = (x.nkb + 3) / 4, last = min(x.nkb, quads * (pp + 1) / SK * 4);
+        x.kb0 = quads * pp / SK * 4;
+        x.nkb = last - x.kb0;
+    }
     return x;
 }
 
@@ -255,9 +260,12 @@ struct ScaleGroup<kFp8GradWeight> {
 
 // CS: CTAs per cluster, 2 (one pair) or 4 (two pairs with neighbouring column tiles
 // of the same rows, which share the A operand by multicast).
-template <int MODE, bool F32, int CS>
+// SK: pairs of a cluster that share one tile's reduction, each a slice of it (CS 2;
+// one tile per cluster).
+template <int MODE, bool F32, int CS, int SK = 1>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
     static_assert(CS == 2 || (CS == 4 && MODE != kFp8GradWeight), "cluster size");
+    static_assert(SK == 1 || CS == 2, "slices of the reduction");
     constexpr int kStages = Ring<MODE>::stages;
     constexpr uint32_t kEpiBytes = Ring<MODE>::block;
     constexpr bool kAMn = MODE != kFp8Forward;          // A operand MN-major
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     const uint32_t rank = crank & 1u, lead = crank & ~1u;   // in the pair; cluster rank of the pair's leader
     const int pp = static_cast<int>(crank >> 1);            // pair in the cluster
     const bool leader = rank == 0;
-    const int pair = static_cast<int>(ptx::cluster_id_x()) * (CS / 2) + pp;
+    const int pair = static_cast<int>(ptx::cluster_id_x()) * (CS / 2) + (SK == 1 ? pp : 0);
     const int npairs = static_cast<int>(ptx::num_clusters_x()) * (CS / 2);
     const uint64_t limit = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
 
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs) {
-                const Tile x = decode_tile<CS>(p, gs, t, g);
+                const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
                 const int m = x.m0 + static_cast<int>(rank) * kHalf;
                 const int half = x.width / 2;
                 const int c = x.c0 + static_cast<int>(rank) * half;
@@ -429,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             uint32_t phase = 0, sphase = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs, ++it) {
-                const Tile x = decode_tile<CS>(p, gs, t, g);
+                const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
                 const int acc = it & 1;
                 const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
                 // The copy of four blocks' scale words is issued a block before the first
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfa + 4,
                                                (kk != 0 || kb != x.kb0) ? 1u : 0u);
-                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), CS == 4 ? 0xFu : 0x3u);
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), CS == 4 ? 0xFu : mine);
                     }
                     __syncwarp();
                     if (++stage == kStages) {
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             return true;
         };
         for (int t = pair; ok && t < tiles; t += npairs) {
-            const Tile x = decode_tile<CS>(p, gs, t, g);
+            const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
             const int m = x.m0 + static_cast<int>(rank) * kHalf;
             for (int i = 0; ok && i < x.nkb; i += 4, ++seq) {
                 if ((seq & 1) != warp - 2) continue;
@@ -557,8 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         const int half = (warp - 4) >> 2;                // even or odd 32-column chunks
         uint8_t* const stage = s_epi + (warp - 4) * kEpiBytes;
         int it = 0, g = 0;
+        bool met = false;                                // SK > 1: the pairs have exchanged their sums
         for (int t = pair; t < tiles; t += npairs, ++it) {
-            const Tile x = decode_tile<CS>(p, gs, t, g);
+            const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
             const int acc = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
             const int m0 = x.m0 + static_cast<int>(rank) * kHalf + q * 32;
@@ -584,18 +593,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                 break;
             }
             ptx::tc_fence_after();
+            // SK > 1: each pair finishes some 32-column chunks.  The others leave their sums of
+            // those in their own shared memory (the ring is idle: the tile's products have read
+            // it), and after all have met it adds them to its own in the order of the slices.
+            auto leave = [&](int ch, const uint32_t (&r)[32]) {
+                uint4* o = reinterpret_cast<uint4*>(smem) + (ch * 4 + q) * 256 + lane;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) o[v * 32] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
+            };
+            auto meet = [&] {
+                __syncwarp();
+                ptx::cluster_sync();
+                met = true;
+            };
+            auto join = [&](int ch, uint32_t (&r)[32]) {
+                const uint32_t at = ptx::smem_addr(smem) + ((ch * 4 + q) * 256 + lane) * 16;
+                float sum[32];
+#pragma unroll
+                for (int s = 0; s < SK; ++s) {
+                    const uint32_t from = ptx::mapa_shared(at, static_cast<uint32_t>(2 * s) + rank);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        uint4 w = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
+                        if (s != pp) w = ptx::ld_cluster_v4(from + v * 512);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sum[4 * v + e] = s == 0 ? __uint_as_float(u[e]) : sum[4 * v + e] + __uint_as_float(u[e]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[j]);
+            };
             if constexpr (MODE == kFp8GradWeight) {
                 // groups of 64 columns: 0, 2 and 1, 3; the second half of the first accumulator from its end
                 uint32_t r[2][32];
+                if constexpr (SK > 1) {                  // group half + 2 i is pair i's to finish
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        if (i == pp) continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int ch = 2 * half + 4 * i + h;
+                            if (ch >= chunks) continue;
+                            ptx::tmem_ld_32x32b_x32(src + static_cast<uint32_t>(32 * ch), r[h]);
+                            ptx::tmem_wait_ld();
+                            leave(ch, r[h]);
+                        }
+                    }
+                    meet();
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int pr = acc == 0 && half == 1 ? 3 - 2 * i : half + 2 * i;
+                    if (SK > 1 && i != pp) continue;
+                    const int pr = SK == 1 && acc == 0 && half == 1 ? 3 - 2 * i : half + 2 * i;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         if (2 * pr + h < chunks) ptx::tmem_ld_32x32b_x32(src + static_cast<uint32_t>(64 * pr + 32 * h), r[h]);
                     ptx::tmem_wait_ld();
-                    if (i == 0 && owner) release_shared();
-                    if (i == 1) release();
+                    if constexpr (SK > 1) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (2 * pr + h < chunks) join(2 * pr + h, r[h]);
+                    } else {
+                        if (i == 0 && owner) release_shared();
+                        if (i == 1) release();
+                    }
                     if (x.nkb == 0) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0u;
@@ -749,6 +812,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                     }
                 }
             };
+            if constexpr (SK > 1) {
+                // chunk 2 i + half is pair i % SK's to finish
+                uint32_t r[2][16];
+#pragma unroll 1
+                for (int i = 0; half + 2 * i < chunks; ++i) {
+                    if (i % SK == pp) continue;
+                    read(half + 2 * i, r);
+                    ptx::tmem_wait_ld();
+                    leave(half + 2 * i, reinterpret_cast<uint32_t(&)[32]>(r));
+                }
+                meet();
+#pragma unroll 1
+                for (int i = pp; half + 2 * i < chunks; i += SK) {
+                    read(half + 2 * i, r);
+                    ptx::tmem_wait_ld();
+                    join(half + 2 * i, reinterpret_cast<uint32_t(&)[32]>(r));
+                    write(half + 2 * i, r);
+                }
+                break;
+            }
             // each chunk is read while the one before it is written
             uint32_t ra[2][16], rb[2][16];
             read(chunk(0), ra);
@@ -766,7 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             release();
             write(chunk(3), rb);
         }
-        if (MODE != kFp8GradWeight && p.zero_rest) {
+        if (SK > 1 && !met) {                            // after a failure: the other warps wait there
+            __syncwarp();
+            ptx::cluster_sync();
+        }
+        if (SK == 1 && MODE != kFp8GradWeight && p.zero_rest) {
             // rows of no group: before the first group's and behind the last one's
             const int head = gs.lo[0], tail = gs.lo[p.groups - 1] + gs.cnt[p.groups - 1];
             const int rest = head + p.n_ext - tail;
@@ -780,6 +867,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         }
         if (lane == 0) ptx::bulk_wait_group_all();       // every block written
         __syncwarp();
+    }
+    if (SK > 1 && warp < 4) {
+        __syncwarp();
+        ptx::cluster_sync();                             // the epilogue's exchange
     }
 
     if (p.sync == kSyncLate) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -799,32 +890,41 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
-template <int MODE, bool F32, int CS>
+template <int MODE, bool F32, int CS, int SK>
 cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, CS, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CS * clusters);
+    cfg.gridDim = dim3(CS * SK * clusters);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<MODE>();
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CS;
+    at[0].val.clusterDim.x = CS * SK;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.sync != kSyncNone ? 2 : 1;
-    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, CS>, p);
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, CS, SK>, p);
     return l != cudaSuccess ? l : cudaGetLastError();
 }
 
-template <int MODE, int CS>
+template <int MODE, int CS, int SK = 1>
 cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
-    return p.out_f32 ? run<MODE, true, CS>(p, clusters, s) : run<MODE, false, CS>(p, clusters, s);
+    return p.out_f32 ? run<MODE, true, CS, SK>(p, clusters, s) : run<MODE, false, CS, SK>(p, clusters, s);
+}
+
+template <int SK>
+cudaError_t run_slices(const Fp8GemmParams& p, int tiles, cudaStream_t s) {
+    switch (p.mode) {
+        case kFp8Forward: return run<kFp8Forward, 2, SK>(p, tiles, s);
+        case kFp8GradInput: return run<kFp8GradInput, 2, SK>(p, tiles, s);
+        default: return run<kFp8GradWeight, 2, SK>(p, tiles, s);
+    }
 }
 
 }  // namespace
@@ -855,6 +955,12 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cuda
     const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
                                                   : p.n_ext / kTile + p.groups;
     const long long most = mt * nt;
+    if (p.slices > 1) {
+        const int tiles = static_cast<int>(mt * ((p.n_ext + kTile - 1) / kTile));
+        return p.slices == 2 ? run_slices<2>(p, tiles, s)
+               : p.slices == 3 ? run_slices<3>(p, tiles, s)
+                               : run_slices<4>(p, tiles, s);
+    }
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {
         case kFp8Forward: return run<kFp8Forward, 2>(p, pairs, s);
@@ -863,30 +969,52 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cuda
     }
 }
 
-// Clusters of four CTAs that the current device holds at once (0: none).
-int fp8_gemm_clusters4() {
-    if (cudaFuncSetAttribute(k_fp8_gemm<kFp8Forward, false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem_bytes<kFp8Forward>())) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kFp8Forward>();
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 4;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_fp8_gemm<kFp8Forward, false, 4>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
+// Clusters of 4, 6 and 8 CTAs that the current device holds at once (0: none).
+void fp8_gemm_clusters(int (&n)[3]) {
+    auto ask = [](auto* kernel, int size) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem_bytes<kFp8Forward>();
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = size;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int most = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem_bytes<kFp8Forward>())) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            most = 0;
+        }
+        return most;
+    };
+    n[0] = ask(k_fp8_gemm<kFp8Forward, false, 4>, 4);
+    n[1] = ask(k_fp8_gemm<kFp8Forward, false, 2, 3>, 6);
+    n[2] = ask(k_fp8_gemm<kFp8Forward, false, 2, 4>, 8);
+}
+
+// Pairs that share a tile's reduction.  A single weight with few tiles leaves most SMs
+// idle, while one pair's ring takes 0.2 us per block of 128 however narrow the tile: up
+// to four pairs of a cluster take a slice each, and add their sums through shared memory.
+// Their meeting costs a microsecond, so a slice has eight blocks or more; of the gradients
+// sixteen: the layer's other product wants the idle SMs too.  All clusters
+// have to fit at once, or a second wave starts.  Measured (forward, one pair -> slices):
+// 9 tokens x 2048 x 6144 16.5 us -> 12.3, 10.7, 10.3 with two, three, four; 9 x 6144 x
+// 6144 16.5 -> 12.3 with two (three, in two waves, 20.6); 256 x 6144 x 6144 20.7 -> 16.4;
+// 2048 x 2048 x 2048 12.1 -> 23.8 in two waves; backward of 2048 tokens of 520 x 1300 30.3
+// -> 39.0 with slices of eight blocks, of 8192 tokens 75.2 -> 70.1.
+int fp8_gemm_slices(const Fp8GemmParams& p, const int (&clusters)[3]) {
+    if (p.offsets != nullptr || p.groups != 1) return 1;
+    const long long tiles = static_cast<long long>((p.m_ext + kTile - 1) / kTile) * ((p.n_ext + kTile - 1) / kTile);
+    const int blocks = p.mode == kFp8GradWeight ? (p.rows + kFp8Block - 1) / kFp8Block : p.kblocks;
+    const int least = p.mode == kFp8Forward ? 8 : 16;
+    for (int s = 4; s > 1; --s)
+        if (blocks >= least * s && tiles <= clusters[s - 2]) return s;
+    return 1;
 }
 
 cudaError_t read_and_clear_fp8_error(int* code) {

@@ -316,6 +316,7 @@ struct Fp8GemmParams {
     int mode;
     int sync;                 // Fp8Sync
     int multicast;            // forward, grad input: clusters of two pairs share A (tm_a: boxes of 64)
+    int slices;               // pairs of a cluster that share each tile's reduction; 1: none
     int out_f32;
     int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only)
     int m_ext;                // extent along the MMA's rows: n (forward, grad weight), k (grad input)
@@ -329,7 +330,8 @@ struct Fp8GemmParams {
 };
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s);
-int fp8_gemm_clusters4();
+void fp8_gemm_clusters(int (&n)[3]);
+int fp8_gemm_slices(const Fp8GemmParams& p, const int (&clusters)[3]);
 bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
                         int clusters4);
 
@@ -393,7 +395,8 @@ int set_last_error(int status, const char* msg);
 
 // What the operators around the step (train_abi.cu) share with it.
 enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpFp8Token, kOpEnd };
-int op_device(int* sms, int* clusters4 = nullptr);   // the current device, checked; its SMs, clusters of four CTAs
+// The current device, checked; its SMs, and how many clusters of 4, 6 and 8 CTAs of fp8_gemm it holds.
+int op_device(int* sms, int (*clusters)[3] = nullptr);
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);
 int op_encode_bytes(CUtensorMap* map, const void* base, long long inner, long long outer, long long batch,
                     int box_inner, int box_outer);

@@ -74,7 +74,7 @@ int fail(int status, const char* fmt, ...) {
 struct DeviceState {
     bool init = false;
     int sms = 0;
-    int clusters4 = -1;                // clusters of four CTAs resident at once (asked for once)
+    int clusters[3] = {-1, -1, -1};    // clusters of 4, 6 and 8 CTAs resident at once (asked for once)
     void* ws = nullptr;
     size_t ws_bytes = 0;
     cudaEvent_t last_use = nullptr;
@@ -1054,15 +1054,15 @@ int ns5_batched_on_workspace(void* const* ptrs, const int* rows, const int* cols
 
 int set_last_error(int status, const char* msg) { return fail(status, "%s", msg); }
 
-int op_device(int* sms, int* clusters4) {
+int op_device(int* sms, int (*clusters)[3]) {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState* d = nullptr;
     const int rc = device_state(&d);
     if (rc != MUON_OK) return rc;
     *sms = d->sms;
-    if (clusters4 != nullptr) {
-        if (d->clusters4 < 0) d->clusters4 = fp8_gemm_clusters4();
-        *clusters4 = d->clusters4;
+    if (clusters != nullptr) {
+        if (d->clusters[0] < 0) fp8_gemm_clusters(d->clusters);
+        for (int i = 0; i < 3; ++i) (*clusters)[i] = d->clusters[i];
     }
     return rc;
 }

@@ -334,8 +334,8 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     if (tokens > 0 && ((rc = check_align(a_scale, scale_align, "a_scale")) != MUON_OK ||
                        (rc = check_align(b_scale, scale_align, "b_scale")) != MUON_OK))
         return rc;
-    int sms = 0, clusters4 = 0;
-    if ((rc = op_device(&sms, &clusters4)) != MUON_OK) return rc;
+    int sms = 0, clusters[3] = {};
+    if ((rc = op_device(&sms, &clusters)) != MUON_OK) return rc;
     if (gw && tokens == 0) {
         const size_t sz = dtype_size(out_dtype);
         const cudaError_t e = cudaMemset2DAsync(out, ld_out * sz, 0, inner * sz, static_cast<size_t>(groups) * n, stream);
@@ -364,6 +364,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
         const long long padded = muon_fp8_padded_rows(tokens, groups);
         p.n_ext = k;
         p.out_batch = static_cast<long long>(n) * ld_out;
+        p.slices = fp8_gemm_slices(p, clusters);
         p.s_a = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
         p.s_b = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
         if ((rc = op_encode_bytes(&p.tm_a, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
@@ -377,7 +378,8 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
         p.s_a = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
                      : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
         p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
-        p.multicast = fp8_gemm_multicast(product, inner, tokens, p.kblocks, groups, sms, clusters4);
+        p.slices = fp8_gemm_slices(p, clusters);
+        p.multicast = p.slices == 1 && fp8_gemm_multicast(product, inner, tokens, p.kblocks, groups, sms, clusters[0]);
         if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, p.multicast ? 64 : 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
@@ -385,7 +387,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
     if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
-    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, clusters4, stream); });
+    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, clusters[0], stream); });
 }
 
 }  // namespace

@@ -483,3 +483,43 @@ def test_backward_on_streams_in_a_graph_and_one_after_the_other():
         torch.cuda.synchronize()
         assert torch.equal(a, dx) and torch.equal(b, dw) and torch.equal(c, dx * 2) and torch.equal(d, dw * 2)
     assert mg.muon_device_status() == 0
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("product,t,inner,red", [
+    ("forward", 40, 5000, 2100), ("forward", 300, 700, 3001), ("forward", 700, 301, 4500), ("forward", 9, 256, 4096),
+    ("grad_input", 40, 2000, 4200), ("grad_input", 300, 700, 6200), ("grad_input", 500, 301, 8200),
+    ("grad_weight", 700, 300, 4100), ("grad_weight", 301, 513, 6200), ("grad_weight", 130, 520, 8200)])
+def test_few_tiles_and_a_long_reduction(product, t, inner, red, out):
+    """Sizes at which two, three or four pairs of SMs share a tile's reduction, with
+    edges in every direction, output rows of a stride, and the same bits each time.
+    (Of the weight gradient `t` is the rows, `red` the tokens.)"""
+    gen = torch.Generator(device=DEV).manual_seed(red)
+    x = (torch.randn(t, red, generator=gen, device=DEV) *
+         torch.exp2(torch.randint(-6, 7, (1, red), generator=gen, device=DEV).float())).to(BF)
+    b = torch.randn(red, inner, generator=gen, device=DEV).to(BF)
+    if product == "grad_weight":
+        _, p = mg.muon_fp8_quantize(x.t().contiguous(), row=False, col=True)
+        _, m = mg.muon_fp8_quantize(b, row=False, col=True)
+        # the same blocks of 128 tokens as rows' blocks of the transposed operands
+        pv = dequantized(mg.muon_fp8_quantize(x)[0])
+        mv = dequantized(mg.muon_fp8_quantize(b.t().contiguous())[0]).t()
+        extra = {"tokens": red}
+    else:
+        p, _ = mg.muon_fp8_quantize(x)
+        m = mg.muon_fp8_quantize_weight(b.t().contiguous() if product == "forward" else b)
+        pv, mv = dequantized(p), dequantized(m)
+        mv = mv.t() if product == "forward" else mv
+        extra = {}
+    ref = pv @ mv
+    tol = red * 2.0 ** -23 * (pv.abs() @ mv.abs()) + (2.0 ** -8 if out == BF else 2.0 ** -23) * ref.abs()
+    y = torch.full((t, inner), 55.0, dtype=out, device=DEV)
+    first = mg.muon_fp8_product(product, p, m, out=y, **extra).clone()
+    assert bool(((first.double() - ref).abs() <= tol).all())
+    for _ in range(5):
+        assert torch.equal(mg.muon_fp8_product(product, p, m, out=y, **extra), first)
+    if product != "grad_weight":
+        wide = torch.full((t, inner + 3), 55.0, dtype=out, device=DEV)
+        mg.muon_fp8_product(product, p, m, out=wide[:, :inner])
+        assert torch.equal(wide[:, :inner], first) and bool((wide[:, inner:] == 55.0).all())
+    assert mg.muon_device_status() == 0
