@@ -25,20 +25,22 @@
 //            and dx_k = w_k u_k on the chosen, 0 elsewhere
 // so only the softmax without renormalisation reads the whole row again.
 //
-// Forward: one warp per token.  A group owns `lanes` lanes, a lane `per_lane`
-// consecutive experts of one group, in index order over the warp: so the lowest
-// index among equal values is the lowest lane's, a group's two largest values
-// meet in log2(lanes) exchanges for all groups at once, and everything stays
-// in registers.  The top_k-th largest lane maximum bounds the choice from
-// below.  The few experts at or
-// above that bound (8 to about 12 of 384) are written to shared memory in index
-// order, a lane takes one each and counts those before it: its place in the
-// result.  Should more than 32 qualify (equal values, few lanes left), the
-// largest is taken top_k times instead.  The choice works on scores from one ex2 and
-// one rcp; the weights of the chosen are computed anew.  Bound by instructions:
+// Forward: a warp chooses for one token.  A group owns `lanes` lanes, a lane
+// `per_lane` consecutive experts of one group, in index order over the warp: so a
+// group's two largest values meet in log2(lanes) exchanges for all groups at once, and
+// everything stays in registers.  The top_k-th largest lane maximum bounds the choice
+// from below, and the few experts at or above that bound (8 to about 12 of 384) are
+// noted in shared memory.  Should more than a pool of them qualify (equal values), or
+// fewer lanes than top_k have an expert left, the largest is taken top_k times instead.
+// Then a lane takes one each, makes its choice value again from its logit by the same
+// operations, counts those before it (its place in the result), and computes its weight
+// anew at full accuracy.  Two tokens go through that second half side by side, 16 lanes
+// each, where top_k and the number of tokens allow it.  The choice works on scores from
+// one ex2 and one rcp.  Bound by instructions:
 // 32768 tokens x 384 experts in fp32, 4 of 8 groups: 73 us with the largest taken
 // top_k times for every token (about 1400 instructions each), 45 with the bound and
-// full-accuracy scores (1050), 34 now (780, four blocks per SM in one wave).
+// full-accuracy scores (1050), 34 with approximate ones (780), 28 with the second half
+// for two tokens at once (614; issue slots 75 % busy).  64 experts 21.3 -> 19.9.
 //
 // Backward: one warp per token, lanes striped over the row in vectors of four.
 // Scores of the chosen are recomputed from their logits; only the softmax without
@@ -143,12 +145,13 @@ constexpr int route_blocks() {
     return NV <= 4 ? 6 : NV <= 12 ? 4 : 2;
 }
 
-template <int NV, bool SIGMOID>
+// W: lanes that finish one token, 16 (then a warp finishes two at once) or 32.
+template <int NV, bool SIGMOID, int W>
 __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __grid_constant__ RouteParams p) {
     extern __shared__ int hist[];
-    __shared__ float2 pool[kWarps][32];                  // choice value, expert
-    __shared__ int order[kWarps][32];                    // experts by place
+    __shared__ int pool[kWarps][32];                     // experts at or above the bound
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t below = (1u << lane) - 1u;
     for (int e = threadIdx.x; e < p.experts; e += kThreads) hist[e] = 0;
     __syncthreads();
 
@@ -164,154 +167,224 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
     for (int j = 0; j < NV; ++j) odd_bias |= !(fabsf(bias[j]) <= FLT_MAX);
     odd_bias = __any_sync(kAll, odd_bias);
 
-    for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < p.tokens;
-         row += static_cast<long long>(gridDim.x) * kWarps) {
-        float c[NV];                                     // logits, then choice values; -inf: masked
-        load_lane<NV>(p, row, e0, n, c);
-        float top = 0.0f, inv = 1.0f;                    // softmax: largest logit, 1 / sum
-        float seen = 0.0f;                               // not finite: masked experts or NaN in this lane
-        if (SIGMOID) {
+    constexpr int kTokens = 32 / W;
+    const int sub = lane & (W - 1), which = lane / W;
+    const long long step = static_cast<long long>(gridDim.x) * kWarps * kTokens;
+    for (long long row0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; row0 < p.tokens; row0 += step) {
+        // of this lane's token: candidates, and what their scores need
+        int total = 0;
+        float t = 0.0f, top = 0.0f, inv = 1.0f;
+        bool ordinary = true;
+#pragma unroll 1
+        for (int h = 0; h < kTokens; ++h) {
+            const long long row = row0 + h;
+            if (row >= p.tokens) break;
+            float c[NV];                                     // logits, then choice values; -inf: masked
+            load_lane<NV>(p, row, e0, n, c);
+            float max_x = 0.0f, norm = 1.0f;                 // softmax: largest logit, 1 / sum
+            float seen = 0.0f;                               // not finite: masked experts or NaN in this lane
+            if (SIGMOID) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) seen += c[j];
-        } else {
-            float m = -INFINITY;
+                for (int j = 0; j < NV; ++j) seen += c[j];
+            } else {
+                float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                m = fmaxf(m, c[j]);
-                seen += c[j];
+                for (int j = 0; j < NV; ++j) {
+                    m = fmaxf(m, c[j]);
+                    seen += c[j];
+                }
+                max_x = warp_max(m);
             }
-            top = warp_max(m);
-        }
-        const bool plain = __all_sync(kAll, fabsf(seen) <= FLT_MAX) && top > -FLT_MAX;
-        uint32_t masked = 0;                             // bit j: no expert, or masked
-        if (!plain) {
+            const bool plain = __all_sync(kAll, fabsf(seen) <= FLT_MAX) && max_x > -FLT_MAX;
+            uint32_t masked = 0;                             // bit j: no expert, or masked
+            if (!plain) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) masked |= (c[j] == -INFINITY ? 1u : 0u) << j;
-        }
-        if (SIGMOID) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) c[j] = rcp_approx(1.0f + exp2_approx(c[j] * -kLog2e));
-        } else {
-            float a = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                c[j] = exp2_approx((c[j] - top) * kLog2e);
-                if (!plain && (masked >> j & 1u)) c[j] = 0.0f;
-                a += c[j];
+                for (int j = 0; j < NV; ++j) masked |= (c[j] == -INFINITY ? 1u : 0u) << j;
             }
-            inv = __fdiv_rn(1.0f, warp_sum(a));
+            // softmax, finite logits of ordinary size: 2^(x log2(e) - shift) with one shift for
+            // all, whose rounding the normalisation takes out again
+            const bool usual = plain && fabsf(max_x) < 1e30f;
+            const float shift = max_x * kLog2e;
+            if (SIGMOID) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) c[j] *= inv;
-        }
+                for (int j = 0; j < NV; ++j) c[j] = rcp_approx(1.0f + exp2_approx(c[j] * -kLog2e));
+            } else {
+                float a = 0.0f;
+                if (usual) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) c[j] += bias[j];
-        if (!plain || odd_bias) {
-            // a NaN orders below every number
+                    for (int j = 0; j < NV; ++j) a += c[j] = exp2_approx(fmaf(c[j], kLog2e, -shift));
+                } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const float v = c[j] == c[j] ? c[j] : -FLT_MAX;
-                c[j] = masked >> j & 1u ? -INFINITY : v;
+                    for (int j = 0; j < NV; ++j) a += c[j] = masked >> j & 1u ? 0.0f : exp2_approx((c[j] - max_x) * kLog2e);
+                }
+                norm = __fdividef(1.0f, warp_sum(a));        // the sum is at least 1, or NaN
             }
-        }
-        // group scores
-        if (p.groups > 1) {
-            float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                m2 = fmaxf(m2, fminf(m1, c[j]));
-                m1 = fmaxf(m1, c[j]);
+            if (which == h) {
+                t = shift;
+                top = max_x;
+                inv = norm;
+                ordinary = usual;
             }
-            for (int o = p.lanes >> 1; o > 0; o >>= 1) {
-                const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
-                m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-                m1 = fmaxf(m1, o1);
-            }
-            const float gv = m2 <= -FLT_MAX ? m1 : m1 + m2;   // one expert left (or one that is not NaN): its own
-            int before = 0;
-            for (int g = 0; g < p.groups; ++g) {
-                const float v = __shfl_sync(kAll, gv, g * p.lanes);
-                before += v > gv || (v == gv && g < group);
-            }
-            if (before >= p.top_groups) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j) c[j] = -INFINITY;
+            for (int j = 0; j < NV; ++j) c[j] = SIGMOID ? __fadd_rn(c[j], bias[j]) : fmaf(c[j], norm, bias[j]);
+            if (!plain || odd_bias) {
+                // a NaN orders below every number
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const float v = c[j] == c[j] ? c[j] : -FLT_MAX;
+                    c[j] = masked >> j & 1u ? -INFINITY : v;
+                }
             }
-        }
-        float best = -INFINITY;
+            // group scores
+            float best = -INFINITY;
+            bool kept = true;                                // this lane's group
+            if (p.groups > 1) {
+                float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) best = fmaxf(best, c[j]);
-        // a bound that at least top_k choice values reach: take the largest lane maximum
-        // away top_k times (equal ones together: the bound is then lower)
-        float bound = -INFINITY, v = best;
-        for (int k = 0; k < p.top_k; ++k) {
-            bound = warp_max(v);
-            v = v == bound ? -INFINITY : v;
-        }
-        int cnt = 0;
+                for (int j = 0; j < NV; ++j) {
+                    m2 = fmaxf(m2, fminf(m1, c[j]));
+                    m1 = fmaxf(m1, c[j]);
+                }
+                best = m1;
+                for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+                    const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+                    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+                    m1 = fmaxf(m1, o1);
+                }
+                const float gv = m2 <= -FLT_MAX ? m1 : m1 + m2;   // one expert left (or one that is not NaN): its own
+                int before = 0;                              // groups ahead of this one: each lane compares some
+                for (int g = 0; g < p.groups; g += p.lanes) {
+                    const int other = g + in_group;
+                    const float v = __shfl_sync(kAll, gv, other * p.lanes);
+                    before += other < p.groups && (v > gv || (v == gv && other < group));
+                }
+                for (int o = p.lanes >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(kAll, before, o);
+                kept = before < p.top_groups;
+                if (!kept) best = -INFINITY;
+            } else {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) cnt += c[j] >= bound;
-        const int upto = warp_inclusive_sum(cnt);
-        const int total = __shfl_sync(kAll, upto, 31);
-        int my_e = -1;
-        if (bound > -INFINITY && total <= 32) {
-            float2* at = &pool[warp][upto - cnt];
-            if (cnt > 0) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    if (c[j] >= bound) *at++ = make_float2(c[j], __int_as_float(e0 + j));
+                for (int j = 0; j < NV; ++j) best = fmaxf(best, c[j]);
             }
-            __syncwarp();
-            const float2 f = pool[warp][lane];
-            const float mine = lane < total ? f.x : -INFINITY;
-            int place = 0;
-            for (int i = 0; i < total; ++i) {
-                const float o = __shfl_sync(kAll, mine, i);
-                place += o > mine || (o == mine && i < lane);
+            // a bound that at least top_k choice values reach: take the largest lane maximum
+            // away top_k times (equal ones together: the bound is then lower)
+            float bound = -INFINITY, v = best;
+            auto lower = [&] {
+                bound = warp_max(v);
+                v = v == bound ? -INFINITY : v;
+            };
+            int k = p.top_k;
+            for (; k >= 4; k -= 4) {
+                lower();
+                lower();
+                lower();
+                lower();
             }
-            if (lane < total && place < p.top_k) order[warp][place] = __float_as_int(f.y);
-            __syncwarp();                                // and the pool has been read
-            if (lane < p.top_k) my_e = order[warp][lane];
-        } else {
-            for (int k = 0; k < p.top_k; ++k) {
-                const float m = warp_max(best);
-                if (m == -INFINITY) break;
-                const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
-                int e = -1;
-                if (lane == w) {
-                    bool found = false;
-                    best = -INFINITY;
+            for (; k > 0; --k) lower();
+            // the experts that reach it, a round for each lane's first, second, ...
+            uint32_t mine = 0;
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        if (!found && c[j] == m) {
-                            found = true;
-                            e = e0 + j;
-                            c[j] = -INFINITY;
+            for (int j = 0; j < NV; ++j) mine |= (c[j] >= bound ? 1u : 0u) << j;
+            if (!kept) mine = 0;
+            int n_at = 0;                                    // candidates
+            if (bound > -INFINITY) {
+                for (uint32_t with = __ballot_sync(kAll, mine != 0); with != 0; with = __ballot_sync(kAll, mine != 0)) {
+                    const int at = n_at + __popc(with & below);
+                    if (mine != 0 && at < W) pool[warp][W * h + at] = e0 + __ffs(mine) - 1;
+                    mine &= mine - 1;
+                    n_at += __popc(with);
+                }
+            }
+            if (n_at < p.top_k || n_at > W) {
+                // few lanes have an expert left, or many values are equal: the largest, top_k times
+                __syncwarp();
+                n_at = 0;
+                if (!kept) {
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) c[j] = -INFINITY;
+                }
+                for (; n_at < p.top_k; ++n_at) {
+                    const float m = warp_max(best);
+                    if (m == -INFINITY) break;
+                    const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
+                    if (lane == w) {
+                        bool found = false;
+                        best = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            if (!found && c[j] == m) {
+                                found = true;
+                                pool[warp][W * h + n_at] = e0 + j;
+                                c[j] = -INFINITY;
+                            }
+                            best = fmaxf(best, c[j]);
                         }
-                        best = fmaxf(best, c[j]);
                     }
                 }
-                e = __shfl_sync(kAll, e, w);
-                if (lane == k) my_e = e;
             }
+            if (which == h) total = n_at;
+        }
+        // The candidates' order: a lane takes one, and counts those before it.  Their
+        // choice values are made again, by the same operations, from their logits.
+        __syncwarp();
+        const long long row = row0 + which;
+        int my_e = -1;
+        float logit = -INFINITY, value = -INFINITY;
+        if (sub < total) {
+            my_e = pool[warp][lane];
+            logit = load_logit(p, row, my_e);
+            const float b = p.bias != nullptr ? p.bias[my_e] : 0.0f;
+            if (SIGMOID) value = __fadd_rn(rcp_approx(1.0f + exp2_approx(logit * -kLog2e)), b);
+            else value = fmaf(exp2_approx(ordinary ? fmaf(logit, kLog2e, -t) : (logit - top) * kLog2e), inv, b);
+            value = value == value ? value : -FLT_MAX;
+        }
+        __syncwarp();                                    // the pool has been read
+        int most = total;
+        if (W < 32) most = max(total, __shfl_xor_sync(kAll, total, W & 31));
+        int place = 0;
+        for (int i = 0; i < most; i += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) place += __shfl_sync(kAll, value, i + u, W) > value;
+        }
+        // places that nobody has: some values are equal, and go by index
+        const uint32_t taken = __reduce_or_sync(kAll, sub < total ? 1u << (W * which + place) : 0u);
+        if (__popc(taken) != __popc(__ballot_sync(kAll, sub < total))) {
+            for (int i = 0; i < most; ++i) {
+                const float o = __shfl_sync(kAll, value, i, W);
+                const int e = __shfl_sync(kAll, my_e, i, W);
+                place += o == value && e < my_e;
+            }
+        }
+        if (sub >= total) {
+            place = sub;                                 // no expert: -1 in the places left over
+        } else if (place >= p.top_k) {
+            my_e = -1;
+            logit = -INFINITY;
         }
         // the scores of the chosen, from their logits
         float w = 0.0f;
-        const float logit = my_e >= 0 ? load_logit(p, row, my_e) : -INFINITY;
         if (SIGMOID) {
             if (my_e >= 0) w = sigmoid_fast(logit);
         } else {
             // renormalised softmax = softmax over the chosen logits, which holds where
             // every chosen score underflows, too (a NaN sum stays one)
-            const float m = p.renormalize ? warp_max(logit) : top;
+            float m = top;
+            if (p.renormalize) {
+                m = logit;
+#pragma unroll
+                for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+            }
             if (my_e >= 0) w = exp_fast(logit - m) * (p.renormalize ? (inv == inv ? 1.0f : inv) : inv);
         }
         if (p.renormalize) {
-            const float t = warp_sum(w);
-            w = t == 0.0f ? 0.0f : __fdiv_rn(w, t);
+            float sum = w;
+#pragma unroll
+            for (int o = W / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            if (SIGMOID && sum < 1e-30f) w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+            else w = sum == 0.0f ? 0.0f : __fdividef(w, sum);
         }
-        if (lane < p.top_k) {
-            p.weights[row * p.top_k + lane] = w * p.scale;
-            p.chosen[row * p.top_k + lane] = my_e;
+        if (row < p.tokens && place < p.top_k) {
+            p.weights[row * p.top_k + place] = w * p.scale;
+            p.chosen[row * p.top_k + place] = my_e;
             if (my_e >= 0) atomicAdd(&hist[my_e], 1);
         }
     }
@@ -468,12 +541,16 @@ template <int NV>
 cudaError_t run_route(const RouteParams& p, int sms, cudaStream_t s) {
     const size_t smem = sizeof(int) * p.experts;
     const int grid = route_grid(p, sms, route_blocks<NV>());
+    // two tokens at once only where every warp has several
+    const bool two = p.top_k <= 16 && p.tokens > static_cast<long long>(grid) * kWarps;
     if (grid > 1) {
         const cudaError_t e = cudaMemsetAsync(p.counts, 0, smem, s);
         if (e != cudaSuccess) return e;
     }
-    if (p.sigmoid) k_route<NV, true><<<grid, kThreads, smem, s>>>(p);
-    else k_route<NV, false><<<grid, kThreads, smem, s>>>(p);
+    if (two && p.sigmoid) k_route<NV, true, 16><<<grid, kThreads, smem, s>>>(p);
+    else if (two) k_route<NV, false, 16><<<grid, kThreads, smem, s>>>(p);
+    else if (p.sigmoid) k_route<NV, true, 32><<<grid, kThreads, smem, s>>>(p);
+    else k_route<NV, false, 32><<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

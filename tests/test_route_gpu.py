@@ -285,3 +285,31 @@ def test_refusals():
         mg.muon_route_backward(w[:3], x, idx)
     with pytest.raises(ValueError, match="chosen"):
         mg.muon_route_backward(w, x, idx.long())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,k,groups,top_groups", [(384, 8, 8, 4), (384, 16, 1, 1), (40, 4, 1, 1), (96, 6, 3, 2), (64, 20, 1, 1),
+                                                   (12, 12, 1, 1)])
+def test_many_tokens_as_few(e, k, groups, top_groups, score):
+    """A long call takes tokens in pairs; each comes out as in a short call, next to
+    rows of equal values, masked ones and ones that are not numbers."""
+    t = 15001
+    _, x = grid_logits(t, e, e + k, torch.float32)
+    gen = torch.Generator(device=DEV).manual_seed(e)
+    kind = torch.randint(0, 12, (t,), generator=gen, device=DEV)
+    x[kind == 0] = 0.25                                  # all equal
+    x[kind == 1] = -math.inf
+    x[kind == 2] = torch.where(torch.rand(x[kind == 2].shape, generator=gen, device=DEV) < 0.8, -math.inf, 1.0)
+    x[kind == 3, e // 2] = math.nan
+    x[kind == 4] = x[kind == 4].round()                  # many equal
+    x[kind == 5] *= 1e36
+    bias = torch.round(torch.randn(e, generator=gen, device=DEV) * 8) / 64
+    kw = dict(bias=bias, score=score, groups=groups, top_groups=top_groups, scale=2.5)
+    for renorm in (True, False):
+        w, idx, counts = mg.muon_route(x, k, renormalize=renorm, **kw)
+        parts = [mg.muon_route(p, k, renormalize=renorm, **kw) for p in x.split(1000)]
+        assert torch.equal(idx, torch.cat([p[1] for p in parts]))
+        assert torch.equal(counts, torch.stack([p[2] for p in parts]).sum(0).int())
+        few = torch.cat([p[0] for p in parts])
+        assert torch.equal(w.isnan(), few.isnan())
+        assert bool(((w - few).abs() <= TOL * few.abs() + 1e-37).logical_or(w.isnan()).all())
