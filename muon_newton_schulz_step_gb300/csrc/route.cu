@@ -40,8 +40,9 @@
 // 32768 tokens x 384 experts in fp32, 4 of 8 groups: 73 us with the largest taken
 // top_k times for every token (about 1400 instructions each), 45 with the bound and
 // full-accuracy scores (1050), 34 with approximate ones (780), 28 with the second half
-// for two tokens at once (614; issue slots 75 % busy), 25 with the counts zeroed beside
-// it.  64 experts 16.8.
+// for two tokens at once (614; issue slots 75 % busy), 25.4 with the counts zeroed beside
+// it.  64 experts 17.5.  (Approximate divisions would save half a microsecond, and leave
+// the weights of a token 4e-9 above their sum on average.)
 //
 // Backward: one warp per token, lanes striped over the row in vectors of four.
 // Scores of the chosen are recomputed from their logits; only the softmax without
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
 #pragma unroll
                     for (int j = 0; j < NV; ++j) a += c[j] = masked >> j & 1u ? 0.0f : exp2_approx((c[j] - max_x) * kLog2e);
                 }
-                norm = __fdividef(1.0f, warp_sum(a));        // the sum is at least 1, or NaN
+                norm = __frcp_rn(warp_sum(a));
             }
             if (which == h) {
                 t = shift;
@@ -383,8 +384,7 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
             float sum = w;
 #pragma unroll
             for (int o = W / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (SIGMOID && sum < 1e-30f) w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
-            else w = sum == 0.0f ? 0.0f : __fdividef(w, sum);
+            w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
         }
         if (row < p.tokens && place < p.top_k) {
             p.weights[row * p.top_k + place] = w * p.scale;
