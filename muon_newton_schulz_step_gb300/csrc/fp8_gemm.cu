@@ -118,15 +118,16 @@ struct Tile {
     int kb0, nkb;    // reduction blocks
 };
 
-// n columns in equal tiles of at most 256, in multiples of `unit`: 32, or the 64
-// columns of the weight gradient's result blocks.  `even`: an even number of tiles,
-// for clusters of two pairs; the last may then be empty (its products are not stored).
-__device__ __forceinline__ int column_tiles(int n, bool even) {
-    return even ? (n + 2 * kTile - 1) / (2 * kTile) * 2 : (n + kTile - 1) / kTile;
+// n columns in equal tiles of at most 256 (2^shift: 256, 128 or 64), in multiples of
+// `unit`: 32, or the 64 columns of the weight gradient's result blocks.  `even`: an even
+// number of tiles, for clusters of two pairs; the last may then be empty (its products
+// are not stored).
+__device__ __forceinline__ int column_tiles(int n, int shift, bool even) {
+    return even ? (n + 2 * kTile - 1) / (2 * kTile) * 2 : (n + (1 << shift) - 1) >> shift;
 }
 
-__device__ __forceinline__ void split_columns(int n, int unit, bool even, int& tiles, int& width) {
-    tiles = column_tiles(n, even);
+__device__ __forceinline__ void split_columns(int n, int shift, int unit, bool even, int& tiles, int& width) {
+    tiles = column_tiles(n, shift, even);
     width = tiles > 0 ? ((n + tiles - 1) / tiles + unit - 1) / unit * unit : unit;
 }
 
@@ -138,7 +139,7 @@ __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups
     const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
     const int n = gw ? p.n_ext : gs.cnt[g];
-    const int nt = column_tiles(n, CS == 4), width = gs.width[g];
+    const int nt = column_tiles(n, p.col_shift, CS == 4), width = gs.width[g];
     int l = t - gs.tile0[g];
     const int full = nt / kPanel * kPanel;
     int m, c;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             const GroupSpan sp = warp_group_spans(p.offsets, p.groups, rows, g0, low);
             const int g = g0 + lane;
             int nt, width;
-            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, MODE == kFp8GradWeight ? 64 : 32, CS == 4, nt, width);
+            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, p.col_shift, MODE == kFp8GradWeight ? 64 : 32, CS == 4, nt, width);
             const int n = g < p.groups ? nt * mt : 0;
             const int nb = (sp.cnt + kFp8Block - 1) / kFp8Block;
             const int it = warp_inclusive_sum(n), ib = warp_inclusive_sum(nb);
@@ -952,11 +953,12 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cuda
         return p.mode == kFp8Forward ? run<kFp8Forward, 4>(p, clusters4, s)
                                      : run<kFp8GradInput, 4>(p, clusters4, s);
     }
-    const long long nt = p.mode == kFp8GradWeight ? static_cast<long long>(p.groups) * ((p.n_ext + kTile - 1) / kTile)
-                                                  : p.n_ext / kTile + p.groups;
+    const long long columns = (p.n_ext + (1 << p.col_shift) - 1) >> p.col_shift;
+    const long long nt = p.mode == kFp8GradWeight ? p.groups * columns
+                                                  : (p.groups == 1 ? columns : p.n_ext / kTile + p.groups);
     const long long most = mt * nt;
     if (p.slices > 1) {
-        const int tiles = static_cast<int>(mt * ((p.n_ext + kTile - 1) / kTile));
+        const int tiles = static_cast<int>(mt * columns);
         return p.slices == 2 ? run_slices<2>(p, tiles, s)
                : p.slices == 3 ? run_slices<3>(p, tiles, s)
                                : run_slices<4>(p, tiles, s);
@@ -997,24 +999,47 @@ void fp8_gemm_clusters(int (&n)[3]) {
     n[2] = ask(k_fp8_gemm<kFp8Forward, false, 2, 4>, 8);
 }
 
-// Pairs that share a tile's reduction.  A single weight with few tiles leaves most SMs
-// idle, while one pair's ring takes 0.2 us per block of 128 however narrow the tile: up
-// to four pairs of a cluster take a slice each, and add their sums through shared memory.
-// Their meeting costs a microsecond, so a slice has eight blocks or more; of the gradients
-// sixteen: the layer's other product wants the idle SMs too.  All clusters
-// have to fit at once, or a second wave starts.  Measured (forward, one pair -> slices):
-// 9 tokens x 2048 x 6144 16.5 us -> 12.3, 10.7, 10.3 with two, three, four; 9 x 6144 x
-// 6144 16.5 -> 12.3 with two (three, in two waves, 20.6); 256 x 6144 x 6144 20.7 -> 16.4;
-// 2048 x 2048 x 2048 12.1 -> 23.8 in two waves; backward of 2048 tokens of 520 x 1300 30.3
-// -> 39.0 with slices of eight blocks, of 8192 tokens 75.2 -> 70.1.
-int fp8_gemm_slices(const Fp8GemmParams& p, const int (&clusters)[3]) {
-    if (p.offsets != nullptr || p.groups != 1) return 1;
-    const long long tiles = static_cast<long long>((p.m_ext + kTile - 1) / kTile) * ((p.n_ext + kTile - 1) / kTile);
-    const int blocks = p.mode == kFp8GradWeight ? (p.rows + kFp8Block - 1) / kFp8Block : p.kblocks;
-    const int least = p.mode == kFp8Forward ? 8 : 16;
-    for (int s = 4; s > 1; --s)
-        if (blocks >= least * s && tiles <= clusters[s - 2]) return s;
-    return 1;
+// How a product of one weight is cut where 256 x 256 tiles leave SMs idle: into narrower
+// column tiles, and the reduction into slices, which up to four pairs of a cluster take
+// and add up through shared memory.  All of it has to fit at once, or a second wave
+// starts.  Forward, by what was measured: a block of 128 of the reduction takes a pair
+// 0.2 us in a tile of 64 columns or fewer (its ring waits for the weight) and 0.27 in one
+// of 256 (the tensor core's rate), all pairs together load 11 MB in a microsecond (8.4 in
+// narrow tiles), a full tile's results take 1.1 us, and a meeting 0.5 to 3.
+// One pair and 256 columns -> this, tokens x n x k: 9 x 6144 x 6144 16.4 us -> 12.4 (three
+// slices, in two waves, 20.6), 9 x 2048 x 6144 16.5 -> 10.1, 256 x 2048 x 6144 20.3 -> 13.2,
+// 1024 x 2048 x 6144 20.7 -> 18.1, 512 x 1024 x 1024 9.5 -> 8.0, 512 x 300 x 500 10.9 -> 7.6.
+// Gradients: the layer's other product wants the idle SMs too, and a slice pays from
+// sixteen blocks on (2048 tokens of 520 x 1300, backward: 30.3 us, 39.0 with slices of
+// eight blocks; 8192 tokens 75.2 -> 65).
+void fp8_gemm_cut(Fp8GemmParams& p, int sms, const int (&clusters)[3]) {
+    p.col_shift = 8;
+    p.slices = 1;
+    if (p.offsets != nullptr || p.groups != 1) return;
+    auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+    const long long mt = up(p.m_ext, kTile), pairs = sms / 2, whole = mt * up(p.n_ext, kTile);
+    const long long blocks = p.mode == kFp8GradWeight ? up(p.rows, kFp8Block) : p.kblocks;
+    if (p.mode != kFp8Forward) {
+        for (int s = 2; s <= 4; ++s)
+            if (blocks >= 16 * s && whole <= clusters[s - 2]) p.slices = s;
+        return;
+    }
+    float best = 0.0f;
+    for (int shift = 8; shift >= 6; --shift) {
+        const long long tiles = mt * up(p.n_ext, 1 << shift);
+        const float width = static_cast<float>(up(up(p.n_ext, up(p.n_ext, 1 << shift)), 32) * 32) / 256.0f;
+        const float loads = tiles * blocks * (1.0f + width) * 32.768e-3f / (width > 0.5f ? 11.0f : 8.4f);
+        for (int s = 1; s <= 4; ++s) {
+            if (tiles * s > pairs || (s > 1 && (blocks < 4 * s || tiles > clusters[s - 2]))) continue;
+            const float ring = up(up(blocks, 4), s) * 4 * (0.2f + 0.093f * fmaxf(0.0f, width - 0.25f));
+            const float t = 6.2f + 1.1f * width + fmaxf(ring, loads) + (s > 1 ? 0.5f + width * (s == 2 ? 1.3f : 2.6f) : 0.0f);
+            if (best == 0.0f || t < 0.98f * best) {
+                best = t;
+                p.col_shift = shift;
+                p.slices = s;
+            }
+        }
+    }
 }
 
 cudaError_t read_and_clear_fp8_error(int* code) {

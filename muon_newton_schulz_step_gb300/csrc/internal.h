@@ -316,6 +316,7 @@ struct Fp8GemmParams {
     int mode;
     int sync;                 // Fp8Sync
     int multicast;            // forward, grad input: clusters of two pairs share A (tm_a: boxes of 64)
+    int col_shift;            // column tiles of at most 2^col_shift: 8, 7 or 6
     int slices;               // pairs of a cluster that share each tile's reduction; 1: none
     int out_f32;
     int vec;                  // output rows start on 16 bytes (forward, grad input: bf16 only)
@@ -331,7 +332,7 @@ struct Fp8GemmParams {
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s);
 void fp8_gemm_clusters(int (&n)[3]);
-int fp8_gemm_slices(const Fp8GemmParams& p, const int (&clusters)[3]);
+void fp8_gemm_cut(Fp8GemmParams& p, int sms, const int (&clusters)[3]);
 bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
                         int clusters4);
 

@@ -364,7 +364,7 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
         const long long padded = muon_fp8_padded_rows(tokens, groups);
         p.n_ext = k;
         p.out_batch = static_cast<long long>(n) * ld_out;
-        p.slices = fp8_gemm_slices(p, clusters);
+        fp8_gemm_cut(p, sms, clusters);
         p.s_a = {as, 0, 1, ldn, 0, static_cast<int>(ldn)};
         p.s_b = {bs, 0, 1, ldk, 0, static_cast<int>(ldk)};
         if ((rc = op_encode_bytes(&p.tm_a, a_codes, ldn, padded, 1, 128, 128)) != MUON_OK) return rc;
@@ -378,8 +378,8 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
         p.s_a = fwd ? Fp8Scale{bs, nb * kb, kb, 1, 7, static_cast<int>(ldn)}
                      : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
         p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
-        p.slices = fp8_gemm_slices(p, clusters);
-        p.multicast = p.slices == 1 && fp8_gemm_multicast(product, inner, tokens, p.kblocks, groups, sms, clusters[0]);
+        fp8_gemm_cut(p, sms, clusters);
+        p.multicast = p.slices == 1 && p.col_shift == 8 && fp8_gemm_multicast(product, inner, tokens, p.kblocks, groups, sms, clusters[0]);
         if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, p.multicast ? 64 : 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;

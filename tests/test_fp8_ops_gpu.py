@@ -523,3 +523,29 @@ def test_few_tiles_and_a_long_reduction(product, t, inner, red, out):
         mg.muon_fp8_product(product, p, m, out=wide[:, :inner])
         assert torch.equal(wide[:, :inner], first) and bool((wide[:, inner:] == 55.0).all())
     assert mg.muon_device_status() == 0
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("t,n,k", [(512, 300, 500), (500, 301, 500), (512, 1024, 1024), (256, 2048, 4100), (130, 520, 2000),
+                                   (700, 130, 130), (1000, 2047, 2048), (65, 256, 6144)])
+def test_narrow_tiles(t, n, k, out):
+    """Sizes that are cut into column tiles of 64 or 128, some with slices of the reduction."""
+    test_few_tiles_and_a_long_reduction("forward", t, n, k, out)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("at", range(9))
+def test_codes_of_windows(at, dtype):
+    """A window of a larger matrix that starts and ends anywhere, in edge tiles in
+    every direction: what lies around it shows in no code and no scale."""
+    for rows, cols, ld in ((150, 131, 143), (150, 137, 160), (97, 263, 264), (260, 120, 129)):
+        _, part = data(rows, cols, at + cols, dtype)
+        whole = torch.full((at + rows * ld + 7,), math.nan, dtype=dtype, device=DEV)
+        x = whole.as_strided((rows, cols), (ld, 1), at)
+        x.copy_(part)
+        for row, col in ((True, False), (False, True), (True, True)):
+            got, want = mg.muon_fp8_quantize(x, row=row, col=col), mg.muon_fp8_quantize(part, row=row, col=col)
+            for g, w in zip(got, want):
+                assert (g is None) == (w is None)
+                if g is not None:
+                    assert torch.equal(g.codes.view(torch.uint8), w.codes.view(torch.uint8)) and torch.equal(g.scale, w.scale)
