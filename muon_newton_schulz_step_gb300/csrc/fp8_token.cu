@@ -4,7 +4,7 @@
 // Serving makes this product for one token at a time: its time is the weight's
 // bytes, read once, and the launch.  The tiled product would load 128 rows per CTA
 // on a third of the SMs and needs the codes of x from a launch before it.  One token
-// x 6144 x 6144: 18.5 us by tiles, 9.2 here (12.3 with the weight from memory, 3.1 TB/s;
+// x 6144 x 6144: 13.8 us by tiles, 9.2 here (12.3 with the weight from memory, 3.1 TB/s;
 // the launch and the rounding of x take about 4).  With experts the tiles fill the SMs
 // and win (32 tokens over 16 experts of 2048 x 6144: 43 us against 56 here), so this
 // kernel serves single weights.
@@ -233,14 +233,17 @@ cudaError_t run(const Fp8TokenParams& p, cudaStream_t s) {
 }  // namespace
 
 // Whether this kernel serves a call: the tokens take one matrix fragment, their codes
-// fit in shared memory, and rounding x in every block does not cost more than the
-// launch that the tiles need for it.  Measured, this kernel against tiles: 8 tokens
-// x 2048 x 6144 (1.0e8 products) 15.8 against 18.8 us, 4 x 6144 x 6144 (1.5e8) 15.0
-// against 18.9, 8 x 6144 x 6144 (3.0e8) 25.8 against 18.4.
+// fit in shared memory, the blocks are resident at once (three per SM), and rounding x
+// in every block costs no more than tiles and the launch that they need for it.  That
+// costs 1.35 us per token and 6144 elements of k, and 2 us and n / 1280 us per 6144 the
+// rest; tiles take 6 us more to begin with, 0.4 + n / 10300 less per 6144.  Measured, this
+// kernel against tiles, the weight in L2: 3 tokens x 6144 x 6144 12.9 us, 13.8; 4 tokens
+// 14.3; 4 x 2048 x 6144 9.7, 11.4; 8 tokens 14.9; 8 x 6144 x 2048 8.7, 9.7; 1 x 16384 x
+// 6144 26.0, 20.8.
 bool fp8_token_serves(long long tokens, long long n, long long k) {
     const long long ldk = (k + 127) / 128 * 128;
     return tokens <= kTokens && token_smem(static_cast<int>(tokens), ldk) <= static_cast<size_t>(kMaxCodes) &&
-           tokens * n * k <= 160000000ll;
+           n <= 152 * 3 * kRows && k * (14000 * (tokens - 1) + 4000 + n) <= 310000000ll;
 }
 
 cudaError_t launch_fp8_token(const Fp8TokenParams& p, cudaStream_t s) {
