@@ -932,12 +932,12 @@ cudaError_t run_slices(const Fp8GemmParams& p, int tiles, cudaStream_t s) {
 
 // Whether clusters of two pairs serve a product: one weight that many column tiles
 // share, a long reduction, and no wave of tiles more than pairs need (a wave of
-// clusters takes 0.95 of one of pairs).  Measured, pairs against clusters:
-// 8192 x 6144 x 6144 185 against 176 us, 2048 x 6144 x 6144 57.4 against 55.4; but
-// 9728 x 4096 x 6144 (8 waves of 76 pairs, 9 of 36 clusters) 139 against 143,
-// 4096 x 6144 x 512 24.5 against 26.6, 8192 x 1024 x 1024 18.5 against 19.9, and weights
-// of 8 to 96 experts 3 to 12 % slower (two pairs hold half as many different weight
-// bytes on their way).
+// clusters takes 0.95 of one of pairs).  Measured, pairs against clusters: 8192 x 6144 x
+// 6144 178.5 against 172.5 us, 4096 x 4096 x 4096 47.6 against 45.7, 2048 x 6144 x 6144
+// 49.9 against 49.3; and, with a stage less, 9728 x 4096 x 6144 (8 waves of 76 pairs, 9 of
+// 36 clusters) 139 against 143, 4096 x 6144 x 512 24.5 against 26.6, 8192 x 1024 x 1024
+// 18.5 against 19.9, and weights of 8 to 96 experts 3 to 12 % slower (two pairs hold half
+// as many different weight bytes on their way).
 bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
                         int clusters4) {
     if (clusters4 < 1 || mode == kFp8GradWeight || groups != 1 || kblocks < 16) return false;
