@@ -318,7 +318,8 @@ MUON_API int muon_grad_clip(void* const* G, void* const* out, const long long* n
  *   s = softmax(logits) or sigmoid(logits); c = s + bias (NULL: 0), for the
  *   choice only; of the `groups` equal groups of experts the top_groups with the
  *   largest sum of their two largest c stay; of their experts the top_k largest c
- *   are chosen, in descending order, equal values by ascending index.
+ *   are chosen, in descending order, equal values by ascending index (an s below
+ *   2^-126 counts as 0 in c).
  *   weights = scale * s / (sum of the chosen s) (renormalize) or scale * s.
  *   logits   tokens x experts, `dtype`, row stride ld >= experts
  *   weights  tokens x top_k (fp32);  chosen  tokens x top_k

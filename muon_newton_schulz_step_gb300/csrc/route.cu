@@ -36,7 +36,8 @@
 // operations, counts those before it (its place in the result), and computes its weight
 // anew at full accuracy.  Two tokens go through that second half side by side, 16 lanes
 // each, where top_k and the number of tokens allow it.  The choice works on scores from
-// one ex2 and one rcp.  Bound by instructions:
+// one ex2 and one rcp, and takes those below 2^-126 as zero, so as equal.  Bound by
+// instructions:
 // 32768 tokens x 384 experts in fp32, 4 of 8 groups: 73 us with the largest taken
 // top_k times for every token (about 1400 instructions each), 45 with the bound and
 // full-accuracy scores (1050), 34 with approximate ones (780), 28 with the second half
@@ -114,6 +115,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 constexpr float kLog2e = 1.44269504f;
 
+// e^(x - max): the difference first.  x log2(e) - (max log2(e) rounded), one operation
+// less, is off by up to half a unit in the last place of max log2(e) in the exponent:
+// 1e-5 of the scores at 200, and no number at all from 1e9 on.
+__device__ __forceinline__ float exp_choice(float x, float max) { return exp2_approx((x - max) * kLog2e); }
+
 // This lane's logits, -inf where it owns no expert.
 template <int NV>
 __device__ __forceinline__ void load_lane(const RouteParams& p, long long row, int e0, int n, float (&x)[NV]) {
@@ -178,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
     for (long long row0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; row0 < p.tokens; row0 += step) {
         // of this lane's token: candidates, and what their scores need
         int total = 0;
-        float t = 0.0f, top = 0.0f, inv = 1.0f;
-        bool ordinary = true;
+        float top = 0.0f, inv = 1.0f;
 #pragma unroll 1
         for (int h = 0; h < kTokens; ++h) {
             const long long row = row0 + h;
@@ -198,37 +203,27 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
                     m = fmaxf(m, c[j]);
                     seen += c[j];
                 }
-                max_x = warp_max(m);
+                m = warp_max(m);
+                if (m > -INFINITY) max_x = m;                // every expert masked: all scores zero
             }
-            const bool plain = __all_sync(kAll, fabsf(seen) <= FLT_MAX) && max_x > -FLT_MAX;
+            const bool plain = __all_sync(kAll, fabsf(seen) <= FLT_MAX);
             uint32_t masked = 0;                             // bit j: no expert, or masked
             if (!plain) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) masked |= (c[j] == -INFINITY ? 1u : 0u) << j;
             }
-            // softmax, finite logits of ordinary size: 2^(x log2(e) - shift) with one shift for
-            // all, whose rounding the normalisation takes out again
-            const bool usual = plain && fabsf(max_x) < 1e30f;
-            const float shift = max_x * kLog2e;
             if (SIGMOID) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) c[j] = rcp_approx(1.0f + exp2_approx(c[j] * -kLog2e));
             } else {
                 float a = 0.0f;
-                if (usual) {
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) a += c[j] = exp2_approx(fmaf(c[j], kLog2e, -shift));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < NV; ++j) a += c[j] = masked >> j & 1u ? 0.0f : exp2_approx((c[j] - max_x) * kLog2e);
-                }
+                for (int j = 0; j < NV; ++j) a += c[j] = exp_choice(c[j], max_x);
                 norm = __frcp_rn(warp_sum(a));
             }
             if (which == h) {
-                t = shift;
                 top = max_x;
                 inv = norm;
-                ordinary = usual;
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) c[j] = SIGMOID ? __fadd_rn(c[j], bias[j]) : fmaf(c[j], norm, bias[j]);
@@ -339,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
             logit = load_logit(p, row, my_e);
             const float b = p.bias != nullptr ? p.bias[my_e] : 0.0f;
             if (SIGMOID) value = __fadd_rn(rcp_approx(1.0f + exp2_approx(logit * -kLog2e)), b);
-            else value = fmaf(exp2_approx(ordinary ? fmaf(logit, kLog2e, -t) : (logit - top) * kLog2e), inv, b);
+            else value = fmaf(exp_choice(logit, top), inv, b);
             value = value == value ? value : -FLT_MAX;
         }
         __syncwarp();                                    // the pool has been read
