@@ -119,27 +119,23 @@ struct Tile {
 };
 
 // n columns in equal tiles of at most 256 (2^shift: 256, 128 or 64), in multiples of
-// `unit`: 32, or the 64 columns of the weight gradient's result blocks.  `even`: an even
-// number of tiles, for clusters of two pairs; the last may then be empty (its products
-// are not stored).
-__device__ __forceinline__ int column_tiles(int n, int shift, bool even) {
-    return even ? (n + 2 * kTile - 1) / (2 * kTile) * 2 : (n + (1 << shift) - 1) >> shift;
-}
+// `unit`: 32, or the 64 columns of the weight gradient's result blocks.
+__device__ __forceinline__ int column_tiles(int n, int shift) { return (n + (1 << shift) - 1) >> shift; }
 
-__device__ __forceinline__ void split_columns(int n, int shift, int unit, bool even, int& tiles, int& width) {
-    tiles = column_tiles(n, shift, even);
+__device__ __forceinline__ void split_columns(int n, int shift, int unit, int& tiles, int& width) {
+    tiles = column_tiles(n, shift);
     width = tiles > 0 ? ((n + tiles - 1) / tiles + unit - 1) / unit * unit : unit;
 }
 
 // Tile t of the launch; `g` only moves forward.  Integer divisions are avoided:
 // four of them took 900 cycles of every tile in every role.
-template <int CS, int SK>
+template <int SK>
 __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups& gs, int t, int& g, int pp) {
     while (t >= gs.tile0[g + 1]) ++g;
     const int mt = (p.m_ext + kTile - 1) / kTile;
     const bool gw = p.mode == kFp8GradWeight;
     const int n = gw ? p.n_ext : gs.cnt[g];
-    const int nt = column_tiles(n, p.col_shift, CS == 4), width = gs.width[g];
+    const int nt = column_tiles(n, p.col_shift), width = gs.width[g];
     int l = t - gs.tile0[g];
     const int full = nt / kPanel * kPanel;
     int m, c;
@@ -158,6 +154,8 @@ __device__ __forceinline__ Tile decode_tile(const Fp8GemmParams& p, const Groups
     x.g = g;
     x.m0 = m * kTile;
     const int off = c * width;
+    // A tile has a column, so neither bound takes effect; without them the compiler's
+    // schedule costs the experts' forward 4 % (443 against 427 us).
     x.cols = max(0, n - off < width ? n - off : width);
     const int unit = gw ? 64 : 32;
     x.width = max(unit, (x.cols + unit - 1) / unit * unit);
@@ -259,14 +257,10 @@ struct ScaleGroup<kFp8GradWeight> {
     }
 };
 
-// CS: CTAs per cluster, 2 (one pair) or 4 (two pairs with neighbouring column tiles
-// of the same rows, which share the A operand by multicast).
-// SK: pairs of a cluster that share one tile's reduction, each a slice of it (CS 2;
-// one tile per cluster).
-template <int MODE, bool F32, int CS, int SK = 1>
+// SK: pairs of a cluster that share one tile's reduction, each a slice of it (one tile
+// per cluster); 1: a cluster is one pair.
+template <int MODE, bool F32, int SK>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmParams p) {
-    static_assert(CS == 2 || (CS == 4 && MODE != kFp8GradWeight), "cluster size");
-    static_assert(SK == 1 || CS == 2, "slices of the reduction");
     constexpr int kStages = Ring<MODE>::stages;
     constexpr uint32_t kEpiBytes = Ring<MODE>::block;
     constexpr bool kAMn = MODE != kFp8Forward;          // A operand MN-major
@@ -287,14 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     const uint32_t rank = crank & 1u, lead = crank & ~1u;   // in the pair; cluster rank of the pair's leader
     const int pp = static_cast<int>(crank >> 1);            // pair in the cluster
     const bool leader = rank == 0;
-    const int pair = static_cast<int>(ptx::cluster_id_x()) * (CS / 2) + (SK == 1 ? pp : 0);
-    const int npairs = static_cast<int>(ptx::num_clusters_x()) * (CS / 2);
+    const int pair = static_cast<int>(ptx::cluster_id_x());     // the tiles are dealt to clusters
+    const int npairs = static_cast<int>(ptx::num_clusters_x());
     const uint64_t limit = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
 
     if (threadIdx.x == 32) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&b.full[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.empty[s]), CS / 2);   // every pair that reads the stage
+            ptx::mbar_init(ptx::smem_addr(&b.empty[s]), 1);
         }
         for (int s = 0; s < kScaleStages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&b.sfull[s]), 2);
@@ -320,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             const GroupSpan sp = warp_group_spans(p.offsets, p.groups, rows, g0, low);
             const int g = g0 + lane;
             int nt, width;
-            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, p.col_shift, MODE == kFp8GradWeight ? 64 : 32, CS == 4, nt, width);
+            split_columns(MODE == kFp8GradWeight ? p.n_ext : sp.cnt, p.col_shift, MODE == kFp8GradWeight ? 64 : 32, nt, width);
             const int n = g < p.groups ? nt * mt : 0;
             const int nb = (sp.cnt + kFp8Block - 1) / kFp8Block;
             const int it = warp_inclusive_sum(n), ib = warp_inclusive_sum(nb);
@@ -363,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs) {
-                const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
+                const Tile x = decode_tile<SK>(p, gs, t, g, pp);
                 const int m = x.m0 + static_cast<int>(rank) * kHalf;
                 const int half = x.width / 2;
                 const int c = x.c0 + static_cast<int>(rank) * half;
@@ -387,13 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                         if (leader) ptx::mbar_arrive_expect_tx(local, bytes);
                         const uint32_t di = ptx::smem_addr(sm_a + stage * kStageA);
                         const uint32_t d_o = ptx::smem_addr(sm_b + stage * kStageB);
-                        if constexpr (CS == 4) {
-                            // half of this CTA's A tile, for itself and its counterpart in the other pair
-                            const uint16_t mask = static_cast<uint16_t>((1u << rank) | (1u << (2u + rank)));
-                            const int h = pp * (kHalf / 2);
-                            ptx::tma_load_3d_pair_mc(di + pp * (kStageA / 2), &p.tm_a, fb, kAMn ? m : kb * kFp8Block,
-                                                     kAMn ? kb * kFp8Block + h : m + h, gb, mask);
-                        } else if (kAMn) {
+                        if (kAMn) {
                             ptx::tma_load_3d_pair(di, &p.tm_a, fb, m, kb * kFp8Block, gb);
                         } else {
                             ptx::tma_load_3d_pair(di, &p.tm_a, fb, kb * kFp8Block, m, gb);
@@ -438,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             uint32_t phase = 0, sphase = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += npairs, ++it) {
-                const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
+                const Tile x = decode_tile<SK>(p, gs, t, g, pp);
                 const int acc = it & 1;
                 const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
                 // The copy of four blocks' scale words is issued a block before the first
@@ -497,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::mma_mxf8_pair(d, ad + kk * a_k, bd + kk * b_k, idesc, sfa, sfa + 4,
                                                (kk != 0 || kb != x.kb0) ? 1u : 0u);
-                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), CS == 4 ? 0xFu : mine);
+                        ptx::mma_commit_pair(ptx::smem_addr(&b.empty[stage]), mine);
                     }
                     __syncwarp();
                     if (++stage == kStages) {
@@ -533,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             return true;
         };
         for (int t = pair; ok && t < tiles; t += npairs) {
-            const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
+            const Tile x = decode_tile<SK>(p, gs, t, g, pp);
             const int m = x.m0 + static_cast<int>(rank) * kHalf;
             for (int i = 0; ok && i < x.nkb; i += 4, ++seq) {
                 if ((seq & 1) != warp - 2) continue;
@@ -568,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         int it = 0, g = 0;
         bool met = false;                                // SK > 1: the pairs have exchanged their sums
         for (int t = pair; t < tiles; t += npairs, ++it) {
-            const Tile x = decode_tile<CS, SK>(p, gs, t, g, pp);
+            const Tile x = decode_tile<SK>(p, gs, t, g, pp);
             const int acc = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1) & 1u;
             const int m0 = x.m0 + static_cast<int>(rank) * kHalf + q * 32;
@@ -891,68 +879,47 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<kFp8Forward>() <= 232448 && smem_bytes<kFp8GradWeight>() <= 232448, "shared memory");
 
-template <int MODE, bool F32, int CS, int SK>
+template <int MODE, bool F32, int SK>
 cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, CS, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE, F32, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem_bytes<MODE>()));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CS * SK * clusters);
+    cfg.gridDim = dim3(2 * SK * clusters);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<MODE>();
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CS * SK;
+    at[0].val.clusterDim.x = 2 * SK;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.sync != kSyncNone ? 2 : 1;
-    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, CS, SK>, p);
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, k_fp8_gemm<MODE, F32, SK>, p);
     return l != cudaSuccess ? l : cudaGetLastError();
 }
 
-template <int MODE, int CS, int SK = 1>
+template <int MODE, int SK>
 cudaError_t run(const Fp8GemmParams& p, int clusters, cudaStream_t s) {
-    return p.out_f32 ? run<MODE, true, CS, SK>(p, clusters, s) : run<MODE, false, CS, SK>(p, clusters, s);
+    return p.out_f32 ? run<MODE, true, SK>(p, clusters, s) : run<MODE, false, SK>(p, clusters, s);
 }
 
 template <int SK>
 cudaError_t run_slices(const Fp8GemmParams& p, int tiles, cudaStream_t s) {
     switch (p.mode) {
-        case kFp8Forward: return run<kFp8Forward, 2, SK>(p, tiles, s);
-        case kFp8GradInput: return run<kFp8GradInput, 2, SK>(p, tiles, s);
-        default: return run<kFp8GradWeight, 2, SK>(p, tiles, s);
+        case kFp8Forward: return run<kFp8Forward, SK>(p, tiles, s);
+        case kFp8GradInput: return run<kFp8GradInput, SK>(p, tiles, s);
+        default: return run<kFp8GradWeight, SK>(p, tiles, s);
     }
 }
 
 }  // namespace
 
-// Whether clusters of two pairs serve a product: one weight that many column tiles
-// share, a long reduction, and no wave of tiles more than pairs need (a wave of
-// clusters takes 0.95 of one of pairs).  Measured, pairs against clusters: 8192 x 6144 x
-// 6144 178.5 against 172.5 us, 4096 x 4096 x 4096 47.6 against 45.7, 2048 x 6144 x 6144
-// 49.9 against 49.3; and, with a stage less, 9728 x 4096 x 6144 (8 waves of 76 pairs, 9 of
-// 36 clusters) 139 against 143, 4096 x 6144 x 512 24.5 against 26.6, 8192 x 1024 x 1024
-// 18.5 against 19.9, and weights of 8 to 96 experts 3 to 12 % slower (two pairs hold half
-// as many different weight bytes on their way).
-bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
-                        int clusters4) {
-    if (clusters4 < 1 || mode == kFp8GradWeight || groups != 1 || kblocks < 16) return false;
-    const long long mt = (m_ext + kTile - 1) / kTile;
-    const long long pairs = mt * ((tokens + kTile - 1) / kTile), fours = mt * ((tokens + 2 * kTile - 1) / (2 * kTile));
-    const long long waves2 = (pairs + sms / 2 - 1) / (sms / 2), waves4 = (fours + clusters4 - 1) / clusters4;
-    return fours >= clusters4 && 95 * waves4 < 100 * waves2;
-}
-
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s) {
     const long long mt = (p.m_ext + kTile - 1) / kTile;
-    if (p.multicast) {
-        return p.mode == kFp8Forward ? run<kFp8Forward, 4>(p, clusters4, s)
-                                     : run<kFp8GradInput, 4>(p, clusters4, s);
-    }
     const long long columns = (p.n_ext + (1 << p.col_shift) - 1) >> p.col_shift;
     const long long nt = p.mode == kFp8GradWeight ? p.groups * columns
                                                   : (p.groups == 1 ? columns : p.n_ext / kTile + p.groups);
@@ -965,9 +932,9 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cuda
     }
     const int pairs = static_cast<int>(most < sms / 2 ? (most > 0 ? most : 1) : sms / 2);
     switch (p.mode) {
-        case kFp8Forward: return run<kFp8Forward, 2>(p, pairs, s);
-        case kFp8GradInput: return run<kFp8GradInput, 2>(p, pairs, s);
-        default: return run<kFp8GradWeight, 2>(p, pairs, s);
+        case kFp8Forward: return run<kFp8Forward, 1>(p, pairs, s);
+        case kFp8GradInput: return run<kFp8GradInput, 1>(p, pairs, s);
+        default: return run<kFp8GradWeight, 1>(p, pairs, s);
     }
 }
 
@@ -994,9 +961,9 @@ void fp8_gemm_clusters(int (&n)[3]) {
         }
         return most;
     };
-    n[0] = ask(k_fp8_gemm<kFp8Forward, false, 4>, 4);
-    n[1] = ask(k_fp8_gemm<kFp8Forward, false, 2, 3>, 6);
-    n[2] = ask(k_fp8_gemm<kFp8Forward, false, 2, 4>, 8);
+    n[0] = ask(k_fp8_gemm<kFp8Forward, false, 2>, 4);
+    n[1] = ask(k_fp8_gemm<kFp8Forward, false, 3>, 6);
+    n[2] = ask(k_fp8_gemm<kFp8Forward, false, 4>, 8);
 }
 
 // How a product of one weight is cut where 256 x 256 tiles leave SMs idle: into narrower

@@ -315,7 +315,6 @@ struct Fp8GemmParams {
     long long out_batch;      // grad weight: elements between groups' outputs
     int mode;
     int sync;                 // Fp8Sync
-    int multicast;            // forward, grad input: clusters of two pairs share A (tm_a: boxes of 64)
     int col_shift;            // column tiles of at most 2^col_shift: 8, 7 or 6
     int slices;               // pairs of a cluster that share each tile's reduction; 1: none
     int out_f32;
@@ -330,11 +329,9 @@ struct Fp8GemmParams {
     unsigned long long wait_ns;
 };
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, int clusters4, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int sms, cudaStream_t s);
 void fp8_gemm_clusters(int (&n)[3]);
 void fp8_gemm_cut(Fp8GemmParams& p, int sms, const int (&clusters)[3]);
-bool fp8_gemm_multicast(int mode, long long m_ext, long long tokens, long long kblocks, int groups, int sms,
-                        int clusters4);
 
 // The forward product of few tokens and one weight, x rounded on the way.
 struct Fp8TokenParams {

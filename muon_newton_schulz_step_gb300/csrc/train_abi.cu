@@ -379,15 +379,14 @@ int fp8_product(int product, const void* a_codes, const void* a_scale, const voi
                      : Fp8Scale{bs, nb * kb, 1, kb, 7, static_cast<int>(ldk)};
         p.s_b = {as, 0, 1, tokens, 0, static_cast<int>(tokens)};
         fp8_gemm_cut(p, sms, clusters);
-        p.multicast = p.slices == 1 && p.col_shift == 8 && fp8_gemm_multicast(product, inner, tokens, p.kblocks, groups, sms, clusters[0]);
-        if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, p.multicast ? 64 : 128)) != MUON_OK) return rc;
+        if ((rc = op_encode_bytes(&p.tm_a, b_codes, ldk, n, groups, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_b, a_codes, lda, tokens, 1, 128, 128)) != MUON_OK) return rc;
         if ((rc = op_encode_bytes(&p.tm_part, a_codes, lda, tokens, 1, 128, 32)) != MUON_OK) return rc;
     }
     if (p.vec && !gw && (rc = op_encode_result(&p.tm_res, out, inner, tokens, ld_out)) != MUON_OK) return rc;
     const double t = static_cast<double>(tokens), flops = 2.0 * t * n * k;
     const double bytes = t * (gw ? n + k : fmax(n, k)) + static_cast<double>(groups) * n * k * (gw ? dtype_size(out_dtype) : 1);
-    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, clusters[0], stream); });
+    return op_launch(kOpFp8Gemm, flops, bytes, stream, [&] { return launch_fp8_gemm(p, sms, stream); });
 }
 
 }  // namespace

@@ -1,0 +1,19 @@
+"""What the compiled sources may not hold.
+
+One library serves every rank of a job, so its tensor loads stay within a CTA
+pair: a load that is multicast over a cluster belongs in code that only runs on
+one GPU use."""
+import glob
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "muon_newton_schulz_step_gb300", "csrc")
+
+
+def sources(pattern):
+    return [(os.path.basename(f), open(f).read()) for f in sorted(glob.glob(os.path.join(CSRC, pattern)))]
+
+
+def test_products_of_8_bits_load_without_multicast():
+    for name, text in sources("fp8_*.cu"):
+        assert not re.search(r"tma_load\w*_mc\b", text), name
