@@ -96,8 +96,6 @@ struct GemmBucket {
     CUtensorMap tmT;          // upper-only symmetric operand (polynomial: A, update: B): box {64, 64, 1}
                               // over its rows, read as MN-major blocks of the transpose
     CUtensorMap tmQ;          // update before an FP8 Gram: E4M3 copy of X' * 2^8, bytes, box {32, 32, 1}
-    int nt2;                  // update on clusters of two pairs: tile pairs along N, ceil(nt / 2)
-    int item0;                // update on clusters of two pairs: first global tile pair of this bucket
 };
 
 struct GemmParams {
@@ -108,7 +106,6 @@ struct GemmParams {
     float a, bcoef, c;
     unsigned long long wait_ns;   // limit of every wait of the launch; 0: the default (2 s)
     int stall;                    // test hook (pair kernel): no MMA is issued, so the waits expire
-    int total_items;              // update on clusters of two pairs: tile pairs of the launch
     int fp8;                      // Gram: E4M3 operands (tmA / tmB over the E4M3 copy, kblocks of 128)
     int fp8_next;                 // update (TMA epilogue): also writes the E4M3 copy of X' through tmQ
     // 1: the symmetric products (Gram, polynomial) store only their tiles with
@@ -358,16 +355,12 @@ cudaError_t launch_norm_finalize(const EwParams& p, cudaStream_t s);
 cudaError_t launch_pack(const EwParams& p, int sms, bool from_momentum, cudaStream_t s);
 cudaError_t launch_unpack(const EwParams& p, int sms, bool weight_update, cudaStream_t s);
 // Pair-CTA variant (ns_gemm_pair.cu): 256 x 256 tiles on clusters of two CTAs.
-// The update product (p.mode == kUpdate) runs on clusters of two pairs that
-// share the A operand by multicast when `multicast` is set and such clusters
-// fit on the device (p.total_items and the buckets' nt2 / item0 must be set);
 // `sms` bounds the grid.
 // `tma_epilogue`: the update moves its epilogue input and output by TMA
 // (the buckets' tmE / tmO must be set).
-cudaError_t launch_gemm_pair(const GemmParams& p, int sms, bool multicast, bool tma_epilogue, cudaStream_t s);
+cudaError_t launch_gemm_pair(const GemmParams& p, int sms, bool tma_epilogue, cudaStream_t s);
 // The same kernel with the fused final epilogue (p.mode must be kUpdate).
-cudaError_t launch_gemm_pair_final(const GemmParams& p, const FinalParams& f, int kind, int sms, bool multicast,
-                                   cudaStream_t s);
+cudaError_t launch_gemm_pair_final(const GemmParams& p, const FinalParams& f, int kind, int sms, cudaStream_t s);
 size_t gemm_pair_smem_bytes();
 cudaError_t read_and_clear_pair_error(int* code);
 

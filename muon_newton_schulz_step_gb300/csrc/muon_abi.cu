@@ -576,11 +576,9 @@ int run(const Call& c, const Plan& pl, DeviceState& d, char* ws, cudaStream_t s,
     });
     std::unique_ptr<GemmParams> gp(new GemmParams());
     // Pair-CTA tiles: 256 x 256 outputs on two SMs
-    // the update product on clusters of two pairs sharing A by multicast
-    const bool multicast = env_flag("MUON_GEMM_MULTICAST");
     // the symmetric products store only their upper tiles (their consumers read the
-    // rest from the transpose); MUON_GEMM_MIRROR=1, or multicast, keeps full storage
-    const bool upper_only = !multicast && !env_flag("MUON_GEMM_MIRROR");
+    // rest from the transpose); MUON_GEMM_MIRROR=1 keeps full storage
+    const bool upper_only = !env_flag("MUON_GEMM_MIRROR");
     // the update's epilogue input and output moved by TMA
     const bool tma_epilogue = fp8 || !env_flag("MUON_GEMM_NO_TMA_EPI");
     const int tm_rows = 256;   // output rows per tile
@@ -629,7 +627,7 @@ int run(const Call& c, const Plan& pl, DeviceState& d, char* ws, cudaStream_t s,
                 p.a = c.coef[3 * it];
                 p.bcoef = c.coef[3 * it + 1];
                 p.c = c.coef[3 * it + 2];
-                int tile = 0, items = 0;
+                int tile = 0;
                 double flops = 0;
                 for (int gi = 0; gi < ng; ++gi) {
                     const int b = order[g0 + gi];
@@ -689,9 +687,6 @@ int run(const Call& c, const Plan& pl, DeviceState& d, char* ws, cudaStream_t s,
                         B.nt = kp / tn_cols;
                         B.kblocks = rp / kBK;
                         B.tiles_per_mat = B.mt * B.nt;
-                        B.nt2 = (B.nt + 1) / 2;
-                        B.item0 = items;
-                        items += B.mt * B.nt2 * bp.nmat;
                         flops += bp.flops_update;
                     }
                     if (rc != MUON_OK) return rc;
@@ -700,7 +695,6 @@ int run(const Call& c, const Plan& pl, DeviceState& d, char* ws, cudaStream_t s,
                     tile += B.tiles_per_mat * bp.nmat;
                 }
                 p.total_tiles = tile;
-                p.total_items = items;
                 const bool final_launch = fuse_final && mode == kUpdate && it == c.steps - 1;
                 if (final_launch) {
                     int nf = 0;
@@ -725,10 +719,10 @@ int run(const Call& c, const Plan& pl, DeviceState& d, char* ws, cudaStream_t s,
                 int rc;
                 if (final_launch) {
                     rc = launch(kind, flops, 0.0, s,
-                                [&] { return launch_gemm_pair_final(*gp, *fp, fin_kind, d.sms, multicast, s); });
+                                [&] { return launch_gemm_pair_final(*gp, *fp, fin_kind, d.sms, s); });
                 } else {
                     rc = launch(kind, flops, 0.0, s,
-                                [&] { return launch_gemm_pair(*gp, d.sms, multicast, tma_epilogue, s); });
+                                [&] { return launch_gemm_pair(*gp, d.sms, tma_epilogue, s); });
                 }
                 if (rc != MUON_OK) return rc;
             }

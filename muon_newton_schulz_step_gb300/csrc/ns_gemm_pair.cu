@@ -101,44 +101,6 @@ __device__ __forceinline__ TileCoord decode_tile(const GemmParams& p, int t) {
     return c;
 }
 
-// Update product on clusters of two pairs: item w is a pair of horizontally
-// adjacent tiles (tm, 2 j) and (tm, 2 j + 1) of one matrix; pair `pp` of the
-// cluster takes the second one.  Both need the same rows of the A operand,
-// which the two pairs load once between them and multicast.  With an odd
-// number of tile columns the last item's second tile lies beyond the matrix
-// (valid = false): its pair loads zeros for B, computes, and stores nothing.
-struct ItemCoord {
-    TileCoord c;
-    bool valid;
-};
-
-template <int CS>
-__device__ __forceinline__ ItemCoord decode_item(const GemmParams& p, int w, int pp) {
-    ItemCoord r;
-    if constexpr (CS == 2) {
-        r.c = decode_tile(p, w);
-        r.valid = true;
-    } else {
-        int bi = 0;
-        while (bi + 1 < p.nbuckets && w >= p.b[bi + 1].item0) ++bi;
-        const GemmBucket& B = p.b[bi];
-        const int per_mat = B.mt * B.nt2;
-        const int local = w - B.item0;
-        r.c.bucket = bi;
-        r.c.mat = local / per_mat;
-        const int q = local - r.c.mat * per_mat;
-        r.c.tm = q / B.nt2;
-        r.c.tn = 2 * (q - r.c.tm * B.nt2) + pp;
-        r.valid = r.c.tn < B.nt;
-    }
-    return r;
-}
-
-template <int CS>
-__device__ __forceinline__ int total_items(const GemmParams& p) {
-    return CS == 2 ? p.total_tiles : p.total_items;
-}
-
 __device__ __forceinline__ void record_failure(volatile int* abort) {
     atomicCAS(&g_muon_pair_error, 0, kErrTimeout);
     *abort = 1;
@@ -397,14 +359,11 @@ __device__ __forceinline__ void fin_prefetch_w(const FinalMat& f, int row, int r
 // XS (symmetric products only): store the tile and its mirror through the
 // per-warp exchange block, 8 cache lines per instruction, instead of one row
 // per lane and 2-byte mirror stores.  ST: pipeline stages.
-// CS: CTAs per cluster -- 2 (one pair) or 4 (two pairs sharing the A operand
-// of the update product by multicast; p.mode must be kUpdate).
 // TE: the update's epilogue moves X and X' by TMA (p.mode must be kUpdate, FK kFinNone).
 // F8: the Gram product on E4M3 operands (p.mode must be kGram).
-template <int FK, int EW, bool XS, int ST, int CS, bool TE, bool F8, class FP>
+template <int FK, int EW, bool XS, int ST, bool TE, bool F8, class FP>
 __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const __grid_constant__ GemmParams p,
                                                                      const __grid_constant__ FP fin) {
-    static_assert(CS == 2 || CS == 4, "cluster size");
     static_assert(!TE || (FK == kFinNone && !XS && ST <= 6), "TMA epilogue: plain update only");
     static_assert(!F8 || (FK == kFinNone && !TE && !XS), "FP8 operands: Gram only");
     extern __shared__ uint8_t smem_raw[];
@@ -434,18 +393,16 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
     const uint32_t crank = ptx::cluster_ctarank();
     const uint32_t rank = crank & 1u;               // in the pair: 0 = leader, 1 = peer
     const uint32_t lead = crank & ~1u;              // cluster rank of this pair's leader
-    const int pp = static_cast<int>(crank >> 1);    // pair within the cluster (CS == 4)
     const bool leader = rank == 0;
     const int pair = static_cast<int>(ptx::cluster_id_x());
     const int npairs = static_cast<int>(ptx::num_clusters_x());
-    const int nitems = total_items<CS>(p);
+    const int ntiles = p.total_tiles;
     const uint64_t wait_limit = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(ptx::smem_addr(&full[s]), 1);
-            // a stage is free once every pair that reads it (CS / 2 of them) is done with it
-            ptx::mbar_init(ptx::smem_addr(&empty[s]), CS / 2);
+            ptx::mbar_init(ptx::smem_addr(&empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&tfull[a]), 1);
@@ -486,21 +443,21 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
             uint32_t armed = 0, armed_parity = 0;
             const bool upd = p.mode == kUpdate;
             // upper-only symmetric operands: K blocks left of the row tile's diagonal come
-            // from the stored transpose (never with clusters of two pairs).  They are
+            // from the stored transpose.  They are
             // loaded by a loop of their own ahead of the main loop, which stays free of any
             // per-K-block choice (the producer feeds the tensor pipe as directly as the MMA
             // issuer: a second TMA path inside that loop, even never taken, cost 12 %)
-            const bool sym_a = CS == 2 && p.upper_only && p.mode != kGram;
-            const bool sym_b = CS == 2 && p.upper_only && p.mode == kPoly;
+            const bool sym_a = p.upper_only && p.mode != kGram;
+            const bool sym_b = p.upper_only && p.mode == kPoly;
             bool ok = true;
-            for (int t = pair; ok && t < nitems; t += npairs) {
-                const TileCoord c = decode_item<CS>(p, t, pp).c;
+            for (int t = pair; ok && t < ntiles; t += npairs) {
+                const TileCoord c = decode_tile(p, t);
                 const GemmBucket& B = p.b[c.bucket];
                 const int arow = c.tm * kTile + static_cast<int>(rank) * kHalf;
                 const int bcol = c.tn * kTile + static_cast<int>(rank) * kHalf;
                 const int kstep = F8 ? 2 * kBK : kBK;   // K elements per stage (128-byte rows)
                 int kb = 0;
-                if constexpr (CS == 2 && !F8) {
+                if constexpr (!F8) {
                     const int a_lim = sym_a ? c.tm * (kTile / kBK) : 0;        // A from the transpose below
                     const int t_end = sym_b ? c.tn * (kTile / kBK) : a_lim;    // B from the transpose below (polynomial)
                     for (; kb < t_end; ++kb) {
@@ -553,16 +510,7 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
                         armed |= 1u << stage;
                         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     }
-                    if constexpr (CS == 2) {
-                        ptx::tma_load_3d_pair(ptx::smem_addr(sA + stage * kStageA), &B.tmA, fb, kb * kstep, arow,
-                                              c.mat);
-                    } else if ((kb & 1) == pp) {
-                        // the A rows of this K block for this CTA and its counterpart in the
-                        // other pair (same rank in its pair): the pairs take turns by K block
-                        const uint16_t mask = static_cast<uint16_t>((1u << rank) | (1u << (2u + rank)));
-                        ptx::tma_load_3d_pair_mc(ptx::smem_addr(sA + stage * kStageA), &B.tmA, fb, kb * kBK, arow,
-                                                 c.mat, mask);
-                    }
+                    ptx::tma_load_3d_pair(ptx::smem_addr(sA + stage * kStageA), &B.tmA, fb, kb * kstep, arow, c.mat);
                     const uint32_t sb = ptx::smem_addr(sB + stage * kStageB);
                     if (upd) {
                         // two 64-column MN-major blocks of X rows [64 kb, +64)
@@ -607,8 +555,8 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
             // (the polynomial's B from the transpose, the update's iterate always).  They run
             // in a loop of their own ahead of the main loop, whose body stays as for full
             // storage (no per-K-block choice there)
-            const bool sym_a = CS == 2 && p.upper_only && p.mode != kGram;
-            const bool sym_b = CS == 2 && p.upper_only && p.mode == kPoly;
+            const bool sym_a = p.upper_only && p.mode != kGram;
+            const bool sym_b = p.upper_only && p.mode == kPoly;
             const uint64_t ad_mn = ptx::sdesc_sw128(ptx::smem_addr(sA), kBK * 128, 1024);
             const uint64_t bd_mn = ptx::sdesc_sw128(ptx::smem_addr(sB), kBK * 128, 1024);
             constexpr uint32_t idesc_tt = ptx::idesc_bf16_f32(kTile, kTile, true, true);
@@ -617,11 +565,10 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
             uint32_t phase = 0;
             bool ok = true;
             int it = 0;
-            // stage release reaches every CTA whose producer may refill the stage
-            const uint16_t empty_mask = CS == 4 ? 0xFu : 0x3u;
+            const uint16_t empty_mask = 0x3u;   // a stage's release reaches both CTAs' producers
             const uint16_t acc_mask = static_cast<uint16_t>(0x3u << lead);
-            for (int t = pair; ok && t < nitems; t += npairs, ++it) {
-                const TileCoord c = decode_item<CS>(p, t, pp).c;
+            for (int t = pair; ok && t < ntiles; t += npairs, ++it) {
+                const TileCoord c = decode_tile(p, t);
                 const GemmBucket& B = p.b[c.bucket];
                 const int acc = it & 1;
                 const uint32_t aphase = static_cast<uint32_t>(it >> 1) & 1u;
@@ -700,9 +647,8 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
         uint32_t te_pending = 0;    // TMA epilogue: input buffers with a load in flight
         int te_stores = 0;          // TMA epilogue: output blocks stored so far (staging parity)
         int it = 0;
-        for (int t = pair; t < nitems; t += npairs, ++it) {
-            const ItemCoord ic = decode_item<CS>(p, t, pp);
-            const TileCoord c = ic.c;
+        for (int t = pair; t < ntiles; t += npairs, ++it) {
+            const TileCoord c = decode_tile(p, t);
             const GemmBucket& B = p.b[c.bucket];
             const int acc = it & 1;
             const uint32_t aphase = static_cast<uint32_t>(it >> 1) & 1u;
@@ -710,15 +656,7 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
             const size_t mat_off = static_cast<size_t>(c.mat) * static_cast<size_t>(B.mat_stride);
             __nv_bfloat16* out = B.out + mat_off;
             const size_t ld = static_cast<size_t>(B.ld);
-            if (!ic.valid) {
-                // a tile beyond the matrix (odd tile columns, clusters of two pairs):
-                // only release its accumulator
-                if (!ptx::wait_parity_cluster_backoff(ptx::smem_addr(&tfull[acc]), aphase, abort, wait_limit, 256)) {
-                    record_failure(abort);
-                    break;
-                }
-                ptx::tc_fence_after();
-            } else if constexpr (FK != kFinNone) {
+            if constexpr (FK != kFinNone) {
                 // ---- fused final update: X arrives by TMA as in the plain update; W
                 // streams through a register ring in the exchanged layout
                 constexpr int D = FinTraits<FK>::depth;
@@ -737,9 +675,8 @@ __global__ void __launch_bounds__(Epi<EW>::threads, 1) ns_gemm_pair_kernel(const
                 };
                 // W is not in L2: bring this tile's lines (first tile) and the next tile's in
                 if (it == 0) fin_prefetch_w<FK>(f, row, rowbase, lane, colb + 32 * ch0, 32 * kChunksPerWarp, fr, fk);
-                const ItemCoord n2 = t + npairs < nitems ? decode_item<CS>(p, t + npairs, pp) : ItemCoord{};
-                if (t + npairs < nitems && n2.valid) {
-                    const TileCoord c2 = n2.c;
+                if (t + npairs < ntiles) {
+                    const TileCoord c2 = decode_tile(p, t + npairs);
                     const FinalMat& f2 = fin.m[p.b[c2.bucket].fin0 + c2.mat];
                     const int row2 = c2.tm * kTile + static_cast<int>(rank) * kHalf + q * 32 + lane;
                     fin_prefetch_w<FK>(f2, row2, row2 - lane, lane, c2.tn * kTile + 32 * ch0, 32 * kChunksPerWarp,
@@ -1063,81 +1000,32 @@ size_t gemm_pair_smem_bytes() { return pair_smem_bytes<kEpiWarps, false, kPairSt
 
 namespace {
 
-// Clusters of CS CTAs that can be resident at once for this instantiation
-// (0 if none), queried once per device.
-template <int FK, int EW, bool XS, int ST, int CS, bool TE, class FP>
-int max_clusters(size_t smem) {
-    static int cached[64];
-    static bool have[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!have[dev]) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(CS, 1, 1);
-        cfg.blockDim = dim3(Epi<EW>::threads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = CS;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, ns_gemm_pair_kernel<FK, EW, XS, ST, CS, TE, false, FP>, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-        cached[dev] = n;
-        have[dev] = true;
-    }
-    return cached[dev];
-}
-
-template <int FK, int EW, bool XS, int ST, int CS, bool TE, class FP, bool F8 = false>
-cudaError_t launch_pair(const GemmParams& p, const FP& f, int nclusters, cudaStream_t s) {
+template <int FK, int EW, bool XS, int ST, bool TE, class FP, bool F8 = false>
+cudaError_t launch_pair(const GemmParams& p, const FP& f, int npairs, cudaStream_t s) {
     const size_t smem = pair_smem_bytes<EW, XS, ST, TE, FK>();
-    cudaError_t e = cudaFuncSetAttribute(ns_gemm_pair_kernel<FK, EW, XS, ST, CS, TE, F8, FP>,
+    cudaError_t e = cudaFuncSetAttribute(ns_gemm_pair_kernel<FK, EW, XS, ST, TE, F8, FP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CS * nclusters, 1, 1);
+    cfg.gridDim = dim3(2 * npairs, 1, 1);
     cfg.blockDim = dim3(Epi<EW>::threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, ns_gemm_pair_kernel<FK, EW, XS, ST, CS, TE, F8, FP>, p, f);
+    e = cudaLaunchKernelEx(&cfg, ns_gemm_pair_kernel<FK, EW, XS, ST, TE, F8, FP>, p, f);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
-// The update product (plain or fused final): on clusters of two pairs sharing
-// A by multicast when asked for and when such clusters fit, else on pairs.
-template <int FK, int EW, int ST, bool TE, class FP>
-cudaError_t launch_update(const GemmParams& p, const FP& f, int sms, bool multicast, cudaStream_t s) {
-    // (the multicast loads read K-major blocks only: not with upper-only storage)
-    if (multicast && p.total_items > 0 && !p.upper_only) {
-        const size_t smem = pair_smem_bytes<EW, false, ST, TE, FK>();
-        if (cudaFuncSetAttribute(ns_gemm_pair_kernel<FK, EW, false, ST, 4, TE, false, FP>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess) {
-            const int n4 = std::min(std::min(max_clusters<FK, EW, false, ST, 4, TE, FP>(smem), sms / 4), p.total_items);
-            if (n4 > 0) return launch_pair<FK, EW, false, ST, 4, TE, FP>(p, f, n4, s);
-        } else {
-            cudaGetLastError();
-        }
-    }
-    return launch_pair<FK, EW, false, ST, 2, TE, FP>(p, f, std::min(p.total_tiles, sms / 2), s);
-}
-
 }  // namespace
 
-cudaError_t launch_gemm_pair(const GemmParams& p, int sms, bool multicast, bool tma_epilogue, cudaStream_t s) {
+cudaError_t launch_gemm_pair(const GemmParams& p, int sms, bool tma_epilogue, cudaStream_t s) {
     // the symmetric products (Gram and polynomial) store through the exchange
     // blocks and give up one pipeline stage for them; the update (K = r) runs 5
     // stages too: the shared memory they leave lets more of the other
@@ -1145,22 +1033,22 @@ cudaError_t launch_gemm_pair(const GemmParams& p, int sms, bool multicast, bool 
     const int npairs = std::min(p.total_tiles, sms / 2);
     if (p.mode == kUpdate) {
         if (tma_epilogue)
-            return launch_update<kFinNone, kUpdateEpiWarps, kPairStages - 1, true>(p, NoFinal{0}, sms, multicast, s);
-        return launch_update<kFinNone, kUpdateEpiWarps, kPairStages - 1, false>(p, NoFinal{0}, sms, multicast, s);
+            return launch_pair<kFinNone, kUpdateEpiWarps, false, kPairStages - 1, true>(p, NoFinal{0}, npairs, s);
+        return launch_pair<kFinNone, kUpdateEpiWarps, false, kPairStages - 1, false>(p, NoFinal{0}, npairs, s);
     }
     if (p.mode == kPoly || (p.mode == kGram && !p.fp8))
-        return launch_pair<kFinNone, kEpiWarps, true, kPairStages - 1, 2, false>(p, NoFinal{0}, npairs, s);
-    if (p.fp8) return launch_pair<kFinNone, kEpiWarps, false, kPairStages, 2, false, NoFinal, true>(p, NoFinal{0}, npairs, s);
-    return launch_pair<kFinNone, kEpiWarps, false, kPairStages, 2, false>(p, NoFinal{0}, npairs, s);
+        return launch_pair<kFinNone, kEpiWarps, true, kPairStages - 1, false>(p, NoFinal{0}, npairs, s);
+    if (p.fp8) return launch_pair<kFinNone, kEpiWarps, false, kPairStages, false, NoFinal, true>(p, NoFinal{0}, npairs, s);
+    return launch_pair<kFinNone, kEpiWarps, false, kPairStages, false>(p, NoFinal{0}, npairs, s);
 }
 
-cudaError_t launch_gemm_pair_final(const GemmParams& p, const FinalParams& f, int kind, int sms, bool multicast,
-                                   cudaStream_t s) {
+cudaError_t launch_gemm_pair_final(const GemmParams& p, const FinalParams& f, int kind, int sms, cudaStream_t s) {
     if (p.mode != kUpdate) return cudaErrorInvalidValue;
+    const int npairs = std::min(p.total_tiles, sms / 2);
     switch (kind) {
-        case kFinStore: return launch_update<kFinStore, kEpiWarps, kPairStages - 1, false>(p, f, sms, multicast, s);
-        case kFinWBf16: return launch_update<kFinWBf16, kEpiWarps, kPairStages - 1, false>(p, f, sms, multicast, s);
-        case kFinWF32: return launch_update<kFinWF32, kEpiWarps, kPairStages - 1, false>(p, f, sms, multicast, s);
+        case kFinStore: return launch_pair<kFinStore, kEpiWarps, false, kPairStages - 1, false>(p, f, npairs, s);
+        case kFinWBf16: return launch_pair<kFinWBf16, kEpiWarps, false, kPairStages - 1, false>(p, f, npairs, s);
+        case kFinWF32: return launch_pair<kFinWF32, kEpiWarps, false, kPairStages - 1, false>(p, f, npairs, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -17,3 +17,9 @@ def sources(pattern):
 def test_products_of_8_bits_load_without_multicast():
     for name, text in sources("fp8_*.cu"):
         assert not re.search(r"tma_load\w*_mc\b", text), name
+
+
+def test_no_tensor_load_is_multicast():
+    for name, text in sources("*.cu") + sources("*.cuh"):
+        for asm in re.findall(r"asm volatile\((.*?)\);", text, re.S):
+            assert not ("cp.async.bulk" in asm and "multicast" in asm), name
