@@ -23,3 +23,10 @@ def test_no_tensor_load_is_multicast():
     for name, text in sources("*.cu") + sources("*.cuh"):
         for asm in re.findall(r"asm volatile\((.*?)\);", text, re.S):
             assert not ("cp.async.bulk" in asm and "multicast" in asm), name
+
+
+def test_traffic_record_is_of_these_sources():
+    """The bench leaves the traffic out where the committed capture is of other sources."""
+    import bench
+
+    assert bench._traffic_record() is not None
