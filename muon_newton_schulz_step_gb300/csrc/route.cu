@@ -519,8 +519,9 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const __grid_consta
             float c = 0.0f, w = 1.0f;                    // score; derivative of its logarithm by the logit
             if (p.sigmoid) {
                 if (e >= 0) {
-                    c = sigmoid_fast(x);
-                    w = 1.0f - c;
+                    const float t = exp_fast(-x);
+                    c = __fdividef(1.0f, 1.0f + t);
+                    w = t <= FLT_MAX ? t * c : 1.0f;     // 1 - c would have no bits left near c = 1
                 }
             } else {
                 const float m = warp_max(x);
