@@ -637,12 +637,17 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 @functools.lru_cache(maxsize=256)
+def _kept_route_opts(top_k, score, groups, top_groups, renormalize, scale):
+    o = _RouteOpts(top_k, groups, top_groups, score, renormalize, scale)
+    return o, ctypes.byref(o)
+
+
 def _route_opts(top_k, score, groups, top_groups, renormalize, scale):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {tuple(_SCORES)}")
-    o = _RouteOpts(int(top_k), int(groups), int(groups if top_groups is None else top_groups), _SCORES[score],
-                   1 if renormalize else 0, float(scale))
-    return o, ctypes.byref(o)
+    # kept by value: a tensor among the arguments may change in place
+    return _kept_route_opts(int(top_k), _SCORES[score], int(groups), int(groups if top_groups is None else top_groups),
+                            1 if renormalize else 0, float(scale))
 
 
 def muon_route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, top_groups=None,

@@ -36,7 +36,7 @@ class _Route(torch.autograd.Function):
 def route(logits, top_k, *, bias=None, score="softmax", groups=1, top_groups=None, renormalize=True, scale=1.0):
     """``muon_route`` with a gradient for the logits: (weights, chosen experts,
     tokens of each expert).  The bias steers the choice and gets no gradient."""
-    return _Route.apply(logits, bias, top_k, score, groups, top_groups, renormalize, scale)
+    return _Route.apply(logits, bias, top_k, score, groups, top_groups, bool(renormalize), float(scale))
 
 
 def sort_tokens(chosen, counts):
