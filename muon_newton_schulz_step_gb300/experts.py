@@ -6,7 +6,7 @@ what a layer of experts runs in front of the optimizer step ("Domyn is training
 a 1T-parameter MoE on Europe's Jupiter supercomputer, and published the
 recipe", table "The model and the machine": 384 experts, 8 chosen).  The
 arithmetic runs in the library's kernels; torch supplies memory, the sort and
-the graph.
+the graph.  The layers have first derivatives alone: a second one is refused.
 """
 import torch
 
@@ -14,6 +14,26 @@ from . import (muon_fp8_linear, muon_fp8_linear_backward, muon_fp8_quantize_weig
                muon_route_backward)
 
 __all__ = ["route", "sort_tokens", "Fp8Linear"]
+
+
+class _Underived(torch.autograd.Function):
+    """A gradient as it is, made of ``sources`` by kernels that have no derivative:
+    going back through it is an error.  (torch's ``once_differentiable`` does not tie
+    the gradient to its sources, and ``torch.autograd.grad`` then leaves this path out
+    without a word.)"""
+
+    @staticmethod
+    def forward(ctx, grad, *sources):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the experts' layers have first derivatives alone: no gradient of their gradients")
+
+
+def _underived(grad, *sources):
+    """``grad`` of ``sources``; without create_graph nothing to do."""
+    return grad if grad is None or not torch.is_grad_enabled() else _Underived.apply(grad, *sources)
 
 
 class _Route(torch.autograd.Function):
@@ -29,8 +49,9 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_weights, _chosen, _counts):
         logits, chosen = ctx.saved_tensors
-        d = muon_route_backward(d_weights.contiguous(), logits, chosen, **ctx.how)
-        return (d,) + (None,) * 7
+        with torch.no_grad():
+            d = muon_route_backward(d_weights.contiguous(), logits, chosen, **ctx.how)
+        return (_underived(d, d_weights, logits),) + (None,) * 7
 
 
 def route(logits, top_k, *, bias=None, score="softmax", groups=1, top_groups=None, renormalize=True, scale=1.0):
@@ -55,16 +76,17 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, codes, offsets):
         ctx.save_for_backward(x, offsets)
         ctx.codes = codes
-        ctx.dw_dtype = weight.dtype
+        ctx.weight = weight
         return muon_fp8_linear(x, codes, offsets=offsets, out_dtype=x.dtype)
 
     @staticmethod
     def backward(ctx, dy):
         x, offsets = ctx.saved_tensors
         need_dx, need_dw = ctx.needs_input_grad[:2]
-        dx, dw = muon_fp8_linear_backward(dy.contiguous(), x, ctx.codes, offsets=offsets, need_dx=need_dx,
-                                          need_dw=need_dw, dx_dtype=x.dtype, dw_dtype=ctx.dw_dtype)
-        return dx, dw, None, None
+        with torch.no_grad():
+            dx, dw = muon_fp8_linear_backward(dy.contiguous(), x, ctx.codes, offsets=offsets, need_dx=need_dx,
+                                              need_dw=need_dw, dx_dtype=x.dtype, dw_dtype=ctx.weight.dtype)
+        return _underived(dx, dy, ctx.weight), _underived(dw, dy, x), None, None
 
 
 class Fp8Linear:
