@@ -30,6 +30,10 @@ class MuonAdamW(torch.optim.Optimizer):
     of a supported dtype; those without a gradient are skipped.
     """
 
+    # of optimizers pickled before there was clipping
+    max_grad_norm = None
+    grad_norm = None
+
     def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.1, nesterov=True, ns_steps=5,
                  adamw_lr=3e-4, betas=(0.9, 0.95), eps=1e-8, adamw_weight_decay=0.0, use_muon=None,
                  max_grad_norm=None):
@@ -39,6 +43,10 @@ class MuonAdamW(torch.optim.Optimizer):
         super().__init__(params, defaults)
         self.max_grad_norm = max_grad_norm
         self.grad_norm = None
+
+    def __getstate__(self):
+        # copies and pickles take what this returns, and the base class knows of its own state alone
+        return {**super().__getstate__(), "max_grad_norm": self.max_grad_norm, "grad_norm": self.grad_norm}
 
     @staticmethod
     def _is_muon(group, p):
