@@ -25,7 +25,11 @@ class MuonAdamW(torch.optim.Optimizer):
     ``adamw_lr``, ``betas``, ``eps``, ``adamw_weight_decay`` (AdamW).
     ``max_grad_norm`` (for all groups together, default none): every step first
     scales the gradients in place by min(1, max_grad_norm / (norm + 1e-6)), norm
-    their global 2-norm; it is kept in ``grad_norm`` (0-dim CUDA tensor).
+    the 2-norm of all gradients of this optimizer; it is kept in ``grad_norm``
+    (0-dim CUDA tensor).  Nothing is reduced over ranks: where ranks hold
+    different parameters (whole matrices placed on ranks) each would clip by a
+    norm of its own, so the option is for one process, or for ranks with the
+    same gradients.
     Parameters must be contiguous CUDA tensors in bf16 or fp32 with gradients
     of a supported dtype; those without a gradient are skipped.
     """
