@@ -120,6 +120,13 @@ constexpr float kLog2e = 1.44269504f;
 // 1e-5 of the scores at 200, and no number at all from 1e9 on.
 __device__ __forceinline__ float exp_choice(float x, float max) { return exp2_approx((x - max) * kLog2e); }
 
+// A choice value as the choice compares it: a NaN as -FLT_MAX, and every finite number
+// above that.  -inf (masked by its bias) stays.
+__device__ __forceinline__ float ordered(float c) {
+    if (c != c) return -FLT_MAX;
+    return c == -FLT_MAX ? -3.40282326e38f : c;
+}
+
 // This lane's logits, -inf where it owns no expert.
 template <int NV>
 __device__ __forceinline__ void load_lane(const RouteParams& p, long long row, int e0, int n, float (&x)[NV]) {
@@ -227,13 +234,10 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) c[j] = SIGMOID ? __fadd_rn(c[j], bias[j]) : fmaf(c[j], norm, bias[j]);
-            if (!plain || odd_bias) {
-                // a NaN orders below every number
+            const bool odd = !plain || odd_bias;             // some may be masked or NaN
+            if (odd) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const float v = c[j] == c[j] ? c[j] : -FLT_MAX;
-                    c[j] = masked >> j & 1u ? -INFINITY : v;
-                }
+                for (int j = 0; j < NV; ++j) c[j] = masked >> j & 1u ? -INFINITY : ordered(c[j]);
             }
             // group scores
             float best = -INFINITY;
@@ -251,7 +255,9 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
                     m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
                     m1 = fmaxf(m1, o1);
                 }
-                const float gv = m2 <= -FLT_MAX ? m1 : m1 + m2;   // one expert left (or one that is not NaN): its own
+                // one expert left (or one that is not NaN): its own; a finite bias of
+                // -FLT_MAX is a number like any other
+                const float gv = m2 <= (odd ? -FLT_MAX : -INFINITY) ? m1 : m1 + m2;
                 int before = 0;                              // groups ahead of this one: each lane compares some
                 for (int g = 0; g < p.groups; g += p.lanes) {
                     const int other = g + in_group;
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, route_blocks<NV>()) k_route(const __
             const float b = p.bias != nullptr ? p.bias[my_e] : 0.0f;
             if (SIGMOID) value = __fadd_rn(rcp_approx(1.0f + exp2_approx(logit * -kLog2e)), b);
             else value = fmaf(exp_choice(logit, top), inv, b);
-            value = value == value ? value : -FLT_MAX;
+            value = ordered(value);
         }
         __syncwarp();                                    // the pool has been read
         int most = total;
