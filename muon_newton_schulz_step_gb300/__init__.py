@@ -777,6 +777,8 @@ def _check_fp8(name, m, kind, codes_shape, scale_shape):
 
 def _check_weight(w, offsets):
     """(n, k, groups, offsets' pointer) of a "block" weight that goes with ``offsets``."""
+    if not isinstance(w, Fp8Matrix) or not isinstance(w.codes, torch.Tensor) or not isinstance(w.scale, torch.Tensor):
+        raise ValueError('the weight must be an Fp8Matrix of kind "block", as muon_fp8_quantize_weight makes it')
     codes, scale = w.codes, w.scale
     shape, k = codes.shape, int(w.cols)
     stacked = len(shape) == 3
