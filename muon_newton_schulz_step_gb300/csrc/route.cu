@@ -84,8 +84,8 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// e^x to about 2 ulp: 2^k with k = x log2(e) rounded, times 1 + (what the rounding
-// left) ln 2.  Arguments beyond +-200 give infinity and zero, NaN gives NaN.
+// e^x to 6 * 2^-24 (ex2's 2^-22 and two roundings): 2^k with k = x log2(e) rounded,
+// times 1 + (what the rounding left) ln 2.  Arguments beyond +-200 give infinity and zero, NaN gives NaN.
 __device__ __forceinline__ float exp_fast(float x) {
     const float c = fminf(fmaxf(x, -200.0f), 200.0f);
     const float k = c * 1.44269504f;
