@@ -36,6 +36,7 @@ constexpr int kTokens = 8;           // most tokens: one matrix fragment's
 constexpr int kRound = 2;            // blocks of x that half a warp loads at a time
 constexpr int kAhead = 3;            // blocks of 128 of the reduction that a warp loads at a time
 constexpr int kMaxCodes = 100 * 1024;
+constexpr int kSms = 152;
 
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
     uint4 v;
@@ -239,11 +240,12 @@ cudaError_t run(const Fp8TokenParams& p, cudaStream_t s) {
 // rest; tiles take 6 us more to begin with, 0.4 + n / 10300 less per 6144.  Measured, this
 // kernel against tiles, the weight in L2: 3 tokens x 6144 x 6144 12.9 us, 13.8; 4 tokens
 // 14.3; 4 x 2048 x 6144 9.7, 11.4; 8 tokens 14.9; 8 x 6144 x 2048 8.7, 9.7; 1 x 16384 x
-// 6144 26.0, 20.8.
+// 6144 26.0, 24.2.  The SMs are this part's 152 and not asked for: the workspace's size
+// depends on the rule, and follows from sizes alone.
 bool fp8_token_serves(long long tokens, long long n, long long k) {
     const long long ldk = (k + 127) / 128 * 128;
     return tokens <= kTokens && token_smem(static_cast<int>(tokens), ldk) <= static_cast<size_t>(kMaxCodes) &&
-           n <= 152 * 3 * kRows && k * (14000 * (tokens - 1) + 4000 + n) <= 310000000ll;
+           n <= kSms * 3 * kRows && k * (14000 * (tokens - 1) + 4000 + n) <= 310000000ll;
 }
 
 cudaError_t launch_fp8_token(const Fp8TokenParams& p, cudaStream_t s) {
