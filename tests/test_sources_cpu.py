@@ -1,8 +1,8 @@
 """What the compiled sources may not hold.
 
-One library serves every rank of a job, so its tensor loads stay within a CTA
-pair: a load that is multicast over a cluster belongs in code that only runs on
-one GPU use."""
+One library serves every rank of a job, so each of its tensor loads goes to one
+CTA: a load that is multicast over a cluster belongs in code that runs on one GPU
+only."""
 import glob
 import os
 import re
