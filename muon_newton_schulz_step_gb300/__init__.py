@@ -727,7 +727,8 @@ def muon_fp8_quantize(x, *, row: bool = True, col: bool = False, offsets=None, s
     """``x`` (2-D, bf16 or fp32) as E4M3 with scales for blocks of 128 along its
     rows (``row``), along its columns (``col``; blocks start anew at each group
     of ``offsets``), or both from one read: (row Fp8Matrix or None, col
-    Fp8Matrix or None)."""
+    Fp8Matrix or None).  With ``col`` and ``offsets`` the codes of rows of no
+    group are not set."""
     rows, cols, ld = _check_rows("x", x, _FLOATS)
     groups, optr = _check_offsets(offsets)
     ldq = _up128(cols)
@@ -817,7 +818,9 @@ def muon_fp8_product(product: str, a, b, *, offsets=None, tokens=None, out=None,
     With ``offsets`` (int32, experts + 1, on the device) rows offsets[g] to
     offsets[g + 1] are expert g's and b (or out) is stacked over experts.
     ``tokens`` (grad_weight): the rows that the operands were made from.
-    ``out``: optional preallocated result, bf16 or fp32 (rows contiguous)."""
+    ``out``: optional preallocated result, bf16 or fp32 (rows contiguous).  Rows of
+    no expert are left as they are in ``out``, and not set in a new result
+    (``muon_fp8_linear`` makes them zero)."""
     if product in ("forward", "grad_input"):
         n, k, groups, optr = _check_weight(b, offsets)
         inner, red = (n, k) if product == "forward" else (k, n)
