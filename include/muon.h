@@ -432,6 +432,88 @@ MUON_API int muon_fp8_linear_backward(const void* dy, int dy_dtype, long long ld
                                       size_t workspace_bytes, void* dx, int dx_dtype, long long ld_dx, void* dw,
                                       int dw_dtype, cudaStream_t stream);
 
+/*
+ * The routed entries sorted by expert.  Entry i (of tokens x top_k, as muon_route
+ * leaves them) belongs to expert chosen[i]; this call's experts are first ..
+ * first + experts - 1 (a rank's share).  Entries of other experts, or of none (-1), come
+ * first; then those of expert `first`, and so on, equal ones in the order they have.
+ *   order    entries: order[p] is the entry at place p
+ *   place    entries: the inverse
+ *   offsets  experts + 1: places offsets[e] .. offsets[e + 1] are expert first + e's, as
+ *            the grouped products take them
+ *   workspace  device, 16-byte aligned; none (NULL) where ..._workspace_bytes is 0
+ * At most 2^30 entries and 1024 experts.
+ */
+MUON_API size_t muon_sort_tokens_workspace_bytes(long long entries, int experts);
+MUON_API int muon_sort_tokens(const int* chosen, long long entries, int first, int experts, void* workspace,
+                              size_t workspace_bytes, int* order, int* place, int* offsets, cudaStream_t stream);
+
+/*
+ * Tokens' rows to the experts: out[place[t, j]] = x[t], of x's dtype (out has tokens *
+ * top_k rows), for the places of an expert, offsets[0] <= place < offsets[groups]; the rows
+ * of the other entries become zero.  place and offsets are muon_sort_tokens'; a place
+ * outside the rows is passed over.  out must not overlap x.  At most 2^30 rows, top_k <= 32.
+ */
+MUON_API int muon_dispatch_tokens(const void* x, int dtype, long long tokens, long long cols, long long ld_x, int top_k,
+                                  const int* place, const int* offsets, int groups, void* out, long long ld_out,
+                                  cudaStream_t stream);
+
+/*
+ * And back: out[t] = sum over j of weights[t, j] * y[place[t, j]] (weights NULL: 1, which
+ * is the gradient of muon_dispatch_tokens), summed in fp32 in the order of j and rounded
+ * once.  Entries without an expert here take no part, whatever their rows and weights hold.
+ */
+MUON_API int muon_combine_tokens(const void* y, int y_dtype, long long ld_y, long long tokens, long long cols, int top_k,
+                                 const int* place, const int* offsets, int groups, const float* weights, void* out,
+                                 int out_dtype, long long ld_out, cudaStream_t stream);
+
+/*
+ * Gradients of muon_combine_tokens from d, its result's: dy[place[t, j]] = weights[t, j] *
+ * d[t] (y's dtype; zero for entries without an expert here; NULL: left out), d_weights[t, j]
+ * = sum over the columns of d[t] * y[place[t, j]] (fp32; 0 without an expert here; NULL: left
+ * out, and y is not read).  dy must not overlap y or d.
+ */
+MUON_API int muon_combine_tokens_backward(const void* d, int d_dtype, long long ld_d, const void* y, int y_dtype,
+                                          long long ld_y, long long tokens, long long cols, int top_k, const int* place,
+                                          const int* offsets, int groups, const float* weights, void* dy, long long ld_dy,
+                                          float* d_weights, cudaStream_t stream);
+
+/*
+ * The gated activation between an expert's projections, out = gate / (1 + exp(-gate)) * up
+ * (rows x cols, one dtype, row strides ld_*), and its gradients from d, its result's.  In
+ * fp32, rounded once.  Results must not overlap operands.
+ */
+MUON_API int muon_swiglu(const void* gate, long long ld_gate, const void* up, long long ld_up, int dtype, long long rows,
+                         long long cols, void* out, long long ld_out, cudaStream_t stream);
+MUON_API int muon_swiglu_backward(const void* d, long long ld_d, const void* gate, long long ld_gate, const void* up,
+                                  long long ld_up, int dtype, long long rows, long long cols, void* d_gate,
+                                  long long ld_dgate, void* d_up, long long ld_dup, cudaStream_t stream);
+
+/*
+ * Weights of 4 bits, for serving: w[n, k] = code[n, k] * scale[k / block, n], codes whole
+ * numbers from -8 to 7 in two's complement, block 32, 64 or 128 columns.
+ *   codes   batch x rows x up128(cols) / 2 bytes, the even column in a byte's low half,
+ *           zeros past the last column; 16-byte aligned
+ *   scale   batch x (up128(cols) / block) x rows, bf16
+ * Rounding of `batch` weights, rows x cols each, contiguous: scale = max|w| / 7 over a
+ * block, to bf16; code = w / scale to the nearest whole number (ties to even), between -7 and 7.
+ * A block with an infinity or a NaN gets the scale NaN; a scale that rounds to zero, zero codes.
+ */
+MUON_API int muon_int4_quantize_weight(const void* w, int dtype, int batch, long long rows, long long cols, int block,
+                                       void* codes, void* scale, cudaStream_t stream);
+
+/*
+ * out = x W^T on weights of 4 bits, for one weight (offsets NULL) or for `groups` experts
+ * over tokens sorted by expert, as the 8-bit products take them; rows outside every group
+ * become zero.  x is not rounded: fp32 x counts with all its bits (from 2^-90 on), sums are
+ * fp32 in units of 2^-11, rounded once to out_dtype.  Made for few tokens (of each expert), where the weights'
+ * bytes are the time.  x 16-byte aligned with rows of a multiple of 16 bytes loads faster.
+ * At most 512 groups.
+ */
+MUON_API int muon_int4_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
+                              const void* w_scale, int block, int n, int k, int groups, const int* offsets, void* out,
+                              int out_dtype, long long ld_out, cudaStream_t stream);
+
 /* Device workspace (bytes) that one call on these shapes needs; 0 on bad args. */
 MUON_API size_t muon_workspace_bytes(const int* rows, const int* cols, int count);
 
@@ -459,7 +541,8 @@ MUON_API void muon_release_workspace(void);
  * launch.  Names: norm_pass, norm_finalize, pack, ns_gemm_gram, ns_gemm_poly,
  * ns_gemm_update, ns_gemm_final (the last update with the weight update or
  * the store of O in its epilogue), ns_small, unpack, adamw, grad_norm, grad_clip,
- * route, route_backward, fp8_quantize, fp8_gemm, fp8_token.
+ * route, route_backward, fp8_quantize, fp8_gemm, fp8_token, token_sort, dispatch,
+ * combine, combine_backward, swiglu, swiglu_backward, int4_quantize, int4_linear.
  */
 typedef struct {
     char name[40];            /* kernel name */

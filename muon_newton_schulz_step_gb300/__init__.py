@@ -18,6 +18,10 @@ The functions mirror the C ABI in ``include/muon.h``:
     muon_route(logits, top_k, ...), muon_route_backward(d_weights, logits, chosen, ...)
     muon_fp8_quantize(x, ...), muon_fp8_quantize_weight(w), muon_fp8_product(product, a, b, ...)
     muon_fp8_linear(x, w, offsets), muon_fp8_linear_backward(dy, x, w, offsets)
+    muon_sort_tokens(chosen, experts, first), muon_dispatch_tokens(x, plan)
+    muon_combine_tokens(y, plan, weights), muon_combine_tokens_backward(d, y, plan, weights)
+    muon_swiglu(gate, up), muon_swiglu_backward(d, gate, up)
+    muon_int4_quantize_weight(w, block), muon_int4_linear(x, w, offsets)
 
 The method: the per-matrix Muon step over whole matrices held on one rank
 ("How PyTorch Scaled a Near-1T MoE on Europe's Public Supercomputer", section
@@ -40,7 +44,9 @@ __all__ = [
     "MUON_STATIC_SCRATCH_BYTES", "muon_step_host", "muon_ns_batched_ex", "muon_adamw_step",
     "muon_grad_norm", "muon_grad_clip", "muon_route", "muon_route_backward", "Fp8Matrix", "muon_fp8_quantize",
     "muon_fp8_quantize_weight", "muon_fp8_product", "muon_fp8_padded_rows", "muon_fp8_linear",
-    "muon_fp8_linear_backward",
+    "muon_fp8_linear_backward", "TokenPlan", "muon_sort_tokens", "muon_dispatch_tokens", "muon_combine_tokens",
+    "muon_combine_tokens_backward", "muon_swiglu", "muon_swiglu_backward", "Int4Matrix", "muon_int4_quantize_weight",
+    "muon_int4_linear",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,7 +62,9 @@ EXPORTS = (
     "muon_adamw_step", "muon_grad_norm_workspace_bytes", "muon_grad_norm", "muon_grad_clip", "muon_route_opts_init",
     "muon_route", "muon_route_backward", "muon_fp8_padded_rows", "muon_fp8_quantize", "muon_fp8_quantize_weight",
     "muon_fp8_product", "muon_fp8_linear_workspace_bytes", "muon_fp8_linear", "muon_fp8_linear_backward_workspace_bytes",
-    "muon_fp8_linear_backward",
+    "muon_fp8_linear_backward", "muon_sort_tokens_workspace_bytes", "muon_sort_tokens", "muon_dispatch_tokens",
+    "muon_combine_tokens", "muon_combine_tokens_backward", "muon_swiglu", "muon_swiglu_backward",
+    "muon_int4_quantize_weight", "muon_int4_linear",
 )
 
 MUON_STATIC_SCRATCH_BYTES = 64 << 20
@@ -168,6 +176,24 @@ def lib():
     L.muon_fp8_linear_backward_workspace_bytes.restype = sz
     L.muon_fp8_linear_backward.argtypes = [vp, ci, ll, vp, ci, ll, ll, vp, vp, ci, ci, ci, vp, vp, sz, vp, ci, ll, vp, ci, vp]
     L.muon_fp8_linear_backward.restype = ci
+    L.muon_sort_tokens_workspace_bytes.argtypes = [ll, ci]
+    L.muon_sort_tokens_workspace_bytes.restype = sz
+    L.muon_sort_tokens.argtypes = [vp, ll, ci, ci, vp, sz, vp, vp, vp, vp]
+    L.muon_sort_tokens.restype = ci
+    L.muon_dispatch_tokens.argtypes = [vp, ci, ll, ll, ll, ci, vp, vp, ci, vp, ll, vp]
+    L.muon_dispatch_tokens.restype = ci
+    L.muon_combine_tokens.argtypes = [vp, ci, ll, ll, ll, ci, vp, vp, ci, vp, vp, ci, ll, vp]
+    L.muon_combine_tokens.restype = ci
+    L.muon_combine_tokens_backward.argtypes = [vp, ci, ll, vp, ci, ll, ll, ll, ci, vp, vp, ci, vp, vp, ll, vp, vp]
+    L.muon_combine_tokens_backward.restype = ci
+    L.muon_swiglu.argtypes = [vp, ll, vp, ll, ci, ll, ll, vp, ll, vp]
+    L.muon_swiglu.restype = ci
+    L.muon_swiglu_backward.argtypes = [vp, ll, vp, ll, vp, ll, ci, ll, ll, vp, ll, vp, ll, vp]
+    L.muon_swiglu_backward.restype = ci
+    L.muon_int4_quantize_weight.argtypes = [vp, ci, ci, ll, ll, ci, vp, vp, vp]
+    L.muon_int4_quantize_weight.restype = ci
+    L.muon_int4_linear.argtypes = [vp, ci, ll, ll, vp, vp, ci, ci, ci, ci, vp, vp, ci, ll, vp]
+    L.muon_int4_linear.restype = ci
     _lib = L
     return L
 
@@ -901,3 +927,233 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
             MUON_F32 if dx_dtype == torch.float32 else MUON_BF16, k, dw.data_ptr() if need_dw else None,
             MUON_F32 if dw_dtype == torch.float32 else MUON_BF16, _handle(stream)))
     return dx, dw
+
+
+# ----------------------------------- between an expert layer's routing and its result --
+class TokenPlan(NamedTuple):
+    """Where the rows of routed tokens lie, sorted by expert (``muon_sort_tokens``;
+    int32).  ``order`` (tokens * top_k): the entry (token * top_k + j) at each place;
+    ``place`` (tokens x top_k): the place of each entry; ``offsets`` (experts + 1): the
+    places of each expert, as the experts' products take them.  Entries without an
+    expert here lie before ``offsets[0]``."""
+    order: torch.Tensor
+    place: torch.Tensor
+    offsets: torch.Tensor
+
+
+def muon_sort_tokens(chosen, experts: int, *, first: int = 0, stream=None) -> TokenPlan:
+    """The entries of ``chosen`` (tokens x top_k, int32, contiguous, as ``muon_route``
+    gives them) sorted by expert, for the ``experts`` experts from number ``first`` on
+    (those that this rank holds).  Entries of other experts, or of none, come first;
+    equal ones keep their order."""
+    tokens, top_k, _ = _check_rows("chosen", chosen, (torch.int32,))
+    if not chosen.is_contiguous():
+        raise ValueError("chosen must be contiguous")
+    experts, first, n = int(experts), int(first), tokens * top_k
+    if experts < 1:
+        raise ValueError(f"experts is {experts}")
+    L = lib()
+    need = L.muon_sort_tokens_workspace_bytes(n, experts)
+    with _on(stream):
+        order = torch.empty(n, dtype=torch.int32, device="cuda")
+        place = torch.empty((tokens, top_k), dtype=torch.int32, device="cuda")
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        _check(L.muon_sort_tokens(chosen.data_ptr(), n, first, experts, None if ws is None else ws.data_ptr(), need,
+                                  order.data_ptr(), place.data_ptr(), offsets.data_ptr(), _handle(stream)))
+    return TokenPlan(order, place, offsets)
+
+
+def _check_plan(plan, tokens=None):
+    """(tokens, top_k, experts) of a plan, whose tensors are checked."""
+    if not isinstance(plan, TokenPlan):
+        raise ValueError("plan must be a TokenPlan, as muon_sort_tokens makes it")
+    place, offsets = plan.place, plan.offsets
+    t, top_k, _ = _check_rows("plan.place", place, (torch.int32,), tokens)
+    if not place.is_contiguous():
+        raise ValueError("plan.place must be contiguous")
+    if top_k < 1:
+        raise ValueError("plan.place has no columns")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("plan.offsets must be a 1-D int32 CUDA tensor of experts + 1 entries")
+    _check_vector("plan.offsets", offsets, torch.int32, offsets.numel())
+    return t, top_k, offsets.numel() - 1
+
+
+def muon_dispatch_tokens(x, plan: TokenPlan, stream=None) -> torch.Tensor:
+    """``x``'s rows (tokens x cols, bf16 or fp32) sorted by expert: tokens * top_k
+    rows, row plan.place[t, j] a copy of x[t]; rows of no expert are zero.  Its gradient
+    is ``muon_combine_tokens`` without weights."""
+    tokens, cols, ld = _check_rows("x", x, _FLOATS)
+    _, top_k, experts = _check_plan(plan, tokens)
+    with _on(stream):
+        out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device="cuda")
+        if cols:
+            _check(lib().muon_dispatch_tokens(x.data_ptr(), _dtype_code(x), tokens, cols, ld, top_k,
+                                              plan.place.data_ptr(), plan.offsets.data_ptr(), experts, out.data_ptr(),
+                                              cols, _handle(stream)))
+    return out
+
+
+def _check_weights(weights, tokens, top_k):
+    if weights is None:
+        return None
+    _check_rows("weights", weights, (torch.float32,), tokens, top_k)
+    if not weights.is_contiguous():
+        raise ValueError("weights must be contiguous")
+    return weights.data_ptr()
+
+
+def muon_combine_tokens(y, plan: TokenPlan, weights=None, *, out_dtype=None, stream=None) -> torch.Tensor:
+    """The way back: out[t] = sum over j of weights[t, j] * y[plan.place[t, j]], summed in
+    fp32 in the order of j.  ``y``: tokens * top_k rows, bf16 or fp32; ``weights``: fp32,
+    tokens x top_k (None: 1); ``out_dtype``: y's unless given.  Entries without an expert
+    here take no part, whatever their rows and weights hold."""
+    tokens, top_k, experts = _check_plan(plan)
+    _, cols, ld = _check_rows("y", y, _FLOATS, tokens * top_k)
+    wptr = _check_weights(weights, tokens, top_k)
+    out_dtype = y.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    with _on(stream):
+        out = torch.empty((tokens, cols), dtype=out_dtype, device="cuda")
+        if cols:
+            _check(lib().muon_combine_tokens(y.data_ptr(), _dtype_code(y), ld, tokens, cols, top_k, plan.place.data_ptr(),
+                                             plan.offsets.data_ptr(), experts, wptr, out.data_ptr(), _dtype_code(out),
+                                             cols, _handle(stream)))
+    return out
+
+
+def muon_combine_tokens_backward(d, y, plan: TokenPlan, weights=None, *, need_dy: bool = True, need_dw: bool = True,
+                                 stream=None):
+    """(dy, d_weights) of ``muon_combine_tokens`` from ``d`` (tokens x cols, bf16 or fp32):
+    dy[plan.place[t, j]] = weights[t, j] * d[t] (y's dtype), d_weights[t, j] = <d[t],
+    y[plan.place[t, j]]> (fp32), both zero for entries without an expert here.  Either may be
+    left out (None); without weights there is no d_weights."""
+    tokens, top_k, experts = _check_plan(plan)
+    _, cols, ld_d = _check_rows("d", d, _FLOATS, tokens)
+    rows, _, ld_y = _check_rows("y", y, _FLOATS, tokens * top_k, cols)
+    wptr = _check_weights(weights, tokens, top_k)
+    need_dw = need_dw and weights is not None
+    dy = dw = None
+    with _on(stream):
+        if need_dy:
+            dy = torch.empty((rows, cols), dtype=y.dtype, device="cuda")
+        if need_dw:
+            dw = (torch.empty if cols else torch.zeros)((tokens, top_k), dtype=torch.float32, device="cuda")
+        if cols:
+            _check(lib().muon_combine_tokens_backward(
+                d.data_ptr(), _dtype_code(d), ld_d, y.data_ptr(), _dtype_code(y), ld_y, tokens, cols, top_k,
+                plan.place.data_ptr(), plan.offsets.data_ptr(), experts, wptr, dy.data_ptr() if need_dy else None, cols,
+                dw.data_ptr() if need_dw else None, _handle(stream)))
+    return dy, dw
+
+
+def _check_gated(gate, up):
+    rows, cols, ld_gate = _check_rows("gate", gate, _FLOATS)
+    _, _, ld_up = _check_rows("up", up, (gate.dtype,), rows, cols)
+    return rows, cols, ld_gate, ld_up
+
+
+def muon_swiglu(gate, up, stream=None) -> torch.Tensor:
+    """gate / (1 + exp(-gate)) * up, in fp32 and rounded once (rows x cols, bf16 or fp32,
+    both of one dtype; views such as the halves of one product are read in place)."""
+    rows, cols, ld_gate, ld_up = _check_gated(gate, up)
+    with _on(stream):
+        out = torch.empty((rows, cols), dtype=gate.dtype, device="cuda")
+        if cols:
+            _check(lib().muon_swiglu(gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, _dtype_code(gate), rows, cols,
+                                     out.data_ptr(), cols, _handle(stream)))
+    return out
+
+
+def muon_swiglu_backward(d, gate, up, *, joined: bool = False, stream=None):
+    """(d_gate, d_up) of ``muon_swiglu`` from ``d``, in its dtype.  ``joined``: the two are
+    halves of one tensor (rows x 2 cols), as the gradient of one product that made gate and
+    up wants them."""
+    rows, cols, ld_gate, ld_up = _check_gated(gate, up)
+    _, _, ld_d = _check_rows("d", d, (gate.dtype,), rows, cols)
+    with _on(stream):
+        if joined:
+            both = torch.empty((rows, 2 * cols), dtype=gate.dtype, device="cuda")
+            d_gate, d_up, ld = both[:, :cols], both[:, cols:], 2 * cols
+        else:
+            d_gate = torch.empty((rows, cols), dtype=gate.dtype, device="cuda")
+            d_up, ld = torch.empty_like(d_gate), cols
+        if cols:
+            _check(lib().muon_swiglu_backward(d.data_ptr(), ld_d, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up,
+                                              _dtype_code(gate), rows, cols, d_gate.data_ptr(), ld, d_up.data_ptr(), ld,
+                                              _handle(stream)))
+    return d_gate, d_up
+
+
+class Int4Matrix(NamedTuple):
+    """A weight of 4 bits: w[n, k] = code[n, k] * scale[k // block, n], codes from -8 to 7.
+
+    ``codes``: uint8, rows x (cols rounded up to 128) / 2, the even column in the low
+    half, zero past ``cols``; ``scale``: bf16, (cols rounded up to 128) / block x rows;
+    both optionally stacked over experts.  ``block``: 32, 64 or 128 columns."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    block: int
+    cols: int
+
+
+def muon_int4_quantize_weight(w, block: int = 128, stream=None) -> Int4Matrix:
+    """A weight (rows x cols, or stacked experts x rows x cols; bf16 or fp32, contiguous) in
+    4 bits, with a scale (max|w| / 7 in bf16) for each ``block`` columns of a row."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3) or not w.is_cuda or w.dtype not in _FLOATS \
+            or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous 2-D or 3-D CUDA tensor of {_FLOATS}")
+    _here("w", w)
+    block = int(block)
+    if block not in (32, 64, 128):
+        raise ValueError("block must be 32, 64 or 128")
+    rows, cols = w.shape[-2:]
+    up = _up128(cols)
+    with _on(stream):
+        m = Int4Matrix(torch.empty((*w.shape[:-1], up // 2), dtype=torch.uint8, device="cuda"),
+                       torch.empty((*w.shape[:-2], up // block, rows), dtype=torch.bfloat16, device="cuda"), block, cols)
+        _check(lib().muon_int4_quantize_weight(w.data_ptr(), _dtype_code(w), w.shape[0] if w.dim() == 3 else 1, rows, cols,
+                                               block, m.codes.data_ptr(), m.scale.data_ptr(), _handle(stream)))
+    return m
+
+
+def _check_int4(w, offsets):
+    """(n, k, groups, offsets' pointer) of a weight of 4 bits that goes with ``offsets``."""
+    if not isinstance(w, Int4Matrix) or not isinstance(w.codes, torch.Tensor) or not isinstance(w.scale, torch.Tensor):
+        raise ValueError("the weight must be an Int4Matrix, as muon_int4_quantize_weight makes it")
+    codes, scale, block, k = w.codes, w.scale, int(w.block), int(w.cols)
+    shape = codes.shape
+    if len(shape) not in (2, 3) or block not in (32, 64, 128):
+        raise ValueError("the weight must be an Int4Matrix with 2-D or 3-D codes and a block of 32, 64 or 128")
+    stacked = len(shape) == 3
+    if stacked != (offsets is not None):
+        raise ValueError("a stacked weight goes with offsets, a single one without")
+    n, up = shape[-2], _up128(k)
+    if codes.dtype != torch.uint8 or shape[-1] != up // 2 or not codes.is_cuda or not codes.is_contiguous():
+        raise ValueError(f"the weight's codes must be a contiguous CUDA tensor of {torch.uint8} with rows of {up // 2}")
+    if scale.dtype != torch.bfloat16 or tuple(scale.shape) != (*shape[:-2], up // block, n) or not scale.is_cuda \
+            or not scale.is_contiguous():
+        raise ValueError(f"the weight's scale must be a contiguous CUDA tensor of {torch.bfloat16} with shape "
+                         f"{(*shape[:-2], up // block, n)}")
+    _here("the weight's codes", codes)
+    _here("the weight's scale", scale)
+    groups, optr = _check_offsets(offsets, shape[0] if stacked else 1)
+    return n, k, groups, optr
+
+
+def muon_int4_linear(x, w: Int4Matrix, *, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = x W^T with a weight of 4 bits (``muon_int4_quantize_weight``), for serving: ``x``
+    (tokens x k, bf16 or fp32) is not rounded.  With ``offsets``, tokens are sorted by expert
+    and ``w`` is stacked over experts; rows of no expert give zero.  The weight has no gradient."""
+    n, k, groups, optr = _check_int4(w, offsets)
+    tokens, _, ld = _check_rows("x", x, _FLOATS, None, k)
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    with _on(stream):
+        out = torch.empty((tokens, n), dtype=out_dtype, device="cuda")
+        _check(lib().muon_int4_linear(x.data_ptr(), _dtype_code(x), tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(),
+                                      int(w.block), n, k, groups, optr, out.data_ptr(), _dtype_code(out), n,
+                                      _handle(stream)))
+    return out

@@ -1,0 +1,168 @@
+// Weights of 4 bits with a scale for each `block` columns of a row (32, 64 or 128).
+//
+// w[n, k] = code[n, k] * scale[k / block, n]; codes are whole numbers from -8 to 7, two to
+// a byte, the even column in the low half; rows end on a multiple of 128 columns.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace muon {
+
+// The reduction is worked off in blocks of 128 columns, each in four steps of 32: in
+// step m lane j of the four that share a row holds the word of eight codes (and the
+// eight elements of x) number chunk(m, j).  A matrix fragment wants 2 + 2 codes from each
+// lane; which columns they are is free, as long as both operands agree.  So a lane's words
+// of one scale lie side by side, and 128-column scales load 16 bytes a lane, 64-column
+// ones 8, 32-column ones 4.
+template <int BLOCK>
+__device__ __forceinline__ constexpr int chunk_of(int m, int j) {
+    return BLOCK == 128 ? 4 * j + m : BLOCK == 64 ? 8 * (m >> 1) + 2 * j + (m & 1) : 4 * m + j;
+}
+
+// Four words of eight codes: one lane's of a row's 128 columns.
+template <int BLOCK>
+__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int kb, int j) {
+    uint4 v;
+    const uint8_t* p = row + kb * 64;
+    if constexpr (BLOCK == 128) {
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p + 16 * j));
+    } else if constexpr (BLOCK == 64) {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p + 8 * j));
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "l"(p + 32 + 8 * j));
+    } else {
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.x) : "l"(p + 4 * j));
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.y) : "l"(p + 16 + 4 * j));
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.z) : "l"(p + 32 + 4 * j));
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.w) : "l"(p + 48 + 4 * j));
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int m) { return m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w; }
+
+// Eight codes as bf16, 2^-11 times their number: element i of pair p is column 4 i + p, exactly.
+// 0x3d80 | u is 2^-4 (1 + u / 128), and a code with its sign bit turned over is code + 8.  With
+// 2^-11 the sum of 128 products is at most half of the largest |x|, so no x overflows before its
+// scale has been applied; kCodeUnit, at the end, takes it back.
+constexpr float kCodeUnit = 2048.0f;
+
+struct EightCodes {
+    uint32_t pair[4];
+};
+
+__device__ __forceinline__ EightCodes decode(uint32_t w) {
+    EightCodes d;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t u = ((w >> (4 * p)) & 0x000f000fu) ^ 0x3d883d88u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d.pair[p]) : "r"(u), "r"(0x3d883d88u));
+    }
+    return d;
+}
+
+// Eight elements of x in the order that decode() gives codes: pair p is (p, 4 + p).
+__device__ __forceinline__ uint4 in_pairs(uint32_t a01, uint32_t a23, uint32_t a45, uint32_t a67) {
+    return make_uint4(__byte_perm(a01, a45, 0x5410), __byte_perm(a01, a45, 0x7632), __byte_perm(a23, a67, 0x5410),
+                      __byte_perm(a23, a67, 0x7632));
+}
+
+// fp32 as three bf16 whose sum it is: 8 bits of the significand each, cut and not rounded, so
+// that the largest numbers stay finite.  Infinities and NaN stay in the first.
+struct ThreeParts {
+    uint16_t part[3];
+};
+
+__device__ __forceinline__ ThreeParts split(float v) {
+    ThreeParts t;
+    uint32_t u = __float_as_uint(v);
+    if ((u & 0x7f800000u) == 0x7f800000u) {
+        t.part[0] = static_cast<uint16_t>((u >> 16) | ((u & 0x007fffffu) != 0u ? 0x40u : 0u));
+        t.part[1] = t.part[2] = 0;
+        return t;
+    }
+    t.part[0] = static_cast<uint16_t>(u >> 16);
+    v -= __uint_as_float(u & 0xffff0000u);
+    u = __float_as_uint(v);
+    t.part[1] = static_cast<uint16_t>(u >> 16);
+    v -= __uint_as_float(u & 0xffff0000u);
+    t.part[2] = static_cast<uint16_t>(__float_as_uint(v) >> 16);
+    return t;
+}
+
+// Eight consecutive elements of x as `PARTS` fragments in decode()'s order; zero past column k.
+template <int PARTS>
+struct EightOfX {
+    uint4 v[PARTS];
+};
+
+template <int PARTS>
+struct RawOfX {
+    uint4 v[PARTS == 1 ? 1 : 2];
+};
+
+template <int PARTS>
+__device__ __forceinline__ RawOfX<PARTS> load_x(const void* row, int col, int k, bool vec) {
+    RawOfX<PARTS> r;
+    if (vec && col + 8 <= k) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<long long>(col) * (PARTS == 1 ? 2 : 4));
+        r.v[0] = __ldg(p);
+        if constexpr (PARTS != 1) r.v[1] = __ldg(p + 1);
+        return r;
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = 0u;
+        if (col + i < k)
+            w[i] = PARTS == 1 ? static_cast<uint32_t>(static_cast<const uint16_t*>(row)[col + i])
+                              : static_cast<const uint32_t*>(row)[col + i];
+    }
+    if constexpr (PARTS == 1) {
+        r.v[0] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+    } else {
+        r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return r;
+}
+
+template <int PARTS>
+__device__ __forceinline__ EightOfX<PARTS> fragments(const RawOfX<PARTS>& r) {
+    EightOfX<PARTS> f;
+    if constexpr (PARTS == 1) {
+        f.v[0] = in_pairs(r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w);
+    } else {
+        const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+        ThreeParts t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = split(__uint_as_float(w[i]));
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            f.v[q] = make_uint4(t[0].part[q] | (static_cast<uint32_t>(t[4].part[q]) << 16),
+                                t[1].part[q] | (static_cast<uint32_t>(t[5].part[q]) << 16),
+                                t[2].part[q] | (static_cast<uint32_t>(t[6].part[q]) << 16),
+                                t[3].part[q] | (static_cast<uint32_t>(t[7].part[q]) << 16));
+    }
+    return f;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A step of 32 columns: two products of 16.
+__device__ __forceinline__ void mma_step(float (&c)[4], const EightCodes& lo, const EightCodes& hi, const uint4& b) {
+    mma_bf16(c, lo.pair[0], hi.pair[0], lo.pair[1], hi.pair[1], b.x, b.y);
+    mma_bf16(c, lo.pair[2], hi.pair[2], lo.pair[3], hi.pair[3], b.z, b.w);
+}
+
+}  // namespace muon

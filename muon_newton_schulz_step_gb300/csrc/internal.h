@@ -347,6 +347,86 @@ bool fp8_token_serves(long long tokens, long long n, long long k);
 cudaError_t launch_fp8_token(const Fp8TokenParams& p, cudaStream_t s);
 cudaError_t read_and_clear_fp8_error(int* code);
 
+// ------------------------------------------------- experts' rows (token_*.cu) --
+constexpr int kSortMaxExperts = 1024;
+constexpr int kRowsMaxTopK = 32;
+
+struct SortParams {
+    const int* chosen;        // entries
+    int* order;               // entries
+    int* place;               // entries
+    int* offsets;             // experts + 1
+    int* table;               // blocks x (experts + 1) counts
+    int entries, first, experts;
+    int blocks, run;          // of the two launches: how many, entries of each
+};
+
+int token_sort_blocks(long long entries);
+cudaError_t launch_token_sort(SortParams p, cudaStream_t s);
+
+// dispatch: x tokens' rows, out sorted rows; combine and its gradient: x sorted rows (y).
+struct RowsParams {
+    const void* x;
+    const void* d;            // gradient of combine's result (tokens)
+    void* out;                // gradient: dy, or nullptr
+    float* dw;                // tokens x top_k, or nullptr
+    const float* weights;     // tokens x top_k, or nullptr: all 1
+    const int* place;         // tokens x top_k
+    const int* offsets;       // groups + 1
+    long long ld_x, ld_d, ld_out;
+    long long tokens, cols;
+    int top_k, groups, rows;  // rows = tokens * top_k
+    int x_bf16, d_bf16, out_bf16;
+    int runs, parts;          // vectors of a row, warps for a row
+};
+
+cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s);
+cudaError_t launch_combine(const RowsParams& p, cudaStream_t s);
+cudaError_t launch_combine_backward(const RowsParams& p, cudaStream_t s);
+
+// ------------------------------------------------------- gated activation --
+struct SwigluParams {
+    const void *gate, *up;
+    const void* d;            // gradient of the result; nullptr: forward
+    void* out;
+    void *d_gate, *d_up;
+    long long ld_gate, ld_up, ld_d, ld_out, ld_dgate, ld_dup;
+    long long rows, cols;
+    unsigned long long by_runs;   // 2^64 / runs, rounded up
+    unsigned runs, total;     // vectors of a row, of the launch
+    int rest;                 // elements past the last vector (one row alone)
+    int bf16;
+};
+
+cudaError_t launch_swiglu(SwigluParams p, cudaStream_t s);
+
+// ------------------------------------------------------ weights of 4 bits --
+struct Int4QuantParams {
+    const void* w;            // batch x rows x cols
+    uint8_t* codes;           // batch x rows x 64 kblocks
+    __nv_bfloat16* scale;     // batch x (128 / block kblocks) x rows
+    long long batch, rows, cols, kblocks;
+    int block, bf16;
+};
+
+cudaError_t launch_int4_quantize(const Int4QuantParams& p, cudaStream_t s);
+
+struct Int4Params {
+    const void* x;            // tokens x k, row stride ld_x
+    const uint8_t* w;         // groups x n x ldw bytes
+    const __nv_bfloat16* scale;
+    void* out;                // tokens x n, row stride ld_out
+    const int* offsets;       // groups + 1, or nullptr: one group
+    long long ld_x, ldw, ld_out;
+    long long w_batch, scale_batch;
+    int tokens, n, k, kblocks, groups;
+    int block;                // columns of a scale
+    int x_bf16, out_f32;
+    int vec;                  // 16-byte loads of x are legal
+};
+
+cudaError_t launch_int4_linear(const Int4Params& p, int sms, cudaStream_t s);
+
 // Launch helpers implemented in the .cu files.
 // `sms`: the grid is one CTA per resident slot on every SM (capped by the tiles).
 cudaError_t launch_momentum_norm(const EwParams& p, int sms, cudaStream_t s);
@@ -385,7 +465,9 @@ int ns5_batched_on_workspace(void* const* ptrs, const int* rows, const int* cols
 int set_last_error(int status, const char* msg);
 
 // What the operators around the step (train_abi.cu) share with it.
-enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpFp8Token, kOpEnd };
+enum OpKind : int { kOpGradNorm = 10, kOpGradClip, kOpRoute, kOpRouteGrad, kOpFp8Quantize, kOpFp8Gemm, kOpFp8Token,
+                    kOpTokenSort, kOpDispatch, kOpCombine, kOpCombineGrad, kOpSwiglu, kOpSwigluGrad, kOpInt4Quantize,
+                    kOpInt4Linear, kOpEnd };
 // The current device, checked; its SMs, and how many clusters of 4, 6 and 8 CTAs of fp8_gemm it holds.
 int op_device(int* sms, int (*clusters)[3] = nullptr);
 int op_launch(int kind, double flops, double bytes, cudaStream_t s, const std::function<cudaError_t()>& f);

@@ -129,7 +129,9 @@ const char* const kKindNames[kNumKinds] = {"norm_pass",    "norm_finalize",  "pa
                                            "ns_gemm_poly", "ns_gemm_update", "ns_small", "unpack",
                                            "adamw",        "ns_gemm_final", "grad_norm", "grad_clip",
                                            "route",        "route_backward", "fp8_quantize", "fp8_gemm",
-                                           "fp8_token"};
+                                           "fp8_token",    "token_sort",     "dispatch", "combine",
+                                           "combine_backward", "swiglu",     "swiglu_backward", "int4_quantize",
+                                           "int4_linear"};
 struct ProfRec {
     int kind;
     cudaEvent_t a, b;

@@ -1,0 +1,201 @@
+// The gated activation between an expert's projections, and its gradient:
+//
+//   s = 1 / (1 + exp(-gate)),  out = gate s up
+//   d_gate = d up s (1 + gate (1 - s)),  d_up = d gate s
+//
+// Bound by memory: 3 and 5 elements move for each one of the result.  A thread takes
+// U runs of up to 16 bytes, kThreads apart, all loaded before the first is used.
+// Operands that lie row behind row are taken as one long row, so that odd widths
+// cost no narrow loads; gate and up as the halves of one product have rows of their
+// own, found by one multiplication (no division) from the run's number.
+//
+// In fp32: exp(-gate) is ex2 of the scaled argument, whose rounding costs |gate| 2^-24
+// of the result's relative error (2^-20 at |gate| = 16, beyond which s is 1 or the
+// result below 2e-6 of up), and the quotient rcp's 1 unit: far below half a step of
+// bf16, and within 1e-6 of the 64-bit result in fp32.  gate = -inf gives NaN, as its
+// product -inf * 0 does.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "vectors.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// Row and first column of run i: i / runs by the multiplier 2^64 / runs + 1, exact for i < 2^32.
+struct Spot {
+    long long row, col;
+};
+
+template <int V>
+__device__ __forceinline__ Spot spot_of(const SwigluParams& p, unsigned i) {
+    const unsigned row = p.runs == 1 ? i : static_cast<unsigned>(__umul64hi(p.by_runs, static_cast<unsigned long long>(i)));
+    return {static_cast<long long>(row), static_cast<long long>(i - row * p.runs) * V};
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Run<T, V> forward(const Run<T, V>& g, const Run<T, V>& u) {
+    Run<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float x = as_float(g.v[i]);
+        o.v[i] = from_float<T>(x * sigmoid(x) * as_float(u.v[i]));
+    }
+    return o;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void backward(const Run<T, V>& g, const Run<T, V>& u, const Run<T, V>& d, Run<T, V>& dg,
+                                         Run<T, V>& du) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float x = as_float(g.v[i]), y = as_float(d.v[i]), s = sigmoid(x);
+        dg.v[i] = from_float<T>(y * as_float(u.v[i]) * (s * fmaf(x, 1.0f - s, 1.0f)));
+        du.v[i] = from_float<T>(y * (x * s));
+    }
+}
+
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(kThreads) k_swiglu(const SwigluParams p) {
+    const T *gate = static_cast<const T*>(p.gate), *up = static_cast<const T*>(p.up);
+    T* out = static_cast<T*>(p.out);
+    const unsigned first = blockIdx.x * (kThreads * U) + threadIdx.x;
+    Run<T, V> g[U], u[U];
+    Spot at[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const unsigned i = first + k * kThreads;
+        if (i >= p.total) break;
+        at[k] = spot_of<V>(p, i);
+        g[k] = load_run<T, V>(gate + at[k].row * p.ld_gate + at[k].col);
+        u[k] = load_run<T, V>(up + at[k].row * p.ld_up + at[k].col);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (first + k * kThreads >= p.total) break;
+        store_run<T, V>(out + at[k].row * p.ld_out + at[k].col, forward<T, V>(g[k], u[k]));
+    }
+    if (first < static_cast<unsigned>(p.rest)) {
+        const long long i = p.cols + first;
+        store_run<T, 1>(out + i, forward<T, 1>(load_run<T, 1>(gate + i), load_run<T, 1>(up + i)));
+    }
+}
+
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(kThreads) k_swiglu_backward(const SwigluParams p) {
+    const T *gate = static_cast<const T*>(p.gate), *up = static_cast<const T*>(p.up), *dy = static_cast<const T*>(p.d);
+    T *d_gate = static_cast<T*>(p.d_gate), *d_up = static_cast<T*>(p.d_up);
+    const unsigned first = blockIdx.x * (kThreads * U) + threadIdx.x;
+    Run<T, V> g[U], u[U], d[U];
+    Spot at[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const unsigned i = first + k * kThreads;
+        if (i >= p.total) break;
+        at[k] = spot_of<V>(p, i);
+        g[k] = load_run<T, V>(gate + at[k].row * p.ld_gate + at[k].col);
+        u[k] = load_run<T, V>(up + at[k].row * p.ld_up + at[k].col);
+        d[k] = load_run<T, V>(dy + at[k].row * p.ld_d + at[k].col);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (first + k * kThreads >= p.total) break;
+        Run<T, V> dg, du;
+        backward<T, V>(g[k], u[k], d[k], dg, du);
+        store_run<T, V>(d_gate + at[k].row * p.ld_dgate + at[k].col, dg);
+        store_run<T, V>(d_up + at[k].row * p.ld_dup + at[k].col, du);
+    }
+    if (first < static_cast<unsigned>(p.rest)) {
+        const long long i = p.cols + first;
+        Run<T, 1> dg, du;
+        backward<T, 1>(load_run<T, 1>(gate + i), load_run<T, 1>(up + i), load_run<T, 1>(dy + i), dg, du);
+        store_run<T, 1>(d_gate + i, dg);
+        store_run<T, 1>(d_up + i, du);
+    }
+}
+
+// Launches of at most 2^31 runs: rows at a time where there are more.
+template <int V, typename F>
+cudaError_t in_parts(SwigluParams p, int size, int u, F&& launch) {
+    const long long runs = p.cols >= V ? p.cols / V : 1;
+    const long long most = (1ll << 31) / runs > 0 ? (1ll << 31) / runs : 1;
+    auto move = [&](const void*& q, long long ld, long long rows) {
+        if (q != nullptr) q = static_cast<const char*>(q) + rows * ld * size;
+    };
+    auto move_out = [&](void*& q, long long ld, long long rows) {
+        if (q != nullptr) q = static_cast<char*>(q) + rows * ld * size;
+    };
+    p.runs = static_cast<unsigned>(runs);
+    p.by_runs = ~0ull / static_cast<unsigned long long>(runs) + 1;
+    for (long long left = p.rows; left > 0;) {
+        const long long rows = left < most ? left : most;
+        p.total = p.cols >= V ? static_cast<unsigned>(rows * runs) : 0u;    // 0: the rest alone
+        const unsigned grid = (p.total + kThreads * u - 1) / (kThreads * u);
+        const cudaError_t e = launch(p, grid > 0 ? grid : 1u);
+        if (e != cudaSuccess) return e;
+        left -= rows;
+        move(p.gate, p.ld_gate, rows);
+        move(p.up, p.ld_up, rows);
+        move(p.d, p.ld_d, rows);
+        move_out(p.out, p.ld_out, rows);
+        move_out(p.d_gate, p.ld_dgate, rows);
+        move_out(p.d_up, p.ld_dup, rows);
+    }
+    return cudaSuccess;
+}
+
+template <typename T, int V>
+cudaError_t run(const SwigluParams& p, cudaStream_t s) {
+    constexpr int kFew = sizeof(T) * V > 16 ? 1 : 2;
+    if (p.d == nullptr)
+        return in_parts<V>(p, sizeof(T), 2 * kFew, [&](const SwigluParams& q, unsigned grid) {
+            k_swiglu<T, V, 2 * kFew><<<grid, kThreads, 0, s>>>(q);
+            return cudaGetLastError();
+        });
+    return in_parts<V>(p, sizeof(T), kFew, [&](const SwigluParams& q, unsigned grid) {
+        k_swiglu_backward<T, V, kFew><<<grid, kThreads, 0, s>>>(q);
+        return cudaGetLastError();
+    });
+}
+
+template <typename T>
+cudaError_t by_width(const SwigluParams& p, int v, cudaStream_t s) {
+    switch (v) {
+        case 8: return run<T, 8>(p, s);
+        case 4: return run<T, 4>(p, s);
+        case 2: return run<T, 2>(p, s);
+        default: return run<T, 1>(p, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(SwigluParams p, cudaStream_t s) {
+    const int size = p.bf16 ? 2 : 4;
+    struct Array {
+        const void* p;
+        long long ld;
+    };
+    const Array arrays[6] = {{p.gate, p.ld_gate}, {p.up, p.ld_up},         {p.d, p.ld_d},
+                             {p.out, p.ld_out},   {p.d_gate, p.ld_dgate}, {p.d_up, p.ld_dup}};
+    bool joined = true;
+    for (const Array& a : arrays) joined = joined && (p.rows == 1 || a.p == nullptr || a.ld == p.cols);
+    p.rest = 0;
+    if (joined && p.cols * p.rows < (1ll << 31)) {       // one long row; what its last whole run leaves goes one by one
+        p.cols *= p.rows;
+        p.rows = 1;
+        p.rest = static_cast<int>(p.cols % 8);
+        p.cols -= p.rest;
+    }
+    RunWidth w(p.cols > 0 ? p.cols : 8);
+    for (const Array& a : arrays)
+        if (a.p != nullptr) w.array(a.p, p.rows == 1 ? w.v : a.ld, size);
+    return p.bf16 ? by_width<__nv_bfloat16>(p, w.v, s) : by_width<float>(p, w.v, s);
+}
+
+}  // namespace muon

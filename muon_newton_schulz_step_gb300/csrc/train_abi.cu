@@ -7,39 +7,15 @@
 
 #include <climits>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <memory>
 
+#include "abi_checks.h"
 #include "internal.h"
 #include "muon.h"
 
 namespace muon {
 namespace {
-
-int fail(int status, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return set_last_error(status, buf);
-}
-
-int check_dtype(int dtype, const char* what) {
-    if (dtype != MUON_BF16 && dtype != MUON_F32) return fail(MUON_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
-    return MUON_OK;
-}
-
-size_t dtype_size(int dtype) { return dtype == MUON_F32 ? 4 : 2; }
-
-int check_align(const void* p, size_t align, const char* what) {
-    if (p == nullptr) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", what);
-    if (reinterpret_cast<uintptr_t>(p) % align != 0)
-        return fail(MUON_ERR_INVALID_ARG, "%s is not %zu-byte aligned", what, align);
-    return MUON_OK;
-}
 
 // ----------------------------------------------------------- gradient norm --
 int check_grads(const void* const* G, const long long* numel, const int* dtypes, int count, const char* what) {
@@ -227,25 +203,6 @@ int fill_route(RouteParams& p, const void* logits, int dtype, long long tokens, 
 }
 
 // --------------------------------------------------------------- 8 bits --
-constexpr long long kMaxRows = 1ll << 30;
-
-int check_groups(long long tokens, int groups, const int* offsets) {
-    if (tokens < 0 || tokens > kMaxRows) return fail(MUON_ERR_INVALID_ARG, "rows is %lld (0 to 2^30)", tokens);
-    if (groups < 1 || groups > kFp8MaxGroups)
-        return fail(MUON_ERR_INVALID_ARG, "groups is %d (1 to %d)", groups, kFp8MaxGroups);
-    if (groups > 1 && offsets == nullptr) return fail(MUON_ERR_INVALID_ARG, "offsets is NULL with %d groups", groups);
-    if (offsets != nullptr && reinterpret_cast<uintptr_t>(offsets) % 4 != 0)
-        return fail(MUON_ERR_INVALID_ARG, "offsets is not 4-byte aligned");
-    return MUON_OK;
-}
-
-int check_dim(long long n, const char* what) {
-    if (n < 1 || n > (1ll << 24)) return fail(MUON_ERR_INVALID_ARG, "%s is %lld (1 to 2^24)", what, n);
-    return MUON_OK;
-}
-
-long long up128(long long n) { return (n + 127) / 128 * 128; }
-
 QuantParams quantize_params(const void* x, int dtype, long long rows, long long cols, long long ld, int groups,
                             const int* offsets, void* row_codes, void* row_scale, void* col_codes, void* col_scale) {
     QuantParams p = {};
@@ -291,14 +248,6 @@ struct ColCodes {
           codes(static_cast<char*>(at)), scale(at != nullptr ? codes + code_bytes : nullptr) {}
     size_t bytes() const { return code_bytes + scale_bytes; }
 };
-
-int check_workspace(const void* ws, size_t have, size_t need) {
-    if (need == 0) return MUON_OK;
-    const int rc = check_align(ws, 16, "workspace");
-    if (rc != MUON_OK) return rc;
-    if (have < need) return fail(MUON_ERR_OOM, "workspace has %zu bytes; %zu are needed", have, need);
-    return MUON_OK;
-}
 
 int check_linear(int dtype, const char* what, long long tokens, long long ld, int cols, int n, int k, int groups,
                  const int* offsets, const void* w_codes, const void* w_scale) {
