@@ -930,6 +930,37 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
 
 
 # ----------------------------------- between an expert layer's routing and its result --
+# torch.empty costs a call of a few microseconds as much again (4 us of 9, measured on a
+# GB300's host between launches); the allocation alone, on the current device, 0.9.
+_allocate = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new_rows(rows, cols, dtype):
+    """A new tensor, rows x cols, on the current device and stream."""
+    if _allocate is None:
+        return torch.empty((rows, cols), dtype=dtype, device="cuda")
+    return _allocate((rows, cols), (cols or 1, 1), dtype)
+
+
+def _new_vector(n, dtype):
+    if _allocate is None:
+        return torch.empty(n, dtype=dtype, device="cuda")
+    return _allocate((n,), (1,), dtype)
+
+
+def _matrix(name, t, rows=None, cols=None):
+    """(rows, cols, row stride, type code) of a 2-D bf16 or fp32 CUDA tensor with contiguous rows."""
+    try:
+        code, (r, c), (ld, inner) = _FLOAT_CODE[t.dtype], t.shape, t.stride()
+        if inner == 1 and ld >= c and (rows is None or r == rows) and (cols is None or c == cols) \
+                and t.is_cuda and t.get_device() == _current_device():
+            return r, c, ld, code
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
+    r, c, ld = _check_rows(name, t, _FLOATS, rows, cols)    # says what is wrong, or takes a form seldom met
+    return r, c, ld, _FLOAT_CODE[t.dtype]
+
+
 class TokenPlan(NamedTuple):
     """Where the rows of routed tokens lie, sorted by expert (``muon_sort_tokens``;
     int32).  ``order`` (tokens * top_k): the entry (token * top_k + j) at each place;
@@ -946,6 +977,9 @@ def muon_sort_tokens(chosen, experts: int, *, first: int = 0, stream=None) -> To
     gives them) sorted by expert, for the ``experts`` experts from number ``first`` on
     (those that this rank holds).  Entries of other experts, or of none, come first;
     equal ones keep their order."""
+    if stream is not None:
+        with _on(stream):
+            return muon_sort_tokens(chosen, experts, first=first)
     tokens, top_k, _ = _check_rows("chosen", chosen, (torch.int32,))
     if not chosen.is_contiguous():
         raise ValueError("chosen must be contiguous")
@@ -954,21 +988,19 @@ def muon_sort_tokens(chosen, experts: int, *, first: int = 0, stream=None) -> To
         raise ValueError(f"experts is {experts}")
     L = lib()
     need = L.muon_sort_tokens_workspace_bytes(n, experts)
-    with _on(stream):
-        order = torch.empty(n, dtype=torch.int32, device="cuda")
-        place = torch.empty((tokens, top_k), dtype=torch.int32, device="cuda")
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device="cuda")
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
-        _check(L.muon_sort_tokens(chosen.data_ptr(), n, first, experts, None if ws is None else ws.data_ptr(), need,
-                                  order.data_ptr(), place.data_ptr(), offsets.data_ptr(), _handle(stream)))
+    order, place, offsets = _new_vector(n, torch.int32), _new_rows(tokens, top_k, torch.int32), \
+        _new_vector(experts + 1, torch.int32)
+    ws = _new_vector(need, torch.uint8) if need else None
+    _check(L.muon_sort_tokens(chosen.data_ptr(), n, first, experts, None if ws is None else ws.data_ptr(), need,
+                              order.data_ptr(), place.data_ptr(), offsets.data_ptr(), _handle(None)))
     return TokenPlan(order, place, offsets)
 
 
 def _check_plan(plan, tokens=None):
-    """(tokens, top_k, experts) of a plan, whose tensors are checked."""
+    """(tokens, top_k, experts, addresses of places and offsets) of a plan, whose tensors are checked."""
     if not isinstance(plan, TokenPlan):
         raise ValueError("plan must be a TokenPlan, as muon_sort_tokens makes it")
-    place, offsets = plan.place, plan.offsets
+    _, place, offsets = plan
     t, top_k, _ = _check_rows("plan.place", place, (torch.int32,), tokens)
     if not place.is_contiguous():
         raise ValueError("plan.place must be contiguous")
@@ -976,22 +1008,24 @@ def _check_plan(plan, tokens=None):
         raise ValueError("plan.place has no columns")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("plan.offsets must be a 1-D int32 CUDA tensor of experts + 1 entries")
-    _check_vector("plan.offsets", offsets, torch.int32, offsets.numel())
-    return t, top_k, offsets.numel() - 1
+    n = offsets.numel()
+    _check_vector("plan.offsets", offsets, torch.int32, n)
+    return t, top_k, n - 1, place.data_ptr(), offsets.data_ptr()
 
 
 def muon_dispatch_tokens(x, plan: TokenPlan, stream=None) -> torch.Tensor:
     """``x``'s rows (tokens x cols, bf16 or fp32) sorted by expert: tokens * top_k
     rows, row plan.place[t, j] a copy of x[t]; rows of no expert are zero.  Its gradient
     is ``muon_combine_tokens`` without weights."""
-    tokens, cols, ld = _check_rows("x", x, _FLOATS)
-    _, top_k, experts = _check_plan(plan, tokens)
-    with _on(stream):
-        out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device="cuda")
-        if cols:
-            _check(lib().muon_dispatch_tokens(x.data_ptr(), _dtype_code(x), tokens, cols, ld, top_k,
-                                              plan.place.data_ptr(), plan.offsets.data_ptr(), experts, out.data_ptr(),
-                                              cols, _handle(stream)))
+    if stream is not None:
+        with _on(stream):
+            return muon_dispatch_tokens(x, plan)
+    tokens, cols, ld, code = _matrix("x", x)
+    _, top_k, experts, place, offsets = _check_plan(plan, tokens)
+    out = _new_rows(tokens * top_k, cols, x.dtype)
+    if cols:
+        _check(lib().muon_dispatch_tokens(x.data_ptr(), code, tokens, cols, ld, top_k, place, offsets, experts,
+                                          out.data_ptr(), cols, _handle(None)))
     return out
 
 
@@ -1009,18 +1043,20 @@ def muon_combine_tokens(y, plan: TokenPlan, weights=None, *, out_dtype=None, str
     fp32 in the order of j.  ``y``: tokens * top_k rows, bf16 or fp32; ``weights``: fp32,
     tokens x top_k (None: 1); ``out_dtype``: y's unless given.  Entries without an expert
     here take no part, whatever their rows and weights hold."""
-    tokens, top_k, experts = _check_plan(plan)
-    _, cols, ld = _check_rows("y", y, _FLOATS, tokens * top_k)
+    if stream is not None:
+        with _on(stream):
+            return muon_combine_tokens(y, plan, weights, out_dtype=out_dtype)
+    tokens, top_k, experts, place, offsets = _check_plan(plan)
+    _, cols, ld, code = _matrix("y", y, tokens * top_k)
     wptr = _check_weights(weights, tokens, top_k)
-    out_dtype = y.dtype if out_dtype is None else out_dtype
-    if out_dtype not in _FLOATS:
+    if out_dtype is None:
+        out_dtype = y.dtype
+    elif out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be one of {_FLOATS}")
-    with _on(stream):
-        out = torch.empty((tokens, cols), dtype=out_dtype, device="cuda")
-        if cols:
-            _check(lib().muon_combine_tokens(y.data_ptr(), _dtype_code(y), ld, tokens, cols, top_k, plan.place.data_ptr(),
-                                             plan.offsets.data_ptr(), experts, wptr, out.data_ptr(), _dtype_code(out),
-                                             cols, _handle(stream)))
+    out = _new_rows(tokens, cols, out_dtype)
+    if cols:
+        _check(lib().muon_combine_tokens(y.data_ptr(), code, ld, tokens, cols, top_k, place, offsets, experts, wptr,
+                                         out.data_ptr(), _FLOAT_CODE[out_dtype], cols, _handle(None)))
     return out
 
 
@@ -1030,40 +1066,43 @@ def muon_combine_tokens_backward(d, y, plan: TokenPlan, weights=None, *, need_dy
     dy[plan.place[t, j]] = weights[t, j] * d[t] (y's dtype), d_weights[t, j] = <d[t],
     y[plan.place[t, j]]> (fp32), both zero for entries without an expert here.  Either may be
     left out (None); without weights there is no d_weights."""
-    tokens, top_k, experts = _check_plan(plan)
-    _, cols, ld_d = _check_rows("d", d, _FLOATS, tokens)
-    rows, _, ld_y = _check_rows("y", y, _FLOATS, tokens * top_k, cols)
+    if stream is not None:
+        with _on(stream):
+            return muon_combine_tokens_backward(d, y, plan, weights, need_dy=need_dy, need_dw=need_dw)
+    tokens, top_k, experts, place, offsets = _check_plan(plan)
+    _, cols, ld_d, d_code = _matrix("d", d, tokens)
+    rows, _, ld_y, code = _matrix("y", y, tokens * top_k, cols)
     wptr = _check_weights(weights, tokens, top_k)
-    need_dw = need_dw and weights is not None
-    dy = dw = None
-    with _on(stream):
-        if need_dy:
-            dy = torch.empty((rows, cols), dtype=y.dtype, device="cuda")
-        if need_dw:
-            dw = (torch.empty if cols else torch.zeros)((tokens, top_k), dtype=torch.float32, device="cuda")
-        if cols:
-            _check(lib().muon_combine_tokens_backward(
-                d.data_ptr(), _dtype_code(d), ld_d, y.data_ptr(), _dtype_code(y), ld_y, tokens, cols, top_k,
-                plan.place.data_ptr(), plan.offsets.data_ptr(), experts, wptr, dy.data_ptr() if need_dy else None, cols,
-                dw.data_ptr() if need_dw else None, _handle(stream)))
+    dy = _new_rows(rows, cols, y.dtype) if need_dy else None
+    dw = _new_rows(tokens, top_k, torch.float32) if need_dw and weights is not None else None
+    if cols:
+        _check(lib().muon_combine_tokens_backward(
+            d.data_ptr(), d_code, ld_d, y.data_ptr(), code, ld_y, tokens, cols, top_k, place, offsets, experts, wptr,
+            None if dy is None else dy.data_ptr(), cols, None if dw is None else dw.data_ptr(), _handle(None)))
+    elif dw is not None:
+        dw.zero_()
     return dy, dw
 
 
 def _check_gated(gate, up):
-    rows, cols, ld_gate = _check_rows("gate", gate, _FLOATS)
-    _, _, ld_up = _check_rows("up", up, (gate.dtype,), rows, cols)
-    return rows, cols, ld_gate, ld_up
+    rows, cols, ld_gate, code = _matrix("gate", gate)
+    _, _, ld_up, up_code = _matrix("up", up, rows, cols)
+    if up_code != code:
+        raise ValueError("gate and up must share one dtype")
+    return rows, cols, ld_gate, ld_up, code
 
 
 def muon_swiglu(gate, up, stream=None) -> torch.Tensor:
     """gate / (1 + exp(-gate)) * up, in fp32 and rounded once (rows x cols, bf16 or fp32,
     both of one dtype; views such as the halves of one product are read in place)."""
-    rows, cols, ld_gate, ld_up = _check_gated(gate, up)
-    with _on(stream):
-        out = torch.empty((rows, cols), dtype=gate.dtype, device="cuda")
-        if cols:
-            _check(lib().muon_swiglu(gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, _dtype_code(gate), rows, cols,
-                                     out.data_ptr(), cols, _handle(stream)))
+    if stream is not None:
+        with _on(stream):
+            return muon_swiglu(gate, up)
+    rows, cols, ld_gate, ld_up, code = _check_gated(gate, up)
+    out = _new_rows(rows, cols, gate.dtype)
+    if cols:
+        _check(lib().muon_swiglu(gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, code, rows, cols, out.data_ptr(), cols,
+                                 _handle(None)))
     return out
 
 
@@ -1071,19 +1110,21 @@ def muon_swiglu_backward(d, gate, up, *, joined: bool = False, stream=None):
     """(d_gate, d_up) of ``muon_swiglu`` from ``d``, in its dtype.  ``joined``: the two are
     halves of one tensor (rows x 2 cols), as the gradient of one product that made gate and
     up wants them."""
-    rows, cols, ld_gate, ld_up = _check_gated(gate, up)
-    _, _, ld_d = _check_rows("d", d, (gate.dtype,), rows, cols)
-    with _on(stream):
-        if joined:
-            both = torch.empty((rows, 2 * cols), dtype=gate.dtype, device="cuda")
-            d_gate, d_up, ld = both[:, :cols], both[:, cols:], 2 * cols
-        else:
-            d_gate = torch.empty((rows, cols), dtype=gate.dtype, device="cuda")
-            d_up, ld = torch.empty_like(d_gate), cols
-        if cols:
-            _check(lib().muon_swiglu_backward(d.data_ptr(), ld_d, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up,
-                                              _dtype_code(gate), rows, cols, d_gate.data_ptr(), ld, d_up.data_ptr(), ld,
-                                              _handle(stream)))
+    if stream is not None:
+        with _on(stream):
+            return muon_swiglu_backward(d, gate, up, joined=joined)
+    rows, cols, ld_gate, ld_up, code = _check_gated(gate, up)
+    _, _, ld_d, d_code = _matrix("d", d, rows, cols)
+    if d_code != code:
+        raise ValueError("d must be of gate's dtype")
+    if joined:
+        both = _new_rows(rows, 2 * cols, gate.dtype)
+        d_gate, d_up, ld = both[:, :cols], both[:, cols:], 2 * cols
+    else:
+        d_gate, d_up, ld = _new_rows(rows, cols, gate.dtype), _new_rows(rows, cols, gate.dtype), cols
+    if cols:
+        _check(lib().muon_swiglu_backward(d.data_ptr(), ld_d, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, code, rows,
+                                          cols, d_gate.data_ptr(), ld, d_up.data_ptr(), ld, _handle(None)))
     return d_gate, d_up
 
 
@@ -1147,13 +1188,14 @@ def muon_int4_linear(x, w: Int4Matrix, *, offsets=None, out_dtype=torch.bfloat16
     """y = x W^T with a weight of 4 bits (``muon_int4_quantize_weight``), for serving: ``x``
     (tokens x k, bf16 or fp32) is not rounded.  With ``offsets``, tokens are sorted by expert
     and ``w`` is stacked over experts; rows of no expert give zero.  The weight has no gradient."""
+    if stream is not None:
+        with _on(stream):
+            return muon_int4_linear(x, w, offsets=offsets, out_dtype=out_dtype)
     n, k, groups, optr = _check_int4(w, offsets)
-    tokens, _, ld = _check_rows("x", x, _FLOATS, None, k)
+    tokens, _, ld, code = _matrix("x", x, None, k)
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be one of {_FLOATS}")
-    with _on(stream):
-        out = torch.empty((tokens, n), dtype=out_dtype, device="cuda")
-        _check(lib().muon_int4_linear(x.data_ptr(), _dtype_code(x), tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(),
-                                      int(w.block), n, k, groups, optr, out.data_ptr(), _dtype_code(out), n,
-                                      _handle(stream)))
+    out = _new_rows(tokens, n, out_dtype)
+    _check(lib().muon_int4_linear(x.data_ptr(), code, tokens, ld, w.codes.data_ptr(), w.scale.data_ptr(), int(w.block), n,
+                                  k, groups, optr, out.data_ptr(), _FLOAT_CODE[out_dtype], n, _handle(None)))
     return out

@@ -128,129 +128,304 @@ __device__ __forceinline__ void zero_rest(const Int4Params& p, const GroupTable&
     }
 }
 
-// ------------------------------------------------------------ few tokens --
-// A block takes 16 rows of a weight and up to eight tokens; its warps take the reduction's
-// blocks of 128 in turn and add their sums up in shared memory at the end, in a fixed order.
-// Codes of kAhead blocks are under way for each warp, the first of the next item's before
-// the sums of this one are added.  x comes through the first level, which the items of a
-// block share.
-constexpr int kRows = 16;
-constexpr int kTokens = 8;
-constexpr int kAhead = 4;
+// -------------------------------------------------------------- products --
+// An item is 16 RT rows of a weight and up to 8 NT tokens of one group; a block takes
+// items, all its warps together: each the reduction's blocks of 128 in turn (a unit), and
+// at an item's end they add their sums up in shared memory, in a fixed order.  So a single
+// token's product fills the SMs (one token x 6144 x 6144 is 384 items), and any number of
+// tokens or groups runs the same way.
+//
+// Codes and scales of kStages - 1 units are under way for each warp by asynchronous copies
+// into a ring of its own, over the ends of items, with no wait between warps.  A row's 64
+// bytes lie there in 16-byte pieces that ldmatrix reads without bank conflicts; it hands lane
+// (r, j) the word of 8 codes that its fragment wants.  Fragment rows r and r + 8 are the
+// weight's rows 2 r and 2 r + 1, whose scales are neighbours.  x comes from L2 through the
+// first level, a step ahead.
+template <int RT>
+struct Unit {
+    uint4 codes[RT * 64];                                  // 16 RT rows of 64 bytes, even rows first
+    uint32_t scale[4][RT * 8];                             // bf16 pairs
+};
 
-template <int BLOCK, int PARTS>
-__global__ void __launch_bounds__(kThreads, 2) k_int4_few(const Int4Params p) {
-    constexpr int kScales = 128 / BLOCK;
+// Shared memory of two blocks per SM (three where RT is 1); sums of one or two items.
+template <int PARTS, int RT, int NT>
+struct Shape {
+    static constexpr int kStages = RT == 1 ? 6 : NT == 4 ? 3 : 4;
+    static constexpr int kTurns = NT == 1 ? 2 : 1;
+    static constexpr int kAheadX = NT == 4 ? 1 : PARTS * NT > 4 ? 2 : 4;       // steps whose x is in registers
+    static constexpr size_t kRing = sizeof(Unit<RT>) * kStages * kWarps;
+};
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Piece m of row `slot` of a unit, in 16 bytes: eight rows' pieces m lie in eight different places modulo 128.
+__device__ __forceinline__ int piece(int slot, int m) { return slot * 4 + (m ^ ((slot >> 1) & 3)); }
+
+template <int BLOCK, int PARTS, int RT, int NT>
+__global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int4_linear(const Int4Params p) {
+    constexpr int kScales = 128 / BLOCK, kSteps = 4 / kScales;
+    constexpr int kRows = 16 * RT, kTokens = 8 * NT, kSize = PARTS == 1 ? 2 : 4;
+    constexpr int kStages = Shape<PARTS, RT, NT>::kStages, kTurns = Shape<PARTS, RT, NT>::kTurns, kAheadX = Shape<PARTS, RT, NT>::kAheadX;
+    extern __shared__ uint4 dynamic[];
     __shared__ GroupTable table;
-    __shared__ float part[kWarps][kTokens][kRows + 1];
+    __shared__ float part[kTurns][kWarps][kTokens][kRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, j = lane & 3;
-    make_table<kTokens>(p, table);
-    const int row_tiles = (p.n + kRows - 1) / kRows;
-    const long long items = static_cast<long long>(table.tile0[p.groups]) * row_tiles;
-
-    uint4 codes[kAhead][2];
-    const uint8_t *w_lo = nullptr, *w_hi = nullptr;
-    auto aim = [&](long long item) {
-        const int tile = static_cast<int>(item / row_tiles), n0 = static_cast<int>(item - static_cast<long long>(tile) * row_tiles) * kRows;
-        const uint8_t* w = p.w + group_of(table, p.groups, tile) * p.w_batch;
-        // rows past the last read the last one's codes; their results are not stored
-        w_lo = w + min(n0 + r, p.n - 1) * p.ldw;
-        w_hi = w + min(n0 + r + 8, p.n - 1) * p.ldw;
-    };
-    auto fetch = [&](int kb0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (kb0 + i * kWarps < p.kblocks) {
-                codes[i][0] = load_codes<BLOCK>(w_lo, kb0 + i * kWarps, j);
-                codes[i][1] = load_codes<BLOCK>(w_hi, kb0 + i * kWarps, j);
-            }
+    Unit<RT>* const ring = reinterpret_cast<Unit<RT>*>(dynamic) + warp * kStages;
+    const uint32_t ring_at = shared_address(ring);
+    const unsigned row_tiles = (p.n + kRows - 1) / kRows;
+    unsigned tiles = (p.tokens + kTokens - 1) / kTokens;
+    if (p.offsets != nullptr) {
+        make_table<kTokens>(p, table);
+        tiles = table.tile0[p.groups];
+    }
+    // this block's first item, and the way from one to the next
+    const unsigned first_tile = blockIdx.x / row_tiles, first_row = blockIdx.x - first_tile * row_tiles;
+    auto next_of = [&](unsigned& tile, unsigned& row) {
+        tile += p.hop_tiles;
+        row += p.hop_rows;
+        if (row >= row_tiles) {
+            row -= row_tiles;
+            ++tile;
         }
     };
-    long long item = blockIdx.x;
-    if (item < items) {
-        aim(item);
-        fetch(warp);
-    }
-    for (; item < items; item += gridDim.x) {
-        const int tile = static_cast<int>(item / row_tiles), n0 = static_cast<int>(item - static_cast<long long>(tile) * row_tiles) * kRows;
-        const int g = group_of(table, p.groups, tile);
-        const int t0 = table.lo[g] + (tile - table.tile0[g]) * kTokens;
-        const int tokens = min(kTokens, table.lo[g] + table.cnt[g] - t0);
-        const __nv_bfloat16* s = p.scale + g * p.scale_batch;
-        const __nv_bfloat16 *s_lo = s + min(n0 + r, p.n - 1), *s_hi = s + min(n0 + r + 8, p.n - 1);
-        // as B fragment a lane holds token r; as accumulator tokens 2 j and 2 j + 1
-        const bool have = r < tokens;
-        const char* x = static_cast<const char*>(p.x) + (t0 + (have ? r : 0)) * p.ld_x * (PARTS == 1 ? 2 : 4);
 
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int kb0 = warp; kb0 < p.kblocks; kb0 += kAhead * kWarps) {
-            if (kb0 != warp) fetch(kb0);
+    // where the copies are: column tile, row tile, block of the reduction; this lane's sources and places
+    unsigned ct = first_tile, cr = first_row;
+    int ckb = warp;
+    const uint8_t* codes[2 * RT];
+    const __nv_bfloat16* scales = nullptr;
+    bool scaled = false;                                   // this lane copies scales of the item
+    const long long scale_hop = static_cast<long long>(kWarps) * kScales * p.n;
+    // rows 8 i + lane / 4, even ones before odd ones; 16 rows on is 16 slots on
+    const int row0 = lane >> 2, slot0 = (row0 & 1) * 8 + (row0 >> 1);
+    const int put[2] = {piece(slot0, lane & 3) * 16, piece(slot0 + 4, lane & 3) * 16};
+    auto aim = [&] {
+        if (ct >= tiles) return;
+        const int g = p.offsets != nullptr ? group_of(table, p.groups, ct) : 0, n0 = static_cast<int>(cr) * kRows;
+        const uint8_t* w = p.w + g * p.w_batch + ckb * 64 + (lane & 3) * 16;
+        // rows past the last are the last one again; their results are not stored
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int kb = kb0 + i * kWarps;
-                if (kb >= p.kblocks) break;
-                float by[kScales][2];
+        for (int i = 0; i < 2 * RT; ++i) codes[i] = w + min(n0 + i * 8 + row0, p.n - 1) * p.ldw;
+        const int q = lane / (8 * RT), at = n0 + 2 * (lane % (8 * RT));
+        scaled = p.pairs && q < kScales && at < p.n;
+        scales = p.scale + g * p.scale_batch + static_cast<long long>(ckb * kScales + q) * p.n + at;
+    };
+    auto copy = [&](int stage) {
+        if (ct < tiles && ckb < p.kblocks) {
+            const uint32_t to = ring_at + stage * static_cast<int>(sizeof(Unit<RT>));
+#pragma unroll
+            for (int i = 0; i < 2 * RT; ++i) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + put[i & 1] + (i >> 1) * 1024), "l"(codes[i]));
+                codes[i] += kWarps * 64;
+            }
+            if (scaled) {                                  // pairs of rows' scales: a lane's, and those 32 lanes on
+#pragma unroll
+                for (int i = 0; i < kScales * RT; i += 4)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + RT * 1024 + (i * 8 + lane) * 4),
+                                 "l"(scales + static_cast<long long>(i / RT) * p.n));
+                scales += scale_hop;
+            }
+            ckb += kWarps;
+            if (ckb >= p.kblocks) {
+                ckb = warp;
+                next_of(ct, cr);
+                aim();
+            }
+        }
+        asm volatile("cp.async.commit_group;");
+    };
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) copy(i);
+    int stage = 0, turn = 0;
+    // ldmatrix: lane 8 m + i names piece m of row i; eight rows on, the pieces lie alike
+    const int get = piece(lane & 7, lane >> 3) * 16;
+
+    // an item: its group, rows, tokens, and where this lane's tokens lie.  As B fragment a lane
+    // holds tokens r, r + 8, ..; as accumulator tokens 2 j and 2 j + 1 of each eight
+    struct Item {
+        int g, n0, t0, tokens;
+        const char* x[NT];
+    };
+    unsigned tile = first_tile, row_tile = first_row;
+    auto here = [&](Item& it) {
+        if (tile >= tiles) return false;
+        it.n0 = static_cast<int>(row_tile) * kRows;
+        it.g = 0;
+        it.t0 = static_cast<int>(tile) * kTokens;
+        int end = p.tokens;
+        if (p.offsets != nullptr) {
+            it.g = group_of(table, p.groups, tile);
+            it.t0 = table.lo[it.g] + (static_cast<int>(tile) - table.tile0[it.g]) * kTokens;
+            end = table.lo[it.g] + table.cnt[it.g];
+        }
+        it.tokens = min(kTokens, end - it.t0);
+        // tokens past the last are the last one again; their results are not stored
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            it.x[t] = static_cast<const char*>(p.x) + ((it.t0 + min(8 * t + r, it.tokens - 1)) * p.ld_x + 8 * j) * kSize;
+        next_of(tile, row_tile);
+        return true;
+    };
+    auto load = [&](RawOfX<PARTS>(&raw)[NT], const Item& it, int kb, int m) {
+        const int col = kb * 128 + 32 * m;                 // of lane 0
+        if (p.vec && kb * 128 + 128 <= p.k) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) raw[t] = load_x<PARTS>(it.x[t] + kb * (128 * kSize) + 32 * kSize * m);
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) raw[t] = load_x_edge<PARTS>(it.x[t] + static_cast<long long>(col) * kSize, p.k - col - 8 * j);
+        }
+    };
+
+    // x of a whole unit ahead: step m's is loaded anew as soon as it is used
+    RawOfX<PARTS> raw[kAheadX][NT];
+    Item it;
+    bool more = here(it);
+    if (kAheadX > 1 && more && warp < p.kblocks) {
+#pragma unroll
+        for (int m = 0; m < kAheadX; ++m) load(raw[m], it, warp, m);
+    }
+    while (more) {
+        const int g = it.g, n0 = it.n0, t0 = it.t0, tokens = it.tokens;
+        bool looked = false;
+        float acc[RT][NT][4] = {};
+        for (int kb = warp; kb < p.kblocks; kb += kWarps) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            const Unit<RT>& u = ring[stage];
+            const uint32_t from = ring_at + stage * static_cast<int>(sizeof(Unit<RT>)) + get;
+            uint32_t w[RT][2][4];
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[a][h][0]), "=r"(w[a][h][1]), "=r"(w[a][h][2]), "=r"(w[a][h][3])
+                                 : "r"(from + a * 1024 + h * 512));
+            uint32_t by[RT][kScales];
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
 #pragma unroll
                 for (int q = 0; q < kScales; ++q) {
-                    by[q][0] = __bfloat162float(s_lo[static_cast<long long>(kb * kScales + q) * p.n]);
-                    by[q][1] = __bfloat162float(s_hi[static_cast<long long>(kb * kScales + q) * p.n]);
+                    if (p.pairs) {
+                        by[a][q] = u.scale[q][a * 8 + r];
+                    } else {
+                        const uint16_t* s = reinterpret_cast<const uint16_t*>(p.scale) + g * p.scale_batch +
+                                            static_cast<long long>(kb * kScales + q) * p.n;
+                        const int row = n0 + a * 16 + 2 * r;
+                        by[a][q] = s[min(row, p.n - 1)] | (static_cast<uint32_t>(s[min(row + 1, p.n - 1)]) << 16);
+                    }
                 }
-                RawOfX<PARTS> raw[4];
+            // into the place of the unit before this one, which every lane has read
+            copy(stage == 0 ? kStages - 1 : stage - 1);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+
+            int next_kb = kb + kWarps;
+            float c[RT][NT][4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < 4; ++m) {
+                if (kAheadX == 1) load(raw[0], it, kb, m);
+                EightCodes lo[RT], hi[RT];
 #pragma unroll
-                    for (int v = 0; v < (PARTS == 1 ? 1 : 2); ++v) raw[m].v[v] = make_uint4(0, 0, 0, 0);
-                    if (have) raw[m] = load_x<PARTS>(x, kb * 128 + chunk_of<BLOCK>(m, j) * 8, p.k, p.vec);
+                for (int a = 0; a < RT; ++a) {
+                    lo[a] = decode(w[a][0][m]);
+                    hi[a] = decode(w[a][1][m]);
                 }
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const EightCodes lo = decode(word_of(codes[i][0], m)), hi = decode(word_of(codes[i][1], m));
-                    const EightOfX<PARTS> b = fragments<PARTS>(raw[m]);
+                for (int t = 0; t < NT; ++t) {
+                    const EightOfX<PARTS> b = fragments<PARTS>(raw[m % kAheadX][t]);
 #pragma unroll
-                    for (int q = PARTS - 1; q >= 0; --q) mma_step(c, lo, hi, b.v[q]);
-                    if ((m + 1) % (4 / kScales) == 0) {
-                        const int q = m / (4 / kScales);
-                        acc[0] = fmaf(c[0], by[q][0], acc[0]);
-                        acc[1] = fmaf(c[1], by[q][0], acc[1]);
-                        acc[2] = fmaf(c[2], by[q][1], acc[2]);
-                        acc[3] = fmaf(c[3], by[q][1], acc[3]);
-                        c[0] = c[1] = c[2] = c[3] = 0.0f;
+                    for (int a = 0; a < RT; ++a)
+#pragma unroll
+                        for (int q = PARTS - 1; q >= 0; --q)
+                            mma_step(c[a][t], q == PARTS - 1 && m % kSteps == 0, lo[a], hi[a], b.v[q]);
+                }
+                if (kAheadX > 1) {
+                    const int at = m + kAheadX;
+                    if (at == 4 && next_kb >= p.kblocks) { // on to the next item's first unit
+                        more = here(it);
+                        looked = true;
+                        next_kb = more ? warp : -1;
+                    }
+                    if (at < 4) load(raw[m % kAheadX], it, kb, at);
+                    else if (next_kb >= 0) load(raw[m % kAheadX], it, next_kb, at - 4);
+                }
+                if ((m + 1) % kSteps == 0) {
+#pragma unroll
+                    for (int a = 0; a < RT; ++a) {
+                        const uint32_t s = by[a][m / kSteps];
+                        const float s_lo = __uint_as_float(s << 16), s_hi = __uint_as_float(s & 0xffff0000u);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            acc[a][t][0] = fmaf(c[a][t][0], s_lo, acc[a][t][0]);
+                            acc[a][t][1] = fmaf(c[a][t][1], s_lo, acc[a][t][1]);
+                            acc[a][t][2] = fmaf(c[a][t][2], s_hi, acc[a][t][2]);
+                            acc[a][t][3] = fmaf(c[a][t][3], s_hi, acc[a][t][3]);
+                        }
                     }
                 }
             }
         }
-        if (item + gridDim.x < items) {
-            aim(item + gridDim.x);
-            fetch(warp);
-        }
-        __syncthreads();                                   // the sums of the item before have been read
-        part[warp][2 * j][r] = acc[0];
-        part[warp][2 * j + 1][r] = acc[1];
-        part[warp][2 * j][r + 8] = acc[2];
-        part[warp][2 * j + 1][r + 8] = acc[3];
-        __syncthreads();
-        if (threadIdx.x < kTokens * kRows) {
-            const int t = threadIdx.x / kRows, n = threadIdx.x % kRows;
-            float sum = 0.0f;
+        // with room for two items' sums, those of the item before the last have been read by now
+        if (kTurns == 1) __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) sum += part[i][t][n];
-            if (t < tokens && n0 + n < p.n) store_out(p, (t0 + t) * p.ld_out + n0 + n, sum * kCodeUnit);
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[turn][warp][8 * t + 2 * j + (i & 1)][16 * a + 2 * r + (i >> 1)] = acc[a][t][i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTokens * kRows; i += kThreads) {
+            const int t = (i + static_cast<int>(threadIdx.x)) / kRows, n = (i + static_cast<int>(threadIdx.x)) % kRows;
+            if (t < tokens && n0 + n < p.n) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) sum += part[turn][k][t][n];
+                store_out(p, (t0 + t) * p.ld_out + n0 + n, sum * kCodeUnit);
+            }
         }
+        turn = kTurns - 1 - turn;
+        if (!looked) more = here(it);                      // (warps past the last block have no units)
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (p.offsets != nullptr) zero_rest(p, table);
 }
 
-template <int BLOCK>
-cudaError_t few(const Int4Params& p, int sms, cudaStream_t s) {
-    const long long tiles = p.tokens / kTokens + (p.groups < p.tokens ? p.groups : p.tokens);
-    const long long items = tiles * ((p.n + kRows - 1) / kRows);
-    const long long most = 2ll * sms;
+template <int BLOCK, int PARTS, int RT, int NT>
+cudaError_t run(Int4Params p, int sms, cudaStream_t s) {
+    const auto kernel = k_int4_linear<BLOCK, PARTS, RT, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Shape<PARTS, RT, NT>::kRing));
+    if (e != cudaSuccess) return e;
+    const long long tiles = p.offsets == nullptr ? (p.tokens + 8 * NT - 1) / (8 * NT)
+                                                 : p.tokens / (8 * NT) + (p.groups < p.tokens ? p.groups : p.tokens);
+    const long long items = tiles * ((p.n + 16 * RT - 1) / (16 * RT)), most = (RT == 1 && PARTS == 1 ? 3ll : 2ll) * sms;
     const unsigned grid = static_cast<unsigned>(items < most ? items : most);
-    if (p.x_bf16) k_int4_few<BLOCK, 1><<<grid, kThreads, 0, s>>>(p);
-    else k_int4_few<BLOCK, 3><<<grid, kThreads, 0, s>>>(p);
+    const unsigned row_tiles = (p.n + 16 * RT - 1) / (16 * RT);
+    p.hop_tiles = grid / row_tiles;
+    p.hop_rows = grid % row_tiles;
+    kernel<<<grid, kThreads, Shape<PARTS, RT, NT>::kRing, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int BLOCK, int PARTS>
+cudaError_t by_shape(const Int4Params& p, int sms, cudaStream_t s) {
+    const long long per = p.tokens / (p.groups < p.tokens ? p.groups : p.tokens);      // tokens of a group, on average
+    if (PARTS == 1 && per > 16) return run<BLOCK, PARTS, 2, PARTS == 1 ? 4 : 2>(p, sms, s);
+    if (per > 8) return run<BLOCK, PARTS, 2, 2>(p, sms, s);
+    const long long rows = static_cast<long long>(p.n) * (p.groups < p.tokens ? p.groups : p.tokens);
+    if (rows > 2 * 32ll * 2 * sms) return run<BLOCK, PARTS, 2, 1>(p, sms, s);
+    return run<BLOCK, PARTS, 1, 1>(p, sms, s);
+}
+
+template <int BLOCK>
+cudaError_t by_type(const Int4Params& p, int sms, cudaStream_t s) {
+    return p.x_bf16 ? by_shape<BLOCK, 1>(p, sms, s) : by_shape<BLOCK, 3>(p, sms, s);
 }
 
 }  // namespace
@@ -264,9 +439,9 @@ cudaError_t launch_int4_quantize(const Int4QuantParams& p, cudaStream_t s) {
 
 cudaError_t launch_int4_linear(const Int4Params& p, int sms, cudaStream_t s) {
     switch (p.block) {
-        case 32: return few<32>(p, sms, s);
-        case 64: return few<64>(p, sms, s);
-        default: return few<128>(p, sms, s);
+        case 32: return by_type<32>(p, sms, s);
+        case 64: return by_type<64>(p, sms, s);
+        default: return by_type<128>(p, sms, s);
     }
 }
 

@@ -10,39 +10,10 @@
 
 namespace muon {
 
-// The reduction is worked off in blocks of 128 columns, each in four steps of 32: in
-// step m lane j of the four that share a row holds the word of eight codes (and the
-// eight elements of x) number chunk(m, j).  A matrix fragment wants 2 + 2 codes from each
-// lane; which columns they are is free, as long as both operands agree.  So a lane's words
-// of one scale lie side by side, and 128-column scales load 16 bytes a lane, 64-column
-// ones 8, 32-column ones 4.
-template <int BLOCK>
-__device__ __forceinline__ constexpr int chunk_of(int m, int j) {
-    return BLOCK == 128 ? 4 * j + m : BLOCK == 64 ? 8 * (m >> 1) + 2 * j + (m & 1) : 4 * m + j;
-}
-
-// Four words of eight codes: one lane's of a row's 128 columns.
-template <int BLOCK>
-__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int kb, int j) {
-    uint4 v;
-    const uint8_t* p = row + kb * 64;
-    if constexpr (BLOCK == 128) {
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(p + 16 * j));
-    } else if constexpr (BLOCK == 64) {
-        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p + 8 * j));
-        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "l"(p + 32 + 8 * j));
-    } else {
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.x) : "l"(p + 4 * j));
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.y) : "l"(p + 16 + 4 * j));
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.z) : "l"(p + 32 + 4 * j));
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v.w) : "l"(p + 48 + 4 * j));
-    }
-    return v;
-}
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int m) { return m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w; }
+// The reduction is worked off in blocks of 128 columns, each in four steps of 32: in step m
+// lane j of the four that share a row holds the word of eight codes (and the eight elements
+// of x) from column 32 m + 8 j on.  A matrix fragment wants 2 + 2 codes from each lane; which
+// columns they are is free, as long as both operands agree.
 
 // Eight codes as bf16, 2^-11 times their number: element i of pair p is column 4 i + p, exactly.
 // 0x3d80 | u is 2^-4 (1 + u / 128), and a code with its sign bit turned over is code + 8.  With
@@ -105,21 +76,24 @@ struct RawOfX {
 };
 
 template <int PARTS>
-__device__ __forceinline__ RawOfX<PARTS> load_x(const void* row, int col, int k, bool vec) {
+__device__ __forceinline__ RawOfX<PARTS> load_x(const char* at) {
     RawOfX<PARTS> r;
-    if (vec && col + 8 <= k) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<long long>(col) * (PARTS == 1 ? 2 : 4));
-        r.v[0] = __ldg(p);
-        if constexpr (PARTS != 1) r.v[1] = __ldg(p + 1);
-        return r;
-    }
+    r.v[0] = __ldg(reinterpret_cast<const uint4*>(at));
+    if constexpr (PARTS != 1) r.v[1] = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+    return r;
+}
+
+// The same of elements that lie on no vector, or of which only `left` are there: zeros past them.
+template <int PARTS>
+__device__ __noinline__ RawOfX<PARTS> load_x_edge(const char* at, int left) {
+    RawOfX<PARTS> r;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         w[i] = 0u;
-        if (col + i < k)
-            w[i] = PARTS == 1 ? static_cast<uint32_t>(static_cast<const uint16_t*>(row)[col + i])
-                              : static_cast<const uint32_t*>(row)[col + i];
+        if (i < left)
+            w[i] = PARTS == 1 ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i])
+                              : reinterpret_cast<const uint32_t*>(at)[i];
     }
     if constexpr (PARTS == 1) {
         r.v[0] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
@@ -150,19 +124,22 @@ __device__ __forceinline__ EightOfX<PARTS> fragments(const RawOfX<PARTS>& r) {
     return f;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// A step of 32 columns: two products of 16.
-__device__ __forceinline__ void mma_step(float (&c)[4], const EightCodes& lo, const EightCodes& hi, const uint4& b) {
-    mma_bf16(c, lo.pair[0], hi.pair[0], lo.pair[1], hi.pair[1], b.x, b.y);
-    mma_bf16(c, lo.pair[2], hi.pair[2], lo.pair[3], hi.pair[3], b.z, b.w);
+// A step of 32 columns: two products of 16; `first`: of a scale's columns, so that the sum begins.
+__device__ __forceinline__ void mma_step(float (&c)[4], bool first, const EightCodes& lo, const EightCodes& hi,
+                                         const uint4& b) {
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (first) mma_bf16(c, zero, lo.pair[0], hi.pair[0], lo.pair[1], hi.pair[1], b.x, b.y);
+    else mma_bf16(c, c, lo.pair[0], hi.pair[0], lo.pair[1], hi.pair[1], b.x, b.y);
+    mma_bf16(c, c, lo.pair[2], hi.pair[2], lo.pair[3], hi.pair[3], b.z, b.w);
 }
 
 }  // namespace muon

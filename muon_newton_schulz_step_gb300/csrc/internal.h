@@ -377,7 +377,7 @@ struct RowsParams {
     long long tokens, cols;
     int top_k, groups, rows;  // rows = tokens * top_k
     int x_bf16, d_bf16, out_bf16;
-    int runs, parts;          // vectors of a row, warps for a row
+    int eights, parts;        // whole eights of a row; warps for a row
 };
 
 cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s);
@@ -423,6 +423,8 @@ struct Int4Params {
     int block;                // columns of a scale
     int x_bf16, out_f32;
     int vec;                  // 16-byte loads of x are legal
+    int pairs;                // scales of rows 2 i and 2 i + 1 load as one
+    unsigned hop_tiles, hop_rows;   // from one item of a block to the next
 };
 
 cudaError_t launch_int4_linear(const Int4Params& p, int sms, cudaStream_t s);

@@ -291,6 +291,7 @@ int muon_int4_linear(const void* x, int x_dtype, long long tokens, long long ld_
     p.x_bf16 = x_dtype == MUON_BF16;
     p.out_f32 = out_dtype == MUON_F32;
     p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * static_cast<long long>(dtype_size(x_dtype)) % 16 == 0;
+    p.pairs = n % 2 == 0 && reinterpret_cast<uintptr_t>(w_scale) % 4 == 0;
     const double some = groups < tokens ? groups : static_cast<double>(tokens);
     const double bytes = some * n * k * (0.5 + 2.0 / block);
     return op_launch(kOpInt4Linear, 2.0 * tokens * n * k, bytes, stream, [&] { return launch_int4_linear(p, sms, stream); });

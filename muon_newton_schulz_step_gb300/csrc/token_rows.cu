@@ -13,18 +13,29 @@
 // Sums are fp32 fused multiply-adds in the order of j, so that a call's result has
 // one value whatever the order of the blocks.
 //
-// Bound by memory.  [8192 tokens x 8 x 6144 bf16; see the figures at each kernel]
+// Rows are worked off in eights of elements that lie on 16 bytes of the row that is
+// written; where the rows that are read lie otherwise (odd widths, views), their eights are
+// put together from the 16-byte vectors around them (SHIFT), and the ends of a row go one
+// by one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "eights.cuh"
 #include "internal.h"
-#include "vectors.cuh"
 
 namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T to_type(float v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return __float2bfloat16_rn(v);
+}
 
 // Lane j's place of a token's entry j; whether it holds a row of an expert is in `held`.
 struct Entries {
@@ -41,241 +52,310 @@ __device__ __forceinline__ Entries entries_of(const RowsParams& p, long long tok
     return e;
 }
 
-// A warp takes U x 32 runs of one token's row.
-template <typename T, int V, int U>
+// A warp takes U x 32 eights of one token's row.
+template <typename T, bool SHIFT, int U>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     const int lane = threadIdx.x & 31;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long token = item / p.parts;
     if (token >= p.tokens) return;
-    const int run0 = static_cast<int>(item - token * p.parts) * (32 * U) + lane;
+    const int part = static_cast<int>(item - token * p.parts), first = part * (32 * U) + lane;
     const Entries e = entries_of(p, token);
     const T* x = static_cast<const T*>(p.x) + token * p.ld_x;
-    Run<T, V> r[U] = {};
-    if (e.held != 0u) {
+    const Extent in = extent_of<T>(p.x, p.tokens, p.ld_x, p.cols);
+    Eight<T> r[U] = {};
+    if (!SHIFT && e.held != 0u) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (run0 + 32 * u < p.runs) r[u] = load_run<T, V>(x + static_cast<long long>(run0 + 32 * u) * V);
+            if (first + 32 * u < p.eights) r[u] = load_eight<T, false>(x + static_cast<long long>(first + 32 * u) * 8, in);
     }
     for (int j = 0; j < p.top_k; ++j) {
         const int place = __shfl_sync(0xffffffffu, e.place, j);
         if (place < 0 || place >= p.rows) continue;
         const bool held = (e.held >> j) & 1u;
         T* out = static_cast<T*>(p.out) + place * p.ld_out;
+        if (!SHIFT) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (first + 32 * u >= p.eights) break;
+                store_eight<T>(out + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{});
+            }
+            continue;
+        }
+        const RowSpan<T> span(out, p.cols);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (run0 + 32 * u >= p.runs) break;
-            store_run<T, V>(out + static_cast<long long>(run0 + 32 * u) * V, held ? r[u] : Run<T, V>{});
+            if (held && first + 32 * u < span.eights)
+                r[u] = load_eight<T, true>(x + span.head + static_cast<long long>(first + 32 * u) * 8, in);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (first + 32 * u >= span.eights) break;
+            store_eight<T>(out + span.head + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{});
+        }
+        if (part == 0) {                               // the ends of the row
+            if (lane < span.head) out[lane] = held ? x[lane] : to_type<T>(0.0f);
+            const long long at = p.cols - span.tail + lane;
+            if (lane < span.tail) out[at] = held ? x[at] : to_type<T>(0.0f);
         }
     }
 }
 
-template <typename T, typename O, int V, int U>
-__global__ void __launch_bounds__(kThreads) k_combine(const RowsParams p) {
-    constexpr int kAhead = 4;                          // entries whose rows are under way together
+// N entries' rows are under way together, U eights of a lane from each.
+template <typename T, bool SHIFT, int N, int U>
+__device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, float weight, unsigned& left, int first,
+                                         int head, int eights, Extent in, float (&acc)[U][8]) {
+    Eight<T> r[N][U];
+    float w[N];
+#pragma unroll
+    for (int a = 0; a < N; ++a) {
+        const int j = __ffs(left) - 1;
+        left &= left - 1u;
+        const long long place = __shfl_sync(0xffffffffu, e.place, j);
+        w[a] = __shfl_sync(0xffffffffu, weight, j);
+        const T* y = static_cast<const T*>(p.x) + place * p.ld_x + head;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + 32 * u < eights) r[a][u] = load_eight<T, SHIFT, !SHIFT>(y + static_cast<long long>(first + 32 * u) * 8, in);
+    }
+#pragma unroll
+    for (int a = 0; a < N; ++a)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(w[a], element<T>(r[a][u], i), acc[u][i]);
+}
+
+template <typename T, typename O, bool SHIFT, int U>
+__global__ void __launch_bounds__(kThreads, SHIFT ? 5 : 3) k_combine(const RowsParams p) {
     const int lane = threadIdx.x & 31;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long token = item / p.parts;
     if (token >= p.tokens) return;
-    const int run0 = static_cast<int>(item - token * p.parts) * (32 * U) + lane;
+    const int part = static_cast<int>(item - token * p.parts), first = part * (32 * U) + lane;
     const Entries e = entries_of(p, token);
     const float weight = p.weights != nullptr && lane < p.top_k ? __ldg(p.weights + token * p.top_k + lane) : 1.0f;
     const T* y = static_cast<const T*>(p.x);
-    float acc[U][V] = {};
-    unsigned left = e.held;
-    while (left != 0u) {
-        Run<T, V> r[kAhead][U];
-        float w[kAhead];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const int j = left != 0u ? __ffs(left) - 1 : -1;
-            left &= left - 1u;
-            const long long place = __shfl_sync(0xffffffffu, e.place, max(j, 0));
-            w[a] = __shfl_sync(0xffffffffu, weight, max(j, 0));
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                r[a][u] = Run<T, V>{};
-                if (j >= 0 && run0 + 32 * u < p.runs)
-                    r[a][u] = load_run<T, V>(y + place * p.ld_x + static_cast<long long>(run0 + 32 * u) * V);
-            }
-            if (j < 0) w[a] = 0.0f;                    // the rows past the last are zeros
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w[a], as_float(r[a][u].v[i]), acc[u][i]);
-    }
+    const Extent in = extent_of<T>(p.x, p.rows, p.ld_x, p.cols);
     O* out = static_cast<O*>(p.out) + token * p.ld_out;
+    const RowSpan<O> span(out, p.cols);
+    const int head = SHIFT ? span.head : 0, eights = SHIFT ? span.eights : p.eights;
+    float acc[U][8] = {};
+    unsigned left = e.held;
+    while (__popc(left) >= 4) add_rows<T, SHIFT, 4, U>(p, e, weight, left, first, head, eights, in, acc);
+    while (left != 0u) add_rows<T, SHIFT, 1, U>(p, e, weight, left, first, head, eights, in, acc);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (run0 + 32 * u >= p.runs) break;
-        Run<O, V> r;
-#pragma unroll
-        for (int i = 0; i < V; ++i) r.v[i] = from_float<O>(acc[u][i]);
-        store_run<O, V>(out + static_cast<long long>(run0 + 32 * u) * V, r);
+        if (first + 32 * u >= eights) break;
+        store_eight<O>(out + head + static_cast<long long>(first + 32 * u) * 8, rounded<O>(acc[u]));
+    }
+    if (SHIFT && part == 0) {                          // the ends of the row
+        const long long at = lane < span.head ? lane : p.cols - span.tail + (lane - span.head);
+        const bool mine = lane < span.head + span.tail;
+        float sum = 0.0f;
+        for (left = e.held; left != 0u; left &= left - 1u) {
+            const int j = __ffs(left) - 1;
+            const long long place = __shfl_sync(0xffffffffu, e.place, j);
+            const float w = __shfl_sync(0xffffffffu, weight, j);
+            if (mine) sum = fmaf(w, to_float(y[place * p.ld_x + at]), sum);
+        }
+        if (mine) out[at] = to_type<O>(sum);
     }
 }
 
-// W warps take one token: each run of d is read once for up to kTogether entries,
-// whose dot products stay in registers to the end of the row.
-template <typename D, typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_combine_backward(const RowsParams p) {
-    constexpr int kTogether = 8;
-    __shared__ float part[kWarps][kTogether];
+// A block takes one token, N of its entries at a time: d is read once for them, and their
+// dot products stay in registers to the end of the row.
+template <typename D, typename T, bool SHIFT, int N, int U>
+__device__ __forceinline__ void backward_of(const RowsParams& p, long long token, const Entries& e, float weight,
+                                            unsigned& left, float (*part)[kRowsMaxTopK]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int in = warp % W;                           // which of the token's warps
-    const long long token = static_cast<long long>(blockIdx.x) * (kWarps / W) + warp / W;
-    const bool here = token < p.tokens;
-    const long long t = here ? token : p.tokens - 1;
-    const Entries e = entries_of(p, t);
-    const float weight = p.weights != nullptr && lane < p.top_k ? __ldg(p.weights + t * p.top_k + lane) : 1.0f;
-    const D* d = static_cast<const D*>(p.d) + t * p.ld_d;
-    const T* y = static_cast<const T*>(p.x);
-    for (int j0 = 0; j0 < p.top_k; j0 += kTogether) {
-        long long at[kTogether];
-        float w[kTogether], dot[kTogether] = {};
-        unsigned held = 0u, there = 0u;
+    const D* d = static_cast<const D*>(p.d) + token * p.ld_d;
+    const Extent in_d = extent_of<D>(p.d, p.tokens, p.ld_d, p.cols), in_y = extent_of<T>(p.x, p.rows, p.ld_x, p.cols);
+    const bool dots = p.dw != nullptr;
+    const T* y[N];
+    T* dy[N];
+    float w[N], dot[N];
+    int js[N];
 #pragma unroll
-        for (int a = 0; a < kTogether; ++a) {
-            const int j = j0 + a;
-            const int place = __shfl_sync(0xffffffffu, e.place, j & 31);
-            w[a] = __shfl_sync(0xffffffffu, weight, j & 31);
-            at[a] = place;
-            if (here && j < p.top_k && place >= 0 && place < p.rows) there |= 1u << a;
-            if (here && j < p.top_k && ((e.held >> j) & 1u)) held |= 1u << a;
-        }
-        for (int run = in * 32 + lane; run < p.runs; run += 32 * W) {
-            const long long col = static_cast<long long>(run) * V;
-            Run<D, V> dr = {};
-            if (held != 0u) dr = load_run<D, V>(d + col);
-            Run<T, V> r[kTogether];
-            if (p.dw != nullptr) {
+    for (int a = 0; a < N; ++a) {
+        js[a] = __ffs(left) - 1;
+        left &= left - 1u;
+        const long long place = __shfl_sync(0xffffffffu, e.place, js[a]);
+        w[a] = __shfl_sync(0xffffffffu, weight, js[a]);
+        y[a] = static_cast<const T*>(p.x) + place * p.ld_x;
+        dy[a] = static_cast<T*>(p.out) + place * p.ld_out;
+        dot[a] = 0.0f;
+    }
+    static_assert(!SHIFT || N == 1, "rows that lie differently go one at a time");
+    // by the eights of y, so that the order of a sum does not depend on where dy lies; dy lies alike as a rule
+    const RowSpan<T> span(dots ? y[0] : dy[0], p.cols);
+    const bool alike = !SHIFT || reinterpret_cast<uintptr_t>(dy[0] + span.head) % 16 == 0;
+    const int head = SHIFT ? span.head : 0, eights = SHIFT ? span.eights : p.eights;
+    for (int at = threadIdx.x; at < eights; at += U * blockDim.x) {
+        Eight<D> g[U];
+        Eight<T> r[U][N];
 #pragma unroll
-                for (int a = 0; a < kTogether; ++a)
-                    if ((held >> a) & 1u) r[a] = load_run<T, V>(y + at[a] * p.ld_x + col);
+        for (int u = 0; u < U; ++u) {
+            const int i = at + u * static_cast<int>(blockDim.x);
+            if (i >= eights) break;
+            const long long col = head + static_cast<long long>(i) * 8;
+            g[u] = load_eight<D, SHIFT>(d + col, in_d);
+            if (dots) {
+#pragma unroll
+                for (int a = 0; a < N; ++a) r[u][a] = load_eight<T, SHIFT>(y[a] + col, in_y);
             }
+        }
 #pragma unroll
-            for (int a = 0; a < kTogether; ++a) {
-                if (p.out != nullptr && ((there >> a) & 1u)) {
-                    Run<T, V> o = {};
-                    if ((held >> a) & 1u) {
+        for (int u = 0; u < U; ++u) {
+            const int i = at + u * static_cast<int>(blockDim.x);
+            if (i >= eights) break;
+            const long long col = head + static_cast<long long>(i) * 8;
+            float v[8];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) o.v[i] = from_float<T>(w[a] * as_float(dr.v[i]));
+            for (int k = 0; k < 8; ++k) v[k] = element<D>(g[u], k);
+#pragma unroll
+            for (int a = 0; a < N; ++a) {
+                if (dots) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dot[a] = fmaf(v[k], element<T>(r[u][a], k), dot[a]);
+                }
+                if (p.out != nullptr) {
+                    float o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = w[a] * v[k];
+                    if (alike) {
+                        store_eight<T>(dy[a] + col, rounded<T>(o));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dy[a][col + k] = to_type<T>(o[k]);
                     }
-                    store_run<T, V>(static_cast<T*>(p.out) + at[a] * p.ld_out + col, o);
-                }
-                if (p.dw != nullptr && ((held >> a) & 1u)) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) dot[a] = fmaf(as_float(dr.v[i]), as_float(r[a].v[i]), dot[a]);
                 }
             }
         }
-        if (p.dw == nullptr) continue;
+    }
+    if (SHIFT && threadIdx.x < span.head + span.tail) {    // the ends of the row
+        const int i = threadIdx.x;
+        const long long col = i < span.head ? i : p.cols - span.tail + (i - span.head);
+        const float v = to_float(d[col]);
+        if (dots) dot[0] = fmaf(v, to_float(y[0][col]), dot[0]);
+        if (p.out != nullptr) dy[0][col] = to_type<T>(w[0] * v);
+    }
+    if (!dots) return;
 #pragma unroll
-        for (int a = 0; a < kTogether; ++a) {
+    for (int a = 0; a < N; ++a) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], o);
+        for (int o = 16; o > 0; o >>= 1) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], o);
+        if (lane == 0) part[warp][js[a]] = dot[a];
+    }
+}
+
+template <typename D, typename T, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsParams p) {
+    constexpr int kU = SHIFT || sizeof(D) + sizeof(T) != 4 ? 1 : 2;   // eights of a lane under way
+    __shared__ float part[kWarps][kRowsMaxTopK];
+    const int lane = threadIdx.x & 31;
+    const long long token = blockIdx.x;
+    const Entries e = entries_of(p, token);
+    const float weight = p.weights != nullptr && lane < p.top_k ? __ldg(p.weights + token * p.top_k + lane) : 1.0f;
+    unsigned left = e.held;
+    if (!SHIFT) {
+        while (__popc(left) >= 4) backward_of<D, T, SHIFT, SHIFT ? 1 : 4, kU>(p, token, e, weight, left, part);
+    }
+    while (left != 0u) backward_of<D, T, SHIFT, 1, kU>(p, token, e, weight, left, part);
+    if (p.out != nullptr) {                            // rows of no expert
+        const unsigned rest = __ballot_sync(0xffffffffu, e.place >= 0 && e.place < p.rows) & ~e.held;
+        for (left = rest; left != 0u; left &= left - 1u) {
+            const long long place = __shfl_sync(0xffffffffu, e.place, __ffs(left) - 1);
+            T* dy = static_cast<T*>(p.out) + place * p.ld_out;
+            const RowSpan<T> span(dy, p.cols);
+            for (int i = threadIdx.x; i < span.eights; i += blockDim.x)
+                store_eight<T>(dy + span.head + static_cast<long long>(i) * 8, Eight<T>{});
+            const int i = threadIdx.x;
+            if (i < span.head + span.tail) dy[i < span.head ? i : p.cols - span.tail + (i - span.head)] = to_type<T>(0.0f);
         }
-        if (W > 1) {
-            __syncthreads();                           // the sums of the entries before have been read
-            if (lane == 0) {
-#pragma unroll
-                for (int a = 0; a < kTogether; ++a) part[warp][a] = dot[a];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int a = 0; a < kTogether; ++a) {
-                dot[a] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < W; ++i) dot[a] += part[warp / W * W + i][a];
-            }
-        }
-        if (here && in == 0) {
-#pragma unroll
-            for (int a = 0; a < kTogether; ++a)
-                if (lane == a && j0 + a < p.top_k) p.dw[t * p.top_k + j0 + a] = (held >> a) & 1u ? dot[a] : 0.0f;
-        }
+    }
+    if (p.dw == nullptr) return;
+    __syncthreads();
+    if (threadIdx.x < p.top_k) {
+        float sum = 0.0f;
+        for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) sum += part[i][threadIdx.x];
+        p.dw[token * p.top_k + threadIdx.x] = (e.held >> lane) & 1u ? sum : 0.0f;
     }
 }
 
 template <int U>
 unsigned warp_items(RowsParams& p) {
-    p.parts = (p.runs + 32 * U - 1) / (32 * U);
+    p.eights = static_cast<int>(p.cols / 8);
+    p.parts = (p.eights + 32 * U - 1) / (32 * U);
+    if (p.parts == 0) p.parts = 1;
     return static_cast<unsigned>((p.tokens * p.parts + kWarps - 1) / kWarps);
 }
 
-template <typename T, int V>
+template <typename T, bool SHIFT>
 cudaError_t dispatch(RowsParams p, cudaStream_t s) {
-    p.runs = static_cast<int>(p.cols / V);
-    const unsigned grid = warp_items<4>(p);
-    k_dispatch<T, V, 4><<<grid, kThreads, 0, s>>>(p);
+    constexpr int kU = sizeof(T) == 2 ? 4 : 2;
+    const unsigned grid = warp_items<kU>(p);
+    k_dispatch<T, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, typename O, int V>
+template <typename T, typename O, bool SHIFT>
 cudaError_t combine(RowsParams p, cudaStream_t s) {
-    p.runs = static_cast<int>(p.cols / V);
-    const unsigned grid = warp_items<2>(p);
-    k_combine<T, O, V, 2><<<grid, kThreads, 0, s>>>(p);
+    constexpr int kU = sizeof(T) == 2 && !SHIFT ? 2 : 1;
+    const unsigned grid = warp_items<kU>(p);
+    k_combine<T, O, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename D, typename T, int V>
+template <typename D, typename T, bool SHIFT>
 cudaError_t combine_backward(RowsParams p, cudaStream_t s) {
-    p.runs = static_cast<int>(p.cols / V);
-    const long long t = p.tokens;
-    // as many warps as the row has runs of 32 for, so that none idles
-    if (p.runs > 128) k_combine_backward<D, T, V, 8><<<static_cast<unsigned>(t), kThreads, 0, s>>>(p);
-    else if (p.runs > 32) k_combine_backward<D, T, V, 4><<<static_cast<unsigned>((t + 1) / 2), kThreads, 0, s>>>(p);
-    else k_combine_backward<D, T, V, 1><<<static_cast<unsigned>((t + 7) / 8), kThreads, 0, s>>>(p);
+    p.eights = static_cast<int>(p.cols / 8);
+    // as many warps as the row has eights for
+    const int warps = p.eights >= 256 ? 8 : p.eights >= 128 ? 4 : p.eights >= 64 ? 2 : 1;
+    k_combine_backward<D, T, SHIFT><<<static_cast<unsigned>(p.tokens), 32 * warps, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+// Rows of whole eights that all lie on 16 bytes.
+bool on_16(const void* p, long long ld, bool bf16) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0;
 }
 
 template <typename F>
-cudaError_t by_width(int v, F&& f) {
-    switch (v) {
-        case 8: return f(std::integral_constant<int, 8>());
-        case 4: return f(std::integral_constant<int, 4>());
-        case 2: return f(std::integral_constant<int, 2>());
-        default: return f(std::integral_constant<int, 1>());
-    }
+cudaError_t by_type(bool bf16, F&& f) {
+    return bf16 ? f(__nv_bfloat16()) : f(float());
 }
 
 }  // namespace
 
 cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s) {
-    const int size = p.x_bf16 ? 2 : 4;
-    RunWidth w(p.cols);
-    w.array(p.x, p.ld_x, size);
-    w.array(p.out, p.ld_out, size);
-    return by_width(w.v, [&](auto v) {
-        return p.x_bf16 ? dispatch<__nv_bfloat16, v()>(p, s) : dispatch<float, v()>(p, s);
+    const bool whole = p.cols % 8 == 0 && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.x_bf16);
+    return by_type(p.x_bf16, [&](auto t) {
+        using T = decltype(t);
+        return whole ? dispatch<T, false>(p, s) : dispatch<T, true>(p, s);
     });
 }
 
 cudaError_t launch_combine(const RowsParams& p, cudaStream_t s) {
-    RunWidth w(p.cols);
-    w.array(p.x, p.ld_x, p.x_bf16 ? 2 : 4);
-    w.array(p.out, p.ld_out, p.out_bf16 ? 2 : 4);
-    return by_width(w.v, [&](auto v) {
-        if (p.x_bf16)
-            return p.out_bf16 ? combine<__nv_bfloat16, __nv_bfloat16, v()>(p, s) : combine<__nv_bfloat16, float, v()>(p, s);
-        return p.out_bf16 ? combine<float, __nv_bfloat16, v()>(p, s) : combine<float, float, v()>(p, s);
+    const bool whole = p.cols % 8 == 0 && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.out_bf16);
+    return by_type(p.x_bf16, [&](auto t) {
+        return by_type(p.out_bf16, [&](auto o) {
+            using T = decltype(t);
+            using O = decltype(o);
+            return whole ? combine<T, O, false>(p, s) : combine<T, O, true>(p, s);
+        });
     });
 }
 
 cudaError_t launch_combine_backward(const RowsParams& p, cudaStream_t s) {
-    RunWidth w(p.cols);
-    w.array(p.d, p.ld_d, p.d_bf16 ? 2 : 4);
-    if (p.dw != nullptr) w.array(p.x, p.ld_x, p.x_bf16 ? 2 : 4);
-    if (p.out != nullptr) w.array(p.out, p.ld_out, p.x_bf16 ? 2 : 4);
-    return by_width(w.v, [&](auto v) {
-        if (p.d_bf16)
-            return p.x_bf16 ? combine_backward<__nv_bfloat16, __nv_bfloat16, v()>(p, s)
-                            : combine_backward<__nv_bfloat16, float, v()>(p, s);
-        return p.x_bf16 ? combine_backward<float, __nv_bfloat16, v()>(p, s) : combine_backward<float, float, v()>(p, s);
+    const bool whole = p.cols % 8 == 0 && on_16(p.d, p.ld_d, p.d_bf16) && (p.dw == nullptr || on_16(p.x, p.ld_x, p.x_bf16)) &&
+                       (p.out == nullptr || on_16(p.out, p.ld_out, p.x_bf16));
+    return by_type(p.d_bf16, [&](auto d) {
+        return by_type(p.x_bf16, [&](auto t) {
+            using D = decltype(d);
+            using T = decltype(t);
+            return whole ? combine_backward<D, T, false>(p, s) : combine_backward<D, T, true>(p, s);
+        });
     });
 }
 
