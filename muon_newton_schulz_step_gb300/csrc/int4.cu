@@ -130,21 +130,21 @@ __device__ __forceinline__ void zero_rest(const Int4Params& p, const GroupTable&
 
 // -------------------------------------------------------------- products --
 // An item is 16 RT rows of a weight and up to 8 NT tokens of one group; a block takes
-// items, all its warps together: each the reduction's blocks of 128 in turn (a unit), and
-// at an item's end they add their sums up in shared memory, in a fixed order.  So a single
-// token's product fills the SMs (one token x 6144 x 6144 is 384 items), and any number of
-// tokens or groups runs the same way.
+// consecutive items, all its warps together: each the reduction's blocks of 128 in turn (a
+// unit), and at an item's end they add their sums up in shared memory, in a fixed order.  So
+// a single token's product fills the SMs (one token x 6144 x 6144 is 384 items), and any
+// number of tokens or groups runs the same way.
 //
 // Codes and scales of kStages - 1 units are under way for each warp by asynchronous copies
 // into a ring of its own, over the ends of items, with no wait between warps.  A row's 64
 // bytes lie there in 16-byte pieces that ldmatrix reads without bank conflicts; it hands lane
 // (r, j) the word of 8 codes that its fragment wants.  Fragment rows r and r + 8 are the
 // weight's rows 2 r and 2 r + 1, whose scales are neighbours.  x comes from L2 through the
-// first level, a step ahead.
+// first level, a unit ahead.
 template <int RT>
 struct Unit {
     uint4 codes[RT * 64];                                  // 16 RT rows of 64 bytes, even rows first
-    uint32_t scale[4][RT * 8];                             // bf16 pairs
+    uint32_t scale[RT * 8][4];                             // bf16 pairs of a pair of rows, the unit's scales
 };
 
 // Shared memory of two blocks per SM (three where RT is 1); sums of one or two items.
@@ -152,7 +152,7 @@ template <int PARTS, int RT, int NT>
 struct Shape {
     static constexpr int kStages = RT == 1 ? 6 : NT == 4 ? 3 : 4;
     static constexpr int kTurns = NT == 1 ? 2 : 1;
-    static constexpr int kAheadX = NT == 4 ? 1 : PARTS * NT > 4 ? 2 : 4;       // steps whose x is in registers
+    static constexpr bool kAheadX = PARTS * NT <= 3;       // else registers do not last
     static constexpr size_t kRing = sizeof(Unit<RT>) * kStages * kWarps;
 };
 
@@ -165,12 +165,13 @@ __device__ __forceinline__ int piece(int slot, int m) { return slot * 4 + (m ^ (
 
 template <int BLOCK, int PARTS, int RT, int NT>
 __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int4_linear(const Int4Params p) {
+    using S = Shape<PARTS, RT, NT>;
     constexpr int kScales = 128 / BLOCK, kSteps = 4 / kScales;
     constexpr int kRows = 16 * RT, kTokens = 8 * NT, kSize = PARTS == 1 ? 2 : 4;
-    constexpr int kStages = Shape<PARTS, RT, NT>::kStages, kTurns = Shape<PARTS, RT, NT>::kTurns, kAheadX = Shape<PARTS, RT, NT>::kAheadX;
+    constexpr int kStages = S::kStages, kUnit = static_cast<int>(sizeof(Unit<RT>));
     extern __shared__ uint4 dynamic[];
     __shared__ GroupTable table;
-    __shared__ float part[kTurns][kWarps][kTokens][kRows + 1];
+    __shared__ float part[S::kTurns][kWarps][kTokens][kRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, j = lane & 3;
     Unit<RT>* const ring = reinterpret_cast<Unit<RT>*>(dynamic) + warp * kStages;
@@ -181,123 +182,120 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
         make_table<kTokens>(p, table);
         tiles = table.tile0[p.groups];
     }
-    // this block's first item, and the way from one to the next
-    const unsigned first_tile = blockIdx.x / row_tiles, first_row = blockIdx.x - first_tile * row_tiles;
-    auto next_of = [&](unsigned& tile, unsigned& row) {
-        tile += p.hop_tiles;
-        row += p.hop_rows;
-        if (row >= row_tiles) {
-            row -= row_tiles;
-            ++tile;
-        }
-    };
+    // this block's items: an equal share, in a row
+    const unsigned items = tiles * row_tiles, share = items / gridDim.x, over = items - share * gridDim.x;
+    const unsigned begin = blockIdx.x * share + min(blockIdx.x, over);
+    const int mine = static_cast<int>(share + (blockIdx.x < over ? 1u : 0u));
+    const unsigned first_tile = begin / row_tiles, first_row = begin - first_tile * row_tiles;
 
-    // where the copies are: column tile, row tile, block of the reduction; this lane's sources and places
-    unsigned ct = first_tile, cr = first_row;
-    int ckb = warp;
-    const uint8_t* codes[2 * RT];
+    // ---- the copies: items left, block of the reduction, this lane's sources and places
+    int c_left = warp < p.kblocks ? mine : 0, ckb = warp;
+    unsigned c_tile = first_tile, c_row = first_row;
+    const uint8_t* codes[2 * RT] = {};
     const __nv_bfloat16* scales = nullptr;
     bool scaled = false;                                   // this lane copies scales of the item
+    int c_group = 0;
     const long long scale_hop = static_cast<long long>(kWarps) * kScales * p.n;
     // rows 8 i + lane / 4, even ones before odd ones; 16 rows on is 16 slots on
     const int row0 = lane >> 2, slot0 = (row0 & 1) * 8 + (row0 >> 1);
     const int put[2] = {piece(slot0, lane & 3) * 16, piece(slot0 + 4, lane & 3) * 16};
+    const int q0 = lane / (8 * RT), at0 = lane % (8 * RT), put_scale = RT * 1024 + (at0 * 4 + q0) * 4;
+    if (p.offsets != nullptr && mine > 0) c_group = group_of(table, p.groups, first_tile);
     auto aim = [&] {
-        if (ct >= tiles) return;
-        const int g = p.offsets != nullptr ? group_of(table, p.groups, ct) : 0, n0 = static_cast<int>(cr) * kRows;
-        const uint8_t* w = p.w + g * p.w_batch + ckb * 64 + (lane & 3) * 16;
+        const int n0 = static_cast<int>(c_row) * kRows;
+        const uint8_t* w = p.w + c_group * p.w_batch + warp * 64 + (lane & 3) * 16;
         // rows past the last are the last one again; their results are not stored
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) codes[i] = w + min(n0 + i * 8 + row0, p.n - 1) * p.ldw;
-        const int q = lane / (8 * RT), at = n0 + 2 * (lane % (8 * RT));
-        scaled = p.pairs && q < kScales && at < p.n;
-        scales = p.scale + g * p.scale_batch + static_cast<long long>(ckb * kScales + q) * p.n + at;
+        const int at = n0 + 2 * at0;
+        scaled = p.pairs && q0 < kScales && at < p.n;
+        scales = p.scale + c_group * p.scale_batch + static_cast<long long>(warp * kScales + q0) * p.n + at;
     };
-    auto copy = [&](int stage) {
-        if (ct < tiles && ckb < p.kblocks) {
-            const uint32_t to = ring_at + stage * static_cast<int>(sizeof(Unit<RT>));
+    auto copy = [&](uint32_t to) {
+        if (c_left > 0) {
 #pragma unroll
             for (int i = 0; i < 2 * RT; ++i) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + put[i & 1] + (i >> 1) * 1024), "l"(codes[i]));
                 codes[i] += kWarps * 64;
             }
-            if (scaled) {                                  // pairs of rows' scales: a lane's, and those 32 lanes on
+            if (scaled) {                                  // a lane's pair, and those that 32 lanes do not reach
 #pragma unroll
                 for (int i = 0; i < kScales * RT; i += 4)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + RT * 1024 + (i * 8 + lane) * 4),
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + put_scale + (i / RT) * 4),
                                  "l"(scales + static_cast<long long>(i / RT) * p.n));
                 scales += scale_hop;
             }
             ckb += kWarps;
             if (ckb >= p.kblocks) {
                 ckb = warp;
-                next_of(ct, cr);
-                aim();
+                if (--c_left > 0) {
+                    if (++c_row == row_tiles) {
+                        c_row = 0;
+                        ++c_tile;
+                        if (p.offsets != nullptr) c_group = group_of(table, p.groups, c_tile);
+                    }
+                    aim();
+                }
             }
         }
         asm volatile("cp.async.commit_group;");
     };
-    aim();
+    if (c_left > 0) aim();
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) copy(i);
+    for (int i = 0; i < kStages - 1; ++i) copy(ring_at + i * kUnit);
     int stage = 0, turn = 0;
     // ldmatrix: lane 8 m + i names piece m of row i; eight rows on, the pieces lie alike
-    const int get = piece(lane & 7, lane >> 3) * 16;
+    const uint32_t get = ring_at + piece(lane & 7, lane >> 3) * 16;
 
-    // an item: its group, rows, tokens, and where this lane's tokens lie.  As B fragment a lane
+    // ---- the items: group, tokens, and where this lane's tokens lie.  As B fragment a lane
     // holds tokens r, r + 8, ..; as accumulator tokens 2 j and 2 j + 1 of each eight
-    struct Item {
-        int g, n0, t0, tokens;
-        const char* x[NT];
-    };
     unsigned tile = first_tile, row_tile = first_row;
-    auto here = [&](Item& it) {
-        if (tile >= tiles) return false;
-        it.n0 = static_cast<int>(row_tile) * kRows;
-        it.g = 0;
-        it.t0 = static_cast<int>(tile) * kTokens;
+    int g = 0, t0 = 0, tokens = 0;
+    const char* x[NT];
+    auto look = [&] {                                      // at a new column tile
+        t0 = static_cast<int>(tile) * kTokens;
         int end = p.tokens;
         if (p.offsets != nullptr) {
-            it.g = group_of(table, p.groups, tile);
-            it.t0 = table.lo[it.g] + (static_cast<int>(tile) - table.tile0[it.g]) * kTokens;
-            end = table.lo[it.g] + table.cnt[it.g];
+            g = group_of(table, p.groups, tile);
+            t0 = table.lo[g] + (static_cast<int>(tile) - table.tile0[g]) * kTokens;
+            end = table.lo[g] + table.cnt[g];
         }
-        it.tokens = min(kTokens, end - it.t0);
+        tokens = min(kTokens, end - t0);
         // tokens past the last are the last one again; their results are not stored
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            it.x[t] = static_cast<const char*>(p.x) + ((it.t0 + min(8 * t + r, it.tokens - 1)) * p.ld_x + 8 * j) * kSize;
-        next_of(tile, row_tile);
-        return true;
+            x[t] = static_cast<const char*>(p.x) + ((t0 + min(8 * t + r, tokens - 1)) * p.ld_x + 8 * j) * kSize;
     };
-    auto load = [&](RawOfX<PARTS>(&raw)[NT], const Item& it, int kb, int m) {
-        const int col = kb * 128 + 32 * m;                 // of lane 0
-        if (p.vec && kb * 128 + 128 <= p.k) {
+    const int whole = p.vec ? p.k / 128 : 0;               // units whose x loads as vectors
+    constexpr int kHeld = S::kAheadX ? 4 : 1;              // steps whose x is in registers
+    RawOfX<PARTS> raw[kHeld][NT];
+    auto load = [&](int kb, int m0) {                      // kHeld steps of unit kb from m0 on
+        if (kb < whole) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) raw[t] = load_x<PARTS>(it.x[t] + kb * (128 * kSize) + 32 * kSize * m);
-        } else {
+            for (int t = 0; t < NT; ++t) {
+                const char* at = x[t] + kb * (128 * kSize);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) raw[t] = load_x_edge<PARTS>(it.x[t] + static_cast<long long>(col) * kSize, p.k - col - 8 * j);
+                for (int m = 0; m < kHeld; ++m) raw[m][t] = load_x<PARTS>(at + 32 * kSize * (m0 + m));
+            }
+            return;
+        }
+#pragma unroll
+        for (int m = 0; m < kHeld; ++m) {
+            const int col = kb * 128 + 32 * (m0 + m);      // of lane 0
+#pragma unroll
+            for (int t = 0; t < NT; ++t) raw[m][t] = load_x_edge<PARTS>(x[t] + static_cast<long long>(col) * kSize, p.k - col - 8 * j);
         }
     };
-
-    // x of a whole unit ahead: step m's is loaded anew as soon as it is used
-    RawOfX<PARTS> raw[kAheadX][NT];
-    Item it;
-    bool more = here(it);
-    if (kAheadX > 1 && more && warp < p.kblocks) {
-#pragma unroll
-        for (int m = 0; m < kAheadX; ++m) load(raw[m], it, warp, m);
-    }
-    while (more) {
-        const int g = it.g, n0 = it.n0, t0 = it.t0, tokens = it.tokens;
-        bool looked = false;
+    if (mine > 0) look();
+    if (S::kAheadX && mine > 0 && warp < p.kblocks) load(warp, 0);
+    for (int left = mine; left > 0; --left) {
+        const int n0 = static_cast<int>(row_tile) * kRows, out_row = t0, out_rows = tokens, group = g;
+        const bool on = row_tile + 1 == row_tiles;         // the next item is of another column tile
         float acc[RT][NT][4] = {};
         for (int kb = warp; kb < p.kblocks; kb += kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
-            const Unit<RT>& u = ring[stage];
-            const uint32_t from = ring_at + stage * static_cast<int>(sizeof(Unit<RT>)) + get;
+            const uint32_t from = get + stage * kUnit;
             uint32_t w[RT][2][4];
 #pragma unroll
             for (int a = 0; a < RT; ++a)
@@ -306,29 +304,36 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
                     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[a][h][0]), "=r"(w[a][h][1]), "=r"(w[a][h][2]), "=r"(w[a][h][3])
                                  : "r"(from + a * 1024 + h * 512));
-            uint32_t by[RT][kScales];
+            uint32_t by[RT][4];
 #pragma unroll
-            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                for (int q = 0; q < kScales; ++q) {
-                    if (p.pairs) {
-                        by[a][q] = u.scale[q][a * 8 + r];
+            for (int a = 0; a < RT; ++a) {
+                if (p.pairs) {
+                    const uint32_t* s = ring[stage].scale[a * 8 + r];
+                    if (kScales == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(s);
+                        by[a][0] = v.x, by[a][1] = v.y, by[a][2] = v.z, by[a][3] = v.w;
                     } else {
-                        const uint16_t* s = reinterpret_cast<const uint16_t*>(p.scale) + g * p.scale_batch +
+#pragma unroll
+                        for (int q = 0; q < kScales; ++q) by[a][q] = s[q];
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kScales; ++q) {
+                        const uint16_t* s = reinterpret_cast<const uint16_t*>(p.scale) + group * p.scale_batch +
                                             static_cast<long long>(kb * kScales + q) * p.n;
                         const int row = n0 + a * 16 + 2 * r;
                         by[a][q] = s[min(row, p.n - 1)] | (static_cast<uint32_t>(s[min(row + 1, p.n - 1)]) << 16);
                     }
                 }
+            }
             // into the place of the unit before this one, which every lane has read
-            copy(stage == 0 ? kStages - 1 : stage - 1);
+            copy(ring_at + (stage == 0 ? kStages - 1 : stage - 1) * kUnit);
             stage = stage == kStages - 1 ? 0 : stage + 1;
 
-            int next_kb = kb + kWarps;
             float c[RT][NT][4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                if (kAheadX == 1) load(raw[0], it, kb, m);
+                if (!S::kAheadX) load(kb, m);
                 EightCodes lo[RT], hi[RT];
 #pragma unroll
                 for (int a = 0; a < RT; ++a) {
@@ -337,22 +342,12 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const EightOfX<PARTS> b = fragments<PARTS>(raw[m % kAheadX][t]);
+                    const EightOfX<PARTS> b = fragments<PARTS>(raw[m % kHeld][t]);
 #pragma unroll
                     for (int a = 0; a < RT; ++a)
 #pragma unroll
                         for (int q = PARTS - 1; q >= 0; --q)
                             mma_step(c[a][t], q == PARTS - 1 && m % kSteps == 0, lo[a], hi[a], b.v[q]);
-                }
-                if (kAheadX > 1) {
-                    const int at = m + kAheadX;
-                    if (at == 4 && next_kb >= p.kblocks) { // on to the next item's first unit
-                        more = here(it);
-                        looked = true;
-                        next_kb = more ? warp : -1;
-                    }
-                    if (at < 4) load(raw[m % kAheadX], it, kb, at);
-                    else if (next_kb >= 0) load(raw[m % kAheadX], it, next_kb, at - 4);
                 }
                 if ((m + 1) % kSteps == 0) {
 #pragma unroll
@@ -369,9 +364,17 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
                     }
                 }
             }
+            if (S::kAheadX) {                              // x of the next unit (at the very end, one more of this item)
+                const bool done = kb + kWarps >= p.kblocks;
+                if (done && on && left > 1) {
+                    ++tile;
+                    look();
+                }
+                load(done ? warp : kb + kWarps, 0);
+            }
         }
         // with room for two items' sums, those of the item before the last have been read by now
-        if (kTurns == 1) __syncthreads();
+        if (S::kTurns == 1) __syncthreads();
 #pragma unroll
         for (int a = 0; a < RT; ++a)
 #pragma unroll
@@ -382,22 +385,26 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
 #pragma unroll
         for (int i = 0; i < kTokens * kRows; i += kThreads) {
             const int t = (i + static_cast<int>(threadIdx.x)) / kRows, n = (i + static_cast<int>(threadIdx.x)) % kRows;
-            if (t < tokens && n0 + n < p.n) {
+            if (t < out_rows && n0 + n < p.n) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kWarps; ++k) sum += part[turn][k][t][n];
-                store_out(p, (t0 + t) * p.ld_out + n0 + n, sum * kCodeUnit);
+                store_out(p, (out_row + t) * p.ld_out + n0 + n, sum * kCodeUnit);
             }
         }
-        turn = kTurns - 1 - turn;
-        if (!looked) more = here(it);                      // (warps past the last block have no units)
+        turn = S::kTurns - 1 - turn;
+        if (on && left > 1 && !(S::kAheadX && warp < p.kblocks)) {     // those that have not looked ahead
+            ++tile;
+            look();
+        }
+        row_tile = on ? 0 : row_tile + 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (p.offsets != nullptr) zero_rest(p, table);
 }
 
 template <int BLOCK, int PARTS, int RT, int NT>
-cudaError_t run(Int4Params p, int sms, cudaStream_t s) {
+cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
     const auto kernel = k_int4_linear<BLOCK, PARTS, RT, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Shape<PARTS, RT, NT>::kRing));
@@ -405,11 +412,7 @@ cudaError_t run(Int4Params p, int sms, cudaStream_t s) {
     const long long tiles = p.offsets == nullptr ? (p.tokens + 8 * NT - 1) / (8 * NT)
                                                  : p.tokens / (8 * NT) + (p.groups < p.tokens ? p.groups : p.tokens);
     const long long items = tiles * ((p.n + 16 * RT - 1) / (16 * RT)), most = (RT == 1 && PARTS == 1 ? 3ll : 2ll) * sms;
-    const unsigned grid = static_cast<unsigned>(items < most ? items : most);
-    const unsigned row_tiles = (p.n + 16 * RT - 1) / (16 * RT);
-    p.hop_tiles = grid / row_tiles;
-    p.hop_rows = grid % row_tiles;
-    kernel<<<grid, kThreads, Shape<PARTS, RT, NT>::kRing, s>>>(p);
+    kernel<<<static_cast<unsigned>(items < most ? items : most), kThreads, Shape<PARTS, RT, NT>::kRing, s>>>(p);
     return cudaGetLastError();
 }
 

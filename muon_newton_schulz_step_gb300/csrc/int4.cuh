@@ -29,7 +29,8 @@ __device__ __forceinline__ EightCodes decode(uint32_t w) {
     EightCodes d;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t u = ((w >> (4 * p)) & 0x000f000fu) ^ 0x3d883d88u;
+        uint32_t u;                                        // (a & b) ^ c
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(w >> (4 * p)), "r"(0x000f000fu), "r"(0x3d883d88u));
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d.pair[p]) : "r"(u), "r"(0x3d883d88u));
     }
     return d;

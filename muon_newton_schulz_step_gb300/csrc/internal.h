@@ -424,7 +424,6 @@ struct Int4Params {
     int x_bf16, out_f32;
     int vec;                  // 16-byte loads of x are legal
     int pairs;                // scales of rows 2 i and 2 i + 1 load as one
-    unsigned hop_tiles, hop_rows;   // from one item of a block to the next
 };
 
 cudaError_t launch_int4_linear(const Int4Params& p, int sms, cudaStream_t s);
