@@ -1,11 +1,14 @@
 """One training step of a small mixture-of-experts layer, end to end.
 
-    python examples/moe_layer_step.py [--steps 20]
+    python examples/moe_layer_step.py [--steps 20] [--fused] [--serve]
 
 Routes tokens to experts (group-limited, with a balance bias), runs the experts'
 gate, up and down projections on 8-bit operands over the tokens sorted by
 expert, takes the gradients back through both, clips them by their global norm
-and steps: Muon for the experts' matrices, AdamW for the router.
+and steps: Muon for the experts' matrices, AdamW for the router.  With --fused the
+sort, the rows' way to the experts and back and the activation run in the library's
+kernels too, each with its gradient; --serve then runs single tokens through the
+trained layer on weights of 4 bits.
 """
 import argparse
 import os
@@ -20,9 +23,10 @@ from muon_newton_schulz_step_gb300 import experts  # noqa: E402
 
 
 class MoeLayer:
-    def __init__(self, hidden=512, width=256, count=16, top_k=4, groups=4, top_groups=2, seed=0):
+    def __init__(self, hidden=512, width=256, count=16, top_k=4, groups=4, top_groups=2, seed=0, fused=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.top_k, self.groups, self.top_groups = top_k, groups, top_groups
+        self.fused = fused
 
         def matrix(*shape, std):
             w = torch.randn(*shape, generator=g, device="cuda") * std
@@ -43,6 +47,11 @@ class MoeLayer:
         logits = h.float() @ self.router.t()
         weights, chosen, counts = experts.route(logits, self.top_k, bias=self.bias, score="sigmoid", groups=self.groups,
                                                 top_groups=self.top_groups)
+        if self.fused:
+            plan = experts.plan_tokens(chosen, counts.numel())
+            x = experts.dispatch(h, plan)
+            y = self.down(experts.swiglu(self.gate(x, plan.offsets), self.up(x, plan.offsets)), plan.offsets)
+            return experts.combine(y, plan, weights, out_dtype=torch.float32), counts
         order, offsets = experts.sort_tokens(chosen, counts)
         token = order // self.top_k
         x = h[token]
@@ -69,10 +78,24 @@ class MoeLayer:
         self.router.grad = None
         return norm
 
+    @torch.no_grad()
+    def serve(self, h, block=64):
+        """The layer's output for a few tokens, on weights of 4 bits (kept from the first call on)."""
+        if not hasattr(self, "served"):
+            both = torch.cat([self.gate.weight, self.up.weight], 1)      # one product makes gate and up
+            self.served = experts.Int4Linear(both, block), experts.Int4Linear(self.down.weight, block)
+        gate_up, down = self.served
+        weights, chosen, _ = mg.muon_route(h.float() @ self.router.t(), self.top_k, bias=self.bias, score="sigmoid",
+                                           groups=self.groups, top_groups=self.top_groups)
+        plan = experts.plan_tokens(chosen, self.bias.numel())
+        x = experts.dispatch(h, plan)
+        y = down(experts.swiglu(gate_up(x, plan.offsets)), plan.offsets)
+        return experts.combine(y, plan, weights, out_dtype=torch.float32)
 
-def train(steps=20, tokens=1024, hidden=512, seed=0):
+
+def train(steps=20, tokens=1024, hidden=512, seed=0, fused=False, layer=None):
     """Losses of fitting the layer to a fixed random target, and the gradients' norms."""
-    layer = MoeLayer(hidden=hidden, seed=seed)
+    layer = MoeLayer(hidden=hidden, seed=seed, fused=fused) if layer is None else layer
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     h = torch.randn(tokens, hidden, generator=g, device="cuda").to(torch.bfloat16)
     target = torch.randn(tokens, hidden, generator=g, device="cuda") * 0.5
@@ -89,6 +112,15 @@ def train(steps=20, tokens=1024, hidden=512, seed=0):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=20)
-    losses, norms = train(ap.parse_args().steps)
+    ap.add_argument("--fused", action="store_true", help="rows and activation by the library's kernels too")
+    ap.add_argument("--serve", action="store_true", help="then single tokens on weights of 4 bits")
+    args = ap.parse_args()
+    layer = MoeLayer(fused=args.fused)
+    losses, norms = train(args.steps, layer=layer)
     for i, (a, b) in enumerate(zip(losses, norms)):
         print(f"step {i:3d}  loss {a:.4f}  gradient norm {b:.4f}")
+    if args.serve:
+        h = torch.randn(4, 512, device="cuda").to(torch.bfloat16)
+        with torch.no_grad():
+            off = layer.serve(h) - layer(h)[0]
+        print(f"4 bits: off by {float(off.norm() / layer(h)[0].norm()):.3f} of the 8-bit layer's output")

@@ -980,9 +980,14 @@ def muon_sort_tokens(chosen, experts: int, *, first: int = 0, stream=None) -> To
     if stream is not None:
         with _on(stream):
             return muon_sort_tokens(chosen, experts, first=first)
-    tokens, top_k, _ = _check_rows("chosen", chosen, (torch.int32,))
-    if not chosen.is_contiguous():
-        raise ValueError("chosen must be contiguous")
+    try:
+        fine, (tokens, top_k) = _plain(chosen, torch.int32), chosen.shape
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        tokens, top_k, _ = _check_rows("chosen", chosen, (torch.int32,))        # says what is wrong
+        if not chosen.is_contiguous():
+            raise ValueError("chosen must be contiguous")
     experts, first, n = int(experts), int(first), tokens * top_k
     if experts < 1:
         raise ValueError(f"experts is {experts}")
@@ -996,12 +1001,24 @@ def muon_sort_tokens(chosen, experts: int, *, first: int = 0, stream=None) -> To
     return TokenPlan(order, place, offsets)
 
 
+def _plain(t, dtype):
+    """Whether ``t`` is a contiguous tensor of ``dtype`` on the current device."""
+    return t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.get_device() == _current_device()
+
+
 def _check_plan(plan, tokens=None):
     """(tokens, top_k, experts, addresses of places and offsets) of a plan, whose tensors are checked."""
     if not isinstance(plan, TokenPlan):
         raise ValueError("plan must be a TokenPlan, as muon_sort_tokens makes it")
     _, place, offsets = plan
-    t, top_k, _ = _check_rows("plan.place", place, (torch.int32,), tokens)
+    try:
+        (t, top_k), (n,) = place.shape, offsets.shape
+        if top_k >= 1 and n >= 2 and (tokens is None or t == tokens) and _plain(place, torch.int32) \
+                and _plain(offsets, torch.int32):
+            return t, top_k, n - 1, place.data_ptr(), offsets.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        pass
+    t, top_k, _ = _check_rows("plan.place", place, (torch.int32,), tokens)      # says what is wrong
     if not place.is_contiguous():
         raise ValueError("plan.place must be contiguous")
     if top_k < 1:
@@ -1032,6 +1049,11 @@ def muon_dispatch_tokens(x, plan: TokenPlan, stream=None) -> torch.Tensor:
 def _check_weights(weights, tokens, top_k):
     if weights is None:
         return None
+    try:
+        if weights.shape == (tokens, top_k) and _plain(weights, torch.float32):
+            return weights.data_ptr()
+    except AttributeError:
+        pass
     _check_rows("weights", weights, (torch.float32,), tokens, top_k)
     if not weights.is_contiguous():
         raise ValueError("weights must be contiguous")
@@ -1107,9 +1129,9 @@ def muon_swiglu(gate, up, stream=None) -> torch.Tensor:
 
 
 def muon_swiglu_backward(d, gate, up, *, joined: bool = False, stream=None):
-    """(d_gate, d_up) of ``muon_swiglu`` from ``d``, in its dtype.  ``joined``: the two are
-    halves of one tensor (rows x 2 cols), as the gradient of one product that made gate and
-    up wants them."""
+    """(d_gate, d_up) of ``muon_swiglu`` from ``d``, in its dtype.  ``joined``: one tensor,
+    rows x 2 cols, d_gate before d_up, as the gradient of one product that made gate and up
+    wants them."""
     if stream is not None:
         with _on(stream):
             return muon_swiglu_backward(d, gate, up, joined=joined)
@@ -1118,14 +1140,14 @@ def muon_swiglu_backward(d, gate, up, *, joined: bool = False, stream=None):
     if d_code != code:
         raise ValueError("d must be of gate's dtype")
     if joined:
-        both = _new_rows(rows, 2 * cols, gate.dtype)
-        d_gate, d_up, ld = both[:, :cols], both[:, cols:], 2 * cols
+        d_gate = d_up = _new_rows(rows, 2 * cols, gate.dtype)
+        ld, on = 2 * cols, cols * gate.element_size()
     else:
-        d_gate, d_up, ld = _new_rows(rows, cols, gate.dtype), _new_rows(rows, cols, gate.dtype), cols
+        d_gate, d_up, ld, on = _new_rows(rows, cols, gate.dtype), _new_rows(rows, cols, gate.dtype), cols, 0
     if cols:
         _check(lib().muon_swiglu_backward(d.data_ptr(), ld_d, gate.data_ptr(), ld_gate, up.data_ptr(), ld_up, code, rows,
-                                          cols, d_gate.data_ptr(), ld, d_up.data_ptr(), ld, _handle(None)))
-    return d_gate, d_up
+                                          cols, d_gate.data_ptr(), ld, d_up.data_ptr() + on, ld, _handle(None)))
+    return d_gate if joined else (d_gate, d_up)
 
 
 class Int4Matrix(NamedTuple):
@@ -1164,23 +1186,24 @@ def _check_int4(w, offsets):
     """(n, k, groups, offsets' pointer) of a weight of 4 bits that goes with ``offsets``."""
     if not isinstance(w, Int4Matrix) or not isinstance(w.codes, torch.Tensor) or not isinstance(w.scale, torch.Tensor):
         raise ValueError("the weight must be an Int4Matrix, as muon_int4_quantize_weight makes it")
-    codes, scale, block, k = w.codes, w.scale, int(w.block), int(w.cols)
-    shape = codes.shape
+    codes, scale, block, k = w
+    shape, k = codes.shape, int(k)
     if len(shape) not in (2, 3) or block not in (32, 64, 128):
         raise ValueError("the weight must be an Int4Matrix with 2-D or 3-D codes and a block of 32, 64 or 128")
     stacked = len(shape) == 3
     if stacked != (offsets is not None):
         raise ValueError("a stacked weight goes with offsets, a single one without")
     n, up = shape[-2], _up128(k)
-    if codes.dtype != torch.uint8 or shape[-1] != up // 2 or not codes.is_cuda or not codes.is_contiguous():
+    if shape[-1] != up // 2 or codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous():
         raise ValueError(f"the weight's codes must be a contiguous CUDA tensor of {torch.uint8} with rows of {up // 2}")
-    if scale.dtype != torch.bfloat16 or tuple(scale.shape) != (*shape[:-2], up // block, n) or not scale.is_cuda \
-            or not scale.is_contiguous():
-        raise ValueError(f"the weight's scale must be a contiguous CUDA tensor of {torch.bfloat16} with shape "
-                         f"{(*shape[:-2], up // block, n)}")
+    want = (shape[0], up // block, n) if stacked else (up // block, n)
+    if scale.shape != want or scale.dtype != torch.bfloat16 or not scale.is_cuda or not scale.is_contiguous():
+        raise ValueError(f"the weight's scale must be a contiguous CUDA tensor of {torch.bfloat16} with shape {want}")
     _here("the weight's codes", codes)
     _here("the weight's scale", scale)
-    groups, optr = _check_offsets(offsets, shape[0] if stacked else 1)
+    if not stacked:
+        return n, k, 1, None
+    groups, optr = _check_offsets(offsets, shape[0])
     return n, k, groups, optr
 
 

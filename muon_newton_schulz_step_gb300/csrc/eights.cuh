@@ -51,10 +51,10 @@ __device__ __noinline__ uint4 load_edge(const char* p, Extent in) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight elements from p on.  SHIFT: p is aligned to its elements alone; the 16-byte vectors
+// Eight elements from p on; `half`: the first four (fp32 alone).  SHIFT: p is aligned to its elements alone; the 16-byte vectors
 // around them are loaded and shifted (all lanes of a warp by the same amount).
 template <typename T, bool SHIFT, bool ONCE = false>
-__device__ __forceinline__ Eight<T> load_eight(const T* p, Extent in) {
+__device__ __forceinline__ Eight<T> load_eight(const T* p, Extent in, bool half = false) {
     constexpr int kWords = Eight<T>::kWords;
     Eight<T> r;
     const char* at = reinterpret_cast<const char*>(p);
@@ -62,7 +62,8 @@ __device__ __forceinline__ Eight<T> load_eight(const T* p, Extent in) {
     if (!SHIFT || off == 0) {
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
-            const uint4 v = load_16<ONCE>(at + 16 * i);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (i == 0 || !half) v = load_16<ONCE>(at + 16 * i);
             r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
         }
         return r;
@@ -88,12 +89,12 @@ __device__ __forceinline__ Eight<T> load_eight(const T* p, Extent in) {
     return r;
 }
 
-// To 16 aligned bytes.
+// To aligned bytes; `half`: the first four.
 template <typename T>
-__device__ __forceinline__ void store_eight(T* p, const Eight<T>& r) {
+__device__ __forceinline__ void store_eight(T* p, const Eight<T>& r, bool half = false) {
 #pragma unroll
     for (int i = 0; i < Eight<T>::kWords / 4; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+        if (i == 0 || !half) reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
 }
 
 template <typename T>

@@ -44,25 +44,12 @@ __device__ __forceinline__ uint4 in_pairs(uint32_t a01, uint32_t a23, uint32_t a
 
 // fp32 as three bf16 whose sum it is: 8 bits of the significand each, cut and not rounded, so
 // that the largest numbers stay finite.  Infinities and NaN stay in the first.
-struct ThreeParts {
-    uint16_t part[3];
-};
-
-__device__ __forceinline__ ThreeParts split(float v) {
-    ThreeParts t;
-    uint32_t u = __float_as_uint(v);
-    if ((u & 0x7f800000u) == 0x7f800000u) {
-        t.part[0] = static_cast<uint16_t>((u >> 16) | ((u & 0x007fffffu) != 0u ? 0x40u : 0u));
-        t.part[1] = t.part[2] = 0;
-        return t;
-    }
-    t.part[0] = static_cast<uint16_t>(u >> 16);
-    v -= __uint_as_float(u & 0xffff0000u);
-    u = __float_as_uint(v);
-    t.part[1] = static_cast<uint16_t>(u >> 16);
-    v -= __uint_as_float(u & 0xffff0000u);
-    t.part[2] = static_cast<uint16_t>(__float_as_uint(v) >> 16);
-    return t;
+__device__ __noinline__ float3 split_odd(float v) {
+    const uint32_t u = __float_as_uint(v);
+    if ((u & 0x7f800000u) == 0x7f800000u)
+        return make_float3(__uint_as_float((u & 0xffff0000u) | ((u & 0x007fffffu) != 0u ? 0x00400000u : 0u)), 0.0f, 0.0f);
+    const float rest = v - __uint_as_float(u & 0xffff0000u);
+    return make_float3(v, rest, rest - __uint_as_float(__float_as_uint(rest) & 0xffff0000u));
 }
 
 // Eight consecutive elements of x as `PARTS` fragments in decode()'s order; zero past column k.
@@ -112,15 +99,23 @@ __device__ __forceinline__ EightOfX<PARTS> fragments(const RawOfX<PARTS>& r) {
         f.v[0] = in_pairs(r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w);
     } else {
         const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-        ThreeParts t[8];
+        float3 t[8];                                       // the upper halves of each are the parts
+        float zero = 0.0f;                                 // NaN if one of the eight is not finite
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = split(__uint_as_float(w[i]));
+        for (int i = 0; i < 8; ++i) {
+            t[i].x = __uint_as_float(w[i]);
+            t[i].y = t[i].x - __uint_as_float(w[i] & 0xffff0000u);
+            t[i].z = t[i].y - __uint_as_float(__float_as_uint(t[i].y) & 0xffff0000u);
+            zero = fmaf(t[i].x, 0.0f, zero);
+        }
+        if (zero != 0.0f) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-            f.v[q] = make_uint4(t[0].part[q] | (static_cast<uint32_t>(t[4].part[q]) << 16),
-                                t[1].part[q] | (static_cast<uint32_t>(t[5].part[q]) << 16),
-                                t[2].part[q] | (static_cast<uint32_t>(t[6].part[q]) << 16),
-                                t[3].part[q] | (static_cast<uint32_t>(t[7].part[q]) << 16));
+            for (int i = 0; i < 8; ++i) t[i] = split_odd(__uint_as_float(w[i]));
+        }
+        auto upper = [](float lo, float hi) { return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632); };
+        f.v[0] = make_uint4(upper(t[0].x, t[4].x), upper(t[1].x, t[5].x), upper(t[2].x, t[6].x), upper(t[3].x, t[7].x));
+        f.v[1] = make_uint4(upper(t[0].y, t[4].y), upper(t[1].y, t[5].y), upper(t[2].y, t[6].y), upper(t[3].y, t[7].y));
+        f.v[2] = make_uint4(upper(t[0].z, t[4].z), upper(t[1].z, t[5].z), upper(t[2].z, t[6].z), upper(t[3].z, t[7].z));
     }
     return f;
 }

@@ -52,6 +52,9 @@ __device__ __forceinline__ Entries entries_of(const RowsParams& p, long long tok
     return e;
 }
 
+// Whether eight i of a row ends in its middle (fp32 rows of 4 modulo 8).
+__device__ __forceinline__ bool half_of(const RowsParams& p, int i) { return p.half != 0 && i == p.eights - 1; }
+
 // A warp takes U x 32 eights of one token's row.
 template <typename T, bool SHIFT, int U>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
@@ -67,7 +70,8 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     if (!SHIFT && e.held != 0u) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (first + 32 * u < p.eights) r[u] = load_eight<T, false>(x + static_cast<long long>(first + 32 * u) * 8, in);
+            if (first + 32 * u < p.eights)
+                r[u] = load_eight<T, false>(x + static_cast<long long>(first + 32 * u) * 8, in, half_of(p, first + 32 * u));
     }
     for (int j = 0; j < p.top_k; ++j) {
         const int place = __shfl_sync(0xffffffffu, e.place, j);
@@ -78,7 +82,8 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (first + 32 * u >= p.eights) break;
-                store_eight<T>(out + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{});
+                store_eight<T>(out + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{},
+                               half_of(p, first + 32 * u));
             }
             continue;
         }
@@ -116,7 +121,9 @@ __device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, 
         const T* y = static_cast<const T*>(p.x) + place * p.ld_x + head;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (first + 32 * u < eights) r[a][u] = load_eight<T, SHIFT, !SHIFT>(y + static_cast<long long>(first + 32 * u) * 8, in);
+            if (first + 32 * u < eights)
+                r[a][u] = load_eight<T, SHIFT, !SHIFT>(y + static_cast<long long>(first + 32 * u) * 8, in,
+                                                       !SHIFT && half_of(p, first + 32 * u));
     }
 #pragma unroll
     for (int a = 0; a < N; ++a)
@@ -147,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, SHIFT ? 5 : 3) k_combine(const RowsP
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (first + 32 * u >= eights) break;
-        store_eight<O>(out + head + static_cast<long long>(first + 32 * u) * 8, rounded<O>(acc[u]));
+        store_eight<O>(out + head + static_cast<long long>(first + 32 * u) * 8, rounded<O>(acc[u]),
+                       !SHIFT && half_of(p, first + 32 * u));
     }
     if (SHIFT && part == 0) {                          // the ends of the row
         const long long at = lane < span.head ? lane : p.cols - span.tail + (lane - span.head);
@@ -199,10 +207,11 @@ __device__ __forceinline__ void backward_of(const RowsParams& p, long long token
             const int i = at + u * static_cast<int>(blockDim.x);
             if (i >= eights) break;
             const long long col = head + static_cast<long long>(i) * 8;
-            g[u] = load_eight<D, SHIFT>(d + col, in_d);
+            const bool half = !SHIFT && half_of(p, i);
+            g[u] = load_eight<D, SHIFT>(d + col, in_d, half);
             if (dots) {
 #pragma unroll
-                for (int a = 0; a < N; ++a) r[u][a] = load_eight<T, SHIFT>(y[a] + col, in_y);
+                for (int a = 0; a < N; ++a) r[u][a] = load_eight<T, SHIFT>(y[a] + col, in_y, half);
             }
         }
 #pragma unroll
@@ -224,7 +233,7 @@ __device__ __forceinline__ void backward_of(const RowsParams& p, long long token
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] = w[a] * v[k];
                     if (alike) {
-                        store_eight<T>(dy[a] + col, rounded<T>(o));
+                        store_eight<T>(dy[a] + col, rounded<T>(o), !SHIFT && half_of(p, i));
                     } else {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) dy[a][col + k] = to_type<T>(o[k]);
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsPara
 
 template <int U>
 unsigned warp_items(RowsParams& p) {
-    p.eights = static_cast<int>(p.cols / 8);
+    p.eights = static_cast<int>((p.cols + 4 * p.half) / 8);
     p.parts = (p.eights + 32 * U - 1) / (32 * U);
     if (p.parts == 0) p.parts = 1;
     return static_cast<unsigned>((p.tokens * p.parts + kWarps - 1) / kWarps);
@@ -309,17 +318,19 @@ cudaError_t combine(RowsParams p, cudaStream_t s) {
 
 template <typename D, typename T, bool SHIFT>
 cudaError_t combine_backward(RowsParams p, cudaStream_t s) {
-    p.eights = static_cast<int>(p.cols / 8);
+    p.eights = static_cast<int>((p.cols + 4 * p.half) / 8);
     // as many warps as the row has eights for
     const int warps = p.eights >= 256 ? 8 : p.eights >= 128 ? 4 : p.eights >= 64 ? 2 : 1;
     k_combine_backward<D, T, SHIFT><<<static_cast<unsigned>(p.tokens), 32 * warps, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-// Rows of whole eights that all lie on 16 bytes.
 bool on_16(const void* p, long long ld, bool bf16) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0;
 }
+
+// Rows that fill 16-byte vectors: eights, or in fp32 alone fours.
+bool fills(const RowsParams& p, bool any_bf16) { return p.cols % (any_bf16 ? 8 : 4) == 0; }
 
 template <typename F>
 cudaError_t by_type(bool bf16, F&& f) {
@@ -328,16 +339,20 @@ cudaError_t by_type(bool bf16, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s) {
-    const bool whole = p.cols % 8 == 0 && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.x_bf16);
+cudaError_t launch_dispatch(const RowsParams& q, cudaStream_t s) {
+    RowsParams p = q;
+    const bool whole = fills(p, p.x_bf16) && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.x_bf16);
+    p.half = whole && p.cols % 8 != 0;
     return by_type(p.x_bf16, [&](auto t) {
         using T = decltype(t);
         return whole ? dispatch<T, false>(p, s) : dispatch<T, true>(p, s);
     });
 }
 
-cudaError_t launch_combine(const RowsParams& p, cudaStream_t s) {
-    const bool whole = p.cols % 8 == 0 && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.out_bf16);
+cudaError_t launch_combine(const RowsParams& q, cudaStream_t s) {
+    RowsParams p = q;
+    const bool whole = fills(p, p.x_bf16 || p.out_bf16) && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.out_bf16);
+    p.half = whole && p.cols % 8 != 0;
     return by_type(p.x_bf16, [&](auto t) {
         return by_type(p.out_bf16, [&](auto o) {
             using T = decltype(t);
@@ -347,9 +362,11 @@ cudaError_t launch_combine(const RowsParams& p, cudaStream_t s) {
     });
 }
 
-cudaError_t launch_combine_backward(const RowsParams& p, cudaStream_t s) {
-    const bool whole = p.cols % 8 == 0 && on_16(p.d, p.ld_d, p.d_bf16) && (p.dw == nullptr || on_16(p.x, p.ld_x, p.x_bf16)) &&
-                       (p.out == nullptr || on_16(p.out, p.ld_out, p.x_bf16));
+cudaError_t launch_combine_backward(const RowsParams& q, cudaStream_t s) {
+    RowsParams p = q;
+    const bool whole = fills(p, p.d_bf16 || p.x_bf16) && on_16(p.d, p.ld_d, p.d_bf16) &&
+                       (p.dw == nullptr || on_16(p.x, p.ld_x, p.x_bf16)) && (p.out == nullptr || on_16(p.out, p.ld_out, p.x_bf16));
+    p.half = whole && p.cols % 8 != 0;
     return by_type(p.d_bf16, [&](auto d) {
         return by_type(p.x_bf16, [&](auto t) {
             using D = decltype(d);

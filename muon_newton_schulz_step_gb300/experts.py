@@ -1,8 +1,10 @@
 """Mixture-of-experts layers on the library's operators, for autograd.
 
-Routing (``route``), the order of the tokens by expert (``sort_tokens``) and
-linear layers on 8-bit operands (``Fp8Linear`` holds a weight and its codes):
-what a layer of experts runs in front of the optimizer step ("Domyn is training
+Routing (``route``), the order of the tokens by expert (``plan_tokens``, or
+``sort_tokens`` by torch alone), their rows on the way to the experts and back
+(``dispatch``, ``combine``), the gated activation (``swiglu``) and linear layers on
+8-bit operands (``Fp8Linear`` holds a weight and its codes), for serving on weights of
+4 bits (``Int4Linear``): what a layer of experts runs in front of the optimizer step ("Domyn is training
 a 1T-parameter MoE on Europe's Jupiter supercomputer, and published the
 recipe", table "The model and the machine": 384 experts, 8 chosen).  The
 arithmetic runs in the library's kernels; torch supplies memory, the sort and
@@ -10,10 +12,11 @@ the graph.  The layers have first derivatives alone: a second one is refused.
 """
 import torch
 
-from . import (muon_fp8_linear, muon_fp8_linear_backward, muon_fp8_quantize_weight, muon_route,
-               muon_route_backward)
+from . import (TokenPlan, muon_combine_tokens, muon_combine_tokens_backward, muon_dispatch_tokens, muon_fp8_linear,
+               muon_fp8_linear_backward, muon_fp8_quantize_weight, muon_int4_linear, muon_int4_quantize_weight,
+               muon_route, muon_route_backward, muon_sort_tokens, muon_swiglu, muon_swiglu_backward)
 
-__all__ = ["route", "sort_tokens", "Fp8Linear"]
+__all__ = ["route", "sort_tokens", "plan_tokens", "dispatch", "combine", "swiglu", "Fp8Linear", "Int4Linear"]
 
 
 class _Underived(torch.autograd.Function):
@@ -71,6 +74,91 @@ def sort_tokens(chosen, counts):
     return order, torch.cat([first, first + ends]).to(torch.int32)
 
 
+def plan_tokens(chosen, experts, first=0):
+    """``muon_sort_tokens``: where the rows of ``chosen`` (tokens x top_k, of ``route``) lie,
+    sorted by expert, for the ``experts`` experts from ``first`` on that are held here."""
+    return muon_sort_tokens(chosen, experts, first=first)
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, *plan):
+        ctx.save_for_backward(*plan)
+        return muon_dispatch_tokens(x, TokenPlan(*plan))
+
+    @staticmethod
+    def backward(ctx, d):
+        with torch.no_grad():
+            dx = muon_combine_tokens(d.contiguous(), TokenPlan(*ctx.saved_tensors))
+        return _underived(dx, d), None, None, None
+
+
+def dispatch(x, plan):
+    """The tokens' rows sorted by expert (``muon_dispatch_tokens``), with a gradient for x."""
+    return _Dispatch.apply(x, *plan)
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, out_dtype, *plan):
+        ctx.save_for_backward(y, weights, *plan)
+        return muon_combine_tokens(y, TokenPlan(*plan), weights, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, d):
+        y, weights, *plan = ctx.saved_tensors
+        need_dy, need_dw = ctx.needs_input_grad[:2]
+        with torch.no_grad():
+            dy, dw = muon_combine_tokens_backward(d.contiguous(), y, TokenPlan(*plan), weights, need_dy=need_dy,
+                                                  need_dw=need_dw)
+        sources = (d, y) if weights is None else (d, y, weights)
+        return (_underived(dy, *sources), _underived(dw, *sources)) + (None,) * 4
+
+
+def combine(y, plan, weights=None, *, out_dtype=None):
+    """The experts' rows back at their tokens, weighted and added up (``muon_combine_tokens``),
+    with gradients for y and the weights."""
+    return _Combine.apply(y, weights, out_dtype, *plan)
+
+
+class _Swiglu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up):
+        ctx.save_for_backward(gate, up)
+        return muon_swiglu(gate, up)
+
+    @staticmethod
+    def backward(ctx, d):
+        gate, up = ctx.saved_tensors
+        with torch.no_grad():
+            d_gate, d_up = muon_swiglu_backward(d.contiguous(), gate, up)
+        return _underived(d_gate, d, gate, up), _underived(d_up, d, gate, up)
+
+
+class _SwigluJoined(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, both):
+        ctx.save_for_backward(both)
+        return muon_swiglu(*both.chunk(2, -1))
+
+    @staticmethod
+    def backward(ctx, d):
+        both, = ctx.saved_tensors
+        with torch.no_grad():
+            d_both = muon_swiglu_backward(d.contiguous(), *both.chunk(2, -1), joined=True)
+        return _underived(d_both, d, both)
+
+
+def swiglu(gate, up=None):
+    """gate / (1 + exp(-gate)) * up (``muon_swiglu``) with gradients for both; without ``up``
+    gate holds both, rows x 2 cols, gate before up, as one product makes them."""
+    if up is not None:
+        return _Swiglu.apply(gate, up)
+    if gate.dim() != 2 or gate.shape[1] % 2:
+        raise ValueError("without up, gate must have an even number of columns: gate's, then up's")
+    return _SwigluJoined.apply(gate)
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, codes, offsets):
@@ -105,3 +193,18 @@ class Fp8Linear:
 
     def __call__(self, x, offsets=None):
         return _Linear.apply(x, self.weight, self.codes, offsets)
+
+
+class Int4Linear:
+    """A weight (out x in, or stacked over experts) in 4 bits, for serving: ``layer(x,
+    offsets)`` is x W^T in x's type.  There are no gradients: neither for the weight, of which
+    the codes alone are kept, nor for x."""
+
+    def __init__(self, weight, block=128):
+        with torch.no_grad():
+            self.codes = muon_int4_quantize_weight(weight.detach(), block)
+
+    def __call__(self, x, offsets=None):
+        if torch.is_grad_enabled() and x.requires_grad:
+            raise RuntimeError("a layer of 4 bits has no gradients: call it under torch.no_grad()")
+        return muon_int4_linear(x, self.codes, offsets=offsets, out_dtype=x.dtype)

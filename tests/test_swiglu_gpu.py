@@ -57,9 +57,8 @@ def test_forward_and_backward(rows, cols, dtype, how):
     want = dd * u * s * f
     off = (dd * u).abs() * (s * (s_off(g) * f.abs() + g.abs() * (s * s_off(g) + U) + 4 * U * f.abs()) + tiny * (1 + g.abs()))
     check(d_gate, want, off)
-    j_gate, j_up = mg.muon_swiglu_backward(d, gate, up, joined=True)
-    assert torch.equal(j_gate, d_gate) and torch.equal(j_up, d_up)
-    assert j_up.data_ptr() == j_gate.data_ptr() + cols * j_gate.element_size()
+    both = mg.muon_swiglu_backward(d, gate, up, joined=True)
+    assert torch.equal(both, torch.cat([d_gate, d_up], 1)) and both.is_contiguous()
 
 
 def test_ends_of_the_range():

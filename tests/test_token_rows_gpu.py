@@ -86,7 +86,8 @@ def matrix(rows, cols, dtype, gen, how):
 
 
 SHAPES = [(1, 1, 1, 1), (1, 8, 1, 16), (5, 3, 7, 9), (17, 4, 130, 8), (9, 32, 64, 40), (64, 2, 513, 6), (33, 6, 1301, 12),
-          (3, 8, 6144, 16), (40, 9, 264, 20), (0, 4, 16, 4)]
+          (3, 8, 6144, 16), (40, 9, 264, 20), (0, 4, 16, 4), (50, 3, 12, 5),
+          (21, 5, 1300, 9), (6, 2, 4, 3)]
 
 
 @pytest.mark.parametrize("tokens,top_k,cols,experts", SHAPES)
