@@ -377,8 +377,7 @@ struct RowsParams {
     long long tokens, cols;
     int top_k, groups, rows;  // rows = tokens * top_k
     int x_bf16, d_bf16, out_bf16;
-    int eights, parts;        // eights of a row; warps for a row
-    int half;                 // the last eight is a four
+    int runs, parts;          // whole runs of a row; warps for a row
 };
 
 cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s);

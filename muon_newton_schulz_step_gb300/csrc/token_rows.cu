@@ -13,15 +13,15 @@
 // Sums are fp32 fused multiply-adds in the order of j, so that a call's result has
 // one value whatever the order of the blocks.
 //
-// Rows are worked off in eights of elements that lie on 16 bytes of the row that is
-// written; where the rows that are read lie otherwise (odd widths, views), their eights are
+// Rows are worked off in runs of elements that lie on 16 bytes of the row that is
+// written; where the rows that are read lie otherwise (odd widths, views), their runs are
 // put together from the 16-byte vectors around them (SHIFT), and the ends of a row go one
 // by one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "eights.cuh"
 #include "internal.h"
+#include "row_runs.cuh"
 
 namespace muon {
 namespace {
@@ -52,11 +52,8 @@ __device__ __forceinline__ Entries entries_of(const RowsParams& p, long long tok
     return e;
 }
 
-// Whether eight i of a row ends in its middle (fp32 rows of 4 modulo 8).
-__device__ __forceinline__ bool half_of(const RowsParams& p, int i) { return p.half != 0 && i == p.eights - 1; }
-
-// A warp takes U x 32 eights of one token's row.
-template <typename T, bool SHIFT, int U>
+// A warp takes U x 32 runs of one token's row.
+template <typename T, int E, bool SHIFT, int U>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     const int lane = threadIdx.x & 31;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -66,12 +63,12 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     const Entries e = entries_of(p, token);
     const T* x = static_cast<const T*>(p.x) + token * p.ld_x;
     const Extent in = extent_of<T>(p.x, p.tokens, p.ld_x, p.cols);
-    Eight<T> r[U] = {};
+    RowRun<T, E> r[U] = {};
     if (!SHIFT && e.held != 0u) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (first + 32 * u < p.eights)
-                r[u] = load_eight<T, false>(x + static_cast<long long>(first + 32 * u) * 8, in, half_of(p, first + 32 * u));
+            if (first + 32 * u < p.runs)
+                r[u] = load_row<T, E, false>(x + static_cast<long long>(first + 32 * u) * E, in);
     }
     for (int j = 0; j < p.top_k; ++j) {
         const int place = __shfl_sync(0xffffffffu, e.place, j);
@@ -81,22 +78,21 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
         if (!SHIFT) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (first + 32 * u >= p.eights) break;
-                store_eight<T>(out + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{},
-                               half_of(p, first + 32 * u));
+                if (first + 32 * u >= p.runs) break;
+                store_row<T, E>(out + static_cast<long long>(first + 32 * u) * E, held ? r[u] : RowRun<T, E>{});
             }
             continue;
         }
-        const RowSpan<T> span(out, p.cols);
+        const RowSpan<T, E> span(out, p.cols);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (held && first + 32 * u < span.eights)
-                r[u] = load_eight<T, true>(x + span.head + static_cast<long long>(first + 32 * u) * 8, in);
+            if (held && first + 32 * u < span.runs)
+                r[u] = load_row<T, E, true>(x + span.head + static_cast<long long>(first + 32 * u) * E, in);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (first + 32 * u >= span.eights) break;
-            store_eight<T>(out + span.head + static_cast<long long>(first + 32 * u) * 8, held ? r[u] : Eight<T>{});
+            if (first + 32 * u >= span.runs) break;
+            store_row<T, E>(out + span.head + static_cast<long long>(first + 32 * u) * E, held ? r[u] : RowRun<T, E>{});
         }
         if (part == 0) {                               // the ends of the row
             if (lane < span.head) out[lane] = held ? x[lane] : to_type<T>(0.0f);
@@ -106,12 +102,14 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     }
 }
 
-// N entries' rows are under way together, U eights of a lane from each.
-template <typename T, bool SHIFT, int N, int U>
+// N entries' rows are under way together, U runs of a lane from each.
+template <typename T, int E, bool SHIFT, int N, int U>
 __device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, float weight, unsigned& left, int first,
-                                         int head, int eights, Extent in, float (&acc)[U][8]) {
-    Eight<T> r[N][U];
+                                         int head, int runs, Extent in, float (&acc)[U][E]) {
+    constexpr int kStep = SHIFT ? kShared : 32;
+    RowRun<T, E> r[N][U] = {};
     float w[N];
+    int off[N];
 #pragma unroll
     for (int a = 0; a < N; ++a) {
         const int j = __ffs(left) - 1;
@@ -119,43 +117,50 @@ __device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, 
         const long long place = __shfl_sync(0xffffffffu, e.place, j);
         w[a] = __shfl_sync(0xffffffffu, weight, j);
         const T* y = static_cast<const T*>(p.x) + place * p.ld_x + head;
+        off[a] = static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (first + 32 * u < eights)
-                r[a][u] = load_eight<T, SHIFT, !SHIFT>(y + static_cast<long long>(first + 32 * u) * 8, in,
-                                                       !SHIFT && half_of(p, first + 32 * u));
+        for (int u = 0; u < U; ++u) {
+            const T* at = y + static_cast<long long>(first + kStep * u) * E;
+            if (SHIFT) {                               // past the last run lies what that one has beyond its vector
+                if (first + kStep * u <= runs) r[a][u] = load_below<T, E>(at, in);
+            } else if (first + kStep * u < runs) {
+                r[a][u] = load_row<T, E, false, true>(at, in);
+            }
+        }
     }
 #pragma unroll
     for (int a = 0; a < N; ++a)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            const RowRun<T, E> v = SHIFT ? finished<T, E>(r[a][u], off[a]) : r[a][u];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(w[a], element<T>(r[a][u], i), acc[u][i]);
+            for (int i = 0; i < E; ++i) acc[u][i] = fmaf(w[a], element<T, E>(v, i), acc[u][i]);
+        }
 }
 
-template <typename T, typename O, bool SHIFT, int U>
-__global__ void __launch_bounds__(kThreads, SHIFT ? 5 : 3) k_combine(const RowsParams p) {
+template <typename T, typename O, int E, bool SHIFT, int U>
+__global__ void __launch_bounds__(kThreads, SHIFT ? 4 : 3) k_combine(const RowsParams p) {
+    constexpr int kStep = SHIFT ? kShared : 32, kRows = SHIFT ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long token = item / p.parts;
     if (token >= p.tokens) return;
-    const int part = static_cast<int>(item - token * p.parts), first = part * (32 * U) + lane;
+    const int part = static_cast<int>(item - token * p.parts), first = part * (kStep * U) + lane;
     const Entries e = entries_of(p, token);
     const float weight = p.weights != nullptr && lane < p.top_k ? __ldg(p.weights + token * p.top_k + lane) : 1.0f;
     const T* y = static_cast<const T*>(p.x);
     const Extent in = extent_of<T>(p.x, p.rows, p.ld_x, p.cols);
     O* out = static_cast<O*>(p.out) + token * p.ld_out;
-    const RowSpan<O> span(out, p.cols);
-    const int head = SHIFT ? span.head : 0, eights = SHIFT ? span.eights : p.eights;
-    float acc[U][8] = {};
+    const RowSpan<O, E> span(out, p.cols);
+    const int head = SHIFT ? span.head : 0, runs = SHIFT ? span.runs : p.runs;
+    float acc[U][E] = {};
     unsigned left = e.held;
-    while (__popc(left) >= 4) add_rows<T, SHIFT, 4, U>(p, e, weight, left, first, head, eights, in, acc);
-    while (left != 0u) add_rows<T, SHIFT, 1, U>(p, e, weight, left, first, head, eights, in, acc);
+    while (__popc(left) >= kRows) add_rows<T, E, SHIFT, kRows, U>(p, e, weight, left, first, head, runs, in, acc);
+    while (left != 0u) add_rows<T, E, SHIFT, 1, U>(p, e, weight, left, first, head, runs, in, acc);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (first + 32 * u >= eights) break;
-        store_eight<O>(out + head + static_cast<long long>(first + 32 * u) * 8, rounded<O>(acc[u]),
-                       !SHIFT && half_of(p, first + 32 * u));
+        if (first + kStep * u >= runs || lane >= kStep) break;
+        store_row<O, E>(out + head + static_cast<long long>(first + kStep * u) * E, rounded<O, E>(acc[u]));
     }
     if (SHIFT && part == 0) {                          // the ends of the row
         const long long at = lane < span.head ? lane : p.cols - span.tail + (lane - span.head);
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, SHIFT ? 5 : 3) k_combine(const RowsP
 
 // A block takes one token, N of its entries at a time: d is read once for them, and their
 // dot products stay in registers to the end of the row.
-template <typename D, typename T, bool SHIFT, int N, int U>
+template <typename D, typename T, int E, bool SHIFT, int N, int U>
 __device__ __forceinline__ void backward_of(const RowsParams& p, long long token, const Entries& e, float weight,
                                             unsigned& left, float (*part)[kRowsMaxTopK]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -195,48 +200,47 @@ __device__ __forceinline__ void backward_of(const RowsParams& p, long long token
         dot[a] = 0.0f;
     }
     static_assert(!SHIFT || N == 1, "rows that lie differently go one at a time");
-    // by the eights of y, so that the order of a sum does not depend on where dy lies; dy lies alike as a rule
-    const RowSpan<T> span(dots ? y[0] : dy[0], p.cols);
+    // by the runs of y, so that the order of a sum does not depend on where dy lies; dy lies alike as a rule
+    const RowSpan<T, E> span(dots ? y[0] : dy[0], p.cols);
     const bool alike = !SHIFT || reinterpret_cast<uintptr_t>(dy[0] + span.head) % 16 == 0;
-    const int head = SHIFT ? span.head : 0, eights = SHIFT ? span.eights : p.eights;
-    for (int at = threadIdx.x; at < eights; at += U * blockDim.x) {
-        Eight<D> g[U];
-        Eight<T> r[U][N];
+    const int head = SHIFT ? span.head : 0, runs = SHIFT ? span.runs : p.runs;
+    for (int at = threadIdx.x; at < runs; at += U * blockDim.x) {
+        RowRun<D, E> g[U];
+        RowRun<T, E> r[U][N];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = at + u * static_cast<int>(blockDim.x);
-            if (i >= eights) break;
-            const long long col = head + static_cast<long long>(i) * 8;
-            const bool half = !SHIFT && half_of(p, i);
-            g[u] = load_eight<D, SHIFT>(d + col, in_d, half);
+            if (i >= runs) break;
+            const long long col = head + static_cast<long long>(i) * E;
+            g[u] = load_row<D, E, SHIFT>(d + col, in_d);
             if (dots) {
 #pragma unroll
-                for (int a = 0; a < N; ++a) r[u][a] = load_eight<T, SHIFT>(y[a] + col, in_y, half);
+                for (int a = 0; a < N; ++a) r[u][a] = load_row<T, E, SHIFT>(y[a] + col, in_y);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = at + u * static_cast<int>(blockDim.x);
-            if (i >= eights) break;
-            const long long col = head + static_cast<long long>(i) * 8;
-            float v[8];
+            if (i >= runs) break;
+            const long long col = head + static_cast<long long>(i) * E;
+            float v[E];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = element<D>(g[u], k);
+            for (int k = 0; k < E; ++k) v[k] = element<D, E>(g[u], k);
 #pragma unroll
             for (int a = 0; a < N; ++a) {
                 if (dots) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dot[a] = fmaf(v[k], element<T>(r[u][a], k), dot[a]);
+                    for (int k = 0; k < E; ++k) dot[a] = fmaf(v[k], element<T, E>(r[u][a], k), dot[a]);
                 }
                 if (p.out != nullptr) {
-                    float o[8];
+                    float o[E];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = w[a] * v[k];
+                    for (int k = 0; k < E; ++k) o[k] = w[a] * v[k];
                     if (alike) {
-                        store_eight<T>(dy[a] + col, rounded<T>(o), !SHIFT && half_of(p, i));
+                        store_row<T, E>(dy[a] + col, rounded<T, E>(o));
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) dy[a][col + k] = to_type<T>(o[k]);
+                        for (int k = 0; k < E; ++k) dy[a][col + k] = to_type<T>(o[k]);
                     }
                 }
             }
@@ -258,9 +262,9 @@ __device__ __forceinline__ void backward_of(const RowsParams& p, long long token
     }
 }
 
-template <typename D, typename T, bool SHIFT>
+template <typename D, typename T, int E, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsParams p) {
-    constexpr int kU = SHIFT || sizeof(D) + sizeof(T) != 4 ? 1 : 2;   // eights of a lane under way
+    constexpr int kU = SHIFT || sizeof(D) + sizeof(T) != 4 ? 1 : 2;   // runs of a lane under way
     __shared__ float part[kWarps][kRowsMaxTopK];
     const int lane = threadIdx.x & 31;
     const long long token = blockIdx.x;
@@ -268,17 +272,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsPara
     const float weight = p.weights != nullptr && lane < p.top_k ? __ldg(p.weights + token * p.top_k + lane) : 1.0f;
     unsigned left = e.held;
     if (!SHIFT) {
-        while (__popc(left) >= 4) backward_of<D, T, SHIFT, SHIFT ? 1 : 4, kU>(p, token, e, weight, left, part);
+        while (__popc(left) >= 4) backward_of<D, T, E, SHIFT, SHIFT ? 1 : 4, kU>(p, token, e, weight, left, part);
     }
-    while (left != 0u) backward_of<D, T, SHIFT, 1, kU>(p, token, e, weight, left, part);
+    while (left != 0u) backward_of<D, T, E, SHIFT, 1, kU>(p, token, e, weight, left, part);
     if (p.out != nullptr) {                            // rows of no expert
         const unsigned rest = __ballot_sync(0xffffffffu, e.place >= 0 && e.place < p.rows) & ~e.held;
         for (left = rest; left != 0u; left &= left - 1u) {
             const long long place = __shfl_sync(0xffffffffu, e.place, __ffs(left) - 1);
             T* dy = static_cast<T*>(p.out) + place * p.ld_out;
-            const RowSpan<T> span(dy, p.cols);
-            for (int i = threadIdx.x; i < span.eights; i += blockDim.x)
-                store_eight<T>(dy + span.head + static_cast<long long>(i) * 8, Eight<T>{});
+            const RowSpan<T, E> span(dy, p.cols);
+            for (int i = threadIdx.x; i < span.runs; i += blockDim.x)
+                store_row<T, E>(dy + span.head + static_cast<long long>(i) * E, RowRun<T, E>{});
             const int i = threadIdx.x;
             if (i < span.head + span.tail) dy[i < span.head ? i : p.cols - span.tail + (i - span.head)] = to_type<T>(0.0f);
         }
@@ -292,36 +296,44 @@ __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsPara
     }
 }
 
-template <int U>
+// STEP runs of a warp U times
+template <int E, int U, int STEP = 32>
 unsigned warp_items(RowsParams& p) {
-    p.eights = static_cast<int>((p.cols + 4 * p.half) / 8);
-    p.parts = (p.eights + 32 * U - 1) / (32 * U);
+    p.runs = static_cast<int>(p.cols / E);
+    p.parts = (p.runs + STEP * U - 1) / (STEP * U);
     if (p.parts == 0) p.parts = 1;
     return static_cast<unsigned>((p.tokens * p.parts + kWarps - 1) / kWarps);
 }
 
+// 16 bytes of one type, 8 elements of two
+template <typename A, typename B>
+constexpr int run_of() {
+    return sizeof(A) == 4 && sizeof(B) == 4 ? 4 : 8;
+}
+
 template <typename T, bool SHIFT>
 cudaError_t dispatch(RowsParams p, cudaStream_t s) {
-    constexpr int kU = sizeof(T) == 2 ? 4 : 2;
-    const unsigned grid = warp_items<kU>(p);
-    k_dispatch<T, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
+    constexpr int E = run_of<T, T>();
+    const unsigned grid = warp_items<E, 4>(p);
+    k_dispatch<T, E, SHIFT, 4><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, typename O, bool SHIFT>
 cudaError_t combine(RowsParams p, cudaStream_t s) {
-    constexpr int kU = sizeof(T) == 2 && !SHIFT ? 2 : 1;
-    const unsigned grid = warp_items<kU>(p);
-    k_combine<T, O, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
+    constexpr int E = run_of<T, O>(), kU = sizeof(T) * E > 16 ? 1 : 2;
+    const unsigned grid = warp_items<E, kU, SHIFT ? kShared : 32>(p);
+    k_combine<T, O, E, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename D, typename T, bool SHIFT>
 cudaError_t combine_backward(RowsParams p, cudaStream_t s) {
-    p.eights = static_cast<int>((p.cols + 4 * p.half) / 8);
-    // as many warps as the row has eights for
-    const int warps = p.eights >= 256 ? 8 : p.eights >= 128 ? 4 : p.eights >= 64 ? 2 : 1;
-    k_combine_backward<D, T, SHIFT><<<static_cast<unsigned>(p.tokens), 32 * warps, 0, s>>>(p);
+    constexpr int E = run_of<D, T>();
+    p.runs = static_cast<int>(p.cols / E);
+    // as many warps as the row has runs for
+    const int warps = p.runs >= 256 ? 8 : p.runs >= 128 ? 4 : p.runs >= 64 ? 2 : 1;
+    k_combine_backward<D, T, E, SHIFT><<<static_cast<unsigned>(p.tokens), 32 * warps, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -329,7 +341,7 @@ bool on_16(const void* p, long long ld, bool bf16) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0;
 }
 
-// Rows that fill 16-byte vectors: eights, or in fp32 alone fours.
+// Rows of whole runs
 bool fills(const RowsParams& p, bool any_bf16) { return p.cols % (any_bf16 ? 8 : 4) == 0; }
 
 template <typename F>
@@ -339,20 +351,16 @@ cudaError_t by_type(bool bf16, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_dispatch(const RowsParams& q, cudaStream_t s) {
-    RowsParams p = q;
+cudaError_t launch_dispatch(const RowsParams& p, cudaStream_t s) {
     const bool whole = fills(p, p.x_bf16) && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.x_bf16);
-    p.half = whole && p.cols % 8 != 0;
     return by_type(p.x_bf16, [&](auto t) {
         using T = decltype(t);
         return whole ? dispatch<T, false>(p, s) : dispatch<T, true>(p, s);
     });
 }
 
-cudaError_t launch_combine(const RowsParams& q, cudaStream_t s) {
-    RowsParams p = q;
+cudaError_t launch_combine(const RowsParams& p, cudaStream_t s) {
     const bool whole = fills(p, p.x_bf16 || p.out_bf16) && on_16(p.x, p.ld_x, p.x_bf16) && on_16(p.out, p.ld_out, p.out_bf16);
-    p.half = whole && p.cols % 8 != 0;
     return by_type(p.x_bf16, [&](auto t) {
         return by_type(p.out_bf16, [&](auto o) {
             using T = decltype(t);
@@ -362,11 +370,9 @@ cudaError_t launch_combine(const RowsParams& q, cudaStream_t s) {
     });
 }
 
-cudaError_t launch_combine_backward(const RowsParams& q, cudaStream_t s) {
-    RowsParams p = q;
+cudaError_t launch_combine_backward(const RowsParams& p, cudaStream_t s) {
     const bool whole = fills(p, p.d_bf16 || p.x_bf16) && on_16(p.d, p.ld_d, p.d_bf16) &&
                        (p.dw == nullptr || on_16(p.x, p.ld_x, p.x_bf16)) && (p.out == nullptr || on_16(p.out, p.ld_out, p.x_bf16));
-    p.half = whole && p.cols % 8 != 0;
     return by_type(p.d_bf16, [&](auto d) {
         return by_type(p.x_bf16, [&](auto t) {
             using D = decltype(d);
