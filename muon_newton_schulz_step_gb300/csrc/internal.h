@@ -359,6 +359,7 @@ struct SortParams {
     int* table;               // blocks x (experts + 1) counts
     int entries, first, experts;
     int blocks, run;          // of the two launches: how many, entries of each
+    int bits;                 // of a bucket's number
 };
 
 int token_sort_blocks(long long entries);

@@ -7,7 +7,7 @@
 // 12 bytes an entry are all that has to move (262144 entries: 0.5 us), so this is
 // bound by latency: as few launches and as short chains as can be.  A block takes
 // 2048 entries at a time, a warp 128 in a row, four times 32: lanes of one bucket
-// find each other by match, and the count of those before is their rank in the
+// find each other by votes, and the count of those before is their rank in the
 // warp; a column sum over the warps' counts turns it into the rank in the block.
 // Up to kAlone entries one block does it all; past that the first of two launches
 // leaves each block's counts (at most kMaxBlocks, each of an equal run of entries),
@@ -34,6 +34,18 @@ __device__ __forceinline__ int bucket_of(const SortParams& p, int expert) {
     // as unsigned numbers: what lies below `first` wraps to the far end
     const unsigned e = static_cast<unsigned>(expert) - static_cast<unsigned>(p.first);
     return e < static_cast<unsigned>(p.experts) ? static_cast<int>(e) + 1 : 0;
+}
+
+// The lanes with this lane's bucket, bit by bit: up to ten votes, where match.any takes its
+// time by the number of different buckets (4096 entries of 384 experts: 9.4 us with it, 7.9).
+__device__ __forceinline__ unsigned lanes_of(int bucket, int bits) {
+    unsigned same = __ballot_sync(0xffffffffu, bucket >= 0);
+    for (int i = 0; i < bits; ++i) {
+        const bool on = (bucket >> i) & 1;
+        const unsigned votes = __ballot_sync(0xffffffffu, on);
+        same &= on ? votes : ~votes;
+    }
+    return same;
 }
 
 __device__ __forceinline__ void count_run(const SortParams& p, int lo, int hi, int* counts) {
@@ -76,9 +88,12 @@ __global__ void __launch_bounds__(kThreads) k_token_places(const SortParams p) {
         const int part = buckets < kThreads ? static_cast<int>(threadIdx.x) / buckets : 0;
         if (part < parts) {
             for (int c = static_cast<int>(threadIdx.x) - part * buckets; c < buckets; c += kThreads) {
+                // every block from a row of its own on: all at the same rows would queue for them
                 int before = 0, all = 0;
+                const int rows = (p.blocks - part + parts - 1) / parts, from = static_cast<int>(blockIdx.x) % rows;
 #pragma unroll 16
-                for (int b = part; b < p.blocks; b += parts) {
+                for (int i = 0; i < rows; ++i) {
+                    const int b = part + (i + from < rows ? i + from : i + from - rows) * parts;
                     const int v = __ldcg(p.table + b * buckets + c);
                     all += v;
                     before += b < static_cast<int>(blockIdx.x) ? v : 0;
@@ -128,7 +143,8 @@ __global__ void __launch_bounds__(kThreads) k_token_places(const SortParams p) {
         uint16_t* const mine = seen + warp * buckets;
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
-            const unsigned same = __match_any_sync(0xffffffffu, b[r]);
+            if (first - lane + 32 * r >= hi) break;        // of the whole warp
+            const unsigned same = lanes_of(b[r], p.bits);
             const int before = __popc(same & ((1u << lane) - 1u));
             const int had = b[r] >= 0 ? mine[b[r]] : 0;
             rank[r] = had + before;
@@ -178,6 +194,8 @@ cudaError_t launch_token_sort(SortParams p, cudaStream_t s) {
     // 41 KB for 1024 experts
     const size_t smem = static_cast<size_t>(buckets) * 8 + (static_cast<size_t>(buckets) * kWarps * 2 + 3) / 4 * 4;
     p.blocks = token_sort_blocks(p.entries);
+    p.bits = 0;
+    while ((1 << p.bits) < buckets) ++p.bits;
     if (p.blocks == 0) {
         k_token_places<true><<<1, kThreads, smem, s>>>(p);
         return cudaGetLastError();
