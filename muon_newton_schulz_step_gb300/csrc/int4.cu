@@ -267,6 +267,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
             x[t] = static_cast<const char*>(p.x) + ((t0 + min(8 * t + r, tokens - 1)) * p.ld_x + 8 * j) * kSize;
     };
     const int whole = p.vec ? p.k / 128 : 0;               // units whose x loads as vectors
+    const char* const x_begin = static_cast<const char*>(p.x);
+    const char* const x_end = x_begin + ((p.tokens - 1) * p.ld_x + p.k) * kSize;
     constexpr int kHeld = S::kAheadX ? 4 : 1;              // steps whose x is in registers
     RawOfX<PARTS> raw[kHeld][NT];
     auto load = [&](int kb, int m0) {                      // kHeld steps of unit kb from m0 on
@@ -283,7 +285,11 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
         for (int m = 0; m < kHeld; ++m) {
             const int col = kb * 128 + 32 * (m0 + m);      // of lane 0
 #pragma unroll
-            for (int t = 0; t < NT; ++t) raw[m][t] = load_x_edge<PARTS>(x[t] + static_cast<long long>(col) * kSize, p.k - col - 8 * j);
+            for (int t = 0; t < NT; ++t) {
+                const char* at = x[t] + static_cast<long long>(col) * kSize;
+                raw[m][t] = S::kAheadX ? load_x_edge<PARTS>(at, p.k - col - 8 * j, x_begin, x_end)
+                                       : call_x_edge<PARTS>(at, p.k - col - 8 * j, x_begin, x_end);
+            }
         }
     };
     if (mine > 0) look();

@@ -71,25 +71,40 @@ __device__ __forceinline__ RawOfX<PARTS> load_x(const char* at) {
     return r;
 }
 
-// The same of elements that lie on no vector, or of which only `left` are there: zeros past them.
+// The same of elements that lie on no vector, or of which only `left` are there (zeros past them):
+// eight whole ones by the words around them, as far as those lie in x ([begin, end)).
 template <int PARTS>
-__device__ __noinline__ RawOfX<PARTS> load_x_edge(const char* at, int left) {
-    RawOfX<PARTS> r;
-    uint32_t w[8];
+__device__ __forceinline__ RawOfX<PARTS> load_x_edge(const char* at, int left, const char* begin, const char* end) {
+    constexpr int kWords = PARTS == 1 ? 4 : 8;
+    uint32_t w[kWords + 1] = {};
+    const int off = PARTS == 1 ? static_cast<int>(reinterpret_cast<uintptr_t>(at) & 2) : 0;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(at - off);
+    if (left >= 8 && at - off >= begin && at + 4 * kWords + off <= end) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = 0u;
-        if (i < left)
-            w[i] = PARTS == 1 ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i])
-                              : reinterpret_cast<const uint32_t*>(at)[i];
-    }
-    if constexpr (PARTS == 1) {
-        r.v[0] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+        for (int i = 0; i < kWords; ++i) w[i] = __ldg(q + i);
+        if (PARTS == 1) {
+            if (off != 0) w[kWords] = __ldg(q + kWords);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
+        }
     } else {
-        r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= left) continue;
+            if (PARTS == 1) w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i]) << (16 * (i & 1));
+            else w[i] = reinterpret_cast<const uint32_t*>(at)[i];
+        }
     }
+    RawOfX<PARTS> r;
+    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (PARTS != 1) r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
     return r;
+}
+
+// Apart from the kernel where its registers are few.
+template <int PARTS>
+__device__ __noinline__ RawOfX<PARTS> call_x_edge(const char* at, int left, const char* begin, const char* end) {
+    return load_x_edge<PARTS>(at, left, begin, end);
 }
 
 template <int PARTS>
