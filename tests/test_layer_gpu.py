@@ -287,3 +287,14 @@ def test_example_runs():
     r = subprocess.run([sys.executable, "examples/moe_layer_step.py", "--steps", "2", "--fused", "--serve"], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "4 bits" in r.stdout, r.stderr[-2000:]
+
+
+def test_results_where_torch_lacks_the_short_allocation(monkeypatch):
+    weights, chosen = routed(50, 12, 3)
+    h = torch.randn(50, 256, device=DEV).to(torch.bfloat16)
+    w4 = mg.muon_int4_quantize_weight(torch.randn(8, 128, 256, device=DEV), 64)
+    want = chain(h, weights, chosen, 8, 2, w4)
+    monkeypatch.setattr(mg, "_allocate", None)
+    got = chain(h, weights, chosen, 8, 2, w4)
+    same(got, want)
+    assert [t.stride() for t in got] == [t.stride() for t in want]
