@@ -5,10 +5,16 @@
 // taken as the sum of three bf16), products of 16 columns run on mma.sync with fp32 sums, and
 // a scale multiplies the sum over its columns, so nothing is rounded before the result.
 //
-// A weight code costs half an instruction to take out and half one to turn into bf16
-// (two at a time); a vector unit's product would cost another per code and token, a
-// matrix fragment of 16 rows x 8 tokens a sixteenth.  (tcgen05 has nothing to add: its
-// operands would take a trip through shared memory, and the tensor core idles either way.)
+// Bound by instructions: a lane's word of eight codes costs 11 to take out and turn into bf16 (two
+// codes at a time: shift, mask and offset in one three-way operation, subtraction); a unit of 32
+// rows x 128 columns is 16 words a lane, 176 instructions of 337 in all, and 16 products of 16 x 16 x
+// 8.  On the vector units each word and token would cost eight more.  (tcgen05 has nothing to add:
+// its operands would take a trip through shared memory, and the tensor core is 12 - 20 % busy.)
+// Device time, bf16 x: one token x 6144 x 6144 9.8 us (weights of 19.5 MB, 2.9 us at the rate of a
+// copy; 12.7 with loads through registers and no ring), 8 tokens 10.4, 64 tokens 33, 512 tokens 203;
+// 256 rows over 96 experts of 2048 x 6144 131 us, with scales of 32 columns 137 (534 MB read, 4.0
+// TB/s; issue slots 61 % busy).  fp32 x, three times the products and its split: 16.7 us for one
+// token.  Two warps to a row's reduction instead of eight: 131 and 135 us for the experts, not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -150,7 +156,7 @@ struct Unit {
 // Shared memory of two blocks per SM (three where RT is 1); sums of one or two items.
 template <int PARTS, int RT, int NT>
 struct Shape {
-    static constexpr int kStages = RT == 1 ? 6 : NT == 4 ? 3 : 4;
+    static constexpr int kStages = RT == 1 ? 6 : 4;
     static constexpr int kTurns = NT == 1 ? 2 : 1;
     static constexpr bool kAheadX = PARTS * NT <= 3;       // else registers do not last
     static constexpr size_t kRing = sizeof(Unit<RT>) * kStages * kWarps;
@@ -422,13 +428,16 @@ cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// Tokens of a tile by what a group has on average; two fragments of rows (x read once for both,
+// and half the epilogues) where 16-row items would go round the SMs more than twice.  6144 x 6144:
+// 16 tokens 13.5 us in a tile of 16, 17.1 in two of 8; 512 tokens 203 and 355 (207 in tiles of 32,
+// whose registers do not last); one token 9.8 us with 16 rows, 10.1 with 32; 256 rows over 96
+// experts 131 us with 32 rows, 188 with 16.
 template <int BLOCK, int PARTS>
 cudaError_t by_shape(const Int4Params& p, int sms, cudaStream_t s) {
-    const long long per = p.tokens / (p.groups < p.tokens ? p.groups : p.tokens);      // tokens of a group, on average
-    if (PARTS == 1 && per > 16) return run<BLOCK, PARTS, 2, PARTS == 1 ? 4 : 2>(p, sms, s);
+    const long long groups = p.groups < p.tokens ? p.groups : p.tokens, per = p.tokens / groups;
     if (per > 8) return run<BLOCK, PARTS, 2, 2>(p, sms, s);
-    const long long rows = static_cast<long long>(p.n) * (p.groups < p.tokens ? p.groups : p.tokens);
-    if (rows > 2 * 32ll * 2 * sms) return run<BLOCK, PARTS, 2, 1>(p, sms, s);
+    if (p.n * groups > 128ll * sms) return run<BLOCK, PARTS, 2, 1>(p, sms, s);
     return run<BLOCK, PARTS, 1, 1>(p, sms, s);
 }
 
