@@ -494,7 +494,8 @@ MUON_API int muon_swiglu_backward(const void* d, long long ld_d, const void* gat
  * numbers from -8 to 7 in two's complement, block 32, 64 or 128 columns.
  *   codes   batch x rows x up128(cols) / 2 bytes, the even column in a byte's low half,
  *           zeros past the last column; 16-byte aligned
- *   scale   batch x (up128(cols) / block) x rows, bf16
+ *   scale   batch x (up128(cols) / block) x rows, bf16; zero where a block lies past the
+ *           last column
  * Rounding of `batch` weights, rows x cols each, contiguous: scale = max|w| / 7 over a
  * block, to bf16; code = w / scale to the nearest whole number (ties to even), between -7 and 7.
  * A block with an infinity or a NaN gets the scale NaN; a scale that rounds to zero, zero codes.

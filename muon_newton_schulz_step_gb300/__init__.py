@@ -1154,8 +1154,8 @@ class Int4Matrix(NamedTuple):
     """A weight of 4 bits: w[n, k] = code[n, k] * scale[k // block, n], codes from -8 to 7.
 
     ``codes``: uint8, rows x (cols rounded up to 128) / 2, the even column in the low
-    half, zero past ``cols``; ``scale``: bf16, (cols rounded up to 128) / block x rows;
-    both optionally stacked over experts.  ``block``: 32, 64 or 128 columns."""
+    half, zero past ``cols``; ``scale``: bf16, (cols rounded up to 128) / block x rows, zero
+    for blocks past ``cols``; both optionally stacked over experts.  ``block``: 32, 64 or 128 columns."""
     codes: torch.Tensor
     scale: torch.Tensor
     block: int
