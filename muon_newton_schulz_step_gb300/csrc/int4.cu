@@ -5,16 +5,16 @@
 // taken as the sum of three bf16), products of 16 columns run on mma.sync with fp32 sums, and
 // a scale multiplies the sum over its columns, so nothing is rounded before the result.
 //
-// Bound by instructions: a lane's word of eight codes costs 11 to take out and turn into bf16 (two
-// codes at a time: shift, mask and offset in one three-way operation, subtraction); a unit of 32
-// rows x 128 columns is 16 words a lane, 176 instructions of 337 in all, and 16 products of 16 x 16 x
+// Bound by instructions: a lane's word of eight codes costs 9 to take out and turn into bf16 (two
+// codes at a time: mask and offset in one three-way operation, one fused multiply-add); a unit of 32
+// rows x 128 columns is 16 words a lane, 144 instructions of 307 in all, and 16 products of 16 x 16 x
 // 8.  On the vector units each word and token would cost eight more.  (tcgen05 has nothing to add:
 // its operands would take a trip through shared memory, and the tensor core is 12 - 20 % busy.)
-// Device time, bf16 x: one token x 6144 x 6144 9.8 us (weights of 19.5 MB, 2.9 us at the rate of a
-// copy; 12.7 with loads through registers and no ring), 8 tokens 10.4, 64 tokens 33, 512 tokens 203;
-// 256 rows over 96 experts of 2048 x 6144 131 us, with scales of 32 columns 137 (534 MB read, 4.0
-// TB/s; issue slots 61 % busy).  fp32 x, three times the products and its split: 16.7 us for one
-// token.  Two warps to a row's reduction instead of eight: 131 and 135 us for the experts, not kept.
+// Device time, bf16 x: one token x 6144 x 6144 9.5 us (weights of 19.5 MB, 2.9 us at the rate of a
+// copy; 12.7 with loads through registers and no ring), 8 tokens 10.2, 64 tokens 32, 512 tokens 196;
+// 256 rows over 96 experts of 2048 x 6144 124 us, with scales of 32 columns 130 (534 MB read, 4.1
+// TB/s).  fp32 x, three times the products and its split: 17 us for one token.  Two warps to a row's
+// reduction instead of eight gained 1 % for the experts, shifts by multiplication lost 10: not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -432,7 +432,7 @@ cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
 // and half the epilogues) where 16-row items would go round the SMs more than twice.  6144 x 6144:
 // 16 tokens 13.5 us in a tile of 16, 17.1 in two of 8; 512 tokens 203 and 355 (207 in tiles of 32,
 // whose registers do not last); one token 9.8 us with 16 rows, 10.1 with 32; 256 rows over 96
-// experts 131 us with 32 rows, 188 with 16.
+// experts 131 us with 32 rows, 188 with 16 (before the codes' last step, which took 3 - 6 % off).
 template <int BLOCK, int PARTS>
 cudaError_t by_shape(const Int4Params& p, int sms, cudaStream_t s) {
     const long long groups = p.groups < p.tokens ? p.groups : p.tokens, per = p.tokens / groups;

@@ -16,9 +16,12 @@ namespace muon {
 // columns they are is free, as long as both operands agree.
 
 // Eight codes as bf16, 2^-11 times their number: element i of pair p is column 4 i + p, exactly.
-// 0x3d80 | u is 2^-4 (1 + u / 128), and a code with its sign bit turned over is code + 8.  With
-// 2^-11 the sum of 128 products is at most half of the largest |x|, so no x overflows before its
-// scale has been applied; kCodeUnit, at the end, takes it back.
+// A code with its sign bit turned over is code + 8, and bf16's numbers from 0 to 255 smallest steps
+// (2^-133 each) are spaced evenly: four bits at either end of a byte are a number as they lie, and one
+// fused multiply-add brings them up and takes the 8 off.  With 2^-11 the sum of 128 products is at
+// most half of the largest |x|, so no x overflows before its scale has been applied; kCodeUnit, at the
+// end, takes it back.  Nine instructions for eight codes; eleven with a shift for each pair and
+// their offset as a larger number's last bits.
 constexpr float kCodeUnit = 2048.0f;
 
 struct EightCodes {
@@ -29,9 +32,13 @@ __device__ __forceinline__ EightCodes decode(uint32_t w) {
     EightCodes d;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
+        const bool up = p & 1;                             // the upper half of the bytes
         uint32_t u;                                        // (a & b) ^ c
-        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(w >> (4 * p)), "r"(0x000f000fu), "r"(0x3d883d88u));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d.pair[p]) : "r"(u), "r"(0x3d883d88u));
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;"
+            : "=r"(u)
+            : "r"(p < 2 ? w : w >> 8), "r"(up ? 0x00f000f0u : 0x000f000fu), "r"(up ? 0x00800080u : 0x00080008u));
+        // times 2^118 or 2^122, less 2^-8
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d.pair[p]) : "r"(u), "r"(up ? 0x7a807a80u : 0x7c807c80u), "r"(0xbb80bb80u));
     }
     return d;
 }
