@@ -112,8 +112,9 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     }
 }
 
-// N entries' rows are under way together, U runs of a lane from each: four entries of two runs,
-// or two of two where they are put together (six blocks of 2 x 1: 121 us for 4096 x 8 x 6143, 95).
+// N entries' rows are under way together, U runs of a lane from each: four entries of two runs, two
+// of four for the layers that choose one or two experts (16384 x 2 x 6144 136 us with 4 x 2, 97), or two
+// of two where they are put together (six blocks of 2 x 1: 121 us for 4096 x 8 x 6143, 95).
 template <typename T, int E, bool SHIFT, int N, int U>
 __device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, float weight, unsigned& left, int first,
                                          int head, int runs, Extent in, float (&acc)[U][E]) {
@@ -151,7 +152,7 @@ __device__ __forceinline__ void add_rows(const RowsParams& p, const Entries& e, 
 
 template <typename T, typename O, int E, bool SHIFT, int U>
 __global__ void __launch_bounds__(kThreads, SHIFT ? 4 : 3) k_combine(const RowsParams p) {
-    constexpr int kStep = SHIFT ? kShared : 32, kRows = SHIFT ? 2 : 4;
+    constexpr int kStep = SHIFT ? kShared : 32, kRows = SHIFT || U == 4 ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long token = item / p.parts;
@@ -167,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, SHIFT ? 4 : 3) k_combine(const RowsP
     float acc[U][E] = {};
     unsigned left = e.held;
     while (__popc(left) >= kRows) add_rows<T, E, SHIFT, kRows, U>(p, e, weight, left, first, head, runs, in, acc);
-    while (left != 0u) add_rows<T, E, SHIFT, 1, U>(p, e, weight, left, first, head, runs, in, acc);
+    if (kRows > 2 && __popc(left) >= 2) add_rows<T, E, SHIFT, 2, U>(p, e, weight, left, first, head, runs, in, acc);
+    if (left != 0u) add_rows<T, E, SHIFT, 1, U>(p, e, weight, left, first, head, runs, in, acc);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (first + kStep * u >= runs || lane >= kStep) break;
@@ -285,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_combine_backward(const RowsPara
     unsigned left = e.held;
     if (!SHIFT) {
         while (__popc(left) >= 4) backward_of<D, T, E, SHIFT, SHIFT ? 1 : 4, kU>(p, token, e, weight, left, part);
+        if (__popc(left) >= 2) backward_of<D, T, E, SHIFT, SHIFT ? 1 : 2, kU>(p, token, e, weight, left, part);
     }
-    while (left != 0u) backward_of<D, T, E, SHIFT, 1, kU>(p, token, e, weight, left, part);
+    while (left != 0u) backward_of<D, T, E, SHIFT, 1, kU == 2 ? 4 : 1>(p, token, e, weight, left, part);
     if (p.out != nullptr) {                            // rows of no expert
         const unsigned rest = __ballot_sync(0xffffffffu, e.place >= 0 && e.place < p.rows) & ~e.held;
         for (left = rest; left != 0u; left &= left - 1u) {
@@ -334,6 +337,11 @@ cudaError_t dispatch(RowsParams p, cudaStream_t s) {
 template <typename T, typename O, bool SHIFT>
 cudaError_t combine(RowsParams p, cudaStream_t s) {
     constexpr int E = run_of<T, O>(), kU = sizeof(T) * E > 16 ? 1 : 2;
+    if (kU == 2 && !SHIFT && p.top_k <= 2) {
+        const unsigned grid = warp_items<E, 4>(p);
+        k_combine<T, O, E, false, 4><<<grid, kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
     const unsigned grid = warp_items<E, kU, SHIFT ? kShared : 32>(p);
     k_combine<T, O, E, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
