@@ -1006,19 +1006,12 @@ def _plain(t, dtype):
     return t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.get_device() == _current_device()
 
 
-def _check_plan(plan, tokens=None):
+def _check_plan(plan):
     """(tokens, top_k, experts, addresses of places and offsets) of a plan, whose tensors are checked."""
     if not isinstance(plan, TokenPlan):
         raise ValueError("plan must be a TokenPlan, as muon_sort_tokens makes it")
     _, place, offsets = plan
-    try:
-        (t, top_k), (n,) = place.shape, offsets.shape
-        if top_k >= 1 and n >= 2 and (tokens is None or t == tokens) and _plain(place, torch.int32) \
-                and _plain(offsets, torch.int32):
-            return t, top_k, n - 1, place.data_ptr(), offsets.data_ptr()
-    except (AttributeError, TypeError, ValueError):
-        pass
-    t, top_k, _ = _check_rows("plan.place", place, (torch.int32,), tokens)      # says what is wrong
+    tokens, top_k, _ = _check_rows("plan.place", place, (torch.int32,))
     if not place.is_contiguous():
         raise ValueError("plan.place must be contiguous")
     if top_k < 1:
@@ -1027,7 +1020,39 @@ def _check_plan(plan, tokens=None):
         raise ValueError("plan.offsets must be a 1-D int32 CUDA tensor of experts + 1 entries")
     n = offsets.numel()
     _check_vector("plan.offsets", offsets, torch.int32, n)
-    return t, top_k, n - 1, place.data_ptr(), offsets.data_ptr()
+    return tokens, top_k, n - 1, place.data_ptr(), offsets.data_ptr()
+
+
+def _check_weights(weights, tokens, top_k):
+    if weights is None:
+        return None
+    _check_rows("weights", weights, (torch.float32,), tokens, top_k)
+    if not weights.is_contiguous():
+        raise ValueError("weights must be contiguous")
+    return weights.data_ptr()
+
+
+def _planned(plan, name, t, sorted_rows, weights=None):
+    """(tokens, top_k, cols, row stride, type code, experts, addresses of places, offsets and weights)
+    of a plan with the tokens' rows ``t``, or their entries' (``sorted_rows``), and weights."""
+    try:
+        _, place, offsets = plan
+        (tokens, top_k), (n,), (rows, cols), (ld, inner) = place.shape, offsets.shape, t.shape, t.stride()
+        here = t.get_device()
+        if type(plan) is TokenPlan and inner == 1 and ld >= cols and rows == (tokens * top_k if sorted_rows else tokens) \
+                and n >= 2 and top_k >= 1 and place.dtype is torch.int32 and offsets.dtype is torch.int32 \
+                and place.is_contiguous() and offsets.is_contiguous() and here >= 0 and place.get_device() == here \
+                and offsets.get_device() == here == _current_device() \
+                and (weights is None or (weights.dtype is torch.float32 and weights.shape == place.shape
+                                         and weights.is_contiguous() and weights.get_device() == here)):
+            return (tokens, top_k, cols, ld, _FLOAT_CODE[t.dtype], n - 1, place.data_ptr(), offsets.data_ptr(),
+                    None if weights is None else weights.data_ptr())
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
+    # one by one: says what is wrong, or takes a form seldom met
+    tokens, top_k, experts, at_place, at_offsets = _check_plan(plan)
+    _, cols, ld, code = _matrix(name, t, tokens * top_k if sorted_rows else tokens)
+    return tokens, top_k, cols, ld, code, experts, at_place, at_offsets, _check_weights(weights, tokens, top_k)
 
 
 def muon_dispatch_tokens(x, plan: TokenPlan, stream=None) -> torch.Tensor:
@@ -1037,27 +1062,12 @@ def muon_dispatch_tokens(x, plan: TokenPlan, stream=None) -> torch.Tensor:
     if stream is not None:
         with _on(stream):
             return muon_dispatch_tokens(x, plan)
-    tokens, cols, ld, code = _matrix("x", x)
-    _, top_k, experts, place, offsets = _check_plan(plan, tokens)
+    tokens, top_k, cols, ld, code, experts, place, offsets, _ = _planned(plan, "x", x, False)
     out = _new_rows(tokens * top_k, cols, x.dtype)
     if cols:
         _check(lib().muon_dispatch_tokens(x.data_ptr(), code, tokens, cols, ld, top_k, place, offsets, experts,
                                           out.data_ptr(), cols, _handle(None)))
     return out
-
-
-def _check_weights(weights, tokens, top_k):
-    if weights is None:
-        return None
-    try:
-        if weights.shape == (tokens, top_k) and _plain(weights, torch.float32):
-            return weights.data_ptr()
-    except AttributeError:
-        pass
-    _check_rows("weights", weights, (torch.float32,), tokens, top_k)
-    if not weights.is_contiguous():
-        raise ValueError("weights must be contiguous")
-    return weights.data_ptr()
 
 
 def muon_combine_tokens(y, plan: TokenPlan, weights=None, *, out_dtype=None, stream=None) -> torch.Tensor:
@@ -1068,9 +1078,7 @@ def muon_combine_tokens(y, plan: TokenPlan, weights=None, *, out_dtype=None, str
     if stream is not None:
         with _on(stream):
             return muon_combine_tokens(y, plan, weights, out_dtype=out_dtype)
-    tokens, top_k, experts, place, offsets = _check_plan(plan)
-    _, cols, ld, code = _matrix("y", y, tokens * top_k)
-    wptr = _check_weights(weights, tokens, top_k)
+    tokens, top_k, cols, ld, code, experts, place, offsets, wptr = _planned(plan, "y", y, True, weights)
     if out_dtype is None:
         out_dtype = y.dtype
     elif out_dtype not in _FLOATS:
@@ -1091,11 +1099,9 @@ def muon_combine_tokens_backward(d, y, plan: TokenPlan, weights=None, *, need_dy
     if stream is not None:
         with _on(stream):
             return muon_combine_tokens_backward(d, y, plan, weights, need_dy=need_dy, need_dw=need_dw)
-    tokens, top_k, experts, place, offsets = _check_plan(plan)
-    _, cols, ld_d, d_code = _matrix("d", d, tokens)
-    rows, _, ld_y, code = _matrix("y", y, tokens * top_k, cols)
-    wptr = _check_weights(weights, tokens, top_k)
-    dy = _new_rows(rows, cols, y.dtype) if need_dy else None
+    tokens, top_k, cols, ld_y, code, experts, place, offsets, wptr = _planned(plan, "y", y, True, weights)
+    _, _, ld_d, d_code = _matrix("d", d, tokens, cols)
+    dy = _new_rows(tokens * top_k, cols, y.dtype) if need_dy else None
     dw = _new_rows(tokens, top_k, torch.float32) if need_dw and weights is not None else None
     if cols:
         _check(lib().muon_combine_tokens_backward(
@@ -1107,6 +1113,14 @@ def muon_combine_tokens_backward(d, y, plan: TokenPlan, weights=None, *, need_dy
 
 
 def _check_gated(gate, up):
+    try:
+        code, here, (rows, cols), (ld_gate, inner), (ld_up, inner_up) = \
+            _FLOAT_CODE[gate.dtype], gate.get_device(), gate.shape, gate.stride(), up.stride()
+        if up.dtype is gate.dtype and up.shape == gate.shape and inner == inner_up == 1 and ld_gate >= cols \
+                and ld_up >= cols and here >= 0 and up.get_device() == here == _current_device():
+            return rows, cols, ld_gate, ld_up, code
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
     rows, cols, ld_gate, code = _matrix("gate", gate)
     _, _, ld_up, up_code = _matrix("up", up, rows, cols)
     if up_code != code:
@@ -1194,9 +1208,16 @@ def _check_int4(w, offsets):
     if stacked != (offsets is not None):
         raise ValueError("a stacked weight goes with offsets, a single one without")
     n, up = shape[-2], _up128(k)
+    here, want = codes.get_device(), ((shape[0], up // block, n) if stacked else (up // block, n))
+    if shape[-1] == up // 2 and scale.shape == want and codes.dtype is torch.uint8 and scale.dtype is torch.bfloat16 \
+            and codes.is_contiguous() and scale.is_contiguous() and here >= 0 \
+            and scale.get_device() == here == _current_device():
+        if not stacked:
+            return n, k, 1, None
+        return n, k, *_check_offsets(offsets, shape[0])
+    # one by one: says what is wrong
     if shape[-1] != up // 2 or codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous():
         raise ValueError(f"the weight's codes must be a contiguous CUDA tensor of {torch.uint8} with rows of {up // 2}")
-    want = (shape[0], up // block, n) if stacked else (up // block, n)
     if scale.shape != want or scale.dtype != torch.bfloat16 or not scale.is_cuda or not scale.is_contiguous():
         raise ValueError(f"the weight's scale must be a contiguous CUDA tensor of {torch.bfloat16} with shape {want}")
     _here("the weight's codes", codes)
