@@ -4,8 +4,7 @@
 //   d_gate = d up s (1 + gate (1 - s)),  d_up = d gate s
 //
 // Bound by memory: 3 and 5 elements move for each one of the result; the gradient of 65536 x
-// 2048 in bf16 takes 190 us (1.34 GB, 7.0 TB/s), the forward of half as many in fp32 115 (7.0).
-// A thread takes
+// 2048 in bf16 takes 191 us (1.34 GB, 7.0 TB/s), the forward 114 (0.81 GB, 7.1).  A thread takes
 // U runs of up to 16 bytes, kThreads apart, all loaded before the first is used.
 // Operands that lie row behind row are taken as one long row, so that odd widths
 // cost no narrow loads; gate and up as the halves of one product have rows of their
@@ -151,28 +150,25 @@ cudaError_t in_parts(SwigluParams p, int size, int u, F&& launch) {
     return cudaSuccess;
 }
 
+// Runs of a thread: one of 16 bytes, two narrower ones.  Forward of 65536 x 2048 in bf16: 114 us with
+// one, 128 with two, 183 with four, whose registers leave few warps; of 65536 x 2046 as halves of one
+// product (4-byte runs) 223, 151 and 177.
 template <typename T, int V>
 cudaError_t run(const SwigluParams& p, cudaStream_t s) {
-    constexpr int kFew = sizeof(T) * V > 16 ? 1 : 2;
-    if (p.d == nullptr)
-        return in_parts<V>(p, sizeof(T), 2 * kFew, [&](const SwigluParams& q, unsigned grid) {
-            k_swiglu<T, V, 2 * kFew><<<grid, kThreads, 0, s>>>(q);
-            return cudaGetLastError();
-        });
-    return in_parts<V>(p, sizeof(T), kFew, [&](const SwigluParams& q, unsigned grid) {
-        k_swiglu_backward<T, V, kFew><<<grid, kThreads, 0, s>>>(q);
+    constexpr int kRuns = sizeof(T) * V >= 16 ? 1 : 2;
+    return in_parts<V>(p, sizeof(T), kRuns, [&](const SwigluParams& q, unsigned grid) {
+        if (q.d == nullptr) k_swiglu<T, V, kRuns><<<grid, kThreads, 0, s>>>(q);
+        else k_swiglu_backward<T, V, kRuns><<<grid, kThreads, 0, s>>>(q);
         return cudaGetLastError();
     });
 }
 
 template <typename T>
 cudaError_t by_width(const SwigluParams& p, int v, cudaStream_t s) {
-    switch (v) {
-        case 8: return run<T, 8>(p, s);
-        case 4: return run<T, 4>(p, s);
-        case 2: return run<T, 2>(p, s);
-        default: return run<T, 1>(p, s);
+    if constexpr (sizeof(T) == 2) {
+        if (v == 8) return run<T, 8>(p, s);
     }
+    return v == 4 ? run<T, 4>(p, s) : v == 2 ? run<T, 2>(p, s) : run<T, 1>(p, s);
 }
 
 }  // namespace
@@ -194,7 +190,8 @@ cudaError_t launch_swiglu(SwigluParams p, cudaStream_t s) {
         p.rest = static_cast<int>(p.cols % 8);
         p.cols -= p.rest;
     }
-    RunWidth w(p.cols > 0 ? p.cols : 8);
+    // 16 bytes at most: a warp's vectors then lie side by side (fp32 in runs of 32 bytes: 4.4 TB/s backward)
+    RunWidth w(p.cols > 0 ? p.cols : 8, 16 / size);
     for (const Array& a : arrays)
         if (a.p != nullptr) w.array(a.p, p.rows == 1 ? w.v : a.ld, size);
     return p.bf16 ? by_width<__nv_bfloat16>(p, w.v, s) : by_width<float>(p, w.v, s);

@@ -25,7 +25,7 @@
 // Rows are worked off in runs of elements that lie on 16 bytes of the row that is
 // written; where the rows that are read lie otherwise (odd widths, views), their runs are
 // put together from the 16-byte vectors around them (SHIFT), and the ends of a row go one
-// by one.  4096 tokens x 8 x 6143 in bf16 against 6144: dispatch 82 us and 70, combine 95 and
+// by one.  4096 tokens x 8 x 6143 in bf16 against 6144: dispatch 81 us and 69, combine 94 and
 // 65, backward 208 and 130.  (Element by element: 93, 133 and 484.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,7 +62,8 @@ __device__ __forceinline__ Entries entries_of(const RowsParams& p, long long tok
     return e;
 }
 
-// A warp takes U x 32 runs of one token's row.
+// A warp takes U x 32 runs of one token's row.  4096 x 8 x 6144 and 6143 in bf16: 68.2 and 95 us with one,
+// 68.6 and 81 with two, 70.0 and 82 with four.
 template <typename T, int E, bool SHIFT, int U>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const RowsParams p) {
     const int lane = threadIdx.x & 31;
@@ -329,8 +330,8 @@ constexpr int run_of() {
 template <typename T, bool SHIFT>
 cudaError_t dispatch(RowsParams p, cudaStream_t s) {
     constexpr int E = run_of<T, T>();
-    const unsigned grid = warp_items<E, 4>(p);
-    k_dispatch<T, E, SHIFT, 4><<<grid, kThreads, 0, s>>>(p);
+    const unsigned grid = warp_items<E, 2>(p);
+    k_dispatch<T, E, SHIFT, 2><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

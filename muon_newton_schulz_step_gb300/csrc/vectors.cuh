@@ -56,11 +56,11 @@ __device__ __forceinline__ float from_float<float>(float v) {
     return v;
 }
 
-// The widest run that every access of a call allows: `cols` in a row, row strides
-// and addresses in elements of `size` bytes.
+// The widest run, of at most `most` elements, that every access of a call allows: `cols` in a
+// row, row strides and addresses in elements of `size` bytes.
 struct RunWidth {
     int v;
-    explicit RunWidth(long long cols) : v(8) { fit(cols); }
+    RunWidth(long long cols, int most) : v(most) { fit(cols); }
     void fit(long long n) {
         while (v > 1 && n % v != 0) v >>= 1;
     }
