@@ -10,10 +10,11 @@
 // rows x 128 columns is 16 words a lane, 144 instructions of 307 in all, and 16 products of 16 x 16 x
 // 8.  On the vector units each word and token would cost eight more.  (tcgen05 has nothing to add:
 // its operands would take a trip through shared memory, and the tensor core is 12 - 20 % busy.)
-// Device time, bf16 x: one token x 6144 x 6144 9.5 us (weights of 19.5 MB, 2.9 us at the rate of a
-// copy; 12.7 with loads through registers and no ring), 8 tokens 10.2, 64 tokens 32, 512 tokens 196;
-// 256 rows over 96 experts of 2048 x 6144 124 us, with scales of 32 columns 130 (534 MB read, 4.1
-// TB/s).  fp32 x, three times the products and its split: 17 us for one token.  Two warps to a row's
+// Device time, bf16 x: one token x 6144 x 6144 8.4 us (weights of 19.5 MB, 2.9 us at the rate of a
+// copy; 9.1 from memory; 12.7 with loads through registers and no ring), 8 tokens 9.0, 64 tokens 32,
+// 512 tokens 195; 256 rows over 96 experts of 2048 x 6144 122 us, with scales of 32 columns 129 (534 MB
+// read, 4.1 TB/s; the copies alone, without products, take 99 and 104).  fp32 x, three times the
+// products and its split: 16 us for one token.  Two warps to a row's
 // reduction instead of eight gained 1 % for the experts, shifts by multiplication lost 10: not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -153,10 +154,13 @@ struct Unit {
     uint32_t scale[RT * 8][4];                             // bf16 pairs of a pair of rows, the unit's scales
 };
 
-// Shared memory of two blocks per SM (three where RT is 1); sums of one or two items.
+// Units under way and the sums of one or two items.  Two blocks per SM, three where RT is 1 (by
+// registers).  With six units (RT 1) the start of a block costs more than it gains, one token x 6144
+// x 6144 9.5 us against 8.4 with three and 8.1 with two (10.1, 9.1 and 9.1 with the weight from
+// memory; a third as many rows 6.6, 6.0 and 6.9).
 template <int PARTS, int RT, int NT>
 struct Shape {
-    static constexpr int kStages = RT == 1 ? 6 : 4;
+    static constexpr int kStages = 3;
     static constexpr int kTurns = NT == 1 ? 2 : 1;
     static constexpr bool kAheadX = PARTS * NT <= 3;       // else registers do not last
     static constexpr size_t kRing = sizeof(Unit<RT>) * kStages * kWarps;
@@ -432,7 +436,7 @@ cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
 // and half the epilogues) where 16-row items would go round the SMs more than twice.  6144 x 6144:
 // 16 tokens 13.5 us in a tile of 16, 17.1 in two of 8; 512 tokens 203 and 355 (207 in tiles of 32,
 // whose registers do not last); one token 9.8 us with 16 rows, 10.1 with 32; 256 rows over 96
-// experts 131 us with 32 rows, 188 with 16 (before the codes' last step, which took 3 - 6 % off).
+// experts 131 us with 32 rows, 188 with 16 (before the last steps, which took 3 - 14 % off).
 template <int BLOCK, int PARTS>
 cudaError_t by_shape(const Int4Params& p, int sms, cudaStream_t s) {
     const long long groups = p.groups < p.tokens ? p.groups : p.tokens, per = p.tokens / groups;
