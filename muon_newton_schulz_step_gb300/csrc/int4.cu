@@ -419,6 +419,12 @@ __global__ void __launch_bounds__(kThreads, RT == 1 && PARTS == 1 ? 3 : 2) k_int
     if (p.offsets != nullptr) zero_rest(p, table);
 }
 
+// Blocks that the SMs hold at once.
+template <int PARTS, int RT>
+long long resident(int sms) {
+    return (RT == 1 && PARTS == 1 ? 3ll : 2ll) * sms;
+}
+
 template <int BLOCK, int PARTS, int RT, int NT>
 cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
     const auto kernel = k_int4_linear<BLOCK, PARTS, RT, NT>;
@@ -427,21 +433,21 @@ cudaError_t run(const Int4Params& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const long long tiles = p.offsets == nullptr ? (p.tokens + 8 * NT - 1) / (8 * NT)
                                                  : p.tokens / (8 * NT) + (p.groups < p.tokens ? p.groups : p.tokens);
-    const long long items = tiles * ((p.n + 16 * RT - 1) / (16 * RT)), most = (RT == 1 && PARTS == 1 ? 3ll : 2ll) * sms;
+    const long long items = tiles * ((p.n + 16 * RT - 1) / (16 * RT)), most = resident<PARTS, RT>(sms);
     kernel<<<static_cast<unsigned>(items < most ? items : most), kThreads, Shape<PARTS, RT, NT>::kRing, s>>>(p);
     return cudaGetLastError();
 }
 
 // Tokens of a tile by what a group has on average; two fragments of rows (x read once for both,
-// and half the epilogues) where 16-row items would go round the SMs more than twice.  6144 x 6144:
-// 16 tokens 13.5 us in a tile of 16, 17.1 in two of 8; 512 tokens 203 and 355 (207 in tiles of 32,
-// whose registers do not last); one token 9.8 us with 16 rows, 10.1 with 32; 256 rows over 96
-// experts 131 us with 32 rows, 188 with 16 (before the last steps, which took 3 - 14 % off).
+// and half the epilogues) unless items of one fit on the SMs at once.  6144 x 6144: 16 tokens 13.5 us
+// in a tile of 16, 17.1 in two of 8; 512 tokens 203 and 355 (207 in tiles of 32, whose registers do
+// not last).  One fragment and two, rows of k = 6144: 2048 4.6 us and 5.9, 6144 8.6 and 9.2, 8192 10.3
+// and 9.2, 12288 14.6 and 12.2; 8 experts of 2048 with a row each 17.5 and 16.4, 30 of them 56 and 46.
 template <int BLOCK, int PARTS>
 cudaError_t by_shape(const Int4Params& p, int sms, cudaStream_t s) {
-    const long long groups = p.groups < p.tokens ? p.groups : p.tokens, per = p.tokens / groups;
-    if (per > 8) return run<BLOCK, PARTS, 2, 2>(p, sms, s);
-    if (p.n * groups > 128ll * sms) return run<BLOCK, PARTS, 2, 1>(p, sms, s);
+    const long long groups = p.groups < p.tokens ? p.groups : p.tokens;
+    if (p.tokens / groups > 8) return run<BLOCK, PARTS, 2, 2>(p, sms, s);
+    if (groups * ((p.n + 15) / 16) > resident<PARTS, 1>(sms)) return run<BLOCK, PARTS, 2, 1>(p, sms, s);
     return run<BLOCK, PARTS, 1, 1>(p, sms, s);
 }
 
