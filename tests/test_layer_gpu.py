@@ -298,3 +298,18 @@ def test_results_where_torch_lacks_the_short_allocation(monkeypatch):
     got = chain(h, weights, chosen, 8, 2, w4)
     same(got, want)
     assert [t.stride() for t in got] == [t.stride() for t in want]
+
+
+def test_profile_names_the_kernels():
+    weights, chosen = routed(50, 12, 3)
+    h = torch.randn(50, 256, device=DEV).to(torch.bfloat16)
+    mg.muon_profile_enable(True)
+    try:
+        chain(h, weights, chosen, 8, 2, mg.muon_int4_quantize_weight(torch.randn(8, 128, 256, device=DEV), 64))
+        torch.cuda.synchronize()
+        seen = {k["name"]: k["launches"] for k in mg.muon_profile_read()}
+    finally:
+        mg.muon_profile_enable(False)
+    for name in ("token_sort", "dispatch", "combine", "combine_backward", "swiglu", "swiglu_backward", "int4_quantize",
+                 "int4_linear"):
+        assert seen[name] == 1, (name, seen)
