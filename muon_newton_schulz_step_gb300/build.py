@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libmuon_gb300.so")
 SOURCES = ["ns_gemm_pair.cu", "ns_small.cu", "elementwise.cu", "muon_abi.cu", "muon_static.cu", "muon_offload.cu", "adamw.cu", "guard.cu",
            "grad_norm.cu", "route.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_token.cu", "train_abi.cu",
            "token_sort.cu", "token_rows.cu", "swiglu.cu", "int4.cu", "layer_abi.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "groups.cuh", "fp8_codes.cuh", "abi_checks.h", "vectors.cuh", "row_runs.cuh", "int4.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "groups.cuh", "fp8_codes.cuh", "abi_checks.h", "vectors.cuh", "row_runs.cuh", "int4.cuh",
+           "sort_split.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

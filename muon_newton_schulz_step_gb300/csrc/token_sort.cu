@@ -9,8 +9,8 @@
 // 2048 entries at a time, a warp 128 in a row, four times 32: lanes of one bucket
 // find each other by votes, and the count of those before is their rank in the
 // warp; a column sum over the warps' counts turns it into the rank in the block.
-// Up to kAlone entries one block does it all; past that the first of two launches
-// leaves each block's counts (at most kMaxBlocks, each of an equal run of entries),
+// Up to kSortAlone entries one block does it all; past that the first of two launches
+// leaves each block's counts (at most kSortMaxBlocks, each of an equal run of entries),
 // and every block of the second adds the table up for itself, which reads
 // 128 x (experts + 1) counts from L2 and saves a launch and a chain of waits between
 // blocks.  The second launch's set-up overlaps the first.  Device time: one token's 8 entries
@@ -20,16 +20,15 @@
 
 #include "groups.cuh"
 #include "internal.h"
+#include "sort_split.h"
 
 namespace muon {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = kSortThreads;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRounds = 4;                         // entries of a lane at a time
-constexpr int kChunk = kThreads * kRounds;
-constexpr int kMaxBlocks = 128;
-constexpr int kAlone = 2 * kChunk;                 // most entries for one block
+constexpr int kRounds = kSortRounds;
+constexpr int kChunk = kSortChunk;
 
 __device__ __forceinline__ int bucket_of(const SortParams& p, int expert) {
     // as unsigned numbers: what lies below `first` wraps to the far end
@@ -85,13 +84,13 @@ __global__ void __launch_bounds__(kThreads) k_token_places(const SortParams p) {
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         // columns of the table to consecutive threads, its rows to as many parts as there is room for
-        const int parts = buckets < kThreads ? kThreads / buckets : 1;
+        const int parts = sort_parts(p.blocks, buckets);
         const int part = buckets < kThreads ? static_cast<int>(threadIdx.x) / buckets : 0;
         if (part < parts) {
             for (int c = static_cast<int>(threadIdx.x) - part * buckets; c < buckets; c += kThreads) {
                 // every block from a row of its own on: all at the same rows would queue for them
                 int before = 0, all = 0;
-                const int rows = (p.blocks - part + parts - 1) / parts, from = static_cast<int>(blockIdx.x) % rows;
+                const int rows = sort_part_rows(p.blocks, parts, part), from = static_cast<int>(blockIdx.x) % rows;
 #pragma unroll 16
                 for (int i = 0; i < rows; ++i) {
                     const int b = part + (i + from < rows ? i + from : i + from - rows) * parts;
@@ -183,12 +182,7 @@ __global__ void __launch_bounds__(kThreads) k_token_places(const SortParams p) {
 
 }  // namespace
 
-// Blocks of the two launches; 0: one block does it all, without a table.
-int token_sort_blocks(long long entries) {
-    if (entries <= kAlone) return 0;
-    const long long n = (entries + kChunk - 1) / kChunk;
-    return static_cast<int>(n < kMaxBlocks ? n : kMaxBlocks);
-}
+int token_sort_blocks(long long entries) { return sort_blocks(entries); }
 
 cudaError_t launch_token_sort(SortParams p, cudaStream_t s) {
     const int buckets = p.experts + 1;
