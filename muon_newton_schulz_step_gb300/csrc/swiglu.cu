@@ -10,11 +10,15 @@
 // cost no narrow loads; gate and up as the halves of one product have rows of their
 // own, found by one multiplication (no division) from the run's number.
 //
-// In fp32: exp(-gate) is ex2 of the scaled argument, whose rounding costs |gate| 2^-24
-// of the result's relative error (2^-20 at |gate| = 16, beyond which s is 1 or the
-// result below 2e-6 of up), and the quotient rcp's 1 unit: far below half a step of
-// bf16, and within 1e-6 of the 64-bit result in fp32.  gate = -inf gives NaN, as its
-// product -inf * 0 does.
+// Sums, quotients and products are fp32 in both types.  fp32 operands take the exponential in full and
+// an exact division: out is off by 5 units of 2^-24 of its value (the exponential 2, the sum, the quotient
+// and the product one each), what gate / (1 + exp(-gate)) * up in fp32 is.  bf16 takes the fast
+// exponential (off by 2 + 1.173 |gate| units of 2^-23 by its documentation, 2^-16 at |gate| = 80) and
+// the fast quotient (2 units): far below half a step of bf16, 2^-8.  In full they cost fp32 nothing where rows
+// load in 16 bytes (28042 x 916 45.4 and 74.9 us, as with the fast ones; 65536 x 2048 229 and 382), and 58 us for 54
+// where they go by single elements (28042 x 915, halves of one product; gradient 82 for 79).  Both lose what lies below their
+// exponents: fp32 gives 0 below gate = -88.7, where exp(-gate) is infinite, bf16 below -87.3, where the fast
+// quotient is 0; there the result is below 2^-119 of up.  gate = -inf gives NaN, as its product -inf * 0 does.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,7 +30,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// y / (1 + exp(-g))
+template <typename T>
+__device__ __forceinline__ float over(float y, float g) {
+    if constexpr (sizeof(T) == 4) return __fdiv_rn(y, 1.0f + expf(-g));
+    else return __fdividef(y, 1.0f + __expf(-g));
+}
 
 // Row and first column of run i: i / runs by the multiplier 2^64 / runs + 1, exact for i < 2^32.
 struct Spot {
@@ -45,7 +54,7 @@ __device__ __forceinline__ Run<T, V> forward(const Run<T, V>& g, const Run<T, V>
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float x = as_float(g.v[i]);
-        o.v[i] = from_float<T>(x * sigmoid(x) * as_float(u.v[i]));
+        o.v[i] = from_float<T>(over<T>(x, x) * as_float(u.v[i]));
     }
     return o;
 }
@@ -55,7 +64,7 @@ __device__ __forceinline__ void backward(const Run<T, V>& g, const Run<T, V>& u,
                                          Run<T, V>& du) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float x = as_float(g.v[i]), y = as_float(d.v[i]), s = sigmoid(x);
+        const float x = as_float(g.v[i]), y = as_float(d.v[i]), s = over<T>(1.0f, x);
         dg.v[i] = from_float<T>(y * as_float(u.v[i]) * (s * fmaf(x, 1.0f - s, 1.0f)));
         du.v[i] = from_float<T>(y * (x * s));
     }
