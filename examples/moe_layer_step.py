@@ -41,6 +41,7 @@ class MoeLayer:
         self.momentum = [torch.zeros_like(w.weight, dtype=torch.float32) for w in self.layers]
         self.adam = [torch.zeros_like(self.router), torch.zeros_like(self.router)]
         self.steps = 0
+        self.kept = {}                               # weights of 4 bits by block, where it serves
 
     def __call__(self, h):
         """h: tokens x hidden in bf16; (output, tokens of each expert)."""
@@ -76,15 +77,22 @@ class MoeLayer:
             w.update()
             w.weight.grad = None
         self.router.grad = None
+        for gate_up, down in self.kept.values():
+            gate_up.update(self.gate_and_up())
+            down.update(self.down.weight)
         return norm
+
+    def gate_and_up(self):
+        return torch.cat([self.gate.weight, self.up.weight], 1)          # one product makes gate and up
 
     @torch.no_grad()
     def serve(self, h, block=64):
-        """The layer's output for a few tokens, on weights of 4 bits (kept from the first call on)."""
-        if not hasattr(self, "served"):
-            both = torch.cat([self.gate.weight, self.up.weight], 1)      # one product makes gate and up
-            self.served = experts.Int4Linear(both, block), experts.Int4Linear(self.down.weight, block)
-        gate_up, down = self.served
+        """The layer's output for a few tokens, on weights of 4 bits with scales of ``block`` columns, made by the
+        first call with it and anew by each step."""
+        if block not in self.kept:
+            self.kept[block] = (experts.Int4Linear(self.gate_and_up(), block),
+                                experts.Int4Linear(self.down.weight, block))
+        gate_up, down = self.served = self.kept[block]
         weights, chosen, _ = mg.muon_route(h.float() @ self.router.t(), self.top_k, bias=self.bias, score="sigmoid",
                                            groups=self.groups, top_groups=self.top_groups)
         plan = experts.plan_tokens(chosen, self.bias.numel())

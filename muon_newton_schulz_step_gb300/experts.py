@@ -198,11 +198,20 @@ class Fp8Linear:
 class Int4Linear:
     """A weight (out x in, or stacked over experts) in 4 bits, for serving: ``layer(x,
     offsets)`` is x W^T in x's type.  There are no gradients: neither for the weight, of which
-    the codes alone are kept, nor for x."""
+    the codes alone are kept, nor for x.  ``layer.update(weight)`` puts another weight of the
+    shape in its place, in the memory that is there: graphs captured of the layer go on with it."""
 
     def __init__(self, weight, block=128):
         with torch.no_grad():
             self.codes = muon_int4_quantize_weight(weight.detach(), block)
+
+    @torch.no_grad()
+    def update(self, weight):
+        new = muon_int4_quantize_weight(weight.detach(), self.codes.block)
+        if new.cols != self.codes.cols or new.codes.shape != self.codes.codes.shape:
+            raise ValueError("the weight must be of the shape that the layer was made with")
+        self.codes.codes.copy_(new.codes)
+        self.codes.scale.copy_(new.scale)
 
     def __call__(self, x, offsets=None):
         if torch.is_grad_enabled() and x.requires_grad:
