@@ -931,8 +931,30 @@ def muon_fp8_linear_backward(dy, x, w, *, offsets=None, need_dx: bool = True, ne
 
 # ----------------------------------- between an expert layer's routing and its result --
 # torch.empty costs a call of a few microseconds as much again (4 us of 9, measured on a
-# GB300's host between launches); the allocation alone, on the current device, 0.9.
-_allocate = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+# GB300's host between launches); the allocation alone, on the current device, 0.9.  It is
+# not of torch's public interface: the first use tries it, and where it is not there or
+# gives anything else, results come from torch.empty.  (They are written whole, so that
+# what torch.empty may fill them with never shows.)
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _allocates(f):
+    """Whether ``f(sizes, strides, dtype)`` makes such a tensor on the current device."""
+    try:
+        t = f((2, 3), (3, 1), torch.bfloat16)
+        return t.is_cuda and t.get_device() == _current_device() and t.dtype is torch.bfloat16 \
+            and tuple(t.shape) == (2, 3) and t.stride() == (3, 1)
+    except Exception:
+        return False
+
+
+def _first_allocation(sizes, strides, dtype):
+    global _allocate
+    _allocate = _empty_strided if _allocates(_empty_strided) else None
+    return torch.empty(sizes, dtype=dtype, device="cuda") if _allocate is None else _allocate(sizes, strides, dtype)
+
+
+_allocate = _first_allocation
 
 
 def _new_rows(rows, cols, dtype):
