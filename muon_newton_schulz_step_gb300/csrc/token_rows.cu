@@ -338,10 +338,12 @@ cudaError_t dispatch(RowsParams p, cudaStream_t s) {
 template <typename T, typename O, bool SHIFT>
 cudaError_t combine(RowsParams p, cudaStream_t s) {
     constexpr int E = run_of<T, O>(), kU = sizeof(T) * E > 16 ? 1 : 2;
-    if (kU == 2 && !SHIFT && p.top_k <= 2) {
-        const unsigned grid = warp_items<E, 4>(p);
-        k_combine<T, O, E, false, 4><<<grid, kThreads, 0, s>>>(p);
-        return cudaGetLastError();
+    if constexpr (kU == 2 && !SHIFT) {
+        if (p.top_k <= 2) {
+            const unsigned grid = warp_items<E, 4>(p);
+            k_combine<T, O, E, false, 4><<<grid, kThreads, 0, s>>>(p);
+            return cudaGetLastError();
+        }
     }
     const unsigned grid = warp_items<E, kU, SHIFT ? kShared : 32>(p);
     k_combine<T, O, E, SHIFT, kU><<<grid, kThreads, 0, s>>>(p);
