@@ -507,9 +507,9 @@ MUON_API int muon_int4_quantize_weight(const void* w, int dtype, int batch, long
  * out = x W^T on weights of 4 bits, for one weight (offsets NULL) or for `groups` experts
  * over tokens sorted by expert, as the 8-bit products take them; rows outside every group
  * become zero.  x is not rounded: fp32 x counts with all its bits (from 2^-90 on), sums are
- * fp32 in units of 2^-11, rounded once to out_dtype.  Made for few tokens (of each expert), where the weights'
- * bytes are the time.  x 16-byte aligned with rows of a multiple of 16 bytes loads faster.
- * At most 512 groups.
+ * fp32 in units of 2^-11, rounded once to out_dtype.  Made for few
+ * tokens (up to 16 of one weight, about 8 of each expert); past those muon_fp8_linear is faster.  x
+ * 16-byte aligned with rows of a multiple of 16 bytes loads faster.  At most 512 groups.
  */
 MUON_API int muon_int4_linear(const void* x, int x_dtype, long long tokens, long long ld_x, const void* w_codes,
                               const void* w_scale, int block, int n, int k, int groups, const int* offsets, void* out,

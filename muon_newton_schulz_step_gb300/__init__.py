@@ -1253,7 +1253,9 @@ def _check_int4(w, offsets):
 def muon_int4_linear(x, w: Int4Matrix, *, offsets=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x W^T with a weight of 4 bits (``muon_int4_quantize_weight``), for serving: ``x``
     (tokens x k, bf16 or fp32) is not rounded.  With ``offsets``, tokens are sorted by expert
-    and ``w`` is stacked over experts; rows of no expert give zero.  The weight has no gradient."""
+    and ``w`` is stacked over experts; rows of no expert give zero.  The weight has no gradient.
+    Made for few tokens: past 16 of one weight, or about 8 of each expert, ``muon_fp8_linear``, which
+    rounds x to 8 bits, is the faster one."""
     if stream is not None:
         with _on(stream):
             return muon_int4_linear(x, w, offsets=offsets, out_dtype=out_dtype)

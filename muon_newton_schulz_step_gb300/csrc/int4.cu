@@ -3,19 +3,25 @@
 // Serving makes these products for one token, or a few for each expert: their time is the
 // weights' bytes, a quarter of bf16's.  Codes become bf16 exactly, x is bf16 (fp32 is
 // taken as the sum of three bf16), products of 16 columns run on mma.sync with fp32 sums, and
-// a scale multiplies the sum over its columns, so nothing is rounded before the result.
+// a scale multiplies the sum over its columns, so no operand is rounded.
 //
-// Bound by instructions: a lane's word of eight codes costs 9 to take out and turn into bf16 (two
-// codes at a time: mask and offset in one three-way operation, one fused multiply-add); a unit of 32
-// rows x 128 columns is 16 words a lane, 144 instructions of 307 in all, and 16 products of 16 x 16 x
-// 8.  On the vector units each word and token would cost eight more.  (tcgen05 has nothing to add:
-// its operands would take a trip through shared memory, and the tensor core is 12 - 20 % busy.)
+// A lane's word of eight codes costs 9 instructions to take out and turn into bf16 (two codes at a
+// time: mask and offset in one three-way operation, one fused multiply-add).  A unit of 32 rows x 128
+// columns is 16 words a lane, 144 instructions of 307 in all with scales of 128 columns, of 328 with 64
+// and 361 with 32, and 16 products of 16 x 16 x 8; one of 16 rows, scales of 128, 278 with its share of
+// the launch's.  On the vector units each word and token would cost eight more.
+//
 // Device time, bf16 x: one token x 6144 x 6144 8.4 us (weights of 19.5 MB, 2.9 us at the rate of a
-// copy; 9.1 from memory; 12.7 with loads through registers and no ring), 8 tokens 9.0, 64 tokens 32,
-// 512 tokens 195; 256 rows over 96 experts of 2048 x 6144 122 us, with scales of 32 columns 129 (534 MB
-// read, 4.1 TB/s; the copies alone, without products, take 99 and 104).  fp32 x, three times the
-// products and its split: 16 us for one token.  Two warps to a row's
-// reduction instead of eight gained 1 % for the experts, shifts by multiplication lost 10: not kept.
+// copy; 9.0 from memory; 12.7 with loads through registers and no ring), 8 tokens 9.1.  A fixed part
+// bounds it: one token takes 4.2 us for 16 rows of k = 6144, 4.7 for 2048, and from 8192 rows (9.2) on 0.69 us
+// for 1024 more (4.7 TB/s); its instructions alone would take 4.4 us of the SMs' issue slots.
+// 256 rows over 96 experts of 2048 x 6144, of which 75 have rows: 122 us, with scales of 32 columns 129
+// (534 MB read, 4.1 TB/s); bound by the copies, which alone, without products, take 99 and 104, with issue slots
+// 57 - 62 % busy beside them.  Past 16 tokens of a weight the time goes with the tokens, 18 us for 32, 32 for
+// 64, 195 for 512: every 16 tokens take the codes out again.  (Below that tcgen05 would add a trip
+// of its operands through shared memory, and the tensor core is 12 - 22 % busy.)  fp32 x, three times the
+// products and its split: 15 us for one token.  Two warps to a row's reduction instead of eight gained 1 % for
+// the experts, shifts by multiplication lost 10: not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -154,10 +160,11 @@ struct Unit {
     uint32_t scale[RT * 8][4];                             // bf16 pairs of a pair of rows, the unit's scales
 };
 
-// Units under way and the sums of one or two items.  Two blocks per SM, three where RT is 1 (by
-// registers).  With six units (RT 1) the start of a block costs more than it gains, one token x 6144
-// x 6144 9.5 us against 8.4 with three and 8.1 with two (10.1, 9.1 and 9.1 with the weight from
-// memory; a third as many rows 6.6, 6.0 and 6.9).
+// Units under way and the sums of one or two items.  Two blocks per SM, three where RT and PARTS are
+// 1 (by registers: the tiles of 16 tokens fill the 128 of two blocks, and keep 16 to 64 bytes of a lane in
+// local memory for scales of 32 and 64 columns, with fp32 x of 64 and 128; those of 8 tokens at most 8).  With six
+// units (RT 1) the start of a block costs more than it gains, one token x 6144 x 6144 9.5 us against 8.4 with
+// three and 8.1 with two (10.1, 9.1 and 9.1 with the weight from memory; a third as many rows 6.6, 6.0 and 6.9).
 template <int PARTS, int RT, int NT>
 struct Shape {
     static constexpr int kStages = 3;

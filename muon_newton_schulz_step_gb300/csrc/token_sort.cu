@@ -36,8 +36,9 @@ __device__ __forceinline__ int bucket_of(const SortParams& p, int expert) {
     return e < static_cast<unsigned>(p.experts) ? static_cast<int>(e) + 1 : 0;
 }
 
-// The lanes with this lane's bucket, bit by bit: up to ten votes, where match.any takes its
-// time by the number of different buckets (4096 entries of 384 experts: 9.4 us with it, 7.9).
+// The lanes with this lane's bucket, bit by bit: a vote for the lanes that have an entry and up to
+// eleven (1025 buckets), where match.any takes its time by the number of different buckets (4096 entries of 384
+// experts: 9.4 us with it, 7.9).
 __device__ __forceinline__ unsigned lanes_of(int bucket, int bits) {
     unsigned same = __ballot_sync(0xffffffffu, bucket >= 0);
     for (int i = 0; i < bits; ++i) {
