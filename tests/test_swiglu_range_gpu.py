@@ -55,3 +55,20 @@ def test_fp32_up_to_where_the_exponential_ends():
     within(d_up, want, want.abs() * 5.01 * U + (x.abs() + 1) * 2.0 ** (20 - 150))
     want = s * (1 + x * (1 - s)) * 2.0 ** 120
     within(d_gate, want, want.abs() * 6.01 * U + x.abs() * 2.0 ** (120 - 150))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [24, 12])                   # one type's runs of 16 bytes, and elements of views below
+def test_ends_of_both_types(dtype, cols):
+    """Gates whose exponential is 0 or infinite: the result is gate * up, or zero."""
+    ends = [-3e38, -1e30, -200.0, -104.0, 0.0, -0.0, 104.0, 200.0, 1e30, 3e38, float("inf"), float("nan")]
+    g = torch.tensor([ends * (cols // 12)] * 3, device="cuda").to(dtype)
+    both = torch.empty(3, 2 * cols + 1, dtype=dtype, device="cuda")
+    for gate, one in ((g, torch.ones_like(g)), (both[:, :cols].copy_(g), both[:, cols + 1:].fill_(1))):
+        out = mg.muon_swiglu(gate, one).float()
+        want = torch.where(g.float() > 0, g.float(), torch.zeros_like(out))
+        assert torch.equal(out.nan_to_num(7.0, float("inf"), -float("inf")), torch.where(g.isnan(), 7.0, want))
+        d_gate, d_up = (t.float() for t in mg.muon_swiglu_backward(one, gate, one))
+        fine = g.isfinite() & (g.abs() > 1)
+        assert torch.equal(d_gate[fine], (g.float() > 0).float()[fine]) and torch.equal(d_up[fine], want[fine])
+        assert (d_gate[(g == 0)] == 0.5).all() and (d_up[g == 0] == 0).all() and d_gate[g.isnan()].isnan().all()
