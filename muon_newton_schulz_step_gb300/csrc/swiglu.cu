@@ -14,11 +14,12 @@
 // an exact division: out is off by 5 units of 2^-24 of its value (the exponential 2, the sum, the quotient
 // and the product one each), what gate / (1 + exp(-gate)) * up in fp32 is.  bf16 takes the fast
 // exponential (off by 2 + 1.173 |gate| units of 2^-23 by its documentation, 2^-16 at |gate| = 80) and
-// the fast quotient (2 units): far below half a step of bf16, 2^-8.  In full they cost fp32 nothing where rows
-// load in 16 bytes (28042 x 916 45.4 and 74.9 us, as with the fast ones; 65536 x 2048 229 and 382), and 58 us for 54
-// where they go by single elements (28042 x 915, halves of one product; gradient 82 for 79).  Both lose what lies below their
-// exponents: fp32 gives 0 below gate = -88.7, where exp(-gate) is infinite, bf16 below -87.3, where the fast
-// quotient is 0; there the result is below 2^-119 of up.  gate = -inf gives NaN, as its product -inf * 0 does.
+// the fast quotient (2 units): far below half a step of bf16, 2^-8.  The full ones cost fp32 nothing where rows
+// load in 16 bytes (28042 x 916 45.4 and 74.9 us, as with the fast ones; 65536 x 2048 229 and 382), and 58 us
+// for 54 where they go by single elements (28042 x 915, halves of one product; gradient 82 for 79).  Both
+// types lose what lies below their exponents: fp32 gives 0 below gate = -88.7, where exp(-gate) is infinite,
+// bf16 below -87.3, where the fast quotient is 0; there the result is below 2^-119 of up.  gate = -inf gives
+// NaN, as its product -inf * 0 does.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
